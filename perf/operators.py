@@ -15,7 +15,8 @@ A pool row holds one token: groups of ``gs`` KV heads (the largest power of
 two up to 8 that divides the head count), each group its heads' E2M1 codes
 (two to a byte, the even element in the low nibble), then one E4M3 scale per
 head and 16 elements, padded to a multiple of 16 bytes.  An element reads as
-``code * block scale * head scale``.
+``code * block scale * head scale``; the store divides by ``block scale *
+head scale`` and rounds to the nearest code.
 
 ``own`` selects the framework's calls; else ``run`` computes the plain form
 with elementary torch operations in 32 bits.
@@ -50,10 +51,10 @@ def quantise_rows(x, head_scale):
     """x fp32 [T, Hkv, d] to pool rows uint8 [T, row_bytes] (padding zero)."""
     T, hkv, d = x.shape
     groups, gs, code, sc, gb = layout(hkv, d)
-    y = (x / head_scale[:, None]).reshape(T, hkv, d // 16, 16)
-    s8 = (y.abs().amax(-1) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
-    s = s8.float()
-    z = torch.where(s[..., None] > 0, y / s[..., None], torch.zeros_like(y))
+    x = x.reshape(T, hkv, d // 16, 16)
+    s8 = (x.abs().amax(-1) / head_scale[:, None] / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    step = (s8.float() * head_scale[:, None])[..., None]
+    z = torch.where(step > 0, x / step, torch.zeros_like(x))
     a = z.abs()
     c = (a > 0.25).to(torch.uint8)
     for edge, up in ((0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
@@ -523,11 +524,12 @@ def single(x):
 
 def exact_rows(x, head_scale):
     """What the store keeps of x [T, Hkv, d] (64 bits): the quotients are single-precision divisions, as the format says."""
-    y = single(x / head_scale.double()[:, None]).reshape(*x.shape[:-1], -1, 16)
-    s = nearest(single(y.abs().amax(-1, keepdim=True) / 6.0), e4m3_table())
-    z = single(y / torch.where(s > 0, s, torch.ones_like(s)))
+    g = head_scale.double()[:, None, None]
+    y = x.reshape(*x.shape[:-1], -1, 16)
+    s = nearest(single(single(y.abs().amax(-1, keepdim=True) / g) / 6.0), e4m3_table())
+    z = single(y / torch.where(s > 0, single(s * g), torch.ones_like(s)))
     kept = torch.where(s > 0, nearest(z.abs(), GRID) * torch.sign(z) * s, torch.zeros_like(z))
-    return kept.reshape(x.shape) * head_scale.double()[:, None]
+    return (kept * g).reshape(x.shape)
 
 
 def exact_values(rows, hkv, d, head_scale):
