@@ -4,6 +4,8 @@
  * Exact attention over a paged KV cache, as a serving engine runs it:
  *   pa_store_kv          write the new tokens' K/V rows into the paged pool
  *   pa_store_kv_fp8      the same into an FP8 (E4M3) pool with per-head scales
+ *   pa_store_kv_fp4      the same into a 4-bit pool (E2M1 with a scale per 16 elements)
+ *   pa_load_kv_fp4       rows of a 4-bit pool back as bf16
  *   pa_rope_store_kv     rotary embedding of q and k fused with the K/V store
  *   pa_rope_cos_sin_table  the rotary cos/sin table (host)
  *   pa_build_seqlens     per-request boundaries from the three lengths (host)
@@ -92,11 +94,15 @@ const char *pa_last_error(void);
  * `stream` first.  *bits receives an OR of PA_DEVERR_* (0 = clean). */
 pa_status pa_device_error(int32_t *bits, void *stream);
 
-/* Element type of the K/V pools read by pa_prefill and pa_decode.  FP8 pools hold E4M3
+/* Element type of the K/V pools read by pa_prefill and pa_decode.  4-bit pools hold the
+ * rows that pa_store_kv_fp4 writes (the layout stands there); on them the contractions run
+ * in f16 with fp32 accumulation, K and V exact in it, q rounded to f16 (exact for bf16
+ * values of magnitude 2^-14 .. 65504; |q| must stay below 65504) and P rounded to f16; the
+ * head scales are factors of the scores and of the output.  FP8 pools hold E4M3
  * codes written by pa_store_kv_fp8 with per-KV-head scales.  On FP8 pools the
  * contractions run in f16 with fp32 accumulation: q * k_scale is rounded to
  * f16 (|q * k_scale| must stay below 65504), P is rounded to f16. */
-typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
+typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_FP4 = 2 } pa_kv_dtype;
 
 /*
  * pa_store_kv - KV-cache store ([T] s.1-2, "RoPE + KV cache store"):
@@ -134,6 +140,56 @@ pa_status pa_store_kv_fp8(const void *k, const void *v, const int32_t *slot_mapp
                           const float *v_scale, void *stream);
 
 /*
+ * 4-bit pools (PA_KV_FP4; the pages name quantized KV layouts in [T] s.19 and
+ * s.24 without fixing one; this library's reading).  A token's row holds, for
+ * K and for V each, its heads in groups of gs = the largest power of two up to
+ * 8 that divides Hkv; group i of a row starts at byte i * group_bytes and is
+ *   gs * head_dim / 2 bytes   E2M1 codes of heads i * gs .. i * gs + gs - 1,
+ *                             two to a byte, element 2j in the low nibble
+ *   gs * head_dim / 16 bytes  E4M3 scales, head-dim block b of 16 elements of
+ *                             the group's head h at byte h * head_dim / 16 + b
+ * padded to a multiple of 16 bytes (padding is neither read nor written).  A
+ * pool is [num_slots, pa_fp4_row_bytes] bytes, slot = page * page_size +
+ * offset as for the other pools: 9 / 32 of a bf16 pool's size.
+ * E2M1: sign, 2 exponent bits, 1 mantissa bit; 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * Element c reads as value(code) * value(scale) * head_scale[h].  The store
+ * computes, in IEEE single operations rounded to nearest even,
+ *   scale = E4M3(max|x| / head_scale / 6), at most 448, over the block,
+ *   code  = E2M1(x / (scale * head_scale)), at most 6 in magnitude,
+ * and zeros where scale * head_scale is 0.  A block that holds a NaN gets the
+ * scale NaN and reads as NaN; infinities saturate.  A head scale of the
+ * head's largest magnitude / 2688 uses the whole range of both.
+ * pa_fp4_row_bytes: bytes of a row of K (or V); 0 for heads it does not hold
+ * (head_dim 64 or 128, Hkv * head_dim <= 4096).
+ */
+int64_t pa_fp4_row_bytes(int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * pa_store_kv_fp4 - KV-cache store into a 4-bit pool.
+ * k, v:             device bf16 [num_tokens, Hkv, head_dim]
+ * k_cache, v_cache: device bytes [num_slots, pa_fp4_row_bytes(Hkv, head_dim)]
+ * k_scale, v_scale: device fp32 [Hkv], positive and finite
+ * slot_mapping: as for pa_store_kv.
+ */
+pa_status pa_store_kv_fp4(const void *k, const void *v, const int32_t *slot_mapping,
+                          int64_t num_tokens, void *k_cache, void *v_cache, int64_t num_slots,
+                          int32_t num_kv_heads, int32_t head_dim, const float *k_scale,
+                          const float *v_scale, void *stream);
+
+/*
+ * pa_load_kv_fp4 - rows of a 4-bit pool as bf16 (a cached prefix handed to
+ * another pool, engine or host): k_out[t, h, c], v_out[t, h, c] = the element
+ * of row slots[t], code * scale exactly, times the head scale rounded in
+ * single precision, then to bf16.  A negative slot gives a row of zeros; a
+ * slot >= num_slots too, and raises PA_DEVERR_PAGE_RANGE.  A slot may occur
+ * any number of times.
+ */
+pa_status pa_load_kv_fp4(const int32_t *slots, int64_t num_tokens, const void *k_cache,
+                         const void *v_cache, int64_t num_slots, int32_t num_kv_heads,
+                         int32_t head_dim, const float *k_scale, const float *v_scale,
+                         void *k_out, void *v_out, void *stream);
+
+/*
  * pa_rope_cos_sin_table - rotary table on the HOST ([T] s.2 "RoPE + KV cache
  * store"; the pages do not define the rotation, this library's reading is
  * the standard rotary embedding): for p < max_pos and i < rot_dim / 2,
@@ -155,8 +211,8 @@ pa_status pa_rope_cos_sin_table(float *cos_sin, int32_t max_pos, int32_t rot_dim
  * for pair i:  (a, b) -> (a*c - b*s, b*c + a*s), each product and the sum
  * rounded in fp32, the result rounded to bf16; elements past rot_dim are
  * copied.  Rotated q goes to q_out (which may be q itself); rotated k and v
- * are stored to row slot_mapping[t] exactly as pa_store_kv (bf16 pools) or
- * pa_store_kv_fp8 (FP8 pools, from the bf16 rotated k) store them; a
+ * are stored to row slot_mapping[t] exactly as pa_store_kv (bf16 pools),
+ * pa_store_kv_fp8 or pa_store_kv_fp4 (from the bf16 rotated k) store them; a
  * negative slot stores nothing (q is still rotated).  A position outside
  * [0, max_pos) writes nothing for that token and raises PA_DEVERR_POSITION.
  */
@@ -174,12 +230,12 @@ typedef struct {
     int64_t num_tokens;
     int32_t num_q_heads;
     int32_t num_kv_heads;
-    int32_t head_dim;            /* multiple of 16 */
-    void *k_cache;               /* [num_slots, Hkv, head_dim] bf16, or E4M3 codes */
+    int32_t head_dim;            /* multiple of 16 (4-bit pools: 64 or 128) */
+    void *k_cache;               /* [num_slots, Hkv, head_dim] bf16, or E4M3 codes, or 4-bit rows */
     void *v_cache;
     int64_t num_slots;
     int32_t kv_dtype;            /* pa_kv_dtype of the pools */
-    const float *k_scale;        /* FP8 pools: device fp32 [Hkv] */
+    const float *k_scale;        /* FP8 and 4-bit pools: device fp32 [Hkv] */
     const float *v_scale;
 } pa_rope_store_params;
 
@@ -263,7 +319,7 @@ typedef struct {
     float *lse;                  /* optional fp32 [Hq, lse_stride]; NULL = not written */
     int64_t lse_stride;          /* >= total_q when lse != NULL */
     int32_t kv_dtype;            /* pa_kv_dtype of k_cache / v_cache (0 = bf16) */
-    const float *k_scale;        /* PA_KV_FP8_E4M3: device fp32 [Hkv]; else unused */
+    const float *k_scale;        /* FP8 and 4-bit pools: device fp32 [Hkv]; else unused */
     const float *v_scale;
     int32_t sliding_window;      /* 0 = none; W > 0: a query at position p sees only keys
                                     j >= p - (W - 1) ([T] s.19 "sliding window" mask) */
@@ -325,9 +381,10 @@ typedef struct {
     void *workspace;             /* device, >= pa_decode_workspace_size(p) bytes */
     size_t workspace_bytes;
     int32_t kv_chunk;            /* minimum keys per split, multiple of 16;
-                                    0 = automatic (max_seqlen_k / 32, >= 64) */
+                                    0 = automatic (max_seqlen_k / 32, >= 64; on 4-bit pools
+                                    less where the batch would not fill the GPU) */
     int32_t kv_dtype;            /* pa_kv_dtype of k_cache / v_cache (0 = bf16) */
-    const float *k_scale;        /* PA_KV_FP8_E4M3: device fp32 [Hkv]; else unused */
+    const float *k_scale;        /* FP8 and 4-bit pools: device fp32 [Hkv]; else unused */
     const float *v_scale;        /* (element = value(code) * scale[kv head]) */
     int32_t sliding_window;      /* 0 = none; W > 0: only the last W keys of each sequence
                                     are read and attended to */
@@ -373,7 +430,8 @@ pa_status pa_decode(const pa_decode_params *p, void *stream);
  *  - Both halves: the same k_cache / v_cache / num_pages / page_size / head
  *    counts / head_dim and pool type (bf16, or FP8 with the same k_scale and
  *    v_scale); an even GQA group and num_kv_heads % 4 == 0; no window or
- *    block mask on the prefill half (a decode window is fine);
+ *    block mask on the prefill half (a decode window is fine); no 4-bit
+ *    pools (a batch of both kinds over them is pa_prefill and pa_decode);
  *    dec->overlap_previous = 0, dec->max_ctas ignored.
  *    Otherwise PA_ERR_UNSUPPORTED / PA_ERR_INVALID, nothing launched.
  *  - A batch with no prefill rows is pa_decode(dec); one with no decode

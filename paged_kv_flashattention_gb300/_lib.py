@@ -69,6 +69,9 @@ SIGNATURES = {
     "pa_device_error": (ctypes.c_int, [ctypes.POINTER(c_i32), c_p]),
     "pa_store_kv": (ctypes.c_int, [c_p, c_p, c_p, c_i64, c_p, c_p, c_i64, c_i32, c_i32, c_p]),
     "pa_store_kv_fp8": (ctypes.c_int, [c_p, c_p, c_p, c_i64, c_p, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p]),
+    "pa_fp4_row_bytes": (c_i64, [c_i32, c_i32]),
+    "pa_store_kv_fp4": (ctypes.c_int, [c_p, c_p, c_p, c_i64, c_p, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p]),
+    "pa_load_kv_fp4": (ctypes.c_int, [c_p, c_i64, c_p, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p, c_p, c_p]),
     "pa_rope_cos_sin_table": (ctypes.c_int, [c_p, c_i32, c_i32, ctypes.c_double]),
     "pa_rope_store_kv": (ctypes.c_int, [ctypes.POINTER(RopeStoreParams), c_p]),
     "pa_build_seqlens": (ctypes.c_int, [c_p, c_p, c_i32, c_p, c_p, c_p, c_p, c_p]),

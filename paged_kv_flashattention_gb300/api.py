@@ -52,15 +52,29 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-PA_KV_BF16, PA_KV_FP8_E4M3 = 0, 1
+PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_FP4 = 0, 1, 2
 _FP8_DTYPES = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
 
 
-def _kv_dtype(k_cache: torch.Tensor, v_cache: torch.Tensor) -> int:
+def _kv_dtype(k_cache: torch.Tensor, v_cache: torch.Tensor, asked: int | None = None) -> int:
     """PA_KV_BF16 for bf16 pools, PA_KV_FP8_E4M3 for E4M3 codes (uint8 or
-    torch.float8_e4m3fn)."""
+    torch.float8_e4m3fn); PA_KV_FP4 only where the caller asks for it (4-bit
+    rows are uint8 as well)."""
     if k_cache.dtype != v_cache.dtype:
         raise TypeError("k_cache and v_cache dtypes differ")
+    if asked is not None and asked not in (PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_FP4):
+        raise ValueError(f"kv_dtype {asked} is not PA_KV_BF16, PA_KV_FP8_E4M3 or PA_KV_FP4")
+    if asked == PA_KV_FP4:
+        if k_cache.dtype != torch.uint8:
+            raise TypeError(f"4-bit pools are uint8 rows, got {k_cache.dtype}")
+        return PA_KV_FP4
+    found = _kv_dtype_of(k_cache)
+    if asked is not None and asked != found:
+        raise TypeError(f"kv_dtype {asked} does not match pools of {k_cache.dtype}")
+    return found
+
+
+def _kv_dtype_of(k_cache: torch.Tensor) -> int:
     if k_cache.dtype == torch.bfloat16:
         return PA_KV_BF16
     if k_cache.dtype in _FP8_DTYPES:
@@ -71,7 +85,7 @@ def _kv_dtype(k_cache: torch.Tensor, v_cache: torch.Tensor) -> int:
 def _need_scales(k_scale, v_scale, Hkv: int, dev):
     for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if t is None:
-            raise ValueError(f"{n} is required for FP8 pools")
+            raise ValueError(f"{n} is required for FP8 and 4-bit pools")
         _need(t, n, torch.float32, dev)
         if t.numel() != Hkv:
             raise ValueError(f"{n} must hold one scale per KV head ({Hkv})")
@@ -153,6 +167,80 @@ def store_kv_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                                num_slots, Hkv, d, _ptr(k_scale), _ptr(v_scale), _stream(k_cache)), lib)
 
 
+def fp4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one token's row in a 4-bit pool of K (or of V): a pool is a
+    uint8 tensor [num_pages, page_size, fp4_row_bytes(Hkv, d)]."""
+    lib = _lib.load()
+    n = int(lib.pa_fp4_row_bytes(int(num_kv_heads), int(head_dim)))
+    if n == 0:
+        raise ValueError(lib.pa_last_error().decode(errors="replace"))
+    return n
+
+
+def _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int, dev):
+    """Checks a pair of 4-bit pools for Hkv heads of size d."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, torch.uint8, dev)
+    _need_scales(k_scale, v_scale, Hkv, dev)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if k_cache.dim() not in (2, 3) or k_cache.shape[-1] != fp4_row_bytes(Hkv, d):
+        raise ValueError(f"a 4-bit pool of {Hkv} heads of size {d} is [num_pages, page_size, {fp4_row_bytes(Hkv, d)}] "
+                         f"bytes, got {tuple(k_cache.shape)}")
+
+
+def store_kv_fp4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                 k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor) -> None:
+    """Write token t's K/V rows into row slot_mapping[t] of 4-bit pools (E2M1
+    codes with an E4M3 scale per 16 elements and an fp32 scale per head).  k,
+    v: bf16 [T, Hkv, d], d 64 or 128; caches: uint8 [num_pages, page_size,
+    fp4_row_bytes(Hkv, d)] or [num_slots, row bytes]; k_scale, v_scale: fp32
+    [Hkv], best the head's largest magnitude / 2688.  A negative slot is
+    skipped."""
+    dev = k_cache.device
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, torch.bfloat16, dev)
+    _need(slot_mapping, "slot_mapping", torch.int32, dev)
+    if k.dim() != 3 or v.shape != k.shape or slot_mapping.numel() != k.shape[0]:
+        raise ValueError("k and v must be [T, Hkv, d] with one slot per token")
+    T, Hkv, d = k.shape
+    _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    lib = _lib.load()
+    with torch.cuda.device(dev):
+        _check(lib.pa_store_kv_fp4(_ptr(k), _ptr(v), _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache),
+                                   k_cache.numel() // k_cache.shape[-1], Hkv, d, _ptr(k_scale), _ptr(v_scale),
+                                   _stream(k_cache)), lib)
+
+
+def load_kv_fp4(slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                v_scale: torch.Tensor, head_dim: int, *, k_out: torch.Tensor | None = None,
+                v_out: torch.Tensor | None = None):
+    """The rows ``slots`` (int32 [T]) of 4-bit pools as bf16 (k, v), each
+    [T, Hkv, head_dim]; Hkv is the number of scales.  A negative slot gives
+    zeros."""
+    dev = k_cache.device
+    _need(slots, "slots", torch.int32, dev)
+    if k_scale is None:
+        raise ValueError("k_scale is required for FP8 and 4-bit pools")
+    T, Hkv, d = slots.numel(), k_scale.numel(), int(head_dim)
+    _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _need(t, n, torch.bfloat16, dev)
+        if tuple(t.shape) != (T, Hkv, d):
+            raise ValueError(f"{n} must be [{T}, {Hkv}, {d}]")
+    lib = _lib.load()
+    with torch.cuda.device(dev):
+        _check(lib.pa_load_kv_fp4(_ptr(slots), T, _ptr(k_cache), _ptr(v_cache), k_cache.numel() // k_cache.shape[-1],
+                                  Hkv, d, _ptr(k_scale), _ptr(v_scale), _ptr(k_out), _ptr(v_out),
+                                  _stream(k_cache)), lib)
+    return k_out, v_out
+
+
 def rope_cos_sin_table(max_pos: int, rot_dim: int, base: float = 10000.0) -> torch.Tensor:
     """Host fp32 [max_pos, rot_dim] rotary table (cos of the rot_dim/2 angles
     p * base^(-2i/rot_dim), then their sin), computed by the C library."""
@@ -167,23 +255,30 @@ def rope_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
                   cos_sin: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
                   v_cache: torch.Tensor, *, q_out: torch.Tensor | None = None,
                   interleaved: bool = False, k_scale: torch.Tensor | None = None,
-                  v_scale: torch.Tensor | None = None) -> torch.Tensor:
+                  v_scale: torch.Tensor | None = None, kv_dtype: int | None = None) -> torch.Tensor:
     """Rotary embedding of q and k at ``positions`` fused with the K/V store.
     q bf16 [T, Hq, d]; k, v bf16 [T, Hkv, d]; cos_sin fp32 [max_pos, rot_dim]
-    on the device; pools bf16 or E4M3 (with ``k_scale``/``v_scale``).  Returns
-    the rotated q (``q_out``, which may be ``q``)."""
+    on the device; pools bf16 or E4M3 (with ``k_scale``/``v_scale``), or with
+    ``kv_dtype=PA_KV_FP4`` 4-bit rows (``store_kv_fp4``).  Returns the rotated
+    q (``q_out``, which may be ``q``)."""
     dev = q.device
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, n, torch.bfloat16, dev)
     _need(positions, "positions", torch.int32, dev)
     _need(slot_mapping, "slot_mapping", torch.int32, dev)
     _need(cos_sin, "cos_sin", torch.float32, dev)
-    kvd = _kv_dtype(k_cache, v_cache)
+    kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n, k_cache.dtype, dev)
     T, Hq, d = q.shape
-    Hkv = k_cache.shape[-2]
-    if k_cache.shape[-1] != d or k.numel() != T * Hkv * d or v.numel() != T * Hkv * d:
+    if kvd == PA_KV_FP4:
+        if k.dim() != 3:
+            raise ValueError("k must be [T, Hkv, d]")
+        Hkv = k.shape[1]
+        _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    else:
+        Hkv = k_cache.shape[-2]
+    if (kvd != PA_KV_FP4 and k_cache.shape[-1] != d) or k.numel() != T * Hkv * d or v.numel() != T * Hkv * d:
         raise ValueError("k/v/pool shapes do not match q")
     if positions.numel() != T or slot_mapping.numel() != T:
         raise ValueError("positions and slot_mapping must hold one entry per token")
@@ -197,11 +292,12 @@ def rope_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
         cos_sin=_ptr(cos_sin), max_pos=cos_sin.shape[0], rot_dim=cos_sin.shape[1],
         interleaved=int(bool(interleaved)), slot_mapping=_ptr(slot_mapping), num_tokens=T,
         num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, k_cache=_ptr(k_cache), v_cache=_ptr(v_cache),
-        num_slots=k_cache.numel() // (Hkv * d), kv_dtype=kvd,
-        k_scale=_ptr(k_scale) if kvd == PA_KV_FP8_E4M3 else None,
-        v_scale=_ptr(v_scale) if kvd == PA_KV_FP8_E4M3 else None)
+        num_slots=k_cache.numel() // (k_cache.shape[-1] if kvd == PA_KV_FP4 else Hkv * d), kv_dtype=kvd,
+        k_scale=_ptr(k_scale) if kvd != PA_KV_BF16 else None,
+        v_scale=_ptr(v_scale) if kvd != PA_KV_BF16 else None)
     lib = _lib.load()
-    _check(lib.pa_rope_store_kv(ctypes.byref(p), _stream(q)), lib)
+    with torch.cuda.device(dev):
+        _check(lib.pa_rope_store_kv(ctypes.byref(p), _stream(q)), lib)
     return q_out
 
 
@@ -265,6 +361,22 @@ def _pool_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, page_size: int 
     return int(num_pages), int(P), int(Hkv), int(d)
 
 
+def _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, d: int):
+    """_pool_geometry of 4-bit pools [pages, page_size, row bytes] or [slots,
+    row bytes]; the heads are counted by the scales."""
+    if k_scale is None:
+        raise ValueError("k_scale is required for FP8 and 4-bit pools")
+    Hkv = k_scale.numel()
+    _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, k_cache.device)
+    if k_cache.dim() == 3:
+        if page_size is not None and page_size != k_cache.shape[1]:
+            raise ValueError("page_size does not match the pool shape")
+        return int(k_cache.shape[0]), int(k_cache.shape[1]), Hkv, d
+    if page_size is None:
+        raise ValueError("page_size is required for a [slots, row bytes] pool")
+    return k_cache.shape[0] // int(page_size), int(page_size), Hkv, d
+
+
 # Zeroed scheduler arrays of pa_prefill, one per (device, stream): launches on
 # one stream run one after the other, so they can share one array (each
 # launch leaves it at zero); launches on different streams get their own.
@@ -309,11 +421,12 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_
             lse: torch.Tensor | None = None, k_scale: torch.Tensor | None = None,
             v_scale: torch.Tensor | None = None, sliding_window: int = 0,
             max_ctas: int = 0, scheduler: torch.Tensor | None = None,
-            block_mask: torch.Tensor | None = None) -> torch.Tensor:
+            block_mask: torch.Tensor | None = None, kv_dtype: int | None = None) -> torch.Tensor:
     """Varlen prefill / extend attention.  q: bf16 [total_q, Hq, d];
     returns out bf16 [total_q, Hq, d]; lse (optional) fp32 [Hq, total_q].
     Pools are bf16, or E4M3 codes (uint8 / float8_e4m3fn) with fp32
-    per-KV-head ``k_scale`` and ``v_scale``.  ``scheduler`` is the int32 [2]
+    per-KV-head ``k_scale`` and ``v_scale``, or, with ``kv_dtype=PA_KV_FP4``,
+    4-bit rows with such scales (``store_kv_fp4``).  ``scheduler`` is the int32 [2]
     work-counter array of the launch (zero between launches); by default the
     array cached for the current stream (``prefill_scheduler``).
     ``block_mask``: optional uint8 [B, nq, nk] on the device; entry
@@ -321,7 +434,7 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_
     (rows counted from the request's first row)."""
     p, out = _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                              max_seqlen_k, causal, scale, page_size, out, lse, k_scale, v_scale, sliding_window,
-                             max_ctas, scheduler, block_mask, PA_PREFILL_SCHEDULER_INTS)
+                             max_ctas, scheduler, block_mask, PA_PREFILL_SCHEDULER_INTS, kv_dtype)
     lib = _lib.load()
     _check(lib.pa_prefill(ctypes.byref(p), _stream(q)), lib)
     return out
@@ -329,11 +442,14 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_
 
 def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                     causal, scale, page_size, out, lse, k_scale, v_scale, sliding_window, max_ctas, scheduler,
-                    block_mask, sched_ints):
+                    block_mask, sched_ints, kv_dtype=None):
     dev = q.device
-    num_pages, P, Hkv, d = _pool_geometry(k_cache, v_cache, page_size)
     _need(q, "q", torch.bfloat16, dev)
-    kvd = _kv_dtype(k_cache, v_cache)
+    kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
+    if kvd == PA_KV_FP4:
+        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, q.shape[-1])
+    else:
+        num_pages, P, Hkv, d = _pool_geometry(k_cache, v_cache, page_size)
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n, k_cache.dtype, dev)
     if kvd == PA_KV_FP8_E4M3:
@@ -369,8 +485,8 @@ def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k,
         num_kv_heads=Hkv, head_dim=d, page_size=P, num_pages=num_pages, causal=int(bool(causal)),
         scale=float(1.0 / math.sqrt(d) if scale is None else scale), out=_ptr(out),
         lse=_ptr(lse), lse_stride=(lse.stride(0) if lse is not None else 0), kv_dtype=kvd,
-        k_scale=_ptr(k_scale) if kvd == PA_KV_FP8_E4M3 else None,
-        v_scale=_ptr(v_scale) if kvd == PA_KV_FP8_E4M3 else None, sliding_window=int(sliding_window),
+        k_scale=_ptr(k_scale) if kvd != PA_KV_BF16 else None,
+        v_scale=_ptr(v_scale) if kvd != PA_KV_BF16 else None, sliding_window=int(sliding_window),
         max_ctas=int(max_ctas), scheduler=_ptr(scheduler), block_mask=_ptr(block_mask),
         block_mask_q_blocks=int(block_mask.shape[1]) if block_mask is not None else 0,
         block_mask_k_blocks=int(block_mask.shape[2]) if block_mask is not None else 0)
@@ -379,12 +495,15 @@ def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k,
 
 def _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k, scale, page_size,
                    out, lse, workspace, kv_chunk, k_scale=None, v_scale=None, sliding_window=0,
-                   max_ctas=0, overlap_previous=False):
-    num_pages, P, Hkv, d = _pool_geometry(k_cache, v_cache, page_size)
+                   max_ctas=0, overlap_previous=False, kv_dtype=None):
+    kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
+    if kvd == PA_KV_FP4:
+        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, q.shape[-1])
+    else:
+        num_pages, P, Hkv, d = _pool_geometry(k_cache, v_cache, page_size)
     B, Hq, dq = q.shape
     if dq != d:
         raise ValueError("head_dim of q and the pool differ")
-    kvd = _kv_dtype(k_cache, v_cache)
     if kvd == PA_KV_FP8_E4M3:
         _need_scales(k_scale, v_scale, Hkv, q.device)
     return _lib.DecodeParams(
@@ -396,29 +515,42 @@ def _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k,
         workspace=_ptr(workspace), workspace_bytes=(workspace.numel() * workspace.element_size()
                                                     if workspace is not None else 0),
         kv_chunk=int(kv_chunk), kv_dtype=kvd,
-        k_scale=_ptr(k_scale) if kvd == PA_KV_FP8_E4M3 else None,
-        v_scale=_ptr(v_scale) if kvd == PA_KV_FP8_E4M3 else None, sliding_window=int(sliding_window),
+        k_scale=_ptr(k_scale) if kvd != PA_KV_BF16 else None,
+        v_scale=_ptr(v_scale) if kvd != PA_KV_BF16 else None, sliding_window=int(sliding_window),
         max_ctas=int(max_ctas), overlap_previous=int(bool(overlap_previous)))
 
 
-def decode_workspace_size(q_shape, k_cache: torch.Tensor, max_seqlen_k: int, *,
-                          page_size: int | None = None, kv_chunk: int = 0) -> int:
-    """Workspace bytes pa_decode needs (0 when a single split suffices)."""
+def _decode_sizes(q_shape, k_cache, max_seqlen_k, page_size, kv_chunk, kv_dtype, num_kv_heads):
+    """The host fields that the decode's split layout depends on."""
     B, Hq, d = q_shape
-    num_pages, P, Hkv, dk = _pool_geometry(k_cache, k_cache, page_size)
-    p = _lib.DecodeParams(num_seqs=B, max_seqlen_k=int(max_seqlen_k), num_q_heads=Hq,
-                          num_kv_heads=Hkv, head_dim=d, page_size=P, num_pages=num_pages,
-                          scale=1.0, kv_chunk=int(kv_chunk))
+    if kv_dtype == PA_KV_FP4:
+        if num_kv_heads is None:
+            raise ValueError("num_kv_heads is required for 4-bit pools")
+        if k_cache.dim() == 2 and page_size is None:
+            raise ValueError("page_size is required for a [slots, row bytes] pool")
+        P = int(k_cache.shape[1] if k_cache.dim() == 3 else page_size)
+        num_pages, Hkv = k_cache.numel() // (k_cache.shape[-1] * P), int(num_kv_heads)
+    else:
+        kv_dtype = PA_KV_BF16                         # FP8 pools split alike
+        num_pages, P, Hkv, _ = _pool_geometry(k_cache, k_cache, page_size)
+    return _lib.DecodeParams(num_seqs=B, max_seqlen_k=int(max_seqlen_k), num_q_heads=Hq,
+                             num_kv_heads=Hkv, head_dim=d, page_size=P, num_pages=num_pages,
+                             scale=1.0, kv_chunk=int(kv_chunk), kv_dtype=kv_dtype)
+
+
+def decode_workspace_size(q_shape, k_cache: torch.Tensor, max_seqlen_k: int, *,
+                          page_size: int | None = None, kv_chunk: int = 0, kv_dtype: int | None = None,
+                          num_kv_heads: int | None = None) -> int:
+    """Workspace bytes pa_decode needs (0 when a single split suffices).
+    4-bit pools need ``kv_dtype=PA_KV_FP4`` and ``num_kv_heads``."""
+    p = _decode_sizes(q_shape, k_cache, max_seqlen_k, page_size, kv_chunk, kv_dtype, num_kv_heads)
     return int(_lib.load().pa_decode_workspace_size(ctypes.byref(p)))
 
 
 def decode_kv_chunk(q_shape, k_cache: torch.Tensor, max_seqlen_k: int, *,
-                    page_size: int | None = None, kv_chunk: int = 0) -> int:
-    B, Hq, d = q_shape
-    num_pages, P, Hkv, dk = _pool_geometry(k_cache, k_cache, page_size)
-    p = _lib.DecodeParams(num_seqs=B, max_seqlen_k=int(max_seqlen_k), num_q_heads=Hq,
-                          num_kv_heads=Hkv, head_dim=d, page_size=P, num_pages=num_pages,
-                          scale=1.0, kv_chunk=int(kv_chunk))
+                    page_size: int | None = None, kv_chunk: int = 0, kv_dtype: int | None = None,
+                    num_kv_heads: int | None = None) -> int:
+    p = _decode_sizes(q_shape, k_cache, max_seqlen_k, page_size, kv_chunk, kv_dtype, num_kv_heads)
     return int(_lib.load().pa_decode_kv_chunk(ctypes.byref(p)))
 
 
@@ -428,14 +560,15 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_t
            lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
            kv_chunk: int = 0, k_scale: torch.Tensor | None = None,
            v_scale: torch.Tensor | None = None, sliding_window: int = 0,
-           max_ctas: int = 0, overlap_previous: bool = False) -> torch.Tensor:
+           max_ctas: int = 0, overlap_previous: bool = False, kv_dtype: int | None = None) -> torch.Tensor:
     """Split-KV decode: q bf16 [B, Hq, d] -> out bf16 [B, Hq, d]; lse fp32 [B, Hq].
     Pools are bf16, or E4M3 codes (uint8 / float8_e4m3fn) with fp32 per-KV-head
-    ``k_scale`` and ``v_scale``.  ``workspace`` (a uint8 CUDA tensor) is
+    ``k_scale`` and ``v_scale``, or, with ``kv_dtype=PA_KV_FP4``, 4-bit rows
+    with such scales (``store_kv_fp4``).  ``workspace`` (a uint8 CUDA tensor) is
     allocated here when not given."""
     dev = q.device
     _need(q, "q", torch.bfloat16, dev)
-    kvd = _kv_dtype(k_cache, v_cache)
+    kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n, k_cache.dtype, dev)
     _need(cache_seqlens, "cache_seqlens", torch.int32, dev)
@@ -447,12 +580,14 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_t
     _need(out, "out", torch.bfloat16, dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
-    need = decode_workspace_size(q.shape, k_cache, max_seqlen_k, page_size=page_size, kv_chunk=kv_chunk)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        need = decode_workspace_size(q.shape, k_cache, max_seqlen_k, page_size=page_size, kv_chunk=kv_chunk, kv_dtype=kvd,
+                                     num_kv_heads=k_scale.numel() if kvd == PA_KV_FP4 and k_scale is not None else None)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     p = _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k, scale, page_size,
                        out, lse, workspace, kv_chunk, k_scale, v_scale, sliding_window, max_ctas,
-                       overlap_previous)
+                       overlap_previous, kvd)
     lib = _lib.load()
     _check(lib.pa_decode(ctypes.byref(p), _stream(q)), lib)
     return out
@@ -504,7 +639,8 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    scale: float | None = None, page_size: int | None = None,
                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                    kv_chunk: int = 0, k_scale: torch.Tensor | None = None,
-                   v_scale: torch.Tensor | None = None, sliding_window: int = 0) -> torch.Tensor:
+                   v_scale: torch.Tensor | None = None, sliding_window: int = 0,
+                   kv_dtype: int | None = None) -> torch.Tensor:
     """Split-KV decode through ``pa_decode_noalloc``: the split partials go to
     the library's fixed 32 MiB device scratch, so no workspace is allocated
     (for callers that may not allocate device memory).  Calls on one device
@@ -513,7 +649,7 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     cannot allocate; they are created here only for convenience."""
     dev = q.device
     _need(q, "q", torch.bfloat16, dev)
-    _kv_dtype(k_cache, v_cache)
+    kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n, k_cache.dtype, dev)
     _need(cache_seqlens, "cache_seqlens", torch.int32, dev)
@@ -526,7 +662,7 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     p = _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k, scale, page_size,
-                       out, lse, None, kv_chunk, k_scale, v_scale, sliding_window)
+                       out, lse, None, kv_chunk, k_scale, v_scale, sliding_window, kv_dtype=kvd)
     lib = _lib.load()
     _check(lib.pa_decode_noalloc(ctypes.byref(p), _stream(q)), lib)
     return out

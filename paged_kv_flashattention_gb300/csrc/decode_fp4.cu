@@ -1,0 +1,500 @@
+// Split-KV decode over 4-bit pools (row layout: fp4.cuh).
+//
+// The method is decode.cu's: persistent CTAs over equal ranges of the batch's
+// work list, online softmax, one partial (O, lse) per range and row, merged by
+// the log-sum-exp combine.  What differs:
+//   - The list counts units of 16 keys that start at multiples of 16 in their
+//     sequence, so that a unit never straddles two 16-token pages: its rows are
+//     one contiguous run of the pool when a row is one head group, and a unit
+//     is two bulk copies (K, V) instead of 32.
+//   - A CTA takes one head group (gs KV heads, one consumer warp each).
+//   - The codes are widened in registers: E2M1 to f16 by the hardware
+//     conversion, times the block's E4M3 scale (exact in f16, fp4.cuh), and
+//     both contractions run in f16 with fp32 accumulation.  The head's K scale
+//     is a factor of the score, its V scale one of the output, so neither q
+//     (bf16 values in f16's range are exact) nor K nor V is rounded; only P is.
+//
+// Fragments of mma.sync m16n8k16 (r8 = lane / 4, q4 = lane % 4).  The order of
+// the contracted index and of the rows is free, so each lane takes what lies
+// together in the row:
+//   S (16 keys x 8 heads) = K Q^T: lane q4 takes elements [D/4 q4, D/4 q4 + D/4)
+//     of its two keys: one 16-byte load per key (8 at D = 64) and two scales.
+//   O^T (D x 8 heads) += V^T P^T: lane r8 takes elements [D/8 r8, + D/8) of its
+//     four keys: one 8-byte load (4) and one scale per key; the words of two
+//     keys are interleaved nibble by nibble, so that a byte holds one element
+//     of both and converts to the pair the fragment wants.
+//   P goes from the score's layout to the second product's with movmatrix.
+// Row r of the score fragment is key r ^ ((r >> 1) & 1): with rows 64 bytes
+// apart modulo the banks' 128 this halves the conflicts of the V loads.
+//
+// The running maximum is lazy as in decode.cu; here a vote decides whether any
+// score exceeds it by more than 2^8, so that the usual unit needs no shuffle.
+#include <cuda_bf16.h>
+
+#include "decode_impl.cuh"
+#include "fp4.cuh"
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+PA_ERROR_WORD_ACCESSOR(error_word_decode_fp4)
+
+namespace {
+
+constexpr int kUnit = 16;         // keys of a unit
+
+struct Fp4DecodeArgs {
+    const __nv_bfloat16 *q;
+    const uint8_t *k_cache;
+    const uint8_t *v_cache;
+    const int32_t *page_table;
+    int64_t pt_stride;
+    const int32_t *cache_seqlens;
+    int32_t num_seqs;
+    int32_t num_q_heads;
+    int32_t group;                // query heads per KV head
+    int32_t page_size;
+    int64_t num_pages;
+    float scale_log2;
+    int32_t min_units;            // smallest range, in units
+    int32_t max_seqlen_k;
+    int32_t max_splits;
+    int32_t head_groups;
+    int32_t row_bytes;
+    float *o_part;
+    float *lse_part;
+    const float *k_scale;
+    const float *v_scale;
+    int32_t window;
+    int32_t *ws_header;           // [0] = T, in units
+    int32_t *ws_prefix;           // [B+1] exclusive prefix of the sequences' units
+};
+
+template <int D, int HPC>
+struct Fp4Smem {
+    static constexpr int kCodes = HPC * D / 2;
+    static constexpr int kRow = (kCodes + HPC * D / 16 + 15) / 16 * 16;    // a key's group: codes, scales, padding
+    static constexpr int kStage = 2 * kUnit * kRow;                        // K rows, then V rows
+    // Ring: about 160 KiB per SM over the CTAs that fit (kCtas below).
+    static constexpr int kCtas = HPC == 8 ? 2 : HPC == 4 ? 3 : HPC == 2 ? 6 : 9;
+    static constexpr int kFit = 184320 / kCtas / kStage;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kRing = kStages * kStage;
+    static_assert(kStages >= 4, "ring too short");
+};
+
+// First key and number of keys of sequence b that its query sees.
+__device__ __forceinline__ int seq_keys(const Fp4DecodeArgs &a, int b, int &lo) {
+    int L = a.cache_seqlens[b];
+    L = L < 0 ? 0 : (L > a.max_seqlen_k ? a.max_seqlen_k : L);
+    lo = (a.window > 0 && L > a.window) ? L - a.window : 0;
+    return L;
+}
+
+// Exclusive prefix of the sequences' units into prefix[0 .. B] (all threads).
+__device__ __forceinline__ void fp4_prefix(const Fp4DecodeArgs &a, int32_t *prefix) {
+    const int B = a.num_seqs;
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
+        const int given = a.cache_seqlens[b];
+        if (given < 0 || given > a.max_seqlen_k) raise_error(PA_DEVERR_SEQLENS);
+        int lo;
+        const int L = seq_keys(a, b, lo);
+        prefix[b + 1] = L > 0 ? (L - 1) / kUnit - lo / kUnit + 1 : 0;
+    }
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int per = (B + 31) / 32;
+        const int from = 1 + lane * per, to = min(B, lane * per + per);
+        int run = 0;
+        for (int i = from; i <= to; ++i) run += prefix[i];
+        int incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int acc = incl - run;
+        for (int i = from; i <= to; ++i) {
+            acc += prefix[i];
+            prefix[i] = acc;
+        }
+    }
+    __syncthreads();
+}
+
+// The producer warp: units [g0, g1) of the list into the ring.
+template <int D, int HPC>
+__device__ void fp4_produce(const Fp4DecodeArgs &a, const int32_t *prefix, int64_t T, int64_t g0, int64_t g1,
+                            uint8_t *ring, uint64_t *full, uint64_t *empty, int lane) {
+    using S = Fp4Smem<D, HPC>;
+    const bool paged = a.page_size == 16;
+    const bool run = paged && a.head_groups == 1;    // a unit is one contiguous run of rows
+    int ctr = 0;
+    SegmentWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
+    int b, hg, u0, u1, split, span;
+    while (walk.next(b, hg, u0, u1, split, span)) {
+        const int32_t *pt = a.page_table + (int64_t)b * a.pt_stride;
+        int lo;
+        const int L = seq_keys(a, b, lo);
+        const int first = lo / kUnit;                // the sequence's unit 0
+        // Page size 16: lane i holds the page of unit c0 + i, the next 32 are
+        // read while these are copied.  Page size 1: lane i the slot of key i
+        // of the unit, read one unit ahead.
+        auto ids = [&](int u) {
+            if (paged) return u + lane < u1 ? pt[first + u + lane] : 0;
+            const int j = (first + u) * kUnit + (lane & 15);
+            return u < u1 && j >= lo && j < L ? pt[j] : 0;
+        };
+        int now = 0, ahead = ids(u0);
+        for (int u = u0; u < u1; ++u, ++ctr) {
+            const int i = paged ? (u - u0) & 31 : 0;
+            if (i == 0) {
+                now = ahead;
+                ahead = ids(u + (paged ? 32 : 1));
+            }
+            const int key = (first + u) * kUnit;
+            const int n0 = max(lo - key, 0), n1 = min(L - key, kUnit);   // keys of the unit that are seen
+            const int slot = ctr % S::kStages, round = ctr / S::kStages;
+            if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1)) return;
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2u * (n1 - n0) * S::kRow);
+            __syncwarp();
+            int64_t page = __shfl_sync(0xffffffffu, now, paged ? i : (lane & 15));
+            const int tok = lane & 15;
+            const bool mine = run ? (lane & 15) == 0 : (tok >= n0 && tok < n1);
+            if (mine) {
+                if (page < 0 || page >= a.num_pages) {           // never read outside the pool
+                    raise_error(PA_DEVERR_PAGE_RANGE);
+                    page = 0;
+                }
+                const int at = run ? n0 : tok;
+                const int64_t row = paged ? page * 16 + at : page;
+                uint8_t *dst = ring + slot * S::kStage + (lane >> 4) * (kUnit * S::kRow) + at * S::kRow;
+                const uint8_t *src = (lane < 16 ? a.k_cache : a.v_cache) + row * a.row_bytes + (int64_t)hg * S::kRow;
+                bulk_g2s(dst, src, (run ? n1 - n0 : 1) * S::kRow, &full[slot]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Consumer warp hw: KV head hg * HPC + hw of each segment of the same range.
+template <int D, int HPC>
+__device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64_t T, int64_t g0, int64_t g1,
+                            const uint8_t *ring, uint64_t *full, uint64_t *empty, int hw, int lane) {
+    using S = Fp4Smem<D, HPC>;
+    constexpr int KS = D / 16;                       // k-steps of the score = tiles of O
+    constexpr int KW = D / 32;                       // words of a lane's part of a K row
+    constexpr int VW = D / 64;                       // words of a lane's part of a V row
+    const int r8 = lane >> 2, q4 = lane & 3;
+    const int G = a.group;
+    auto place = [](int r) { return r ^ ((r >> 1) & 1); };       // row of the fragment -> key of the unit
+    const int tk = place(r8);                        // keys tk and tk + 8
+    const int t0 = place(2 * q4), t1 = place(2 * q4 + 1);        // keys t0, t1, t0 + 8, t1 + 8
+    const int k_off = tk * S::kRow + hw * (D / 2) + q4 * (D / 8);
+    const int ks_off = tk * S::kRow + S::kCodes + hw * (D / 16) + q4 * (D / 64);
+    const int v_in = kUnit * S::kRow + hw * (D / 2) + r8 * (D / 16);
+    const int vs_in = kUnit * S::kRow + S::kCodes + hw * (D / 16) + (D == 128 ? r8 : r8 >> 1);
+    int ctr = 0;
+    SegmentWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
+    int b, hg, u0, u1, split, span;
+    while (walk.next(b, hg, u0, u1, split, span)) {
+        const int kvh = hg * HPC + hw;
+        const int h0 = kvh * G;
+        int lo;
+        const int L = seq_keys(a, b, lo);
+        const int first = lo / kUnit;
+        const float sl2 = a.scale_log2 * __ldg(a.k_scale + kvh);
+        uint32_t qb[KS][2];
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) qb[kk][0] = qb[kk][1] = 0u;
+        if (r8 < G) {
+            const uint2 *qrow = reinterpret_cast<const uint2 *>(a.q + ((int64_t)b * a.num_q_heads + h0 + r8) * D + q4 * (D / 4));
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                const uint2 w = __ldg(qrow + kk);
+                qb[kk][0] = f16x2_bits(bf16lo(w.x), bf16hi(w.x));
+                qb[kk][1] = f16x2_bits(bf16lo(w.y), bf16hi(w.y));
+            }
+        }
+        float oacc[KS][4];
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) oacc[mt][0] = oacc[mt][1] = oacc[mt][2] = oacc[mt][3] = 0.f;
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        for (int u = u0; u < u1; ++u, ++ctr) {
+            const int slot = ctr % S::kStages, round = ctr / S::kStages;
+            if (!mbar_wait(&full[slot], round & 1)) return;
+            __syncwarp();
+            const uint8_t *st = ring + slot * S::kStage;
+            const int key = (first + u) * kUnit;
+            const int n0 = lo - key, n1 = L - key;   // keys n0 .. n1 - 1 of the unit are seen
+            const bool part = n0 > 0 || n1 < kUnit;
+            // V's words and scales, so that they arrive while the scores are made
+            uint32_t vw[4][VW], vs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = ((i & 1) ? t1 : t0) + 8 * (i >> 1);
+                const uint8_t *p = st + t * S::kRow;
+                if constexpr (VW == 2) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(p + v_in);
+                    vw[i][0] = w.x; vw[i][1] = w.y;
+                } else {
+                    vw[i][0] = *reinterpret_cast<const uint32_t *>(p + v_in);
+                }
+                vs[i] = p[vs_in];
+                // keys that are not seen may hold anything: a zero scale makes them 0
+                if (part && (t < n0 || t >= n1)) vs[i] = 0u;
+            }
+            // ---- scores
+            float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t kw[2][KW], ks[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *p = st + 8 * i * S::kRow;
+                if constexpr (KW == 4) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(p + k_off);
+                    kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
+                    ks[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(p + ks_off));
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(p + k_off);
+                    kw[i][0] = w.x; kw[i][1] = w.y;
+                    ks[i] = e4m3x2_to_f16x2(p[ks_off]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {           // a word is two k-steps
+                uint32_t x[4], y[4];
+                e2m1x8_to_f16x8(kw[0][w], x);
+                e2m1x8_to_f16x8(kw[1][w], y);
+                const uint32_t s0 = w < 2 ? f16_dup_lo(ks[0]) : f16_dup_hi(ks[0]);
+                const uint32_t s1 = w < 2 ? f16_dup_lo(ks[1]) : f16_dup_hi(ks[1]);
+                uint32_t fa[4] = {hmul2_bits(x[0], s0), hmul2_bits(y[0], s1), hmul2_bits(x[1], s0), hmul2_bits(y[1], s1)};
+                uint32_t fb[4] = {hmul2_bits(x[2], s0), hmul2_bits(y[2], s1), hmul2_bits(x[3], s0), hmul2_bits(y[3], s1)};
+                mma_f16_16816(sc, fa, qb[2 * w][0], qb[2 * w][1]);
+                mma_f16_16816(sd, fb, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+            }
+            // ---- online softmax in the log2 domain
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = (sc[i] + sd[i]) * sl2;
+            if (part) {
+                const bool s0 = tk >= n0 && tk < n1, s1 = tk + 8 >= n0 && tk + 8 < n1;
+                x[0] = s0 ? x[0] : -INFINITY;
+                x[1] = s0 ? x[1] : -INFINITY;
+                x[2] = s1 ? x[2] : -INFINITY;
+                x[3] = s1 ? x[3] : -INFINITY;
+            }
+            const bool more = fmaxf(x[0], x[2]) > m_run[0] + kLazyRescale || fmaxf(x[1], x[3]) > m_run[1] + kLazyRescale;
+            if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(x[j], x[2 + j]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    if (mx > m_run[j] + kLazyRescale) {
+                        const float alpha = fast_exp2(m_run[j] - mx);    // 0 when m_run = -inf
+                        l_run[j] *= alpha;
+#pragma unroll
+                        for (int mt = 0; mt < KS; ++mt) {
+                            oacc[mt][j] *= alpha;
+                            oacc[mt][2 + j] *= alpha;
+                        }
+                        m_run[j] = mx;
+                    }
+                }
+            }
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[i] - m_run[i & 1]);
+            l_run[0] += p[0] + p[2];
+            l_run[1] += p[1] + p[3];
+            const uint32_t pb0 = movmatrix_trans(f16x2_bits(p[0], p[1]));
+            const uint32_t pb1 = movmatrix_trans(f16x2_bits(p[2], p[3]));
+            // ---- O^T += V^T P^T
+            const uint32_t sa = e4m3x2_to_f16x2(vs[0] | (vs[1] << 8)), sb = e4m3x2_to_f16x2(vs[2] | (vs[3] << 8));
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                constexpr uint32_t m = 0x0f0f0f0fu;
+                // even elements of both keys in one word, odd ones in another
+                uint32_t ea[4], oa[4], eb[4], ob[4];
+                e2m1x8_to_f16x8((vw[0][w] & m) | ((vw[1][w] << 4) & ~m), ea);
+                e2m1x8_to_f16x8(((vw[0][w] >> 4) & m) | (vw[1][w] & ~m), oa);
+                e2m1x8_to_f16x8((vw[2][w] & m) | ((vw[3][w] << 4) & ~m), eb);
+                e2m1x8_to_f16x8(((vw[2][w] >> 4) & m) | (vw[3][w] & ~m), ob);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t f[4] = {hmul2_bits(ea[i], sa), hmul2_bits(oa[i], sa), hmul2_bits(eb[i], sb), hmul2_bits(ob[i], sb)};
+                    mma_f16_16816(oacc[4 * w + i], f, pb0, pb1);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+        }
+        // ---- the segment's partial: lane r8 holds elements D/8 r8 .. of its two heads
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float l = l_run[j];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int hh = 2 * q4 + j;
+            if (hh >= G) continue;
+            if (split < 0 || split + span > a.max_splits) {      // cannot happen for valid lengths
+                raise_error(PA_DEVERR_SEQLENS);
+                continue;
+            }
+            const float inv = (l > 0.f ? 1.f / l : 0.f) * __ldg(a.v_scale + kvh);
+            const int64_t r = ((int64_t)b * a.num_q_heads + h0 + hh) * a.max_splits + split;
+            float *orow = a.o_part + r * D + r8 * (D / 8);
+#pragma unroll
+            for (int mt = 0; mt < KS; mt += 2)
+                *reinterpret_cast<float4 *>(orow + 2 * mt) =
+                    make_float4(oacc[mt][j] * inv, oacc[mt][2 + j] * inv, oacc[mt + 1][j] * inv, oacc[mt + 1][2 + j] * inv);
+            if (r8 == 0) {
+                a.lse_part[r] = l > 0.f ? (m_run[j] + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                for (int e = 1; e < span; ++e) a.lse_part[r + e] = -INFINITY;
+            }
+        }
+    }
+}
+
+template <int D, int HPC>
+__global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas) decode_fp4_kernel(const Fp4DecodeArgs a) {
+    using S = Fp4Smem<D, HPC>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kRing);
+    uint64_t *empty = full + S::kStages;
+    int32_t *prefix = reinterpret_cast<int32_t *>(empty + S::kStages);        // [B + 1]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], HPC);
+        }
+        fence_mbar_init();
+    }
+    fp4_prefix(a, prefix);
+    const int B = a.num_seqs;
+    const int64_t total = (int64_t)a.head_groups * prefix[B];
+    int64_t T = (total + gridDim.x - 1) / gridDim.x;
+    if (T < a.min_units) T = a.min_units;
+    if (blockIdx.x == 0) {
+        for (int b = threadIdx.x; b <= B; b += blockDim.x) a.ws_prefix[b] = prefix[b];
+        if (threadIdx.x == 0) a.ws_header[0] = (int32_t)T;
+    }
+    const int64_t g0 = (int64_t)blockIdx.x * T, g1 = min(g0 + T, total);
+    if (warp == HPC) fp4_produce<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, lane);
+    else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
+}
+
+template <int D, int HPC>
+cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const pa_decode_params &p, int64_t useful, cudaStream_t stream) {
+    using S = Fp4Smem<D, HPC>;
+    const size_t smem = S::kRing + 2 * S::kStages * sizeof(uint64_t) + ((size_t)a.num_seqs + 1) * sizeof(int32_t);
+    auto kern = decode_fp4_kernel<D, HPC>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (HPC + 1) * 32, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    int64_t grid = (int64_t)num_sms() * per_sm;
+    if (p.max_ctas > 0 && grid > p.max_ctas) grid = p.max_ctas;
+    if (grid > useful) grid = useful;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((HPC + 1) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = p.overlap_previous ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+DecodePlan plan_decode_fp4(const pa_decode_params &p) {
+    DecodePlan plan{};
+    const Fp4Layout lay = fp4_layout(p.num_kv_heads, p.head_dim);
+    plan.heads_per_cta = lay.gs;
+    // Smallest range: the caller's, else what spreads the batch at its longest
+    // over every SM, between 64 keys and 1/32 of the longest context.
+    int32_t chunk = p.kv_chunk;
+    if (chunk <= 0) {
+        int32_t most = (p.max_seqlen_k / 32 + 15) / 16 * 16;
+        if (most < 64) most = 64;
+        const int64_t keys = (int64_t)p.num_seqs * p.max_seqlen_k * lay.groups;
+        const int64_t even = (keys / num_sms() + 15) / 16 * 16;
+        chunk = even < 64 ? 64 : even > most ? most : (int32_t)even;
+    }
+    plan.kv_chunk = chunk;
+    plan.max_splits = (p.max_seqlen_k + chunk - 1) / chunk + 1;
+    const size_t rows = (size_t)p.num_seqs * p.num_q_heads * plan.max_splits;
+    const size_t header = 256 + (((size_t)p.num_seqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
+    const size_t obytes = (rows * p.head_dim * sizeof(float) + 255) / 256 * 256;
+    plan.workspace_bytes = header + obytes + rows * sizeof(float);
+    return plan;
+}
+
+cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream) {
+    if (p.num_seqs == 0) return cudaSuccess;
+    const DecodeArgs w = decode_setup(p, plan);      // the workspace layout
+    const Fp4Layout lay = fp4_layout(p.num_kv_heads, p.head_dim);
+    Fp4DecodeArgs a{};
+    a.q = w.q;
+    a.k_cache = w.k_cache;
+    a.v_cache = w.v_cache;
+    a.page_table = p.page_table;
+    a.pt_stride = p.page_table_stride;
+    a.cache_seqlens = p.cache_seqlens;
+    a.num_seqs = p.num_seqs;
+    a.num_q_heads = p.num_q_heads;
+    a.group = p.num_q_heads / p.num_kv_heads;
+    a.page_size = p.page_size;
+    a.num_pages = p.num_pages;
+    a.scale_log2 = w.scale_log2;
+    a.min_units = plan.kv_chunk / kUnit;
+    a.max_seqlen_k = p.max_seqlen_k;
+    a.max_splits = plan.max_splits;
+    a.head_groups = lay.groups;
+    a.row_bytes = lay.row_bytes;
+    a.o_part = w.o_part;
+    a.lse_part = w.lse_part;
+    a.k_scale = p.k_scale;
+    a.v_scale = p.v_scale;
+    a.window = p.sliding_window;
+    a.ws_header = w.ws_header;
+    a.ws_prefix = w.ws_prefix;
+    // every sequence at its longest, ranges at their smallest
+    const int64_t units = ((int64_t)p.max_seqlen_k + kUnit - 1) / kUnit * p.num_seqs * lay.groups;
+    const int64_t useful = (units + a.min_units - 1) / a.min_units + 1;
+    cudaError_t e = cudaErrorInvalidValue;
+    if (p.head_dim == 64) {
+        if (lay.gs == 1) e = launch_fp4_t<64, 1>(a, p, useful, stream);
+        if (lay.gs == 2) e = launch_fp4_t<64, 2>(a, p, useful, stream);
+        if (lay.gs == 4) e = launch_fp4_t<64, 4>(a, p, useful, stream);
+        if (lay.gs == 8) e = launch_fp4_t<64, 8>(a, p, useful, stream);
+    } else {
+        if (lay.gs == 1) e = launch_fp4_t<128, 1>(a, p, useful, stream);
+        if (lay.gs == 2) e = launch_fp4_t<128, 2>(a, p, useful, stream);
+        if (lay.gs == 4) e = launch_fp4_t<128, 4>(a, p, useful, stream);
+        if (lay.gs == 8) e = launch_fp4_t<128, 8>(a, p, useful, stream);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_lse_combine(a.o_part, a.lse_part, nullptr, a.ws_header, a.ws_prefix, a.head_groups,
+                              a.group * lay.gs, p.num_q_heads, p.num_seqs * p.num_q_heads, plan.max_splits,
+                              p.head_dim, p.out, p.lse, stream);
+}
+
+}  // namespace pa

@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "fp4.cuh"
 #include "pa.h"
 #include "pa_internal.h"
 
@@ -46,6 +47,14 @@ pa_status check_heads(int32_t hq, int32_t hkv, int32_t d, int32_t page_size) {
     if (page_size != 1 && page_size != 16)
         return fail(PA_ERR_UNSUPPORTED, "page_size %d not in {1,16}", page_size);
     if ((int64_t)hkv * d > 4096) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads * head_dim > 4096");
+    return PA_OK;
+}
+
+// The heads a 4-bit row can hold.
+pa_status check_fp4_heads(int32_t hkv, int32_t d) {
+    if (hkv <= 0 || d <= 0) return fail(PA_ERR_INVALID, "num_kv_heads and head_dim must be positive");
+    if (d != 64 && d != 128) return fail(PA_ERR_UNSUPPORTED, "4-bit pools: head_dim %d not in {64,128}", d);
+    if ((int64_t)hkv * d > 4096) return fail(PA_ERR_UNSUPPORTED, "4-bit pools: num_kv_heads * head_dim > 4096");
     return PA_OK;
 }
 }  // namespace
@@ -86,7 +95,8 @@ const char *pa_last_error(void) { return pa::g_last_error; }
 pa_status pa_device_error(int32_t *bits, void *stream) {
     if (bits == nullptr) return fail(PA_ERR_INVALID, "bits is NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t (*getters[])(int **) = {error_word_store, error_word_decode, error_word_prefill, error_word_mixed};
+    cudaError_t (*getters[])(int **) = {error_word_store, error_word_decode, error_word_prefill, error_word_mixed,
+                                      error_word_fp4, error_word_decode_fp4};
     int32_t acc = 0;
     for (auto get : getters) {
         int *addr = nullptr;
@@ -140,6 +150,57 @@ pa_status pa_store_kv_fp8(const void *k, const void *v, const int32_t *slot_mapp
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "store_kv_fp8 launch");
 }
 
+int64_t pa_fp4_row_bytes(int32_t num_kv_heads, int32_t head_dim) {
+    g_last_error[0] = 0;
+    if (check_fp4_heads(num_kv_heads, head_dim) != PA_OK) return 0;
+    return fp4_layout(num_kv_heads, head_dim).row_bytes;
+}
+
+// Checks that the 4-bit store and read-back share; *nothing = no token.
+static pa_status check_fp4_move(const void *k, const void *v, const int32_t *slots, int64_t num_tokens,
+                                const void *k_cache, const void *v_cache, int64_t num_slots, int32_t num_kv_heads,
+                                int32_t head_dim, const float *k_scale, const float *v_scale, bool *nothing) {
+    *nothing = false;
+    if (num_tokens < 0 || num_slots < 0) return fail(PA_ERR_INVALID, "negative num_tokens or num_slots");
+    pa_status st = check_fp4_heads(num_kv_heads, head_dim);
+    if (st != PA_OK) return st;
+    if (num_tokens > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens in one call");
+    if (num_tokens == 0) {
+        *nothing = true;
+        return PA_OK;
+    }
+    if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return fail(PA_ERR_INVALID, "NULL pointer");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_INVALID, "K/V pointers must be 16-byte aligned");
+    return PA_OK;
+}
+
+pa_status pa_store_kv_fp4(const void *k, const void *v, const int32_t *slot_mapping, int64_t num_tokens,
+                          void *k_cache, void *v_cache, int64_t num_slots, int32_t num_kv_heads,
+                          int32_t head_dim, const float *k_scale, const float *v_scale, void *stream) {
+    g_last_error[0] = 0;
+    bool nothing = false;
+    pa_status st = check_fp4_move(k, v, slot_mapping, num_tokens, k_cache, v_cache, num_slots, num_kv_heads, head_dim,
+                                  k_scale, v_scale, &nothing);
+    if (st != PA_OK || nothing) return st;
+    cudaError_t e = launch_store_kv_fp4(k, v, slot_mapping, num_tokens, k_cache, v_cache, num_slots, num_kv_heads,
+                                        head_dim, k_scale, v_scale, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "store_kv_fp4 launch");
+}
+
+pa_status pa_load_kv_fp4(const int32_t *slots, int64_t num_tokens, const void *k_cache, const void *v_cache,
+                         int64_t num_slots, int32_t num_kv_heads, int32_t head_dim, const float *k_scale,
+                         const float *v_scale, void *k_out, void *v_out, void *stream) {
+    g_last_error[0] = 0;
+    bool nothing = false;
+    pa_status st = check_fp4_move(k_out, v_out, slots, num_tokens, k_cache, v_cache, num_slots, num_kv_heads, head_dim,
+                                  k_scale, v_scale, &nothing);
+    if (st != PA_OK || nothing) return st;
+    cudaError_t e = launch_load_kv_fp4(slots, num_tokens, k_cache, v_cache, num_slots, num_kv_heads, head_dim, k_scale,
+                                       v_scale, k_out, v_out, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "load_kv_fp4 launch");
+}
+
 pa_status pa_rope_cos_sin_table(float *cos_sin, int32_t max_pos, int32_t rot_dim, double base) {
     g_last_error[0] = 0;
     if (max_pos < 0 || rot_dim <= 0 || rot_dim % 2 != 0) return fail(PA_ERR_INVALID, "max_pos >= 0 and an even rot_dim > 0 are required");
@@ -167,18 +228,24 @@ pa_status pa_rope_store_kv(const pa_rope_store_params *p, void *stream) {
     if (p->rot_dim <= 0 || p->rot_dim % 16 != 0 || p->rot_dim > p->head_dim)
         return fail(PA_ERR_UNSUPPORTED, "rot_dim %d must be a positive multiple of 16 <= head_dim", p->rot_dim);
     if (p->interleaved != 0 && p->interleaved != 1) return fail(PA_ERR_INVALID, "interleaved must be 0 or 1");
-    if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3)
-        return fail(PA_ERR_INVALID, "kv_dtype %d is neither PA_KV_BF16 nor PA_KV_FP8_E4M3", p->kv_dtype);
+    if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4)
+        return fail(PA_ERR_INVALID, "kv_dtype %d is not a pa_kv_dtype", p->kv_dtype);
+    if (p->kv_dtype == PA_KV_FP4) {
+        pa_status st = check_fp4_heads(p->num_kv_heads, p->head_dim);
+        if (st != PA_OK) return st;
+        if (p->num_tokens > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens in one call");
+    }
     if (p->num_tokens == 0) return PA_OK;
     if (!p->q || !p->q_out || !p->k || !p->v || !p->positions || !p->cos_sin || !p->slot_mapping ||
         !p->k_cache || !p->v_cache)
         return fail(PA_ERR_INVALID, "NULL pointer");
-    if (p->kv_dtype == PA_KV_FP8_E4M3 && (!p->k_scale || !p->v_scale))
-        return fail(PA_ERR_INVALID, "FP8 pools need k_scale and v_scale");
+    if (p->kv_dtype != PA_KV_BF16 && (!p->k_scale || !p->v_scale))
+        return fail(PA_ERR_INVALID, "FP8 and 4-bit pools need k_scale and v_scale");
     if (!aligned16(p->q) || !aligned16(p->q_out) || !aligned16(p->k) || !aligned16(p->v) ||
         !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->cos_sin))
         return fail(PA_ERR_INVALID, "q, q_out, k, v, the pools and the table must be 16-byte aligned");
-    cudaError_t e = launch_rope_store(*p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = p->kv_dtype == PA_KV_FP4 ? launch_rope_store_fp4(*p, static_cast<cudaStream_t>(stream))
+                                             : launch_rope_store(*p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "rope_store launch");
 }
 
@@ -300,6 +367,11 @@ pa_status pa_prefill(const pa_prefill_params *p, void *stream) {
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "prefill launch");
 }
 
+// The plan of a decode call, by the type of its pools.
+static DecodePlan decode_plan(const pa_decode_params &p) {
+    return p.kv_dtype == PA_KV_FP4 ? plan_decode_fp4(p) : plan_decode(p);
+}
+
 static pa_status check_decode(const pa_decode_params *p) {
     if (p == nullptr) return fail(PA_ERR_INVALID, "params is NULL");
     pa_status st = check_heads(p->num_q_heads, p->num_kv_heads, p->head_dim, p->page_size);
@@ -314,8 +386,8 @@ static pa_status check_decode(const pa_decode_params *p) {
     if (!(p->scale > 0.f) || p->scale == INFINITY) return fail(PA_ERR_INVALID, "scale must be finite and > 0");
     if (p->num_pages > (int64_t)INT32_MAX / p->page_size)
         return fail(PA_ERR_UNSUPPORTED, "pool larger than 2^31 slots");
-    if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3)
-        return fail(PA_ERR_INVALID, "kv_dtype %d is neither PA_KV_BF16 nor PA_KV_FP8_E4M3", p->kv_dtype);
+    if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4)
+        return fail(PA_ERR_INVALID, "kv_dtype %d is not a pa_kv_dtype", p->kv_dtype);
     if (p->kv_dtype == PA_KV_FP8_E4M3 && p->num_seqs > 0 && (!p->k_scale || !p->v_scale))
         return fail(PA_ERR_INVALID, "FP8 pools need k_scale and v_scale");
     if (p->sliding_window < 0) return fail(PA_ERR_INVALID, "sliding_window must be >= 0");
@@ -326,7 +398,7 @@ static pa_status check_decode(const pa_decode_params *p) {
     // share prefix pages can reach sums beyond that, so bound them here.
     const int64_t eff = (p->sliding_window > 0 && p->sliding_window < p->max_seqlen_k) ? p->sliding_window
                                                                                        : p->max_seqlen_k;
-    const int64_t groups = p->num_kv_heads / plan_decode(*p).heads_per_cta;
+    const int64_t groups = p->num_kv_heads / decode_plan(*p).heads_per_cta;
     if ((int64_t)p->num_seqs * eff * groups > (int64_t)INT32_MAX)
         return fail(PA_ERR_UNSUPPORTED,
                     "num_seqs * max_seqlen_k * KV-head groups = %lld exceeds 2^31 - 1 keys in one decode call",
@@ -336,12 +408,12 @@ static pa_status check_decode(const pa_decode_params *p) {
 
 size_t pa_decode_workspace_size(const pa_decode_params *p) {
     if (check_decode(p) != PA_OK) return 0;
-    return plan_decode(*p).workspace_bytes;
+    return decode_plan(*p).workspace_bytes;
 }
 
 int32_t pa_decode_kv_chunk(const pa_decode_params *p) {
     if (check_decode(p) != PA_OK) return 0;
-    return plan_decode(*p).kv_chunk;
+    return decode_plan(*p).kv_chunk;
 }
 
 // The checks pa_decode makes after check_decode for a non-empty batch.
@@ -350,9 +422,11 @@ static pa_status check_decode_buffers(const pa_decode_params *p) {
     if (p->page_table_stride < ncols) return fail(PA_ERR_INVALID, "page_table_stride too small for max_seqlen_k");
     if (!p->q || !p->k_cache || !p->v_cache || !p->page_table || !p->cache_seqlens || !p->out)
         return fail(PA_ERR_INVALID, "NULL pointer");
+    if (p->kv_dtype == PA_KV_FP4 && (!p->k_scale || !p->v_scale))
+        return fail(PA_ERR_INVALID, "4-bit pools need k_scale and v_scale");
     if (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->out))
         return fail(PA_ERR_INVALID, "q, caches and out must be 16-byte aligned");
-    const DecodePlan plan = plan_decode(*p);
+    const DecodePlan plan = decode_plan(*p);
     if (plan.workspace_bytes > 0) {
         if (p->workspace == nullptr || p->workspace_bytes < plan.workspace_bytes)
             return fail(PA_ERR_INVALID, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes, p->workspace_bytes);
@@ -368,8 +442,9 @@ pa_status pa_decode(const pa_decode_params *p, void *stream) {
     if (p->num_seqs == 0) return PA_OK;
     st = check_decode_buffers(p);
     if (st != PA_OK) return st;
-    const DecodePlan plan = plan_decode(*p);
-    cudaError_t e = launch_decode(*p, plan, static_cast<cudaStream_t>(stream));
+    const DecodePlan plan = decode_plan(*p);
+    cudaError_t e = p->kv_dtype == PA_KV_FP4 ? launch_decode_fp4(*p, plan, static_cast<cudaStream_t>(stream))
+                                             : launch_decode(*p, plan, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode launch");
 }
 
@@ -385,6 +460,8 @@ pa_status pa_mixed_batch(const pa_prefill_params *pre, const pa_decode_params *d
     if (no_prefill && no_decode) return PA_OK;
     if (no_prefill) return pa_decode(dec, stream);
     if (no_decode) return pa_prefill(pre, stream);
+    if (pre->kv_dtype == PA_KV_FP4 || dec->kv_dtype == PA_KV_FP4)
+        return fail(PA_ERR_UNSUPPORTED, "the mixed-batch launch takes no 4-bit pools; call pa_prefill and pa_decode");
     st = check_decode_buffers(dec);
     if (st != PA_OK) return st;
     if (pre->k_cache != dec->k_cache || pre->v_cache != dec->v_cache || pre->num_pages != dec->num_pages ||
@@ -414,7 +491,7 @@ pa_status pa_decode_noalloc(const pa_decode_params *p, void *stream) {
     pa_status st = check_decode(p);
     if (st != PA_OK) return st;
     if (p->num_seqs == 0) return PA_OK;
-    const DecodePlan plan = plan_decode(*p);
+    const DecodePlan plan = decode_plan(*p);
     if (plan.workspace_bytes > kDecodeNoAllocScratchBytes)
         return fail(PA_ERR_UNSUPPORTED,
                     "pa_decode_noalloc: these sizes need %zu bytes of split scratch, more than its fixed "

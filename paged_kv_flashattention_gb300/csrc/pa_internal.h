@@ -20,6 +20,15 @@ cudaError_t launch_store_kv_fp8(const void *k, const void *v, const int32_t *slo
 
 cudaError_t launch_rope_store(const pa_rope_store_params &p, cudaStream_t stream);
 
+// The 4-bit pools' store, rotary store and read-back (kv_fp4.cu).
+cudaError_t launch_store_kv_fp4(const void *k, const void *v, const int32_t *slot_mapping, int64_t num_tokens,
+                                void *k_cache, void *v_cache, int64_t num_slots, int32_t num_kv_heads,
+                                int32_t head_dim, const float *k_scale, const float *v_scale, cudaStream_t stream);
+cudaError_t launch_rope_store_fp4(const pa_rope_store_params &p, cudaStream_t stream);
+cudaError_t launch_load_kv_fp4(const int32_t *slots, int64_t num_tokens, const void *k_cache, const void *v_cache,
+                               int64_t num_slots, int32_t num_kv_heads, int32_t head_dim, const float *k_scale,
+                               const float *v_scale, void *k_out, void *v_out, cudaStream_t stream);
+
 cudaError_t launch_build_page_table(const int32_t *token_table, int64_t tt_stride, int64_t tt_rows,
                                     const int32_t *table_idx, int32_t num_seqs, int32_t ncols,
                                     int32_t page_size, int32_t *page_table, int32_t pt_stride,
@@ -33,7 +42,9 @@ struct DecodePlan {
     size_t workspace_bytes;
 };
 DecodePlan plan_decode(const pa_decode_params &p);
+DecodePlan plan_decode_fp4(const pa_decode_params &p);      // 4-bit pools (decode_fp4.cu)
 cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream);
+cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream);
 
 // Merge split partials.  Row r's split count is splits_per_row[r] if given;
 // else, with seg_header / seg_prefix (decode), the number of T-row CTA ranges
@@ -62,5 +73,7 @@ cudaError_t error_word_store(int **addr);
 cudaError_t error_word_decode(int **addr);
 cudaError_t error_word_prefill(int **addr);
 cudaError_t error_word_mixed(int **addr);
+cudaError_t error_word_fp4(int **addr);
+cudaError_t error_word_decode_fp4(int **addr);
 
 }  // namespace pa

@@ -1,0 +1,70 @@
+"""Malformed 4-bit calls that libpa must reject on the host, before any
+launch; run as a script with no GPU visible (the pointers are made up), it
+prints one JSON object {case id: [status, last error]}."""
+from __future__ import annotations
+
+import ctypes
+import json
+import os
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+if ROOT not in sys.path:
+    sys.path.insert(0, ROOT)
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+
+# k, v, slots, tokens, k_cache, v_cache, slots, hkv, d, k_scale, v_scale, stream
+STORE = (0x1000, 0x2000, 0x3000, 4, 0x4000, 0x5000, 64, 2, 64, 0x6000, 0x7000, None)
+STORE_CASES = [
+    ("misaligned_k", {0: 0x1008}, INVALID),
+    ("misaligned_pool", {4: 0x4001}, INVALID),
+    ("null_scale", {9: None}, INVALID),
+    ("null_slots", {2: None}, INVALID),
+    ("negative_tokens", {3: -1}, INVALID),
+    ("negative_slots", {6: -1}, INVALID),
+    ("head_dim96", {8: 96}, UNSUPPORTED),
+    ("no_heads", {7: 0}, INVALID),
+    ("row_too_long", {7: 64, 8: 128}, UNSUPPORTED),
+    ("too_many_tokens", {3: 1 << 31}, UNSUPPORTED),
+    ("zero_tokens", {0: None, 1: None, 2: None, 3: 0, 4: None, 5: None, 9: None, 10: None}, OK),
+]
+ROPE = dict(q=0x1000, q_out=0x1000, k=0x2000, v=0x3000, positions=0x4000, cos_sin=0x5000, max_pos=64, rot_dim=64,
+            interleaved=0, slot_mapping=0x6000, num_tokens=4, num_q_heads=8, num_kv_heads=2, head_dim=64, k_cache=0x7000,
+            v_cache=0x8000, num_slots=64, kv_dtype=2, k_scale=0x9000, v_scale=0x9100)
+ROPE_CASES = [
+    ("no_scales", dict(k_scale=None), INVALID),
+    ("head_dim32", dict(head_dim=32, rot_dim=32), UNSUPPORTED),
+    ("kv_dtype3", dict(kv_dtype=3), INVALID),
+    ("misaligned_pool", dict(v_cache=0x8008), INVALID),
+]
+
+
+def expected():
+    out = {f"store/{i}": s for i, _, s in STORE_CASES}
+    out.update({f"load/{i}": s for i, _, s in STORE_CASES})
+    out.update({f"rope/{i}": s for i, _, s in ROPE_CASES})
+    return out
+
+
+def run_all() -> dict:
+    from paged_kv_flashattention_gb300 import _lib
+    lib = _lib.load()
+    res = {}
+
+    def rec(key, status):
+        res[key] = [int(status), lib.pa_last_error().decode(errors="replace")]
+
+    for i, change, _ in STORE_CASES:
+        a = [change.get(n, x) for n, x in enumerate(STORE)]
+        rec(f"store/{i}", lib.pa_store_kv_fp4(*a))
+        # slots, tokens, k_cache, v_cache, slots, hkv, d, scales, k_out, v_out, stream
+        rec(f"load/{i}", lib.pa_load_kv_fp4(a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[0], a[1], None))
+    for i, kw, _ in ROPE_CASES:
+        p = _lib.RopeStoreParams(**{**ROPE, **kw})
+        rec(f"rope/{i}", lib.pa_rope_store_kv(ctypes.byref(p), None))
+    return res
+
+
+if __name__ == "__main__":
+    print(json.dumps(run_all()))

@@ -1,0 +1,82 @@
+"""Refusals of the 4-bit entry points and of the batch plan, on the host: the
+C calls run in a child process that sees no GPU (their pointers are made up),
+the binding's checks on CPU tensors."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import fp4_reject_cases
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def rejections():
+    from paged_kv_flashattention_gb300 import build
+    build.build()
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "tests", "fp4_reject_cases.py")],
+                       capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0, r.stderr
+    return json.loads(r.stdout.strip().splitlines()[-1])
+
+
+@pytest.mark.parametrize("case", sorted(fp4_reject_cases.expected()))
+def test_rejects_before_launch(rejections, case):
+    status, message = rejections[case]
+    want = fp4_reject_cases.expected()[case]
+    assert status == want, f"{case}: status {status} ({message}), expected {want}"
+    if want != 0:
+        assert message, f"{case}: no error message"
+
+
+def _pools(hkv=8, d=64, pages=4, page=16):
+    import paged_kv_flashattention_gb300 as pa
+    return [torch.zeros((pages, page, pa.fp4_row_bytes(hkv, d)), dtype=torch.uint8) for _ in range(2)]
+
+
+def test_binding_store_checks():
+    import paged_kv_flashattention_gb300 as pa
+    kc, vc = _pools()
+    k = torch.zeros((3, 8, 64), dtype=torch.bfloat16)
+    sm = torch.zeros(3, dtype=torch.int32)
+    g = torch.ones(8)
+    with pytest.raises(TypeError):
+        pa.store_kv_fp4(k.float(), k, sm, kc, vc, g, g)
+    with pytest.raises(TypeError):
+        pa.store_kv_fp4(k, k, sm, kc.view(torch.int8), vc, g, g)
+    with pytest.raises(ValueError):
+        pa.store_kv_fp4(k, k, sm[:2], kc, vc, g, g)
+    with pytest.raises(ValueError):
+        pa.store_kv_fp4(k, k, sm, kc, vc, g[:7], g)
+    with pytest.raises(ValueError):
+        pa.store_kv_fp4(k, k, sm, kc[..., :-16].contiguous(), vc[..., :-16].contiguous(), g, g)
+    with pytest.raises(ValueError):
+        pa.store_kv_fp4(k, k, sm, kc, vc[:2], g, g)
+    with pytest.raises(ValueError):
+        pa.store_kv_fp4(k.transpose(0, 1).contiguous().transpose(0, 1), k, sm, kc, vc, g, g)
+    with pytest.raises(ValueError):
+        pa.load_kv_fp4(sm, kc, vc, g, g, 128)
+    with pytest.raises(ValueError):
+        pa.load_kv_fp4(sm, kc, vc, g, g, 64, k_out=k[:2])
+    with pytest.raises(ValueError):
+        pa.load_kv_fp4(sm, kc, vc, None, g, 64)
+
+
+def test_binding_kv_dtype_checks():
+    """4-bit rows are used only where the caller says so, and a kv_dtype that
+    the pools are not is refused."""
+    from paged_kv_flashattention_gb300 import api
+    u8, b16 = torch.zeros(4, dtype=torch.uint8), torch.zeros(4, dtype=torch.bfloat16)
+    assert api._kv_dtype(u8, u8) == api.PA_KV_FP8_E4M3
+    assert api._kv_dtype(u8, u8, api.PA_KV_FP4) == api.PA_KV_FP4
+    assert api._kv_dtype(b16, b16, api.PA_KV_BF16) == api.PA_KV_BF16
+    for pool, asked in ((b16, api.PA_KV_FP4), (u8, api.PA_KV_BF16), (b16, api.PA_KV_FP8_E4M3)):
+        with pytest.raises(TypeError):
+            api._kv_dtype(pool, pool, asked)
+    with pytest.raises(ValueError):
+        api._kv_dtype(u8, u8, 3)
