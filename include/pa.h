@@ -10,6 +10,7 @@
  *   pa_rope_cos_sin_table  the rotary cos/sin table (host)
  *   pa_build_seqlens     per-request boundaries from the three lengths (host)
  *   pa_build_page_table  per-request page table from the token-granular table
+ *   pa_build_batch       boundaries, positions, slots and page table from lengths on the device
  *   pa_prefill           varlen causal prefill / extend attention
  *   pa_decode            one-query-per-sequence split-KV decode attention
  *   pa_decode_noalloc    the same, with fixed library-owned split scratch
@@ -84,6 +85,7 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT 4      /* a bounded wait in a kernel gave up */
 #define PA_DEVERR_POSITION 8     /* a RoPE position outside the cos/sin table */
 #define PA_DEVERR_TABLE_INDEX 16 /* a table_idx entry outside the token table's rows */
+#define PA_DEVERR_NO_PAGES 32    /* pa_build_batch: more new pages than the free list holds */
 
 int pa_abi_version(void);
 const char *pa_status_string(int status);
@@ -275,6 +277,61 @@ pa_status pa_build_page_table(const int32_t *token_table, int64_t token_table_st
                               int32_t max_seqlen_k, int32_t page_size, int32_t *page_table,
                               int32_t page_table_stride, void *stream);
 
+/*
+ * pa_build_batch - a batch's metadata in one launch from request lengths that
+ * live on the device ([M], "from ledger to tensors"; pa_build_seqlens and
+ * pa_build_page_table make the same from host lengths).  Nothing is read on
+ * the host, so a captured graph follows the lengths from replay to replay.
+ * For request b, with device_len = cached_len + extend_len:
+ *   cu_seqlens_q, cu_seqlens_k [num_seqs+1], cache_seqlens [num_seqs] as
+ *     pa_build_seqlens gives them;
+ *   for its token i < extend_len, at t = cu_seqlens_q[b] + i < num_tokens:
+ *     positions[t] = cached_len + i, slot_mapping[t] = its slot;
+ *   page_table[b * page_table_stride + c] for c < ceil(device_len / page_size)
+ *     as pa_build_page_table gives it; further columns are not written.
+ * Entries t >= cu_seqlens_q[num_seqs] of the num_tokens get position 0 and slot
+ * -1 (padding that the stores skip).  totals [4]: new tokens, longest
+ * extend_len, longest device_len, new pages needed.
+ * free_pages NULL: the token table already holds the new tokens' slots.  Else
+ * they are assigned here: a token goes on its request's last page while that
+ * has room, then on pages taken from free_pages in request order; the slots are
+ * also written to token_table[table_idx[b], cached_len ..].  The first
+ * totals[3] entries of free_pages are then in use.  Rows of table_idx must
+ * differ, and slots below cached_len on one page be consecutive, as this call
+ * assigns them.
+ * Device data that breaks the call's bounds: a negative length or device_len >
+ * max_seqlen_k counts as an empty request and raises PA_DEVERR_SEQLENS, as do
+ * more than num_tokens new tokens (those past the end are not written); a
+ * table_idx entry outside the table gives slots and pages -1, takes no pages
+ * and raises PA_DEVERR_TABLE_INDEX; a free list that is too short gives slots
+ * and pages -1 for the rest and raises PA_DEVERR_NO_PAGES.
+ * All pointers are device int32.  num_seqs <= 16384; num_seqs * max_seqlen_k
+ * and num_tokens below 2^31.
+ */
+typedef struct {
+    const int32_t *cached_len;   /* [num_seqs] */
+    const int32_t *extend_len;   /* [num_seqs] */
+    int32_t num_seqs;
+    int32_t max_seqlen_k;        /* >= every device_len; the table's rows are this long at least */
+    int32_t page_size;
+    int32_t *token_table;        /* [token_table_rows, token_table_stride]; written if free_pages is set */
+    int64_t token_table_stride;
+    int64_t token_table_rows;
+    const int32_t *table_idx;    /* [num_seqs] */
+    const int32_t *free_pages;   /* [num_free_pages] or NULL */
+    int32_t num_free_pages;
+    int64_t num_tokens;          /* entries of positions and slot_mapping */
+    int32_t *cu_seqlens_q;
+    int32_t *cu_seqlens_k;
+    int32_t *cache_seqlens;
+    int32_t *positions;
+    int32_t *slot_mapping;
+    int32_t *page_table;
+    int32_t page_table_stride;
+    int32_t *totals;
+} pa_batch_params;
+
+pa_status pa_build_batch(const pa_batch_params *p, void *stream);
 
 /*
  * pa_prefill - varlen prefill / extend attention ([T] s.10-15, [M]).

@@ -61,6 +61,16 @@ class RopeStoreParams(ctypes.Structure):
     ]
 
 
+class BatchParams(ctypes.Structure):
+    _fields_ = [
+        ("cached_len", c_p), ("extend_len", c_p), ("num_seqs", c_i32), ("max_seqlen_k", c_i32), ("page_size", c_i32),
+        ("token_table", c_p), ("token_table_stride", c_i64), ("token_table_rows", c_i64), ("table_idx", c_p),
+        ("free_pages", c_p), ("num_free_pages", c_i32), ("num_tokens", c_i64), ("cu_seqlens_q", c_p),
+        ("cu_seqlens_k", c_p), ("cache_seqlens", c_p), ("positions", c_p), ("slot_mapping", c_p), ("page_table", c_p),
+        ("page_table_stride", c_i32), ("totals", c_p),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "pa_abi_version": (ctypes.c_int, []),
@@ -76,6 +86,7 @@ SIGNATURES = {
     "pa_rope_store_kv": (ctypes.c_int, [ctypes.POINTER(RopeStoreParams), c_p]),
     "pa_build_seqlens": (ctypes.c_int, [c_p, c_p, c_i32, c_p, c_p, c_p, c_p, c_p]),
     "pa_build_page_table": (ctypes.c_int, [c_p, c_i64, c_i64, c_p, c_i32, c_i32, c_i32, c_p, c_i32, c_p]),
+    "pa_build_batch": (ctypes.c_int, [ctypes.POINTER(BatchParams), c_p]),
     "pa_prefill": (ctypes.c_int, [ctypes.POINTER(PrefillParams), c_p]),
     "pa_decode_workspace_size": (c_size, [ctypes.POINTER(DecodeParams)]),
     "pa_decode_kv_chunk": (c_i32, [ctypes.POINTER(DecodeParams)]),

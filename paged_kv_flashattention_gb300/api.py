@@ -101,6 +101,7 @@ PA_DEVERR_SEQLENS = 2
 PA_DEVERR_TIMEOUT = 4
 PA_DEVERR_POSITION = 8
 PA_DEVERR_TABLE_INDEX = 16
+PA_DEVERR_NO_PAGES = 32
 
 
 def device_error() -> int:
@@ -341,6 +342,55 @@ def build_page_table(token_table: torch.Tensor, table_idx: torch.Tensor, max_seq
                                    int(max_seqlen_k), int(page_size), _ptr(out), out.stride(0),
                                    _stream(token_table)), lib)
     return out
+
+
+def build_batch(cached_len: torch.Tensor, extend_len: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor,
+                page_size: int, max_seqlen_k: int, *, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                cache_seqlens: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                page_table: torch.Tensor, totals: torch.Tensor, free_pages: torch.Tensor | None = None) -> None:
+    """A batch's metadata from lengths on the device, in one launch
+    (``pa_build_batch``; ``metadata.BatchPlanner`` owns the outputs).
+    cached_len, extend_len, table_idx: int32 [B]; token_table: int32 [rows, >=
+    max_seqlen_k].  Outputs: cu_seqlens_q, cu_seqlens_k [B+1], cache_seqlens
+    [B], positions and slot_mapping [T] (padded with 0 and -1 past the batch's
+    tokens), page_table [>= B, >= ceil(max_seqlen_k / page_size)] (columns past
+    a request's pages are left as they were), totals [4] (new tokens, longest
+    extend, longest length, new pages).  ``free_pages`` (int32): take the new
+    tokens' pages from it and enter their slots in ``token_table``."""
+    dev = token_table.device
+    B = cached_len.numel()
+    for t, n in ((cached_len, "cached_len"), (extend_len, "extend_len"), (table_idx, "table_idx"),
+                 (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k"), (cache_seqlens, "cache_seqlens"),
+                 (positions, "positions"), (slot_mapping, "slot_mapping"), (totals, "totals")):
+        _need(t, n, torch.int32, dev)
+    for t, n in ((token_table, "token_table"), (page_table, "page_table")):
+        _need(t, n, torch.int32, dev, contiguous=False)
+        if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{n} must be 2-D with unit column stride and rows that do not overlap")
+    if free_pages is not None:
+        _need(free_pages, "free_pages", torch.int32, dev)
+    max_k, P = int(max_seqlen_k), int(page_size)
+    if P <= 0:
+        raise ValueError("page_size must be positive")
+    if extend_len.numel() != B or table_idx.numel() != B:
+        raise ValueError("cached_len, extend_len and table_idx must hold one entry per request")
+    if cu_seqlens_q.numel() < B + 1 or cu_seqlens_k.numel() < B + 1 or cache_seqlens.numel() < B or totals.numel() < 4:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must hold B + 1 entries, cache_seqlens B, totals 4")
+    if positions.numel() != slot_mapping.numel():
+        raise ValueError("positions and slot_mapping must have the same size")
+    if token_table.shape[1] < max_k or page_table.shape[0] < B or page_table.shape[1] < -(-max_k // P):
+        raise ValueError(f"token_table must be at least {max_k} wide, page_table at least [{B}, {-(-max_k // P)}]")
+    p = _lib.BatchParams(
+        cached_len=_ptr(cached_len), extend_len=_ptr(extend_len), num_seqs=B, max_seqlen_k=max_k, page_size=P,
+        token_table=_ptr(token_table), token_table_stride=max(token_table.stride(0), token_table.shape[1]),
+        token_table_rows=token_table.shape[0], table_idx=_ptr(table_idx), free_pages=_ptr(free_pages),
+        num_free_pages=free_pages.numel() if free_pages is not None else 0, num_tokens=positions.numel(),
+        cu_seqlens_q=_ptr(cu_seqlens_q), cu_seqlens_k=_ptr(cu_seqlens_k), cache_seqlens=_ptr(cache_seqlens),
+        positions=_ptr(positions), slot_mapping=_ptr(slot_mapping), page_table=_ptr(page_table),
+        page_table_stride=max(page_table.stride(0), page_table.shape[1]), totals=_ptr(totals))
+    lib = _lib.load()
+    with torch.cuda.device(dev):
+        _check(lib.pa_build_batch(ctypes.byref(p), _stream(token_table)), lib)
 
 
 def _pool_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, page_size: int | None):

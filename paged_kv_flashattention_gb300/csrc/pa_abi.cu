@@ -96,7 +96,8 @@ pa_status pa_device_error(int32_t *bits, void *stream) {
     if (bits == nullptr) return fail(PA_ERR_INVALID, "bits is NULL");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t (*getters[])(int **) = {error_word_store, error_word_decode, error_word_prefill, error_word_mixed,
-                                      error_word_fp4, error_word_decode_fp4};
+                                      error_word_fp4, error_word_decode_fp4,
+                                      error_word_batch};
     int32_t acc = 0;
     for (auto get : getters) {
         int *addr = nullptr;
@@ -303,6 +304,28 @@ pa_status pa_build_page_table(const int32_t *token_table, int64_t token_table_st
                                             (int32_t)ncols, page_size, page_table, page_table_stride,
                                             static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_page_table launch");
+}
+
+pa_status pa_build_batch(const pa_batch_params *p, void *stream) {
+    g_last_error[0] = 0;
+    if (p == nullptr) return fail(PA_ERR_INVALID, "params is NULL");
+    if (p->num_seqs < 0 || p->max_seqlen_k < 0 || p->num_tokens < 0 || p->token_table_rows < 0 || p->num_free_pages < 0)
+        return fail(PA_ERR_INVALID, "negative sizes");
+    if (p->page_size <= 0) return fail(PA_ERR_INVALID, "page_size must be positive");
+    if (p->num_seqs > 16384) return fail(PA_ERR_UNSUPPORTED, "more than 16384 requests in one batch");
+    if ((int64_t)p->num_seqs * p->max_seqlen_k > INT32_MAX || p->num_tokens > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs * max_seqlen_k and num_tokens must stay below 2^31");
+    const int64_t ncols = ((int64_t)p->max_seqlen_k + p->page_size - 1) / p->page_size;
+    if (p->page_table_stride < ncols) return fail(PA_ERR_INVALID, "page_table_stride %d < %lld columns", p->page_table_stride, (long long)ncols);
+    if (p->token_table_stride < p->max_seqlen_k)
+        return fail(PA_ERR_INVALID, "token_table_stride %lld < max_seqlen_k %d", (long long)p->token_table_stride, p->max_seqlen_k);
+    if (!p->cu_seqlens_q || !p->cu_seqlens_k || !p->totals) return fail(PA_ERR_INVALID, "NULL pointer");
+    if (p->num_seqs > 0 && (!p->cached_len || !p->extend_len || !p->token_table || !p->table_idx || !p->cache_seqlens ||
+                            !p->page_table))
+        return fail(PA_ERR_INVALID, "NULL pointer");
+    if (p->num_tokens > 0 && (!p->positions || !p->slot_mapping)) return fail(PA_ERR_INVALID, "NULL pointer");
+    cudaError_t e = launch_build_batch(*p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_batch launch");
 }
 
 // Validation of a pa_prefill call; *nothing = the call has no query rows

@@ -34,6 +34,8 @@ cudaError_t launch_build_page_table(const int32_t *token_table, int64_t tt_strid
                                     int32_t page_size, int32_t *page_table, int32_t pt_stride,
                                     cudaStream_t stream);
 
+cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream);
+
 // Decode plan: keys per split, splits of the longest sequence, KV heads per CTA.
 struct DecodePlan {
     int32_t kv_chunk;
@@ -74,6 +76,7 @@ cudaError_t error_word_decode(int **addr);
 cudaError_t error_word_prefill(int **addr);
 cudaError_t error_word_mixed(int **addr);
 cudaError_t error_word_fp4(int **addr);
+cudaError_t error_word_batch(int **addr);
 cudaError_t error_word_decode_fp4(int **addr);
 
 }  // namespace pa

@@ -155,3 +155,62 @@ class MixedMetadataBuilder:
                            cu_seqlens_q=d[o:o + Bd + 1], cu_seqlens_k=d[o + nd:o + nd + Bd + 1],
                            cache_seqlens=d[o + 2 * nd:o + 2 * nd + Bd], page_table=pt[:Bd], h2d_bytes=3 * nd * 4)
         return mp, md
+
+
+@dataclass
+class DeviceBatch:
+    """Metadata built on the device by ``BatchPlanner`` (views of its buffers).
+    ``totals``: new tokens, longest extend, longest length, new pages."""
+    num_seqs: int
+    page_size: int
+    max_seqlen_k: int              # the planner's bound
+    cu_seqlens_q: torch.Tensor     # int32 [B+1]
+    cu_seqlens_k: torch.Tensor     # int32 [B+1]
+    cache_seqlens: torch.Tensor    # int32 [B]
+    positions: torch.Tensor        # int32 [max_tokens], 0 past the batch's tokens
+    slot_mapping: torch.Tensor     # int32 [max_tokens], -1 past the batch's tokens
+    page_table: torch.Tensor       # int32 [B, ceil(max_seqlen_k / page_size)]
+    totals: torch.Tensor           # int32 [4]
+
+
+class BatchPlanner:
+    """The batch's metadata from lengths that live on the device, without the
+    host: boundaries, positions, slots and page table in one launch into fixed
+    buffers, so a captured graph (``build``, the stores, the attention) follows
+    the lengths from replay to replay.  Page-table entries past a request's
+    pages keep what earlier batches left there (-1 at first); the attention
+    never reads them.  Each ``build`` overwrites the buffers of the one before:
+    use one planner per batch in flight."""
+
+    def __init__(self, device, max_seqs: int, max_tokens: int, max_seqlen_k: int, page_size: int):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.max_seqs, self.max_tokens = int(max_seqs), int(max_tokens)
+        self.max_seqlen_k, self.page_size = int(max_seqlen_k), int(page_size)
+        if self.max_seqs < 0 or self.max_tokens < 0 or self.max_seqlen_k < 0 or self.page_size <= 0:
+            raise ValueError("sizes must not be negative, page_size positive")
+        n = self.max_seqs
+        self.cu_seqlens = torch.zeros((2, n + 1), dtype=torch.int32, device=self.device)
+        self.cache_seqlens = torch.zeros(n, dtype=torch.int32, device=self.device)
+        self.tokens = torch.zeros((2, self.max_tokens), dtype=torch.int32, device=self.device)
+        self.totals = torch.zeros(4, dtype=torch.int32, device=self.device)
+        cols = -(-self.max_seqlen_k // self.page_size)
+        self.page_table = torch.full((n, max(cols, 1)), -1, dtype=torch.int32, device=self.device)
+
+    def build(self, cached_len: torch.Tensor, extend_len: torch.Tensor, token_table: torch.Tensor,
+              table_idx: torch.Tensor, *, free_pages: torch.Tensor | None = None) -> DeviceBatch:
+        """Plan the batch of cached_len / extend_len (int32 [B], B <= max_seqs)
+        whose requests are the rows table_idx of token_table."""
+        B = cached_len.numel()
+        if B > self.max_seqs:
+            raise ValueError(f"batch of {B} requests > planner capacity {self.max_seqs}")
+        b = DeviceBatch(num_seqs=B, page_size=self.page_size, max_seqlen_k=self.max_seqlen_k,
+                        cu_seqlens_q=self.cu_seqlens[0, :B + 1], cu_seqlens_k=self.cu_seqlens[1, :B + 1],
+                        cache_seqlens=self.cache_seqlens[:B], positions=self.tokens[0], slot_mapping=self.tokens[1],
+                        page_table=self.page_table[:B], totals=self.totals)
+        api.build_batch(cached_len, extend_len, token_table, table_idx, self.page_size, self.max_seqlen_k,
+                        cu_seqlens_q=b.cu_seqlens_q, cu_seqlens_k=b.cu_seqlens_k, cache_seqlens=b.cache_seqlens,
+                        positions=b.positions, slot_mapping=b.slot_mapping, page_table=b.page_table, totals=b.totals,
+                        free_pages=free_pages)
+        return b

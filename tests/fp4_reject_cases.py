@@ -1,4 +1,4 @@
-"""Malformed 4-bit calls that libpa must reject on the host, before any
+"""Malformed calls of the 4-bit entry points and the batch plan that libpa must reject on the host, before any
 launch; run as a script with no GPU visible (the pointers are made up), it
 prints one JSON object {case id: [status, last error]}."""
 from __future__ import annotations
@@ -39,11 +39,50 @@ ROPE_CASES = [
     ("misaligned_pool", dict(v_cache=0x8008), INVALID),
 ]
 
+DECODE = dict(q=0x1000, k_cache=0x2000, v_cache=0x3000, page_table=0x4000, page_table_stride=64, cache_seqlens=0x5000,
+              num_seqs=2, max_seqlen_k=512, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16, num_pages=1000,
+              scale=0.1, out=0x7000, lse=None, workspace=0x8000, workspace_bytes=1 << 30, kv_chunk=0, kv_dtype=2,
+              k_scale=0x9000, v_scale=0x9100)
+DECODE_CASES = [
+    ("no_scales", dict(k_scale=None), INVALID),
+    ("head_dim96", dict(head_dim=96), UNSUPPORTED),
+    ("page8", dict(page_size=8), UNSUPPORTED),
+    ("group3", dict(num_q_heads=6), UNSUPPORTED),
+    ("small_workspace", dict(workspace_bytes=4096), INVALID),
+    ("misaligned_pool", dict(k_cache=0x2008), INVALID),
+    ("table_stride", dict(page_table_stride=31), INVALID),
+    ("scale_zero", dict(scale=0.0), INVALID),
+    ("keys_overflow_int32", dict(num_seqs=16384, max_seqlen_k=1 << 18, page_table_stride=1 << 14, num_pages=1 << 20,
+                                 kv_chunk=1 << 16), UNSUPPORTED),
+    ("no_sequences", dict(num_seqs=0), OK),
+]
+BATCH = dict(cached_len=0x1000, extend_len=0x2000, num_seqs=4, max_seqlen_k=100, page_size=16, token_table=0x3000,
+             token_table_stride=100, token_table_rows=8, table_idx=0x4000, free_pages=0x5000, num_free_pages=8, num_tokens=40,
+             cu_seqlens_q=0x6000, cu_seqlens_k=0x7000, cache_seqlens=0x8000, positions=0x9000, slot_mapping=0xA000,
+             page_table=0xB000, page_table_stride=7, totals=0xC000)
+BATCH_CASES = [
+    ("negative_seqs", dict(num_seqs=-1), INVALID),
+    ("negative_tokens", dict(num_tokens=-1), INVALID),
+    ("negative_free", dict(num_free_pages=-1), INVALID),
+    ("page0", dict(page_size=0), INVALID),
+    ("too_many_seqs", dict(num_seqs=16385), UNSUPPORTED),
+    ("keys_overflow_int32", dict(num_seqs=16384, max_seqlen_k=1 << 17, token_table_stride=1 << 17,
+                                 page_table_stride=1 << 13), UNSUPPORTED),
+    ("too_many_tokens", dict(num_tokens=1 << 31), UNSUPPORTED),
+    ("page_table_stride", dict(page_table_stride=6), INVALID),
+    ("token_table_stride", dict(token_table_stride=99), INVALID),
+    ("null_lens", dict(extend_len=None), INVALID),
+    ("null_slots", dict(slot_mapping=None), INVALID),
+    ("null_totals", dict(totals=None), INVALID),
+]
+
 
 def expected():
     out = {f"store/{i}": s for i, _, s in STORE_CASES}
     out.update({f"load/{i}": s for i, _, s in STORE_CASES})
     out.update({f"rope/{i}": s for i, _, s in ROPE_CASES})
+    out.update({f"decode/{i}": s for i, _, s in DECODE_CASES})
+    out.update({f"batch/{i}": s for i, _, s in BATCH_CASES})
     return out
 
 
@@ -63,6 +102,12 @@ def run_all() -> dict:
     for i, kw, _ in ROPE_CASES:
         p = _lib.RopeStoreParams(**{**ROPE, **kw})
         rec(f"rope/{i}", lib.pa_rope_store_kv(ctypes.byref(p), None))
+    for i, kw, _ in DECODE_CASES:
+        p = _lib.DecodeParams(**{**DECODE, **kw})
+        rec(f"decode/{i}", lib.pa_decode(ctypes.byref(p), None))
+    for i, kw, _ in BATCH_CASES:
+        p = _lib.BatchParams(**{**BATCH, **kw})
+        rec(f"batch/{i}", lib.pa_build_batch(ctypes.byref(p), None))
     return res
 
 

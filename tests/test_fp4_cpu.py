@@ -80,3 +80,42 @@ def test_binding_kv_dtype_checks():
             api._kv_dtype(pool, pool, asked)
     with pytest.raises(ValueError):
         api._kv_dtype(u8, u8, 3)
+
+
+def test_binding_batch_checks():
+    import paged_kv_flashattention_gb300 as pa
+    pl = pa.BatchPlanner("cpu", 4, 16, 100, 16)
+    assert pl.page_table.shape == (4, 7) and bool((pl.page_table == -1).all())
+    c = torch.zeros(3, dtype=torch.int32)
+    tt, idx = torch.zeros((5, 100), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        pl.build(torch.zeros(5, dtype=torch.int32), c, tt, idx)           # more than the planner holds
+    with pytest.raises(ValueError):
+        pl.build(c, c[:2], tt, idx)
+    with pytest.raises(ValueError):
+        pl.build(c, c, tt[:, :99], idx)                                   # narrower than max_seqlen_k
+    with pytest.raises(TypeError):
+        pl.build(c.long(), c, tt, idx)
+    with pytest.raises(TypeError):
+        pl.build(c, c, tt, idx, free_pages=torch.zeros(4))
+    with pytest.raises(ValueError):
+        pl.build(c, c, tt.t().contiguous().t(), idx)
+    with pytest.raises(ValueError):
+        pl.build(c, c, tt[:1].expand(5, 100), idx)                        # rows on top of each other
+    for bad in ((-1, 1, 1, 1), (1, 1, 1, 0)):
+        with pytest.raises(ValueError):
+            pa.BatchPlanner("cpu", *bad)
+
+
+def test_binding_decode_sizes():
+    import paged_kv_flashattention_gb300 as pa
+    kc, _ = _pools(pages=300)
+    shape = (3, 32, 64)
+    n = pa.decode_workspace_size(shape, kc, 4096, kv_dtype=pa.PA_KV_FP4, num_kv_heads=8)
+    assert n > 0 and pa.decode_kv_chunk(shape, kc, 4096, kv_dtype=pa.PA_KV_FP4, num_kv_heads=8) % 16 == 0
+    flat = kc.view(-1, kc.shape[-1])
+    assert n == pa.decode_workspace_size(shape, flat, 4096, page_size=16, kv_dtype=pa.PA_KV_FP4, num_kv_heads=8)
+    with pytest.raises(ValueError):
+        pa.decode_workspace_size(shape, kc, 4096, kv_dtype=pa.PA_KV_FP4)
+    with pytest.raises(ValueError):
+        pa.decode_workspace_size(shape, flat, 4096, kv_dtype=pa.PA_KV_FP4, num_kv_heads=8)
