@@ -97,7 +97,7 @@ pa_status pa_device_error(int32_t *bits, void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t (*getters[])(int **) = {error_word_store, error_word_decode, error_word_prefill, error_word_mixed,
                                       error_word_fp4, error_word_decode_fp4,
-                                      error_word_batch};
+                                      error_word_prefill_fp4, error_word_batch};
     int32_t acc = 0;
     for (auto get : getters) {
         int *addr = nullptr;
@@ -360,10 +360,10 @@ static pa_status check_prefill(const pa_prefill_params *p, bool *nothing) {
     if (p->lse != nullptr && p->lse_stride <= 0) return fail(PA_ERR_INVALID, "lse_stride must be positive");
     if (p->num_pages > (int64_t)INT32_MAX / p->page_size)
         return fail(PA_ERR_UNSUPPORTED, "pool larger than 2^31 slots");
-    if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3)
-        return fail(PA_ERR_INVALID, "kv_dtype %d is neither PA_KV_BF16 nor PA_KV_FP8_E4M3", p->kv_dtype);
-    if (p->kv_dtype == PA_KV_FP8_E4M3 && (!p->k_scale || !p->v_scale))
-        return fail(PA_ERR_INVALID, "FP8 pools need k_scale and v_scale");
+    if (p->kv_dtype != PA_KV_BF16 && p->kv_dtype != PA_KV_FP8_E4M3 && p->kv_dtype != PA_KV_FP4)
+        return fail(PA_ERR_INVALID, "kv_dtype %d is not a pa_kv_dtype", p->kv_dtype);
+    if (p->kv_dtype != PA_KV_BF16 && (!p->k_scale || !p->v_scale))
+        return fail(PA_ERR_INVALID, "FP8 and 4-bit pools need k_scale and v_scale");
     if (p->sliding_window < 0) return fail(PA_ERR_INVALID, "sliding_window must be >= 0");
     if (p->max_ctas < 0) return fail(PA_ERR_INVALID, "max_ctas must be >= 0");
     if (p->scheduler == nullptr) return fail(PA_ERR_INVALID, "scheduler (device int32[2], zero-initialised) is NULL");
@@ -385,7 +385,8 @@ pa_status pa_prefill(const pa_prefill_params *p, void *stream) {
     bool nothing = false;
     pa_status st = check_prefill(p, &nothing);
     if (st != PA_OK || nothing) return st;
-    cudaError_t e = launch_prefill(*p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = p->kv_dtype == PA_KV_FP4 ? launch_prefill_fp4(*p, static_cast<cudaStream_t>(stream))
+                                             : launch_prefill(*p, static_cast<cudaStream_t>(stream));
     if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "prefill configuration not supported by this library");
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "prefill launch");
 }

@@ -59,6 +59,7 @@ cudaError_t launch_lse_combine(const float *o_partial, const float *lse_partial,
                                cudaStream_t stream);
 
 cudaError_t launch_prefill(const pa_prefill_params &p, cudaStream_t stream);
+cudaError_t launch_prefill_fp4(const pa_prefill_params &p, cudaStream_t stream);
 cudaError_t launch_mixed(const pa_prefill_params &pre, const pa_decode_params &dec, cudaStream_t stream);
 
 int num_sms();
@@ -76,6 +77,7 @@ cudaError_t error_word_decode(int **addr);
 cudaError_t error_word_prefill(int **addr);
 cudaError_t error_word_mixed(int **addr);
 cudaError_t error_word_fp4(int **addr);
+cudaError_t error_word_prefill_fp4(int **addr);
 cudaError_t error_word_batch(int **addr);
 cudaError_t error_word_decode_fp4(int **addr);
 

@@ -55,6 +55,15 @@
 // into f16 q * k_scale.
 // The MMAs then run with f16 operands (P is written to TMEM as f16) and the
 // epilogue multiplies by v_scale.
+//
+// 4-bit pools (F4; row layout: fp4.cuh) take the same path: a tile's 128 x d/2
+// bytes of codes and 128 x 16 bytes that hold the head's scales land inside
+// the f16 slot (two TMA boxes per page, or row gathers at page size 1), rows 0
+// - 63 and 64 - 127 each where the warp that widens them will write, so that a
+// warp reads its part into registers and overwrites it without meeting the
+// other: E2M1 to f16 by the hardware conversion, times the block's scale
+// (exact in f16).  k_scale is a factor of
+// the scores here, so Q only changes from bf16 to f16.
 #pragma once
 
 #include <cuda.h>
@@ -63,6 +72,7 @@
 
 #include <mutex>
 
+#include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -114,6 +124,9 @@ struct PrefillArgs {
     const uint8_t *bmask;         // block-sparse mask [num_seqs][bm_q][bm_k] over 128 x 128 blocks, or null
     int32_t bm_q, bm_k;
     int32_t max_q, max_k;         // the call's max_seqlen_q / max_seqlen_k (bounds of the device lengths)
+    CUtensorMap ksmap;            // 4-bit pools: the scales of kmap's and vmap's rows
+    CUtensorMap vsmap;
+    Fp4Layout lay;                // 4-bit pools
     int32_t num_ctas;             // CTAs that run the work loop (the last of them resets sched);
                                   // 0: the count passed to prefill_body
 };
@@ -246,11 +259,11 @@ __device__ void prefill_sched_done(const PrefillArgs &a, int num_ctas) {
 // tiles ahead of the MMAs: with one CTA per SM the loads from L2 are latency
 // bound, and bytes in flight set the rate (at d = 128 with two heads, 4
 // slots measured as fast as 5).
-template <int D, int T, bool F8>
+template <int D, int T, bool F8, bool F4 = false>
 struct PrefillSmem {
     static constexpr int kHalves = D / 64;                 // 64-column (128-byte) halves
     static constexpr int kTileBytes = kHalves * 128 * 128; // 128 rows x D, 16-bit elements
-    static constexpr int kLTile = F8 ? kTileBytes / 2 : kTileBytes;   // a tile as loaded
+    static constexpr int kLTile = F4 ? kBN * (D / 2 + 16) : F8 ? kTileBytes / 2 : kTileBytes;   // a tile as loaded
     static constexpr int kQ = 0;                           // T query tiles
     static constexpr int kRing = T * kTileBytes;           // ring of loaded tiles
     static constexpr int kStageBytes = 4 * T * 4096;      // 32 rows x 64 columns bf16 per warp
@@ -260,7 +273,9 @@ struct PrefillSmem {
     // goes) and is widened where it lies, so the slots serve both rings.
     // FP8, d = 64: a ring of widened f16 tiles (2..4 slots) and a separate
     // ring of loaded tiles from the rest.
-    static constexpr bool kInPlace = F8 && D == 128;
+    // 4-bit: in place at either head size (the tile is in registers when the
+    // slot is overwritten).
+    static constexpr bool kInPlace = F4 || (F8 && D == 128);
     static constexpr int kFitTiles = kAvail / kTileBytes;
     static constexpr int kCSlotsFit = (kAvail / 2) / kTileBytes;
     static constexpr int kCSlots = !F8 ? 0
@@ -269,7 +284,11 @@ struct PrefillSmem {
     static constexpr int kSlotsFit = kInPlace ? kCSlots : (kAvail - kCSlots * kTileBytes) / kLTile;
     static constexpr int kSlots = kSlotsFit > 8 ? 8 : kSlotsFit;
     static constexpr int kLStride = kInPlace ? kTileBytes : kLTile;       // landing slot stride
-    static constexpr int kLOff = kInPlace ? kTileBytes - kLTile : 0;      // landing offset in a slot
+    static constexpr int kLOff = F4 ? kTileBytes - 16384 : kInPlace ? kTileBytes - kLTile : 0;   // landing offset in a slot
+    // 4-bit landing area: per 64 rows (8 KiB apart) D/2 bytes of codes a row,
+    // then 16 bytes with the scales a row.
+    static constexpr int code_off(int r) { return (r >> 6) * 8192 + (r & 63) * (D / 2); }
+    static constexpr int scale_off(int r) { return (r >> 6) * 8192 + 32 * D + (r & 63) * 16; }
     static constexpr int kConv = kInPlace ? kRing : kRing + kSlots * kLTile;
     static constexpr int kStage = kInPlace ? kRing + kCSlots * kTileBytes : kConv + kCSlots * kTileBytes;
     static constexpr int kBars = kStage + kStageBytes;
@@ -333,9 +352,10 @@ cudaError_t check_register_split(Kernel kern) {
 
 // EXT: the instantiation for sliding windows and block-sparse masks (plain
 // launches keep that arithmetic out of their registers).
-template <int D, int T, bool F8, bool EXT>
+template <int D, int T, bool F8, bool EXT, bool F4 = false>
 __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_ctas = 0) {
-    using S = PrefillSmem<D, T, F8>;
+    static_assert(!F4 || F8, "4-bit pools use the widening path");
+    using S = PrefillSmem<D, T, F8, F4>;
     // A kernel launched after this one as a programmatic dependent (decode
     // sharing the GPU) may start once every CTA of this grid is resident.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -426,7 +446,45 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             rows[rr] = key < it.kv_end ? pt[key] : -1;
         }
     };
+    // 4-bit rows: where a KV head's codes start, and the 16 bytes that hold its
+    // scales (two heads' at d = 128, four at d = 64).
+    auto codes_at = [&](int kvh) { return (kvh / a.lay.gs) * a.lay.group_bytes + (kvh & (a.lay.gs - 1)) * (D / 2); };
+    auto scales_at = [&](int kvh) {
+        return (kvh / a.lay.gs) * a.lay.group_bytes + a.lay.code_bytes + (((kvh & (a.lay.gs - 1)) * (D / 16)) & ~15);
+    };
     auto gather_copy = [&](const PrefillItem &it, int c, int st, int gl, const int (&rows)[kBN / 32]) {
+        if constexpr (F4) {
+            constexpr int kChunks = D / 32;               // 16-byte chunks of a row's codes
+            constexpr int kRowsPerIssue = 32 / kChunks;
+            uint8_t *dst = land(gl % NS);
+            const uint8_t *src = (c & 1) ? a.v_cache : a.k_cache;
+            const int co = codes_at(it.kvh), so = scales_at(it.kvh);
+            const int key0 = (it.j0 + st) * kBN;
+            const int q = lane % kChunks, sub = lane / kChunks;
+            auto copy = [&](int off, int row, int in_row) {
+                if (row >= 0)
+                    cp_async16(dst + off, src + (int64_t)row * a.lay.row_bytes + in_row);
+                else
+                    *reinterpret_cast<uint4 *>(dst + off) = make_uint4(0, 0, 0, 0);
+            };
+#pragma unroll 1
+            for (int rr = 0; rr < kBN / 32; ++rr) {
+                int row = rr == 0 ? rows[0] : rr == 1 ? rows[1] : rr == 2 ? rows[2] : rows[3];
+                if (key0 + rr * 32 + lane < it.kv_end && (row < 0 || row >= a.num_slots)) {
+                    raise_error(PA_DEVERR_PAGE_RANGE);
+                    row = -1;
+                }
+                copy(S::scale_off(rr * 32 + lane), row, so);
+#pragma unroll
+                for (int i = 0; i < 32 / kRowsPerIssue; ++i) {
+                    const int rl = i * kRowsPerIssue + sub;
+                    const int rowv = __shfl_sync(0xffffffffu, row, rl);
+                    copy(S::code_off(rr * 32 + rl) + q * 16, rowv, co + q * 16);
+                }
+            }
+            cp_async_commit();
+            return;
+        }
         if constexpr (F8) {
             // E4M3 rows of D bytes, copied as they are (row-major, no swizzle)
             constexpr int kChunks = D / 16;
@@ -520,6 +578,48 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         return true;
     };
 
+    // Tile c of item `it` from its 4-bit landing area to f16 in the swizzled
+    // layout: warp cw widens rows [64 cw, 64 cw + 64).  A lane takes 16-byte
+    // chunks of codes (32 elements, two blocks) of the rows = lane mod 8, so
+    // that each store of a warp's quarter covers all banks.  The warp reads all
+    // of its rows before it writes over them.  Rows at keys >= kv_end hold slots the store never wrote: a zero scale clears them.
+    auto widen4 = [&](const PrefillItem &it, int c, int cw, const uint8_t *src, uint8_t *dst) {
+        constexpr int kChunks = D / 32;               // chunks of a row
+        constexpr int kRows = 32 / kChunks;           // rows of a pass: 8 or 16
+        constexpr int kPasses = 64 / kRows;
+        int live = kBN;
+        if (c >= 2 * it.n_kv - 2 && StepCursor().at<EXT>(a, it, it.n_kv - 1) == it.n_all - 1)
+            live = it.kv_end - (it.j0 + it.n_all - 1) * kBN;
+        const int sub = D == 128 ? (it.kvh & (a.lay.gs - 1) & 1) * 8 : (it.kvh & (a.lay.gs - 1) & 3) * 4;
+        const int ch = lane / kRows;
+        uint4 x[kPasses];
+        uint32_t sc[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = 64 * cw + i * kRows + lane % kRows;
+            x[i] = *reinterpret_cast<const uint4 *>(src + S::code_off(r) + ch * 16);
+            sc[i] = *reinterpret_cast<const uint16_t *>(src + S::scale_off(r) + sub + 2 * ch);
+            if (r >= live) sc[i] = 0u;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = 64 * cw + i * kRows + lane % kRows;
+            const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+            const uint32_t s[2] = {f16_dup_lo(s2), f16_dup_hi(s2)};
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint8_t *row = dst + (ch / 2) * 16384 + r * 128;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                uint32_t f[4];
+                e2m1x8_to_f16x8(w[p], f);
+                const uint32_t sp = s[p / 2];
+                *reinterpret_cast<uint4 *>(row + ((((ch & 1) * 4 + p) ^ (r & 7)) * 16)) =
+                    make_uint4(hmul2_bits(f[0], sp), hmul2_bits(f[1], sp), hmul2_bits(f[2], sp), hmul2_bits(f[3], sp));
+            }
+        }
+    };
+
     if (warp >= kProducer) {
         // ------------------------------------- producer / MMA warpgroup ----
         if (T == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
@@ -528,6 +628,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         if (lane == 0) {
             prefetch_tmap(&a.qmap);
             if (paged16) { prefetch_tmap(&a.kmap); prefetch_tmap(&a.vmap); }
+            if (F4 && paged16) { prefetch_tmap(&a.ksmap); prefetch_tmap(&a.vsmap); }
         }
         // K/V tiles are re-read by the other items of their request:
         // evict-last keeps them in L2 beside a concurrent stream (a decode
@@ -601,7 +702,15 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                     // lanes 0..7 each own one 16-token page of the tile
                     if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kLTile);
                     __syncwarp();
-                    if (lane < kBN / 16) {
+                    if constexpr (F4) {               // lanes 0-7 a page's codes, lanes 8-15 its scales
+                        const int s0 = __shfl_sync(0xffffffffu, slot0, lane & 7);
+                        if (lane < 8)
+                            tma_load_3d_hint(dst + S::code_off(lane * 16), (c & 1) ? &a.vmap : &a.kmap, codes_at(it.kvh), 0, s0,
+                                             &full[slot], kv_pol);
+                        else if (lane < 16)
+                            tma_load_3d_hint(dst + S::scale_off((lane - 8) * 16), (c & 1) ? &a.vsmap : &a.ksmap,
+                                             scales_at(it.kvh), 0, s0, &full[slot], kv_pol);
+                    } else if (lane < kBN / 16) {
                         const CUtensorMap *map = (c & 1) ? &a.vmap : &a.kmap;
                         if constexpr (F8) {           // one (D bytes x 16 rows) box per page
                             tma_load_3d_hint(dst + lane * 16 * D, map, 0, it.kvh, slot0, &full[slot], kv_pol);
@@ -660,7 +769,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             // Q tiles: bf16 -> f16 of q * k_scale, in place
             if (!__all_sync(0xffffffffu, mbar_wait(q_full, local & 1))) break;
             ++local;
-            const float ksc = __ldg(a.k_scale + it.kvh);
+            const float ksc = F4 ? 1.f : __ldg(a.k_scale + it.kvh);
 #pragma unroll 4
             for (int i = cw * 32 + lane; i < T * S::kTileBytes / 16; i += 64) {
                 uint4 *pq = reinterpret_cast<uint4 *>(sQ + i * 16);
@@ -679,6 +788,13 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if (!ok) break;
                 const uint8_t *src = land(ls);
                 uint8_t *dst = smem + S::kConv + cs * S::kTileBytes;
+                if constexpr (F4) {
+                    widen4(it, c, cw, src, dst);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cfull[cs]);
+                    continue;
+                }
                 // groups of 4 x 512 bytes: all reads of a group, then (in
                 // place, after the warp has read them) the writes, which
                 // overwrite only rows of the same group
@@ -840,7 +956,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_tm = tmem + lane_base + 128 * k;
         const uint32_t o_tm = tmem + lane_base + 256 + kOCols * k;
-        const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
+        float sl2 = a.scale_log2;                     // 4-bit pools: times the item's k_scale
+        float2 c2 = make_float2(sl2, sl2);
         int fin = 0, gs = 0, local = 0;
         bool ok = true;
         PrefillItem it;
@@ -854,6 +971,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         ++local;
         if (v < 0) break;
         prefill_item<T, EXT>(a, v, it);
+        if constexpr (F4) {
+            sl2 = a.scale_log2 * __ldg(a.k_scale + it.kvh);
+            c2 = make_float2(sl2, sl2);
+        }
         const int n_kv = it.n_kv, Lk = it.Lk, off = it.off, min_vis = it.min_vis;
         const int qi = it.tile * kBM + r;             // query index within the request
         const bool row_valid = r < it.rows_here;
@@ -896,7 +1017,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], __uint_as_float(sr[c + i]));
             const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-            const float m_cand = mt * a.scale_log2;
+            const float m_cand = mt * sl2;
             // lazy maximum: move it only when the tile maximum exceeds it by
             // more than kLazy; then O_k (PV_k(j-1) is complete: the commit of
             // S_k(j) tracks it) and l are rescaled
@@ -1042,6 +1163,19 @@ bool make_map_fp8(CUtensorMap *m, const void *base, int d, int heads, int64_t ro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D byte map (row bytes, 1, rows) of a 4-bit pool with a (box_bytes, 1, 16) box.
+bool make_map_fp4(CUtensorMap *m, const void *base, int row_bytes, int64_t rows, int box_bytes) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)row_bytes, 1, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes};
+    cuuint32_t box[3] = {(cuuint32_t)box_bytes, 1, 16};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Fill the kernel arguments of a validated pa_prefill call (tensor maps,
 // metadata pointers, the work-item count; T = query heads per item).
 cudaError_t prefill_setup(const pa_prefill_params &p, PrefillArgs &a, int &T) {
@@ -1049,7 +1183,15 @@ cudaError_t prefill_setup(const pa_prefill_params &p, PrefillArgs &a, int &T) {
     const int64_t num_slots = p.num_pages * p.page_size;
     if (!make_map(&a.qmap, p.q, p.head_dim, p.num_q_heads, p.total_q, kBM)) return cudaErrorNotSupported;
     const bool f8 = p.kv_dtype == PA_KV_FP8_E4M3;
-    if (p.page_size == 16) {
+    if (p.kv_dtype == PA_KV_FP4) {
+        a.lay = fp4_layout(p.num_kv_heads, p.head_dim);
+        if (p.page_size == 16 &&
+            (!make_map_fp4(&a.kmap, p.k_cache, a.lay.row_bytes, num_slots, p.head_dim / 2) ||
+             !make_map_fp4(&a.vmap, p.v_cache, a.lay.row_bytes, num_slots, p.head_dim / 2) ||
+             !make_map_fp4(&a.ksmap, p.k_cache, a.lay.row_bytes, num_slots, 16) ||
+             !make_map_fp4(&a.vsmap, p.v_cache, a.lay.row_bytes, num_slots, 16)))
+            return cudaErrorNotSupported;
+    } else if (p.page_size == 16) {
         auto mk = f8 ? make_map_fp8 : make_map;
         if (!mk(&a.kmap, p.k_cache, p.head_dim, p.num_kv_heads, num_slots, 16)) return cudaErrorNotSupported;
         if (!mk(&a.vmap, p.v_cache, p.head_dim, p.num_kv_heads, num_slots, 16)) return cudaErrorNotSupported;
