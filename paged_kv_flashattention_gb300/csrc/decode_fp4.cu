@@ -179,30 +179,147 @@ __device__ void fp4_produce(const Fp4DecodeArgs &a, const int32_t *prefix, int64
     }
 }
 
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
+// What a consumer lane knows of its place in the fragments (bytes from the
+// start of a stage).
+template <int D, int HPC>
+struct Fp4Lane {
+    using S = Fp4Smem<D, HPC>;
+    int tk, t0, t1;               // keys tk, tk + 8 of the scores; t0, t1, t0 + 8, t1 + 8 of the second product
+    int k_off, ks_off;            // codes and scales of key tk
+    int v_off0, v_off1;           // codes of keys t0, t1
+    int vs_off0, vs_off1;         // their scales
+    __device__ Fp4Lane(int hw, int lane) {
+        const int r8 = lane >> 2, q4 = lane & 3;
+        auto place = [](int r) { return r ^ ((r >> 1) & 1); };   // row of the fragment -> key of the unit
+        tk = place(r8);
+        t0 = place(2 * q4);
+        t1 = place(2 * q4 + 1);
+        k_off = tk * S::kRow + hw * (D / 2) + q4 * (D / 8);
+        ks_off = tk * S::kRow + S::kCodes + hw * (D / 16) + q4 * (D / 64);
+        const int v = kUnit * S::kRow + hw * (D / 2) + r8 * (D / 16);
+        const int vs = kUnit * S::kRow + S::kCodes + hw * (D / 16) + (D == 128 ? r8 : r8 >> 1);
+        v_off0 = v + t0 * S::kRow;
+        v_off1 = v + t1 * S::kRow;
+        vs_off0 = vs + t0 * S::kRow;
+        vs_off1 = vs + t1 * S::kRow;
+    }
+};
+
+// Raw scores of a unit: x[0], x[1] of key tk and heads 2 q4, 2 q4 + 1; x[2],
+// x[3] of key tk + 8.  Keys outside [n0, n1) give -inf.
+template <int D, int HPC>
+__device__ __forceinline__ void fp4_scores(const Fp4Lane<D, HPC> &ln, const uint8_t *st, const uint32_t (&qb)[D / 16][2],
+                                           int n0, int n1, float *x) {
+    using S = Fp4Smem<D, HPC>;
+    constexpr int KW = D / 32;                       // words of a lane's part of a row
+    float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t kw[2][KW], ks[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t *p = st + 8 * i * S::kRow;
+        if constexpr (KW == 4) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(p + ln.k_off);
+            kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
+            ks[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(p + ln.ks_off));
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p + ln.k_off);
+            kw[i][0] = w.x; kw[i][1] = w.y;
+            ks[i] = e4m3x2_to_f16x2(p[ln.ks_off]);
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {                   // a word is two k-steps
+        uint32_t a[4], b[4];
+        e2m1x8_to_f16x8(kw[0][w], a);
+        e2m1x8_to_f16x8(kw[1][w], b);
+        const uint32_t s0 = w < 2 ? f16_dup_lo(ks[0]) : f16_dup_hi(ks[0]);
+        const uint32_t s1 = w < 2 ? f16_dup_lo(ks[1]) : f16_dup_hi(ks[1]);
+        const uint32_t fa[4] = {hmul2_bits(a[0], s0), hmul2_bits(b[0], s1), hmul2_bits(a[1], s0), hmul2_bits(b[1], s1)};
+        const uint32_t fb[4] = {hmul2_bits(a[2], s0), hmul2_bits(b[2], s1), hmul2_bits(a[3], s0), hmul2_bits(b[3], s1)};
+        mma_f16_16816(sc, fa, qb[2 * w][0], qb[2 * w][1]);
+        mma_f16_16816(sd, fb, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = sc[i] + sd[i];
+    if (n0 > 0 || n1 < kUnit) {
+        const bool s0 = ln.tk >= n0 && ln.tk < n1, s1 = ln.tk + 8 >= n0 && ln.tk + 8 < n1;
+        x[0] = s0 ? x[0] : -INFINITY;
+        x[1] = s0 ? x[1] : -INFINITY;
+        x[2] = s1 ? x[2] : -INFINITY;
+        x[3] = s1 ? x[3] : -INFINITY;
+    }
+}
+
+// oacc += V^T P^T of a unit, P the weights of fp4_scores' places.
+template <int D, int HPC>
+__device__ __forceinline__ void fp4_values(const Fp4Lane<D, HPC> &ln, const uint8_t *st, const float *p, int n0, int n1,
+                                           float (&oacc)[D / 16][4]) {
+    using S = Fp4Smem<D, HPC>;
+    constexpr int VW = D / 64;                       // words of a lane's part of a row
+    uint32_t vw[4][VW], vs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t *q = st + 8 * (i >> 1) * S::kRow;
+        const int off = (i & 1) ? ln.v_off1 : ln.v_off0;
+        if constexpr (VW == 2) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(q + off);
+            vw[i][0] = w.x; vw[i][1] = w.y;
+        } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t *>(q + off);
+        }
+        vs[i] = q[(i & 1) ? ln.vs_off1 : ln.vs_off0];
+    }
+    if (n0 > 0 || n1 < kUnit) {                      // keys that are not seen may hold anything: a zero scale clears them
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = ((i & 1) ? ln.t1 : ln.t0) + 8 * (i >> 1);
+            if (t < n0 || t >= n1) vs[i] = 0u;
+        }
+    }
+    const uint32_t pb0 = movmatrix_trans(f16x2_of(p[0], p[1]));
+    const uint32_t pb1 = movmatrix_trans(f16x2_of(p[2], p[3]));
+    const uint32_t sa = e4m3x2_to_f16x2(vs[0] | (vs[1] << 8)), sb = e4m3x2_to_f16x2(vs[2] | (vs[3] << 8));
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+        constexpr uint32_t m = 0x0f0f0f0fu;
+        // even elements of both keys in one word, odd ones in another
+        uint32_t ea[4], oa[4], eb[4], ob[4];
+        e2m1x8_to_f16x8((vw[0][w] & m) | ((vw[1][w] << 4) & ~m), ea);
+        e2m1x8_to_f16x8(((vw[0][w] >> 4) & m) | (vw[1][w] & ~m), oa);
+        e2m1x8_to_f16x8((vw[2][w] & m) | ((vw[3][w] << 4) & ~m), eb);
+        e2m1x8_to_f16x8(((vw[2][w] >> 4) & m) | (vw[3][w] & ~m), ob);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {hmul2_bits(ea[i], sa), hmul2_bits(oa[i], sa), hmul2_bits(eb[i], sb), hmul2_bits(ob[i], sb)};
+            mma_f16_16816(oacc[4 * w + i], f, pb0, pb1);
+        }
+    }
+}
+
 // Consumer warp hw: KV head hg * HPC + hw of each segment of the same range.
+// Units are taken in pairs: one vote and one maximum for 32 keys, and two
+// independent score chains in flight.
 template <int D, int HPC>
 __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64_t T, int64_t g0, int64_t g1,
                             const uint8_t *ring, uint64_t *full, uint64_t *empty, int hw, int lane) {
     using S = Fp4Smem<D, HPC>;
     constexpr int KS = D / 16;                       // k-steps of the score = tiles of O
-    constexpr int KW = D / 32;                       // words of a lane's part of a K row
-    constexpr int VW = D / 64;                       // words of a lane's part of a V row
     const int r8 = lane >> 2, q4 = lane & 3;
     const int G = a.group;
-    auto place = [](int r) { return r ^ ((r >> 1) & 1); };       // row of the fragment -> key of the unit
-    const int tk = place(r8);                        // keys tk and tk + 8
-    const int t0 = place(2 * q4), t1 = place(2 * q4 + 1);        // keys t0, t1, t0 + 8, t1 + 8
-    const int k_off = tk * S::kRow + hw * (D / 2) + q4 * (D / 8);
-    const int ks_off = tk * S::kRow + S::kCodes + hw * (D / 16) + q4 * (D / 64);
-    const int v_in = kUnit * S::kRow + hw * (D / 2) + r8 * (D / 16);
-    const int vs_in = kUnit * S::kRow + S::kCodes + hw * (D / 16) + (D == 128 ? r8 : r8 >> 1);
-    int ctr = 0;
+    const Fp4Lane<D, HPC> ln(hw, lane);
+    int slot = 0;
+    uint32_t phase = 0;
     SegmentWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
     int b, hg, u0, u1, split, span;
     while (walk.next(b, hg, u0, u1, split, span)) {
@@ -211,7 +328,8 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64
         int lo;
         const int L = seq_keys(a, b, lo);
         const int first = lo / kUnit;
-        const float sl2 = a.scale_log2 * __ldg(a.k_scale + kvh);
+        const float sl2 = a.scale_log2 * __ldg(a.k_scale + kvh);     // raw score -> log2 units
+        const float lazy = kLazyRescale / sl2;
         uint32_t qb[KS][2];
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) qb[kk][0] = qb[kk][1] = 0u;
@@ -220,123 +338,71 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 const uint2 w = __ldg(qrow + kk);
-                qb[kk][0] = f16x2_bits(bf16lo(w.x), bf16hi(w.x));
-                qb[kk][1] = f16x2_bits(bf16lo(w.y), bf16hi(w.y));
+                qb[kk][0] = f16x2_of(bf16lo(w.x), bf16hi(w.x));
+                qb[kk][1] = f16x2_of(bf16lo(w.y), bf16hi(w.y));
             }
         }
         float oacc[KS][4];
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) oacc[mt][0] = oacc[mt][1] = oacc[mt][2] = oacc[mt][3] = 0.f;
-        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-        for (int u = u0; u < u1; ++u, ++ctr) {
-            const int slot = ctr % S::kStages, round = ctr / S::kStages;
-            if (!mbar_wait(&full[slot], round & 1)) return;
-            __syncwarp();
-            const uint8_t *st = ring + slot * S::kStage;
+        // the running maximum in log2 units, the raw score beyond which it moves
+        float m_run[2] = {-INFINITY, -INFINITY}, limit[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        for (int u = u0; u < u1; u += 2) {
+            const bool two = u + 1 < u1;
             const int key = (first + u) * kUnit;
-            const int n0 = lo - key, n1 = L - key;   // keys n0 .. n1 - 1 of the unit are seen
-            const bool part = n0 > 0 || n1 < kUnit;
-            // V's words and scales, so that they arrive while the scores are made
-            uint32_t vw[4][VW], vs[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = ((i & 1) ? t1 : t0) + 8 * (i >> 1);
-                const uint8_t *p = st + t * S::kRow;
-                if constexpr (VW == 2) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(p + v_in);
-                    vw[i][0] = w.x; vw[i][1] = w.y;
-                } else {
-                    vw[i][0] = *reinterpret_cast<const uint32_t *>(p + v_in);
-                }
-                vs[i] = p[vs_in];
-                // keys that are not seen may hold anything: a zero scale makes them 0
-                if (part && (t < n0 || t >= n1)) vs[i] = 0u;
-            }
-            // ---- scores
-            float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t kw[2][KW], ks[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t *p = st + 8 * i * S::kRow;
-                if constexpr (KW == 4) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(p + k_off);
-                    kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
-                    ks[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(p + ks_off));
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(p + k_off);
-                    kw[i][0] = w.x; kw[i][1] = w.y;
-                    ks[i] = e4m3x2_to_f16x2(p[ks_off]);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < KW; ++w) {           // a word is two k-steps
-                uint32_t x[4], y[4];
-                e2m1x8_to_f16x8(kw[0][w], x);
-                e2m1x8_to_f16x8(kw[1][w], y);
-                const uint32_t s0 = w < 2 ? f16_dup_lo(ks[0]) : f16_dup_hi(ks[0]);
-                const uint32_t s1 = w < 2 ? f16_dup_lo(ks[1]) : f16_dup_hi(ks[1]);
-                uint32_t fa[4] = {hmul2_bits(x[0], s0), hmul2_bits(y[0], s1), hmul2_bits(x[1], s0), hmul2_bits(y[1], s1)};
-                uint32_t fb[4] = {hmul2_bits(x[2], s0), hmul2_bits(y[2], s1), hmul2_bits(x[3], s0), hmul2_bits(y[3], s1)};
-                mma_f16_16816(sc, fa, qb[2 * w][0], qb[2 * w][1]);
-                mma_f16_16816(sd, fb, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+            const int na = lo - key, nb = L - key;   // keys na .. nb - 1 from the first unit's start are seen
+            const uint8_t *sta = ring + slot * S::kStage;
+            uint64_t *ea = &empty[slot], *eb = nullptr;
+            if (!mbar_wait(&full[slot], phase)) return;
+            __syncwarp();
+            if (++slot == S::kStages) { slot = 0; phase ^= 1u; }
+            float x[8];
+            fp4_scores<D, HPC>(ln, sta, qb, na, nb, x);
+            const uint8_t *stb = ring + slot * S::kStage;
+            if (two) {
+                eb = &empty[slot];
+                if (!mbar_wait(&full[slot], phase)) return;
+                __syncwarp();
+                if (++slot == S::kStages) { slot = 0; phase ^= 1u; }
+                fp4_scores<D, HPC>(ln, stb, qb, na - kUnit, nb - kUnit, x + 4);
+            } else {
+                x[4] = x[5] = x[6] = x[7] = -INFINITY;
             }
             // ---- online softmax in the log2 domain
-            float x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = (sc[i] + sd[i]) * sl2;
-            if (part) {
-                const bool s0 = tk >= n0 && tk < n1, s1 = tk + 8 >= n0 && tk + 8 < n1;
-                x[0] = s0 ? x[0] : -INFINITY;
-                x[1] = s0 ? x[1] : -INFINITY;
-                x[2] = s1 ? x[2] : -INFINITY;
-                x[3] = s1 ? x[3] : -INFINITY;
-            }
-            const bool more = fmaxf(x[0], x[2]) > m_run[0] + kLazyRescale || fmaxf(x[1], x[3]) > m_run[1] + kLazyRescale;
-            if (__any_sync(0xffffffffu, more)) {
+            float top[2] = {fmaxf(fmaxf(x[0], x[2]), fmaxf(x[4], x[6])), fmaxf(fmaxf(x[1], x[3]), fmaxf(x[5], x[7]))};
+            if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float mx = fmaxf(x[j], x[2 + j]);
+                    float mx = top[j];
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    if (mx > m_run[j] + kLazyRescale) {
-                        const float alpha = fast_exp2(m_run[j] - mx);    // 0 when m_run = -inf
+                    if (mx > limit[j]) {
+                        const float alpha = fast_exp2(m_run[j] - mx * sl2);      // 0 when m_run = -inf
                         l_run[j] *= alpha;
 #pragma unroll
                         for (int mt = 0; mt < KS; ++mt) {
                             oacc[mt][j] *= alpha;
                             oacc[mt][2 + j] *= alpha;
                         }
-                        m_run[j] = mx;
+                        m_run[j] = mx * sl2;
+                        limit[j] = mx + lazy;
                     }
                 }
             }
-            float p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[i] - m_run[i & 1]);
-            l_run[0] += p[0] + p[2];
-            l_run[1] += p[1] + p[3];
-            const uint32_t pb0 = movmatrix_trans(f16x2_bits(p[0], p[1]));
-            const uint32_t pb1 = movmatrix_trans(f16x2_bits(p[2], p[3]));
+            for (int i = 0; i < 8; ++i) x[i] = fast_exp2(fmaf(x[i], sl2, -m_run[i & 1]));
+            l_run[0] += (x[0] + x[2]) + (x[4] + x[6]);
+            l_run[1] += (x[1] + x[3]) + (x[5] + x[7]);
             // ---- O^T += V^T P^T
-            const uint32_t sa = e4m3x2_to_f16x2(vs[0] | (vs[1] << 8)), sb = e4m3x2_to_f16x2(vs[2] | (vs[3] << 8));
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                constexpr uint32_t m = 0x0f0f0f0fu;
-                // even elements of both keys in one word, odd ones in another
-                uint32_t ea[4], oa[4], eb[4], ob[4];
-                e2m1x8_to_f16x8((vw[0][w] & m) | ((vw[1][w] << 4) & ~m), ea);
-                e2m1x8_to_f16x8(((vw[0][w] >> 4) & m) | (vw[1][w] & ~m), oa);
-                e2m1x8_to_f16x8((vw[2][w] & m) | ((vw[3][w] << 4) & ~m), eb);
-                e2m1x8_to_f16x8(((vw[2][w] >> 4) & m) | (vw[3][w] & ~m), ob);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t f[4] = {hmul2_bits(ea[i], sa), hmul2_bits(oa[i], sa), hmul2_bits(eb[i], sb), hmul2_bits(ob[i], sb)};
-                    mma_f16_16816(oacc[4 * w + i], f, pb0, pb1);
-                }
-            }
+            fp4_values<D, HPC>(ln, sta, x, na, nb, oacc);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (lane == 0) mbar_arrive(ea);
+            if (two) {
+                fp4_values<D, HPC>(ln, stb, x + 4, na - kUnit, nb - kUnit, oacc);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(eb);
+            }
         }
         // ---- the segment's partial: lane r8 holds elements D/8 r8 .. of its two heads
 #pragma unroll
@@ -351,7 +417,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64
                 raise_error(PA_DEVERR_SEQLENS);
                 continue;
             }
-            const float inv = (l > 0.f ? 1.f / l : 0.f) * __ldg(a.v_scale + kvh);
+            const float inv = (l == 0.f ? 0.f : 1.f / l) * __ldg(a.v_scale + kvh);       // a NaN stays one
             const int64_t r = ((int64_t)b * a.num_q_heads + h0 + hh) * a.max_splits + split;
             float *orow = a.o_part + r * D + r8 * (D / 8);
 #pragma unroll
@@ -359,7 +425,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64
                 *reinterpret_cast<float4 *>(orow + 2 * mt) =
                     make_float4(oacc[mt][j] * inv, oacc[mt][2 + j] * inv, oacc[mt + 1][j] * inv, oacc[mt + 1][2 + j] * inv);
             if (r8 == 0) {
-                a.lse_part[r] = l > 0.f ? (m_run[j] + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                a.lse_part[r] = l == 0.f ? -INFINITY : (m_run[j] + __log2f(l)) * 0.69314718055994531f;
                 for (int e = 1; e < span; ++e) a.lse_part[r + e] = -INFINITY;
             }
         }
@@ -393,6 +459,100 @@ __global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas) decode
     const int64_t g0 = (int64_t)blockIdx.x * T, g1 = min(g0 + T, total);
     if (warp == HPC) fp4_produce<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, lane);
     else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
+}
+
+// The log-sum-exp combine (decode.cu's, with its split count): W warps share a
+// row's slots.  One warp per row reads 140 slots (a single long sequence) in
+// 20 us, eight warps in 3; batches have rows enough and few slots each.
+// A NaN among the partials stays one.
+constexpr int kCombineThreads = 256;
+
+template <int D, int W>
+__global__ void __launch_bounds__(kCombineThreads) fp4_combine_kernel(
+    const float *__restrict__ o_part, const float *__restrict__ lse_part, const int32_t *__restrict__ header,
+    const int32_t *__restrict__ prefix, int32_t head_groups, int32_t heads_per_group, int32_t heads_per_seq,
+    int32_t num_rows, int32_t max_splits, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse_out) {
+    constexpr int kLanes = D / 4;                    // lanes of a slot, four elements each
+    constexpr int kSlots = 32 * W / kLanes;          // slots in flight
+    __shared__ float top[kCombineThreads / 32], dens[kCombineThreads / kLanes];
+    __shared__ float4 part[kCombineThreads];
+    const int t = threadIdx.x % (32 * W), lane = t & 31;
+    const int row = blockIdx.x * (kCombineThreads / (32 * W)) + threadIdx.x / (32 * W);
+    asm volatile("griddepcontrol.wait;" ::: "memory");           // the partials are complete
+    int n = 0;
+    if (row < num_rows) {
+        const int64_t T = header[0];
+        const int b = row / heads_per_seq, hg = (row % heads_per_seq) / heads_per_group;
+        const int U = prefix[b + 1] - prefix[b];
+        const int64_t rs = (int64_t)head_groups * prefix[b] + (int64_t)hg * U;
+        n = U > 0 ? min((int)((rs + U - 1) / T - rs / T + 1), max_splits) : 0;
+    }
+    const float *lrow = lse_part + (int64_t)row * max_splits;
+    float M = -INFINITY;
+    for (int s = t; s < n; s += 32 * W) M = fmaxf(M, lrow[s]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (W > 1) {
+        if (lane == 0) top[threadIdx.x >> 5] = M;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, top[(threadIdx.x >> 5) / W * W + w]);
+    }
+    const float *obase = o_part + (int64_t)row * max_splits * D + (t % kLanes) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+#pragma unroll 4
+    for (int s = t / kLanes; s < n; s += kSlots) {
+        const float l = lrow[s];
+        if (l == -INFINITY) continue;                // an empty slot may hold anything
+        const float w = __expf(l - M);
+        const float4 x = *reinterpret_cast<const float4 *>(obase + (int64_t)s * D);
+        den += w;
+        acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w;
+    }
+    if (kSlots > 1) {                                // the lane groups' sums
+        part[threadIdx.x] = acc;
+        if (t % kLanes == 0) dens[threadIdx.x / kLanes] = den;
+        if (W > 1) __syncthreads(); else __syncwarp();
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        den = 0.f;
+        const int base = threadIdx.x - t;
+#pragma unroll
+        for (int g = 0; g < kSlots; ++g) {
+            const float4 x = part[base + g * kLanes + t % kLanes];
+            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+            den += dens[base / kLanes + g];
+        }
+    }
+    if (row >= num_rows || t >= kLanes) return;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    *reinterpret_cast<uint2 *>(out + (int64_t)row * D + t * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lse_out != nullptr && t == 0) lse_out[row] = den == 0.f ? -INFINITY : M + __logf(den);
+}
+
+cudaError_t launch_fp4_combine(const Fp4DecodeArgs &a, const pa_decode_params &p, int heads_per_group,
+                               const DecodePlan &plan, cudaStream_t stream) {
+    const int rows = p.num_seqs * p.num_q_heads;
+    // A CTA per row while all of them fit on the GPU at once and a row may have
+    // more than a few slots.
+    const bool share = plan.max_splits >= 8 && rows <= num_sms() * 8;
+    const int per_block = share ? 1 : kCombineThreads / 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + per_block - 1) / per_block));
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    constexpr int W = kCombineThreads / 32;
+    auto kern = p.head_dim == 64 ? (share ? fp4_combine_kernel<64, W> : fp4_combine_kernel<64, 1>)
+                                 : (share ? fp4_combine_kernel<128, W> : fp4_combine_kernel<128, 1>);
+    return cudaLaunchKernelEx(&cfg, kern, (const float *)a.o_part, (const float *)a.lse_part, (const int32_t *)a.ws_header,
+                              (const int32_t *)a.ws_prefix, a.head_groups, (int32_t)heads_per_group, p.num_q_heads,
+                              (int32_t)rows, plan.max_splits, static_cast<__nv_bfloat16 *>(p.out), p.lse);
 }
 
 template <int D, int HPC>
@@ -492,9 +652,7 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
         if (lay.gs == 8) e = launch_fp4_t<128, 8>(a, p, useful, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_lse_combine(a.o_part, a.lse_part, nullptr, a.ws_header, a.ws_prefix, a.head_groups,
-                              a.group * lay.gs, p.num_q_heads, p.num_seqs * p.num_q_heads, plan.max_splits,
-                              p.head_dim, p.out, p.lse, stream);
+    return launch_fp4_combine(a, p, a.group * lay.gs, plan, stream);
 }
 
 }  // namespace pa

@@ -187,6 +187,22 @@ def test_nan_scale_stays_in_its_head(cuda_device):
     check(out, lse, ref, "beside a NaN block")
 
 
+@pytest.mark.parametrize("B", [1, 40])
+def test_nan_key_reaches_the_output(cuda_device, B):
+    """A key whose scale is NaN makes the rows that see it NaN, through both
+    forms of the combine."""
+    L = np.full(B, 600, np.int32)
+    p = W.small_problem(45, L - 1, np.ones_like(L), num_q_heads=32, num_kv_heads=8, head_dim=128)
+    f = FP4Problem(p, cuda_device, 46)
+    slot = int(p.token_table[B - 1, 333])
+    f.k_cache.view(-1, f.k_cache.shape[-1])[slot, 512 + 5 * 8] = 255          # head 5, block 0
+    out, lse = f.decode()
+    want = torch.zeros((B, 32), dtype=torch.bool, device=cuda_device)
+    want[B - 1, 20:24] = True
+    assert torch.equal(torch.isnan(out).all(-1), want) and torch.equal(torch.isnan(out).any(-1), want)
+    assert torch.equal(torch.isnan(lse), want)
+
+
 def test_captured_with_new_lengths(cuda_device):
     """One captured call serves other lengths and other rows; two graphs with
     their own workspaces run side by side."""
