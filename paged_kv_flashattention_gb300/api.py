@@ -6,7 +6,9 @@ non-zero status.  No arithmetic of the attention path happens here.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import functools
 import math
 import threading
 
@@ -32,9 +34,28 @@ def _check(status: int, lib=None):
         raise PagedAttentionError(status, f"{name}: {msg}")
 
 
+# The raw handle of the current stream of a device index; without it (another
+# torch) through the Stream object, 2 us instead of 0.1.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor | None = None) -> int:
+    if t is not None and t.is_cuda and _raw_stream is not None:
+        return _raw_stream(t.get_device())
     dev = t.device if t is not None else None
     return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _call(fn, t: torch.Tensor, *args):
+    """fn(*args, current stream) of libpa with t's device current."""
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    stream = _stream(t)
+    if t.get_device() == torch.cuda.current_device():
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, stream))
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -44,7 +65,7 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 def _need(t: torch.Tensor, name: str, dtype, device=None, contiguous=True):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
@@ -168,26 +189,34 @@ def store_kv_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                                num_slots, Hkv, d, _ptr(k_scale), _ptr(v_scale), _stream(k_cache)), lib)
 
 
-def fp4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
-    """Bytes of one token's row in a 4-bit pool of K (or of V): a pool is a
-    uint8 tensor [num_pages, page_size, fp4_row_bytes(Hkv, d)]."""
+@functools.lru_cache(maxsize=None)
+def _fp4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
     lib = _lib.load()
-    n = int(lib.pa_fp4_row_bytes(int(num_kv_heads), int(head_dim)))
+    n = int(lib.pa_fp4_row_bytes(num_kv_heads, head_dim))
     if n == 0:
         raise ValueError(lib.pa_last_error().decode(errors="replace"))
     return n
 
 
-def _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int, dev):
-    """Checks a pair of 4-bit pools for Hkv heads of size d."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, torch.uint8, dev)
+def fp4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one token's row in a 4-bit pool of K (or of V): a pool is a
+    uint8 tensor [num_pages, page_size, fp4_row_bytes(Hkv, d)]."""
+    return _fp4_row_bytes(int(num_kv_heads), int(head_dim))
+
+
+def _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int, dev) -> int:
+    """Checks a pair of 4-bit pools for Hkv heads of size d; returns their
+    slots."""
+    _need(k_cache, "k_cache", torch.uint8, dev)
+    _need(v_cache, "v_cache", torch.uint8, dev)
     _need_scales(k_scale, v_scale, Hkv, dev)
-    if v_cache.shape != k_cache.shape:
+    shape, row = k_cache.shape, _fp4_row_bytes(Hkv, d)
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    if k_cache.dim() not in (2, 3) or k_cache.shape[-1] != fp4_row_bytes(Hkv, d):
-        raise ValueError(f"a 4-bit pool of {Hkv} heads of size {d} is [num_pages, page_size, {fp4_row_bytes(Hkv, d)}] "
-                         f"bytes, got {tuple(k_cache.shape)}")
+    if len(shape) not in (2, 3) or shape[-1] != row:
+        raise ValueError(f"a 4-bit pool of {Hkv} heads of size {d} is [num_pages, page_size, {row}] bytes, got "
+                         f"{tuple(shape)}")
+    return k_cache.numel() // row
 
 
 def store_kv_fp4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
@@ -200,18 +229,16 @@ def store_kv_fp4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     [Hkv], best the head's largest magnitude / 2688.  A negative slot is
     skipped."""
     dev = k_cache.device
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n, torch.bfloat16, dev)
+    _need(k, "k", torch.bfloat16, dev)
+    _need(v, "v", torch.bfloat16, dev)
     _need(slot_mapping, "slot_mapping", torch.int32, dev)
-    if k.dim() != 3 or v.shape != k.shape or slot_mapping.numel() != k.shape[0]:
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or slot_mapping.numel() != shape[0]:
         raise ValueError("k and v must be [T, Hkv, d] with one slot per token")
-    T, Hkv, d = k.shape
-    _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        _check(lib.pa_store_kv_fp4(_ptr(k), _ptr(v), _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache),
-                                   k_cache.numel() // k_cache.shape[-1], Hkv, d, _ptr(k_scale), _ptr(v_scale),
-                                   _stream(k_cache)), lib)
+    T, Hkv, d = shape
+    slots = _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    _call(_lib.load().pa_store_kv_fp4, k_cache, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T,
+          k_cache.data_ptr(), v_cache.data_ptr(), slots, Hkv, d, k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def load_kv_fp4(slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -225,20 +252,20 @@ def load_kv_fp4(slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if k_scale is None:
         raise ValueError("k_scale is required for FP8 and 4-bit pools")
     T, Hkv, d = slots.numel(), k_scale.numel(), int(head_dim)
-    _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    num_slots = _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    shape = (T, Hkv, d)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(k_out, "k_out", torch.bfloat16, dev)
     if v_out is None:
-        v_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _need(t, n, torch.bfloat16, dev)
-        if tuple(t.shape) != (T, Hkv, d):
-            raise ValueError(f"{n} must be [{T}, {Hkv}, {d}]")
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        _check(lib.pa_load_kv_fp4(_ptr(slots), T, _ptr(k_cache), _ptr(v_cache), k_cache.numel() // k_cache.shape[-1],
-                                  Hkv, d, _ptr(k_scale), _ptr(v_scale), _ptr(k_out), _ptr(v_out),
-                                  _stream(k_cache)), lib)
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(v_out, "v_out", torch.bfloat16, dev)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"k_out and v_out must be [{T}, {Hkv}, {d}]")
+    _call(_lib.load().pa_load_kv_fp4, k_cache, slots.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(), num_slots,
+          Hkv, d, k_scale.data_ptr(), v_scale.data_ptr(), k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 
@@ -269,8 +296,6 @@ def rope_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     _need(slot_mapping, "slot_mapping", torch.int32, dev)
     _need(cos_sin, "cos_sin", torch.float32, dev)
     kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, k_cache.dtype, dev)
     T, Hq, d = q.shape
     if kvd == PA_KV_FP4:
         if k.dim() != 3:
@@ -278,6 +303,8 @@ def rope_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
         Hkv = k.shape[1]
         _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
     else:
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, n, k_cache.dtype, dev)
         Hkv = k_cache.shape[-2]
     if (kvd != PA_KV_FP4 and k_cache.shape[-1] != d) or k.numel() != T * Hkv * d or v.numel() != T * Hkv * d:
         raise ValueError("k/v/pool shapes do not match q")
@@ -296,9 +323,7 @@ def rope_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
         num_slots=k_cache.numel() // (k_cache.shape[-1] if kvd == PA_KV_FP4 else Hkv * d), kv_dtype=kvd,
         k_scale=_ptr(k_scale) if kvd != PA_KV_BF16 else None,
         v_scale=_ptr(v_scale) if kvd != PA_KV_BF16 else None)
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        _check(lib.pa_rope_store_kv(ctypes.byref(p), _stream(q)), lib)
+    _call(_lib.load().pa_rope_store_kv, q, ctypes.byref(p))
     return q_out
 
 
@@ -359,38 +384,57 @@ def build_batch(cached_len: torch.Tensor, extend_len: torch.Tensor, token_table:
     tokens' pages from it and enter their slots in ``token_table``."""
     dev = token_table.device
     B = cached_len.numel()
-    for t, n in ((cached_len, "cached_len"), (extend_len, "extend_len"), (table_idx, "table_idx"),
-                 (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k"), (cache_seqlens, "cache_seqlens"),
+    for t, n in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k"), (cache_seqlens, "cache_seqlens"),
                  (positions, "positions"), (slot_mapping, "slot_mapping"), (totals, "totals")):
         _need(t, n, torch.int32, dev)
-    for t, n in ((token_table, "token_table"), (page_table, "page_table")):
-        _need(t, n, torch.int32, dev, contiguous=False)
-        if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{n} must be 2-D with unit column stride and rows that do not overlap")
-    if free_pages is not None:
-        _need(free_pages, "free_pages", torch.int32, dev)
+    _need_rows(page_table, "page_table", dev)
     max_k, P = int(max_seqlen_k), int(page_size)
     if P <= 0:
         raise ValueError("page_size must be positive")
-    if extend_len.numel() != B or table_idx.numel() != B:
-        raise ValueError("cached_len, extend_len and table_idx must hold one entry per request")
     if cu_seqlens_q.numel() < B + 1 or cu_seqlens_k.numel() < B + 1 or cache_seqlens.numel() < B or totals.numel() < 4:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must hold B + 1 entries, cache_seqlens B, totals 4")
     if positions.numel() != slot_mapping.numel():
         raise ValueError("positions and slot_mapping must have the same size")
-    if token_table.shape[1] < max_k or page_table.shape[0] < B or page_table.shape[1] < -(-max_k // P):
-        raise ValueError(f"token_table must be at least {max_k} wide, page_table at least [{B}, {-(-max_k // P)}]")
+    if page_table.shape[0] < B or page_table.shape[1] < -(-max_k // P):
+        raise ValueError(f"page_table must be at least [{B}, {-(-max_k // P)}]")
+    out = _BatchOut(cu_seqlens_q, cu_seqlens_k, cache_seqlens, positions, slot_mapping, page_table, totals)
+    _build_batch(cached_len, extend_len, token_table, table_idx, P, max_k, out, free_pages)
+
+
+_BatchOut = collections.namedtuple("_BatchOut", "cu_seqlens_q cu_seqlens_k cache_seqlens positions slot_mapping "
+                                                "page_table totals")
+
+
+def _need_rows(t, name, dev):
+    _need(t, name, torch.int32, dev, contiguous=False)
+    if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
+
+
+def _build_batch(cached_len, extend_len, token_table, table_idx, page_size, max_seqlen_k, out, free_pages):
+    """build_batch into checked outputs (the attributes of ``out``)."""
+    dev = out.totals.device
+    _need(cached_len, "cached_len", torch.int32, dev)
+    _need(extend_len, "extend_len", torch.int32, dev)
+    _need(table_idx, "table_idx", torch.int32, dev)
+    _need_rows(token_table, "token_table", dev)
+    if free_pages is not None:
+        _need(free_pages, "free_pages", torch.int32, dev)
+    B, width = cached_len.numel(), token_table.shape[1]
+    if extend_len.numel() != B or table_idx.numel() != B:
+        raise ValueError("cached_len, extend_len and table_idx must hold one entry per request")
+    if width < max_seqlen_k:
+        raise ValueError(f"token_table must be at least {max_seqlen_k} wide")
+    pt = out.page_table
+    # an empty list is a list all the same: NULL would mean none
+    free_ptr = None if free_pages is None else free_pages.data_ptr() or out.totals.data_ptr()
     p = _lib.BatchParams(
-        cached_len=_ptr(cached_len), extend_len=_ptr(extend_len), num_seqs=B, max_seqlen_k=max_k, page_size=P,
-        token_table=_ptr(token_table), token_table_stride=max(token_table.stride(0), token_table.shape[1]),
-        token_table_rows=token_table.shape[0], table_idx=_ptr(table_idx), free_pages=_ptr(free_pages),
-        num_free_pages=free_pages.numel() if free_pages is not None else 0, num_tokens=positions.numel(),
-        cu_seqlens_q=_ptr(cu_seqlens_q), cu_seqlens_k=_ptr(cu_seqlens_k), cache_seqlens=_ptr(cache_seqlens),
-        positions=_ptr(positions), slot_mapping=_ptr(slot_mapping), page_table=_ptr(page_table),
-        page_table_stride=max(page_table.stride(0), page_table.shape[1]), totals=_ptr(totals))
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        _check(lib.pa_build_batch(ctypes.byref(p), _stream(token_table)), lib)
+        cached_len.data_ptr(), extend_len.data_ptr(), B, max_seqlen_k, page_size, token_table.data_ptr(),
+        max(token_table.stride(0), width), token_table.shape[0], table_idx.data_ptr(), free_ptr,
+        0 if free_pages is None else free_pages.numel(), out.positions.numel(), out.cu_seqlens_q.data_ptr(),
+        out.cu_seqlens_k.data_ptr(), out.cache_seqlens.data_ptr(), out.positions.data_ptr(), out.slot_mapping.data_ptr(),
+        pt.data_ptr(), max(pt.stride(0), pt.shape[1]), out.totals.data_ptr())
+    _call(_lib.load().pa_build_batch, out.totals, ctypes.byref(p))
 
 
 def _pool_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, page_size: int | None):
@@ -411,20 +455,21 @@ def _pool_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, page_size: int 
     return int(num_pages), int(P), int(Hkv), int(d)
 
 
-def _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, d: int):
+def _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, d: int, dev):
     """_pool_geometry of 4-bit pools [pages, page_size, row bytes] or [slots,
     row bytes]; the heads are counted by the scales."""
     if k_scale is None:
         raise ValueError("k_scale is required for FP8 and 4-bit pools")
     Hkv = k_scale.numel()
-    _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, k_cache.device)
-    if k_cache.dim() == 3:
-        if page_size is not None and page_size != k_cache.shape[1]:
+    slots = _fp4_pools(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    shape = k_cache.shape
+    if len(shape) == 3:
+        if page_size is not None and page_size != shape[1]:
             raise ValueError("page_size does not match the pool shape")
-        return int(k_cache.shape[0]), int(k_cache.shape[1]), Hkv, d
+        return shape[0], shape[1], Hkv, d
     if page_size is None:
         raise ValueError("page_size is required for a [slots, row bytes] pool")
-    return k_cache.shape[0] // int(page_size), int(page_size), Hkv, d
+    return slots // int(page_size), int(page_size), Hkv, d
 
 
 # Zeroed scheduler arrays of pa_prefill, one per (device, stream): launches on
@@ -485,8 +530,7 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_
     p, out = _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                              max_seqlen_k, causal, scale, page_size, out, lse, k_scale, v_scale, sliding_window,
                              max_ctas, scheduler, block_mask, PA_PREFILL_SCHEDULER_INTS, kv_dtype)
-    lib = _lib.load()
-    _check(lib.pa_prefill(ctypes.byref(p), _stream(q)), lib)
+    _call(_lib.load().pa_prefill, q, ctypes.byref(p))
     return out
 
 
@@ -497,11 +541,13 @@ def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k,
     _need(q, "q", torch.bfloat16, dev)
     kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
     if kvd == PA_KV_FP4:
-        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, q.shape[-1])
+        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, q.shape[-1],
+                                                  q.device)
     else:
         num_pages, P, Hkv, d = _pool_geometry(k_cache, v_cache, page_size)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, k_cache.dtype, dev)
+    if kvd != PA_KV_FP4:                              # (4-bit pools: _fp4_geometry)
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, n, k_cache.dtype, dev)
     if kvd == PA_KV_FP8_E4M3:
         _need_scales(k_scale, v_scale, Hkv, dev)
     for t, n in ((page_table, "page_table"), (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k")):
@@ -548,7 +594,8 @@ def _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k,
                    max_ctas=0, overlap_previous=False, kv_dtype=None):
     kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
     if kvd == PA_KV_FP4:
-        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, q.shape[-1])
+        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, q.shape[-1],
+                                                  q.device)
     else:
         num_pages, P, Hkv, d = _pool_geometry(k_cache, v_cache, page_size)
     B, Hq, dq = q.shape
@@ -619,15 +666,17 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_t
     dev = q.device
     _need(q, "q", torch.bfloat16, dev)
     kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, k_cache.dtype, dev)
+    if kvd != PA_KV_FP4:                              # (4-bit pools: _fp4_geometry)
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, n, k_cache.dtype, dev)
     _need(cache_seqlens, "cache_seqlens", torch.int32, dev)
     _need(page_table, "page_table", torch.int32, dev, contiguous=False)
     if page_table.dim() != 2 or page_table.stride(1) != 1:
         raise ValueError("page_table must be 2-D with unit column stride")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, dev)
+    else:
+        _need(out, "out", torch.bfloat16, dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if workspace is None:
@@ -638,8 +687,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_t
     p = _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k, scale, page_size,
                        out, lse, workspace, kv_chunk, k_scale, v_scale, sliding_window, max_ctas,
                        overlap_previous, kvd)
-    lib = _lib.load()
-    _check(lib.pa_decode(ctypes.byref(p), _stream(q)), lib)
+    _call(_lib.load().pa_decode, q, ctypes.byref(p))
     return out
 
 
@@ -713,8 +761,7 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         _need(lse, "lse", torch.float32, dev)
     p = _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k, scale, page_size,
                        out, lse, None, kv_chunk, k_scale, v_scale, sliding_window, kv_dtype=kvd)
-    lib = _lib.load()
-    _check(lib.pa_decode_noalloc(ctypes.byref(p), _stream(q)), lib)
+    _call(_lib.load().pa_decode_noalloc, q, ctypes.byref(p))
     return out
 
 

@@ -184,8 +184,10 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_pa
 
 cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream) {
     const size_t smem = 3 * ((size_t)p.num_seqs + 1) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(build_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 40 * 1024) {                          // more than a CTA has without asking (with the static part)
+        cudaError_t e = cudaFuncSetAttribute(build_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        if (e != cudaSuccess) return e;
+    }
     const int64_t cols = ((int64_t)p.max_seqlen_k + p.page_size - 1) / p.page_size;
     int64_t blocks = (p.num_tokens + cols * p.num_seqs + kThreads - 1) / kThreads;
     const int64_t cap = (int64_t)num_sms() * 4;

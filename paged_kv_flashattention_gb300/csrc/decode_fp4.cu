@@ -31,6 +31,8 @@
 // score exceeds it by more than 2^8, so that the usual unit needs no shuffle.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "decode_impl.cuh"
 #include "fp4.cuh"
 #include "pa_device.cuh"
@@ -125,15 +127,41 @@ __device__ __forceinline__ void fp4_prefix(const Fp4DecodeArgs &a, int32_t *pref
     __syncthreads();
 }
 
+// SegmentWalk (decode_impl.cuh) over the list of units, in 32 bits: the call
+// has fewer than 2^31 keys over all head groups, so fewer units.
+struct UnitWalk {
+    const int32_t *pb;
+    int B, HG, T, g, g1;
+    __device__ __forceinline__ bool next(int &b, int &hg, int &u0, int &u1, int &split, int &span) {
+        if (g >= g1) return false;
+        int lo = 0, hi = B;           // HG * pb[lo] <= g < HG * pb[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (HG * pb[mid] <= g) lo = mid; else hi = mid;
+        }
+        b = lo;
+        const int U = pb[b + 1] - pb[b];                  // > 0 by the invariant
+        const int local = g - HG * pb[b];
+        hg = local / U;
+        u0 = local - hg * U;
+        u1 = min(u0 + (g1 - g), U);
+        const int first = g / T;
+        split = first - (g - u0) / T;
+        span = (g + (u1 - u0) - 1) / T - first + 1;
+        g += u1 - u0;
+        return true;
+    }
+};
+
 // The producer warp: units [g0, g1) of the list into the ring.
 template <int D, int HPC>
-__device__ void fp4_produce(const Fp4DecodeArgs &a, const int32_t *prefix, int64_t T, int64_t g0, int64_t g1,
+__device__ void fp4_produce(const Fp4DecodeArgs &a, const int32_t *prefix, int T, int g0, int g1,
                             uint8_t *ring, uint64_t *full, uint64_t *empty, int lane) {
     using S = Fp4Smem<D, HPC>;
     const bool paged = a.page_size == 16;
     const bool run = paged && a.head_groups == 1;    // a unit is one contiguous run of rows
     int ctr = 0;
-    SegmentWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
+    UnitWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
     int b, hg, u0, u1, split, span;
     while (walk.next(b, hg, u0, u1, split, span)) {
         const int32_t *pt = a.page_table + (int64_t)b * a.pt_stride;
@@ -190,40 +218,42 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return r;
 }
 
-// What a consumer lane knows of its place in the fragments (bytes from the
-// start of a stage).
+// mma_f16_16816 into a fresh accumulator (no registers to clear first).
+__device__ __forceinline__ void mma_f16_16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Where a consumer lane finds its part of a stage (bytes from its start).
 template <int D, int HPC>
 struct Fp4Lane {
     using S = Fp4Smem<D, HPC>;
-    int tk, t0, t1;               // keys tk, tk + 8 of the scores; t0, t1, t0 + 8, t1 + 8 of the second product
-    int k_off, ks_off;            // codes and scales of key tk
-    int v_off0, v_off1;           // codes of keys t0, t1
-    int vs_off0, vs_off1;         // their scales
-    __device__ Fp4Lane(int hw, int lane) {
+    int k_off, ks_off;            // codes and scales of key place(r8); those of key + 8 are 8 rows on
+    int v_off, vs_off;            // codes and scale of key place(2 q4)
+    int v_next;                   // from there to key place(2 q4 + 1)
+    static __device__ __forceinline__ int place(int r) { return r ^ ((r >> 1) & 1); }   // fragment row -> key of the unit
+    __device__ __forceinline__ Fp4Lane(int hw, int lane) {
         const int r8 = lane >> 2, q4 = lane & 3;
-        auto place = [](int r) { return r ^ ((r >> 1) & 1); };   // row of the fragment -> key of the unit
-        tk = place(r8);
-        t0 = place(2 * q4);
-        t1 = place(2 * q4 + 1);
-        k_off = tk * S::kRow + hw * (D / 2) + q4 * (D / 8);
-        ks_off = tk * S::kRow + S::kCodes + hw * (D / 16) + q4 * (D / 64);
-        const int v = kUnit * S::kRow + hw * (D / 2) + r8 * (D / 16);
-        const int vs = kUnit * S::kRow + S::kCodes + hw * (D / 16) + (D == 128 ? r8 : r8 >> 1);
-        v_off0 = v + t0 * S::kRow;
-        v_off1 = v + t1 * S::kRow;
-        vs_off0 = vs + t0 * S::kRow;
-        vs_off1 = vs + t1 * S::kRow;
+        k_off = place(r8) * S::kRow + hw * (D / 2) + q4 * (D / 8);
+        ks_off = place(r8) * S::kRow + S::kCodes + hw * (D / 16) + q4 * (D / 64);
+        const int v = (kUnit + place(2 * q4)) * S::kRow;
+        v_off = v + hw * (D / 2) + r8 * (D / 16);
+        vs_off = v + S::kCodes + hw * (D / 16) + (D == 128 ? r8 : r8 >> 1);
+        v_next = (place(2 * q4 + 1) - place(2 * q4)) * S::kRow;
     }
 };
 
-// Raw scores of a unit: x[0], x[1] of key tk and heads 2 q4, 2 q4 + 1; x[2],
-// x[3] of key tk + 8.  Keys outside [n0, n1) give -inf.
+// Raw scores of a unit: x[0], x[1] of key place(r8) and heads 2 q4, 2 q4 + 1;
+// x[2], x[3] of the key 8 on.  Keys outside [n0, n1) give -inf.
 template <int D, int HPC>
 __device__ __forceinline__ void fp4_scores(const Fp4Lane<D, HPC> &ln, const uint8_t *st, const uint32_t (&qb)[D / 16][2],
                                            int n0, int n1, float *x) {
     using S = Fp4Smem<D, HPC>;
     constexpr int KW = D / 32;                       // words of a lane's part of a row
-    float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+    float sc[4], sd[4];
     uint32_t kw[2][KW], ks[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -247,13 +277,19 @@ __device__ __forceinline__ void fp4_scores(const Fp4Lane<D, HPC> &ln, const uint
         const uint32_t s1 = w < 2 ? f16_dup_lo(ks[1]) : f16_dup_hi(ks[1]);
         const uint32_t fa[4] = {hmul2_bits(a[0], s0), hmul2_bits(b[0], s1), hmul2_bits(a[1], s0), hmul2_bits(b[1], s1)};
         const uint32_t fb[4] = {hmul2_bits(a[2], s0), hmul2_bits(b[2], s1), hmul2_bits(a[3], s0), hmul2_bits(b[3], s1)};
-        mma_f16_16816(sc, fa, qb[2 * w][0], qb[2 * w][1]);
-        mma_f16_16816(sd, fb, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        if (w == 0) {
+            mma_f16_16816_zero(sc, fa, qb[0][0], qb[0][1]);
+            mma_f16_16816_zero(sd, fb, qb[1][0], qb[1][1]);
+        } else {
+            mma_f16_16816(sc, fa, qb[2 * w][0], qb[2 * w][1]);
+            mma_f16_16816(sd, fb, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = sc[i] + sd[i];
     if (n0 > 0 || n1 < kUnit) {
-        const bool s0 = ln.tk >= n0 && ln.tk < n1, s1 = ln.tk + 8 >= n0 && ln.tk + 8 < n1;
+        const int tk = Fp4Lane<D, HPC>::place((threadIdx.x & 31) >> 2);
+        const bool s0 = tk >= n0 && tk < n1, s1 = tk + 8 >= n0 && tk + 8 < n1;
         x[0] = s0 ? x[0] : -INFINITY;
         x[1] = s0 ? x[1] : -INFINITY;
         x[2] = s1 ? x[2] : -INFINITY;
@@ -271,19 +307,19 @@ __device__ __forceinline__ void fp4_values(const Fp4Lane<D, HPC> &ln, const uint
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint8_t *q = st + 8 * (i >> 1) * S::kRow;
-        const int off = (i & 1) ? ln.v_off1 : ln.v_off0;
+        const int off = ln.v_off + ((i & 1) ? ln.v_next : 0);
         if constexpr (VW == 2) {
             const uint2 w = *reinterpret_cast<const uint2 *>(q + off);
             vw[i][0] = w.x; vw[i][1] = w.y;
         } else {
             vw[i][0] = *reinterpret_cast<const uint32_t *>(q + off);
         }
-        vs[i] = q[(i & 1) ? ln.vs_off1 : ln.vs_off0];
+        vs[i] = q[ln.vs_off + ((i & 1) ? ln.v_next : 0)];
     }
     if (n0 > 0 || n1 < kUnit) {                      // keys that are not seen may hold anything: a zero scale clears them
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = ((i & 1) ? ln.t1 : ln.t0) + 8 * (i >> 1);
+            const int t = Fp4Lane<D, HPC>::place(2 * (threadIdx.x & 3) + (i & 1)) + 8 * (i >> 1);
             if (t < n0 || t >= n1) vs[i] = 0u;
         }
     }
@@ -311,7 +347,7 @@ __device__ __forceinline__ void fp4_values(const Fp4Lane<D, HPC> &ln, const uint
 // Units are taken in pairs: one vote and one maximum for 32 keys, and two
 // independent score chains in flight.
 template <int D, int HPC>
-__device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64_t T, int64_t g0, int64_t g1,
+__device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T, int g0, int g1,
                             const uint8_t *ring, uint64_t *full, uint64_t *empty, int hw, int lane) {
     using S = Fp4Smem<D, HPC>;
     constexpr int KS = D / 16;                       // k-steps of the score = tiles of O
@@ -320,7 +356,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int64
     const Fp4Lane<D, HPC> ln(hw, lane);
     int slot = 0;
     uint32_t phase = 0;
-    SegmentWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
+    UnitWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
     int b, hg, u0, u1, split, span;
     while (walk.next(b, hg, u0, u1, split, span)) {
         const int kvh = hg * HPC + hw;
@@ -449,14 +485,14 @@ __global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas) decode
     }
     fp4_prefix(a, prefix);
     const int B = a.num_seqs;
-    const int64_t total = (int64_t)a.head_groups * prefix[B];
-    int64_t T = (total + gridDim.x - 1) / gridDim.x;
+    const int total = a.head_groups * prefix[B];
+    int T = (total - 1) / (int)gridDim.x + 1;
     if (T < a.min_units) T = a.min_units;
     if (blockIdx.x == 0) {
         for (int b = threadIdx.x; b <= B; b += blockDim.x) a.ws_prefix[b] = prefix[b];
-        if (threadIdx.x == 0) a.ws_header[0] = (int32_t)T;
+        if (threadIdx.x == 0) a.ws_header[0] = T;
     }
-    const int64_t g0 = (int64_t)blockIdx.x * T, g1 = min(g0 + T, total);
+    const int g0 = (int)min((int64_t)blockIdx.x * T, (int64_t)total), g1 = min(total - g0, T) + g0;
     if (warp == HPC) fp4_produce<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, lane);
     else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
 }
@@ -560,12 +596,25 @@ cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const pa_decode_params &p, int6
     using S = Fp4Smem<D, HPC>;
     const size_t smem = S::kRing + 2 * S::kStages * sizeof(uint64_t) + ((size_t)a.num_seqs + 1) * sizeof(int32_t);
     auto kern = decode_fp4_kernel<D, HPC>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // CTAs per SM of the last (device, size), so that a serving loop's calls
+    // skip both queries; the limit is raised to the device's once and for all.
+    static std::atomic<uint64_t> last{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t key = ((uint64_t)(dev + 1) << 40) | ((uint64_t)smem << 8);
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (HPC + 1) * 32, smem);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const uint64_t seen = last.load(std::memory_order_relaxed);
+    if ((seen & ~uint64_t(255)) == key) {
+        per_sm = (int)(seen & 255);
+    } else {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        if (e != cudaSuccess) return e;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (HPC + 1) * 32, smem);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        last.store(key | (uint64_t)per_sm, std::memory_order_relaxed);
+    }
     int64_t grid = (int64_t)num_sms() * per_sm;
     if (p.max_ctas > 0 && grid > p.max_ctas) grid = p.max_ctas;
     if (grid > useful) grid = useful;

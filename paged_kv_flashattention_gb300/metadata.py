@@ -197,20 +197,21 @@ class BatchPlanner:
         self.totals = torch.zeros(4, dtype=torch.int32, device=self.device)
         cols = -(-self.max_seqlen_k // self.page_size)
         self.page_table = torch.full((n, max(cols, 1)), -1, dtype=torch.int32, device=self.device)
+        self._batches: dict[int, DeviceBatch] = {}
 
     def build(self, cached_len: torch.Tensor, extend_len: torch.Tensor, token_table: torch.Tensor,
               table_idx: torch.Tensor, *, free_pages: torch.Tensor | None = None) -> DeviceBatch:
         """Plan the batch of cached_len / extend_len (int32 [B], B <= max_seqs)
         whose requests are the rows table_idx of token_table."""
         B = cached_len.numel()
-        if B > self.max_seqs:
-            raise ValueError(f"batch of {B} requests > planner capacity {self.max_seqs}")
-        b = DeviceBatch(num_seqs=B, page_size=self.page_size, max_seqlen_k=self.max_seqlen_k,
-                        cu_seqlens_q=self.cu_seqlens[0, :B + 1], cu_seqlens_k=self.cu_seqlens[1, :B + 1],
-                        cache_seqlens=self.cache_seqlens[:B], positions=self.tokens[0], slot_mapping=self.tokens[1],
-                        page_table=self.page_table[:B], totals=self.totals)
-        api.build_batch(cached_len, extend_len, token_table, table_idx, self.page_size, self.max_seqlen_k,
-                        cu_seqlens_q=b.cu_seqlens_q, cu_seqlens_k=b.cu_seqlens_k, cache_seqlens=b.cache_seqlens,
-                        positions=b.positions, slot_mapping=b.slot_mapping, page_table=b.page_table, totals=b.totals,
-                        free_pages=free_pages)
+        b = self._batches.get(B)
+        if b is None:                                # the views for this batch size
+            if B > self.max_seqs:
+                raise ValueError(f"batch of {B} requests > planner capacity {self.max_seqs}")
+            b = self._batches[B] = DeviceBatch(
+                num_seqs=B, page_size=self.page_size, max_seqlen_k=self.max_seqlen_k,
+                cu_seqlens_q=self.cu_seqlens[0, :B + 1], cu_seqlens_k=self.cu_seqlens[1, :B + 1],
+                cache_seqlens=self.cache_seqlens[:B], positions=self.tokens[0], slot_mapping=self.tokens[1],
+                page_table=self.page_table[:B], totals=self.totals)
+        api._build_batch(cached_len, extend_len, token_table, table_idx, self.page_size, self.max_seqlen_k, b, free_pages)
         return b

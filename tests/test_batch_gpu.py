@@ -77,6 +77,7 @@ def test_broken_requests(cuda_device):
     run(cuda_device, cached, extend, tt, idx, page, max_k, 80, free)
     run(cuda_device, cached, extend, tt, idx, page, max_k, 30, free)      # tokens past the end
     run(cuda_device, cached, extend, tt, idx, page, max_k, 80, free[:2])  # the list runs out
+    run(cuda_device, cached, extend, tt, idx, page, max_k, 80, free[:0])  # no page at all
     idx[3] = -1
     run(cuda_device, cached, extend, tt, idx, page, max_k, 80)
 
