@@ -57,13 +57,19 @@
 // epilogue multiplies by v_scale.
 //
 // 4-bit pools (F4; row layout: fp4.cuh) take the same path: a tile's 128 x d/2
-// bytes of codes and 128 x 16 bytes that hold the head's scales land inside
-// the f16 slot (two TMA boxes per page, or row gathers at page size 1), rows 0
-// - 63 and 64 - 127 each where the warp that widens them will write, so that a
-// warp reads its part into registers and overwrites it without meeting the
-// other: E2M1 to f16 by the hardware conversion, times the block's scale
-// (exact in f16).  k_scale is a factor of
+// bytes of codes and 128 x 16 bytes that hold the head's scales land in a slot
+// of their own (two TMA boxes per page, or row gathers at page size 1) and the
+// same two warps widen them into an f16 slot: E2M1 to f16 by the hardware
+// conversion, times the block's scale (exact in f16).  k_scale is a factor of
 // the scores here, so Q only changes from bf16 to f16.
+// What bounds it: the two warps' way from a landed tile to a widened one
+// (loads, conversion, stores, proxy fence) and the second box per page.  Timing
+// copies on eight extend requests (171 GFLOP): as built 241 us; nothing widened
+// 234; the scales not loaded either 181, which is the bf16 kernel's 180.
+// Slower: a fourth warpgroup for the widening (248 - 298 us; the softmax then
+// spills), one warp per tile (267), scales read by the widening warps from
+// global memory (335), scales by cp.async in the producer (255), four slots
+// widened in place (262).
 #pragma once
 
 #include <cuda.h>
@@ -273,22 +279,22 @@ struct PrefillSmem {
     // goes) and is widened where it lies, so the slots serve both rings.
     // FP8, d = 64: a ring of widened f16 tiles (2..4 slots) and a separate
     // ring of loaded tiles from the rest.
-    // 4-bit: in place at either head size (the tile is in registers when the
-    // slot is overwritten).
-    static constexpr bool kInPlace = F4 || (F8 && D == 128);
+    // 4-bit: 3 to 6 widened tiles, the rest loaded ones (10 KiB at d = 128).
+    static constexpr bool kInPlace = F8 && !F4 && D == 128;
     static constexpr int kFitTiles = kAvail / kTileBytes;
     static constexpr int kCSlotsFit = (kAvail / 2) / kTileBytes;
     static constexpr int kCSlots = !F8 ? 0
+                                 : F4 ? (D == 64 ? 6 : T == 2 ? 3 : 4)
                                  : kInPlace ? (kFitTiles > 8 ? 8 : kFitTiles)
                                             : (kCSlotsFit > 4 ? 4 : (kCSlotsFit < 2 ? 2 : kCSlotsFit));
     static constexpr int kSlotsFit = kInPlace ? kCSlots : (kAvail - kCSlots * kTileBytes) / kLTile;
     static constexpr int kSlots = kSlotsFit > 8 ? 8 : kSlotsFit;
     static constexpr int kLStride = kInPlace ? kTileBytes : kLTile;       // landing slot stride
-    static constexpr int kLOff = F4 ? kTileBytes - 16384 : kInPlace ? kTileBytes - kLTile : 0;   // landing offset in a slot
-    // 4-bit landing area: per 64 rows (8 KiB apart) D/2 bytes of codes a row,
-    // then 16 bytes with the scales a row.
-    static constexpr int code_off(int r) { return (r >> 6) * 8192 + (r & 63) * (D / 2); }
-    static constexpr int scale_off(int r) { return (r >> 6) * 8192 + 32 * D + (r & 63) * 16; }
+    static constexpr int kLOff = kInPlace ? kTileBytes - kLTile : 0;   // landing offset in a slot
+    // 4-bit landing slot: D/2 bytes of codes a row, then 16 bytes with the
+    // scales a row.
+    static constexpr int code_off(int r) { return r * (D / 2); }
+    static constexpr int scale_off(int r) { return kBN * (D / 2) + r * 16; }
     static constexpr int kConv = kInPlace ? kRing : kRing + kSlots * kLTile;
     static constexpr int kStage = kInPlace ? kRing + kCSlots * kTileBytes : kConv + kCSlots * kTileBytes;
     static constexpr int kBars = kStage + kStageBytes;
@@ -578,11 +584,12 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         return true;
     };
 
-    // Tile c of item `it` from its 4-bit landing area to f16 in the swizzled
+    // Tile c of item `it` from its 4-bit landing slot to f16 in the swizzled
     // layout: warp cw widens rows [64 cw, 64 cw + 64).  A lane takes 16-byte
     // chunks of codes (32 elements, two blocks) of the rows = lane mod 8, so
-    // that each store of a warp's quarter covers all banks.  The warp reads all
-    // of its rows before it writes over them.  Rows at keys >= kv_end hold slots the store never wrote: a zero scale clears them.
+    // that each store of a warp's quarter covers all banks; all its loads go out
+    // first (in groups of four chunks 282 us against 267, of two 299).  Rows at
+    // keys >= kv_end hold slots the store never wrote: a zero scale clears them.
     auto widen4 = [&](const PrefillItem &it, int c, int cw, const uint8_t *src, uint8_t *dst) {
         constexpr int kChunks = D / 32;               // chunks of a row
         constexpr int kRows = 32 / kChunks;           // rows of a pass: 8 or 16
@@ -601,7 +608,6 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             sc[i] = *reinterpret_cast<const uint16_t *>(src + S::scale_off(r) + sub + 2 * ch);
             if (r >= live) sc[i] = 0u;
         }
-        __syncwarp();
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = 64 * cw + i * kRows + lane % kRows;
@@ -792,7 +798,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                     widen4(it, c, cw, src, dst);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&cfull[cs]);
+                    if (lane == 0) {
+                        mbar_arrive(&cfull[cs]);
+                        mbar_arrive(&empty[ls]);
+                    }
                     continue;
                 }
                 // groups of 4 x 512 bytes: all reads of a group, then (in
