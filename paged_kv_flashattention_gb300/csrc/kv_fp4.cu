@@ -9,13 +9,15 @@
 // is below about 6 g 2^-10) stores zeros.  A NaN in a block makes its scale
 // NaN, so that the whole block reads as NaN; infinities saturate.
 //
-// All three kernels give a lane one block: 16 elements are two 16-byte loads,
-// and the block's maximum stays inside the lane.  d/16 lanes make a head,
-// 32 / (d/16) heads a unit of work; a warp takes `upw` units of one token, so
-// that a long batch loads a token's cos / sin once for all its heads while a
-// short one still spreads over the GPU.
-// Bound: HBM for long batches (per element 2 bytes in, 9/16 out), launch
-// latency for short ones.
+// All three kernels give a lane 16 elements: two 16-byte loads, and a block's
+// maximum stays inside the lane.  d/16 lanes make a head, 32 / (d/16) heads a
+// unit of work; a warp takes `upw` units of one token, so that a long batch
+// loads a token's cos / sin once for all its heads while a short one still
+// spreads over the GPU.  The rotary gives a lane both members of its eight
+// pairs; keys then change places by shuffles for the quantiser.
+// Bound: long batches by HBM and the latency of the loads in flight (rotary,
+// 8192 tokens: 4.6 TB/s; store 3.1, most of it the divisions; load 4.3), short
+// ones by launch latency (2 to 4 us).
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -50,12 +52,6 @@ struct Fp4StoreArgs {
     Fp4Layout lay;
     int32_t upw;                  // units a warp takes
 };
-
-__device__ __forceinline__ void load16(const uint8_t *p, uint32_t (&w)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p), b = *reinterpret_cast<const uint4 *>(p + 16);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-}
 
 // Codes (8 bytes) and scale of a block of 16 bf16.
 __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], float g, uint2 &codes, uint32_t &scale) {
@@ -109,77 +105,98 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], float g, uint
     codes = make_uint2(c[0], c[1]);
 }
 
-// The lane's cos and sin: group j (elements 8 w .. 8 w + 7 of a head, w = 2 blk
-// + j) becomes own * c + partner * s, the sign of the rotation inside s.
+// The rotary's eight pairs of a lane.  Pairs (i, i + h), h half the rotated
+// width: the first rot/16 lanes of a head hold elements 8 blk .. + 7 and h + 8
+// blk .. + 7.  Pairs (2i, 2i + 1): elements 16 blk .. + 15.  Lanes past the
+// rotated width copy elements 16 blk .. + 15.
 struct RopeLane {
-    float c[2][8], s[2][8];
-    int partner[2];               // byte offset of the partner group within the head; -1: not rotated
+    float2 c[4], s[4];            // cos and sin of pairs 2 i, 2 i + 1
+    bool turn;
+    int lo, hi;                   // byte offsets of the lane's two groups of eight in the head
 };
 
-__device__ __forceinline__ void rope_lane(const Fp4StoreArgs &a, int pos, int blk, RopeLane &rl) {
-    const int rot = a.rot_dim, h = rot / 2;
-    const float *row = a.cos_sin + (int64_t)pos * rot;
+__device__ __forceinline__ RopeLane rope_place(const Fp4StoreArgs &a, int blk) {
+    RopeLane rl;
+    rl.turn = 16 * blk < a.rot_dim;
+    const bool split = rl.turn && !a.interleaved;
+    rl.lo = split ? 16 * blk : 32 * blk;
+    rl.hi = split ? a.rot_dim + 16 * blk : 32 * blk + 16;
+    return rl;
+}
+
+__device__ __forceinline__ void rope_load(const Fp4StoreArgs &a, int pos, int blk, RopeLane &rl) {
+    if (!rl.turn) return;
+    const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + 8 * blk);
+    const float4 *s = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * a.rot_dim + a.rot_dim / 2 + 8 * blk);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int e = 16 * blk + 8 * j;
-        rl.partner[j] = -1;
-        if (e >= rot) continue;
-        if (a.interleaved) {
-            rl.partner[j] = 2 * e;                       // pairs lie inside the group
-            const float4 c = *reinterpret_cast<const float4 *>(row + e / 2);
-            const float4 s = *reinterpret_cast<const float4 *>(row + h + e / 2);
-            const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+    for (int i = 0; i < 2; ++i) {
+        const float4 x = c[i], y = s[i];
+        rl.c[2 * i] = make_float2(x.x, x.y);
+        rl.c[2 * i + 1] = make_float2(x.z, x.w);
+        rl.s[2 * i] = make_float2(y.x, y.y);
+        rl.s[2 * i + 1] = make_float2(y.z, y.w);
+    }
+}
+
+// (a, b) -> (a c - b s, b c + a s) of the lane's pairs as the unfused rotary
+// computes it: products and sum rounded in fp32, the result to bf16.
+__device__ __forceinline__ void rotate16(const RopeLane &rl, bool interleaved, uint32_t (&w)[8]) {
+    if (!rl.turn) return;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                rl.c[j][2 * i] = rl.c[j][2 * i + 1] = cv[i];
-                rl.s[j][2 * i] = -sv[i];
-                rl.s[j][2 * i + 1] = sv[i];
-            }
+    for (int i = 0; i < 4; ++i) {
+        float2 a, b;
+        if (interleaved) {
+            a = make_float2(bf16lo(w[2 * i]), bf16lo(w[2 * i + 1]));
+            b = make_float2(bf16hi(w[2 * i]), bf16hi(w[2 * i + 1]));
         } else {
-            const bool first = e < h;
-            const int i0 = first ? e : e - h;
-            rl.partner[j] = 2 * (first ? e + h : e - h);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 c = *reinterpret_cast<const float4 *>(row + i0 + 4 * i);
-                const float4 s = *reinterpret_cast<const float4 *>(row + h + i0 + 4 * i);
-                rl.c[j][4 * i] = c.x; rl.c[j][4 * i + 1] = c.y; rl.c[j][4 * i + 2] = c.z; rl.c[j][4 * i + 3] = c.w;
-                const float f = first ? -1.f : 1.f;
-                rl.s[j][4 * i] = f * s.x; rl.s[j][4 * i + 1] = f * s.y;
-                rl.s[j][4 * i + 2] = f * s.z; rl.s[j][4 * i + 3] = f * s.w;
-            }
+            a = make_float2(bf16lo(w[i]), bf16hi(w[i]));
+            b = make_float2(bf16lo(w[4 + i]), bf16hi(w[4 + i]));
+        }
+        // scalar: packed f32x2 products and sums came out fused
+        const float2 c = rl.c[i], n = rl.s[i];
+        const float2 x = make_float2(__fsub_rn(__fmul_rn(a.x, c.x), __fmul_rn(b.x, n.x)),
+                                     __fsub_rn(__fmul_rn(a.y, c.y), __fmul_rn(b.y, n.y)));
+        const float2 y = make_float2(__fadd_rn(__fmul_rn(b.x, c.x), __fmul_rn(a.x, n.x)),
+                                     __fadd_rn(__fmul_rn(b.y, c.y), __fmul_rn(a.y, n.y)));
+        if (interleaved) {
+            w[2 * i] = pack_bf16x2(x.x, y.x);
+            w[2 * i + 1] = pack_bf16x2(x.y, y.y);
+        } else {
+            w[i] = pack_bf16x2(x.x, x.y);
+            w[4 + i] = pack_bf16x2(y.x, y.y);
         }
     }
 }
 
-// Rotate the lane's block w of the head at `head` (16 bf16), as the unfused
-// rotary does: products and sum rounded in fp32, the result to bf16.
-__device__ __forceinline__ void rotate16(const Fp4StoreArgs &a, const RopeLane &rl, const uint8_t *head, uint32_t (&w)[8]) {
+// From the places of pairs (i, i + h) to 16 consecutive elements per lane (the
+// quantiser's blocks).  Every lane of the warp calls it; `first` is the head's
+// first lane.
+__device__ __forceinline__ void regroup16(const Fp4StoreArgs &a, int first, int blk, uint32_t (&w)[8]) {
+    const int half = a.rot_dim / 16;                 // groups of eight of the first elements; lanes that turn
+    uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        if (rl.partner[j] < 0) continue;
-        uint32_t p[4];
-        if (a.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = __byte_perm(w[4 * j + i], 0u, 0x1032);
-        } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(head + rl.partner[j]);
-            p[0] = x.x; p[1] = x.y; p[2] = x.z; p[3] = x.w;
-        }
+        const int g = 2 * blk + j;                   // the group wanted
+        const int src = first + (g < half ? g : g < 2 * half ? g - half : g >> 1);
+        const bool second = g < half ? false : g < 2 * half ? true : g & 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t o = w[4 * j + i];
-            const float lo = __fadd_rn(__fmul_rn(bf16lo(o), rl.c[j][2 * i]), __fmul_rn(bf16lo(p[i]), rl.s[j][2 * i]));
-            const float hi = __fadd_rn(__fmul_rn(bf16hi(o), rl.c[j][2 * i + 1]), __fmul_rn(bf16hi(p[i]), rl.s[j][2 * i + 1]));
-            p[i] = pack_bf16x2(lo, hi);
+            const uint32_t x = __shfl_sync(0xffffffffu, w[i], src), y = __shfl_sync(0xffffffffu, w[4 + i], src);
+            o[4 * j + i] = second ? y : x;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * j + i] = p[i];
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = o[i];
 }
 
-template <int D, bool ROPE>
-__global__ void __launch_bounds__(256) fp4_store_kernel(const Fp4StoreArgs a) {
+// UG: units whose loads go out together.  The rotary on 8192 tokens (32 + 8
+// heads of 128, 178 MB): two units at 64 registers 38.8 us, at 80 44.0, at 106
+// 53.5; one unit at 64 41.8; four at 123 50.9.  When a lane held 16 consecutive
+// elements and fetched their partners through memory it was 63 us, by shuffles
+// 49.  The plain store of the same tokens (43 MB) is 14 us with one unit, 15 to
+// 16 with more.
+template <int D, bool ROPE, int UG>
+__global__ void __launch_bounds__(256, 4) fp4_store_kernel(const Fp4StoreArgs a) {
     constexpr int kLanes = D / 16;                   // lanes of a head
     constexpr int kHeads = 32 / kLanes;              // heads of a unit
     const int lane = threadIdx.x & 31;
@@ -187,56 +204,72 @@ __global__ void __launch_bounds__(256) fp4_store_kernel(const Fp4StoreArgs a) {
     const int uq = (a.num_q_heads + kHeads - 1) / kHeads, uk = (a.num_kv_heads + kHeads - 1) / kHeads;
     const int units = uq + 2 * uk;
     const int parts = (units + a.upw - 1) / a.upw;   // warps of a token
+    const bool inter = a.interleaved != 0;
     const int64_t warps_total = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < a.num_tokens * parts;
          i += warps_total) {
         const int64_t t = i / parts;
         const int u0 = (int)(i - t * parts) * a.upw, u1 = min(u0 + a.upw, units);
-        const int64_t slot = a.slot_mapping[t];
+        const int slot = a.slot_mapping[t];
         const bool store = slot >= 0 && slot < a.num_slots;
-        if (slot >= a.num_slots && lane == 0) raise_error(PA_DEVERR_PAGE_RANGE);
+        if (u0 == 0 && slot >= a.num_slots && lane == 0) raise_error(PA_DEVERR_PAGE_RANGE);
         RopeLane rl;
         if (ROPE) {
             const int pos = a.positions[t];
             if (pos < 0 || pos >= a.max_pos) {       // nothing of this token is written
-                if (lane == 0) raise_error(PA_DEVERR_POSITION);
+                if (u0 == 0 && lane == 0) raise_error(PA_DEVERR_POSITION);
                 continue;
             }
-            rope_lane(a, pos, blk, rl);
+            rl = rope_place(a, blk);
+            rope_load(a, pos, blk, rl);
         } else if (!store) {
             continue;
         }
-        for (int u = u0; u < u1; ++u) {
-            if (ROPE && u < uq) {
-                const int h = u * kHeads + sub;
-                const int64_t off = ((t * a.num_q_heads + h) * D) * 2;
-                uint32_t w[8];
-                if (h < a.num_q_heads) {
-                    load16(a.q + off + blk * 32, w);
-                    rotate16(a, rl, a.q + off, w);
-                }
-                __syncwarp();                        // q_out may be q: every partner is read first
-                if (h < a.num_q_heads) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.q_out + off + blk * 32);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-                continue;
+        for (int u = u0; u < u1; u += UG) {
+            uint32_t w[UG][8];
+            int off[UG];                             // the head's byte offset in its token; -1: no such head
+#pragma unroll
+            for (int g = 0; g < UG; ++g) {           // q, then k, then v
+                const int n = u + g;
+                const bool is_q = n < uq, is_k = n < uq + uk;
+                const int h = (is_q ? n : n - uq - (is_k ? 0 : uk)) * kHeads + sub;
+                const int heads = is_q ? a.num_q_heads : a.num_kv_heads;
+                off[g] = n < u1 && h < heads && (is_q || store) ? h * (2 * D) : -1;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[g][e] = 0u;
+                if (off[g] < 0) continue;
+                const uint8_t *head = (is_q ? a.q : is_k ? a.k : a.v) + t * heads * (2 * D) + off[g];
+                const bool pairs = ROPE && is_k;
+                const uint4 x = *reinterpret_cast<const uint4 *>(head + (pairs ? rl.lo : 32 * blk));
+                const uint4 y = *reinterpret_cast<const uint4 *>(head + (pairs ? rl.hi : 32 * blk + 16));
+                w[g][0] = x.x; w[g][1] = x.y; w[g][2] = x.z; w[g][3] = x.w;
+                w[g][4] = y.x; w[g][5] = y.y; w[g][6] = y.z; w[g][7] = y.w;
             }
-            const bool is_k = u < uq + uk;
-            const int h = (u - uq - (is_k ? 0 : uk)) * kHeads + sub;
-            if (!store || h >= a.num_kv_heads) continue;
-            const uint8_t *head = (is_k ? a.k : a.v) + ((t * a.num_kv_heads + h) * D) * 2;
-            uint32_t w[8];
-            load16(head + blk * 32, w);
-            if (ROPE && is_k) rotate16(a, rl, head, w);
-            uint2 codes;
-            uint32_t scale;
-            quantise16(w, __ldg((is_k ? a.k_scale : a.v_scale) + h), codes, scale);
-            const int hg = h & (a.lay.gs - 1);       // gs is a power of two
-            uint8_t *row = (is_k ? a.k_cache : a.v_cache) + slot * a.lay.row_bytes + (h / a.lay.gs) * a.lay.group_bytes;
-            *reinterpret_cast<uint2 *>(row + hg * (D / 2) + blk * 8) = codes;
-            row[a.lay.code_bytes + hg * kLanes + blk] = (uint8_t)scale;
+#pragma unroll
+            for (int g = 0; g < UG; ++g) {
+                const int n = u + g;
+                if (n >= u1) break;
+                const bool is_q = n < uq, is_k = n < uq + uk;
+                if (ROPE && is_k) rotate16(rl, inter, w[g]);
+                if (is_q) {                          // (in place too: a lane writes what it alone read)
+                    if (off[g] < 0) continue;
+                    uint8_t *dst = a.q_out + t * a.num_q_heads * (2 * D) + off[g];
+                    *reinterpret_cast<uint4 *>(dst + rl.lo) = make_uint4(w[g][0], w[g][1], w[g][2], w[g][3]);
+                    *reinterpret_cast<uint4 *>(dst + rl.hi) = make_uint4(w[g][4], w[g][5], w[g][6], w[g][7]);
+                    continue;
+                }
+                if (ROPE && is_k && !inter) regroup16(a, lane - blk, blk, w[g]);
+                if (off[g] < 0) continue;
+                const int h = off[g] / (2 * D);
+                uint2 codes;
+                uint32_t scale;
+                quantise16(w[g], __ldg((is_k ? a.k_scale : a.v_scale) + h), codes, scale);
+                const int hg = h & (a.lay.gs - 1);   // gs is a power of two
+                uint8_t *row = (is_k ? a.k_cache : a.v_cache) + (int64_t)slot * a.lay.row_bytes +
+                               (h / a.lay.gs) * a.lay.group_bytes;
+                *reinterpret_cast<uint2 *>(row + hg * (D / 2) + blk * 8) = codes;
+                row[a.lay.code_bytes + hg * kLanes + blk] = (uint8_t)scale;
+            }
         }
     }
 }
@@ -299,14 +332,14 @@ struct StoreGrid {
 };
 StoreGrid store_grid(int64_t tokens, int units) {
     const int64_t want = (int64_t)num_sms() * 32;
-    int64_t upw = tokens * units / want;
-    if (upw < 1) upw = 1;
-    if (upw > units) upw = units;
+    int64_t parts = (want + tokens - 1) / tokens;    // warps of a token
+    if (parts > units) parts = units;
+    const int upw = (int)((units + parts - 1) / parts);
     const int64_t warps = tokens * ((units + upw - 1) / upw);
     int64_t blocks = (warps + 7) / 8;
     const int64_t cap = (int64_t)num_sms() * 16;
     if (blocks > cap) blocks = cap;
-    return {(int32_t)upw, (unsigned)blocks};
+    return {upw, (unsigned)blocks};
 }
 
 template <bool ROPE>
@@ -315,8 +348,9 @@ cudaError_t launch_store_t(Fp4StoreArgs &a, int d, cudaStream_t stream) {
     const int units = (a.num_q_heads + heads - 1) / heads + 2 * ((a.num_kv_heads + heads - 1) / heads);
     const StoreGrid g = store_grid(a.num_tokens, units);
     a.upw = g.upw;
-    if (d == 64) fp4_store_kernel<64, ROPE><<<g.blocks, 256, 0, stream>>>(a);
-    else fp4_store_kernel<128, ROPE><<<g.blocks, 256, 0, stream>>>(a);
+    constexpr int UG = ROPE ? 2 : 1;
+    if (d == 64) fp4_store_kernel<64, ROPE, UG><<<g.blocks, 256, 0, stream>>>(a);
+    else fp4_store_kernel<128, ROPE, UG><<<g.blocks, 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
