@@ -22,6 +22,7 @@
 // size 16) for large tables.
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pdl.cuh"
 
 namespace pa {
 
@@ -95,6 +96,7 @@ __device__ __forceinline__ int free_page(const pa_batch_params &p, int n) {
 __global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_params p) {
     extern __shared__ int32_t smem[];
     __shared__ int32_t warp_sums[kThreads / 32];
+    after_previous();
     const int B = p.num_seqs, P = p.page_size;
     const bool take = p.free_pages != nullptr;
     int32_t *cq = smem;                              // [B + 1] new tokens
@@ -193,8 +195,7 @@ cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream) {
     const int64_t cap = (int64_t)num_sms() * 4;
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;
-    build_batch_kernel<<<(unsigned)blocks, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(build_batch_kernel, (unsigned)blocks, kThreads, smem, stream, p);
 }
 
 }  // namespace pa

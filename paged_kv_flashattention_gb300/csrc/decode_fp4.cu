@@ -29,6 +29,15 @@
 //
 // The running maximum is lazy as in decode.cu; here a vote decides whether any
 // score exceeds it by more than 2^8, so that the usual unit needs no shuffle.
+//
+// What bounds it: HBM delivers a unit of a head (2304 bytes at D = 128) every 98
+// clocks per SM, its consumer warps need about 300 instructions for it and issue
+// 2.5 per clock (64 conversions, 64 multiplies, 16 MMAs, the rest of the softmax
+// and addresses).  256 log-uniform contexts up to 32768 (2.38 GB): 423 us, 5.6
+// TB/s, 0.83 of the measured copy bandwidth; one unit at a time 428 us, with
+// 64-bit walks and six more live registers 448 (spills), 472 before the pairs.
+// At D = 64 half the bytes come with more than half the instructions: 64
+// sequences of up to 4096 keys 24 us, 0.40.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -37,6 +46,7 @@
 #include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pdl.cuh"
 
 namespace pa {
 
@@ -69,6 +79,7 @@ struct Fp4DecodeArgs {
     const float *k_scale;
     const float *v_scale;
     int32_t window;
+    int32_t overlap_previous;     // do not wait for the kernel before
     int32_t *ws_header;           // [0] = T, in units
     int32_t *ws_prefix;           // [B+1] exclusive prefix of the sequences' units
 };
@@ -483,6 +494,7 @@ __global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas) decode
         }
         fence_mbar_init();
     }
+    if (!a.overlap_previous) after_previous();
     fp4_prefix(a, prefix);
     const int B = a.num_seqs;
     const int total = a.head_groups * prefix[B];
@@ -514,7 +526,7 @@ __global__ void __launch_bounds__(kCombineThreads) fp4_combine_kernel(
     __shared__ float4 part[kCombineThreads];
     const int t = threadIdx.x % (32 * W), lane = t & 31;
     const int row = blockIdx.x * (kCombineThreads / (32 * W)) + threadIdx.x / (32 * W);
-    asm volatile("griddepcontrol.wait;" ::: "memory");           // the partials are complete
+    after_previous();                                // the partials are complete
     int n = 0;
     if (row < num_rows) {
         const int64_t T = header[0];
@@ -574,21 +586,12 @@ cudaError_t launch_fp4_combine(const Fp4DecodeArgs &a, const pa_decode_params &p
     // more than a few slots.
     const bool share = plan.max_splits >= 8 && rows <= num_sms() * 8;
     const int per_block = share ? 1 : kCombineThreads / 32;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + per_block - 1) / per_block));
-    cfg.blockDim = dim3(kCombineThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     constexpr int W = kCombineThreads / 32;
     auto kern = p.head_dim == 64 ? (share ? fp4_combine_kernel<64, W> : fp4_combine_kernel<64, 1>)
                                  : (share ? fp4_combine_kernel<128, W> : fp4_combine_kernel<128, 1>);
-    return cudaLaunchKernelEx(&cfg, kern, (const float *)a.o_part, (const float *)a.lse_part, (const int32_t *)a.ws_header,
-                              (const int32_t *)a.ws_prefix, a.head_groups, (int32_t)heads_per_group, p.num_q_heads,
-                              (int32_t)rows, plan.max_splits, static_cast<__nv_bfloat16 *>(p.out), p.lse);
+    return launch_after(kern, (unsigned)((rows + per_block - 1) / per_block), kCombineThreads, 0, stream, a.o_part,
+                        a.lse_part, a.ws_header, a.ws_prefix, a.head_groups, heads_per_group, p.num_q_heads, rows,
+                        plan.max_splits, static_cast<__nv_bfloat16 *>(p.out), p.lse);
 }
 
 template <int D, int HPC>
@@ -618,17 +621,7 @@ cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const pa_decode_params &p, int6
     int64_t grid = (int64_t)num_sms() * per_sm;
     if (p.max_ctas > 0 && grid > p.max_ctas) grid = p.max_ctas;
     if (grid > useful) grid = useful;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((HPC + 1) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = p.overlap_previous ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return launch_after(kern, (unsigned)grid, (HPC + 1) * 32, smem, stream, a);
 }
 
 }  // namespace
@@ -683,6 +676,7 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
     a.k_scale = p.k_scale;
     a.v_scale = p.v_scale;
     a.window = p.sliding_window;
+    a.overlap_previous = p.overlap_previous;
     a.ws_header = w.ws_header;
     a.ws_prefix = w.ws_prefix;
     // every sequence at its longest, ranges at their smallest

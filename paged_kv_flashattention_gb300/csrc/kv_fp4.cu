@@ -23,6 +23,7 @@
 #include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pdl.cuh"
 
 namespace pa {
 
@@ -199,6 +200,7 @@ template <int D, bool ROPE, int UG>
 __global__ void __launch_bounds__(256, 4) fp4_store_kernel(const Fp4StoreArgs a) {
     constexpr int kLanes = D / 16;                   // lanes of a head
     constexpr int kHeads = 32 / kLanes;              // heads of a unit
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int blk = lane % kLanes, sub = lane / kLanes;
     const int uq = (a.num_q_heads + kHeads - 1) / kHeads, uk = (a.num_kv_heads + kHeads - 1) / kHeads;
@@ -284,6 +286,7 @@ __global__ void __launch_bounds__(256) fp4_load_kernel(const int32_t *__restrict
                                                        const float *__restrict__ v_scale, uint8_t *k_out,
                                                        uint8_t *v_out, Fp4Layout lay, int32_t upw) {
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int blk = lane % kLanes, sub = lane / kLanes;
     const int uk = (num_kv_heads + kHeads - 1) / kHeads, units = 2 * uk;
@@ -349,9 +352,8 @@ cudaError_t launch_store_t(Fp4StoreArgs &a, int d, cudaStream_t stream) {
     const StoreGrid g = store_grid(a.num_tokens, units);
     a.upw = g.upw;
     constexpr int UG = ROPE ? 2 : 1;
-    if (d == 64) fp4_store_kernel<64, ROPE, UG><<<g.blocks, 256, 0, stream>>>(a);
-    else fp4_store_kernel<128, ROPE, UG><<<g.blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    auto kern = d == 64 ? fp4_store_kernel<64, ROPE, UG> : fp4_store_kernel<128, ROPE, UG>;
+    return launch_after(kern, g.blocks, 256, 0, stream, a);
 }
 
 }  // namespace
@@ -404,11 +406,10 @@ cudaError_t launch_load_kv_fp4(const int32_t *slots, int64_t num_tokens, const v
     const int heads = 32 / (head_dim / 16);
     const StoreGrid g = store_grid(num_tokens, 2 * ((num_kv_heads + heads - 1) / heads));
     auto kern = head_dim == 64 ? fp4_load_kernel<64> : fp4_load_kernel<128>;
-    kern<<<g.blocks, 256, 0, stream>>>(slots, num_tokens, static_cast<const uint8_t *>(k_cache),
-                                       static_cast<const uint8_t *>(v_cache), num_slots, num_kv_heads, k_scale, v_scale,
-                                       static_cast<uint8_t *>(k_out), static_cast<uint8_t *>(v_out),
-                                       fp4_layout(num_kv_heads, head_dim), g.upw);
-    return cudaGetLastError();
+    return launch_after(kern, g.blocks, 256, 0, stream, slots, num_tokens, static_cast<const uint8_t *>(k_cache),
+                        static_cast<const uint8_t *>(v_cache), num_slots, num_kv_heads, k_scale, v_scale,
+                        static_cast<uint8_t *>(k_out), static_cast<uint8_t *>(v_out), fp4_layout(num_kv_heads, head_dim),
+                        g.upw);
 }
 
 }  // namespace pa

@@ -1,0 +1,37 @@
+// Programmatic dependent launches.  A kernel launched with launch_after starts
+// while the kernel before it in the stream drains, and calls after_previous()
+// before it touches memory: that returns once the earlier grid has completed
+// and its writes are visible.  Every thread that can exit calls it, so "this
+// grid has completed" implies the same of all before it.  Measured on the small
+// calls: 0.3 to 0.6 us less per kernel.  Letting the next kernel's CTAs onto the
+// SMs at the start of this one (griddepcontrol.launch_dependents) costs more
+// than it gives: 64 decode sequences 24.2 -> 26.3 us, a batch plan 12.6 -> 14.1.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace pa {
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                         Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
+}
+
+}  // namespace pa
