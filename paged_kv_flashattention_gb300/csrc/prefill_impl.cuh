@@ -57,19 +57,19 @@
 // epilogue multiplies by v_scale.
 //
 // 4-bit pools (F4; row layout: fp4.cuh) take the same path: a tile's 128 x d/2
-// bytes of codes and 128 x 16 bytes that hold the head's scales land in a slot
-// of their own (two TMA boxes per page, or row gathers at page size 1) and the
-// same two warps widen them into an f16 slot: E2M1 to f16 by the hardware
-// conversion, times the block's scale (exact in f16).  k_scale is a factor of
-// the scores here, so Q only changes from bf16 to f16.
+// bytes of codes (a TMA box per page) and 128 x 16 bytes that hold the head's
+// scales (cp.async; both by row gathers at page size 1) land in a slot of their
+// own and the same two warps widen them into an f16 slot: E2M1 to f16 by the
+// hardware conversion, times the block's scale (exact in f16).  k_scale is a
+// factor of the scores here, so Q only changes from bf16 to f16.
 // What bounds it: the two warps' way from a landed tile to a widened one
-// (loads, conversion, stores, proxy fence) and the second box per page.  Timing
-// copies on eight extend requests (171 GFLOP): as built 241 us; nothing widened
-// 234; the scales not loaded either 181, which is the bf16 kernel's 180.
-// Slower: a fourth warpgroup for the widening (248 - 298 us; the softmax then
-// spills), one warp per tile (267), scales read by the widening warps from
-// global memory (335), scales by cp.async in the producer (255), four slots
-// widened in place (262).
+// (loads, conversion, stores, proxy fence).  Eight extend requests (171 GFLOP):
+// as built 230 us; a timing copy without the scales 224; that with nothing
+// widened 181, which is the bf16 kernel's 180.
+// Slower: the scales as a second TMA box per page (239), read by the widening
+// warps from global memory (335); a fourth warpgroup for the widening (248 -
+// 298: the softmax spills); one warp per tile (267); four slots widened in place
+// (262).
 #pragma once
 
 #include <cuda.h>
@@ -130,8 +130,6 @@ struct PrefillArgs {
     const uint8_t *bmask;         // block-sparse mask [num_seqs][bm_q][bm_k] over 128 x 128 blocks, or null
     int32_t bm_q, bm_k;
     int32_t max_q, max_k;         // the call's max_seqlen_q / max_seqlen_k (bounds of the device lengths)
-    CUtensorMap ksmap;            // 4-bit pools: the scales of kmap's and vmap's rows
-    CUtensorMap vsmap;
     Fp4Layout lay;                // 4-bit pools
     int32_t num_ctas;             // CTAs that run the work loop (the last of them resets sched);
                                   // 0: the count passed to prefill_body
@@ -326,6 +324,15 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __forceinline__ void cp_async_mbar_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The same as one of the arrivals the mbarrier was set up for.
+__device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// 16 bytes global -> shared, or 16 zeros (src is not read then).
+__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
 // Page size 1: warps that gather K/V rows (the producer and the two warps of
 // the control warpgroup that have no other role, fewer if the ring is
 // shorter), loads dealt out round robin.  bf16: each warp waits for its
@@ -411,7 +418,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], paged16 ? 1 : 32);
+            mbar_init(&full[s], paged16 ? (F4 ? 33 : 1) : 32);   // 4-bit: the boxes, and every lane's scales
             mbar_init(&empty[s], (F8 && !kInPlace) ? kConverters : 1);
         }
         if (F8) {
@@ -634,7 +641,6 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         if (lane == 0) {
             prefetch_tmap(&a.qmap);
             if (paged16) { prefetch_tmap(&a.kmap); prefetch_tmap(&a.vmap); }
-            if (F4 && paged16) { prefetch_tmap(&a.ksmap); prefetch_tmap(&a.vsmap); }
         }
         // K/V tiles are re-read by the other items of their request:
         // evict-last keeps them in L2 beside a concurrent stream (a decode
@@ -706,16 +712,22 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                     if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1)) { ok = false; break; }
                     uint8_t *dst = land(slot);
                     // lanes 0..7 each own one 16-token page of the tile
-                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kLTile);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], F4 ? kBN * D / 2 : S::kLTile);
                     __syncwarp();
-                    if constexpr (F4) {               // lanes 0-7 a page's codes, lanes 8-15 its scales
-                        const int s0 = __shfl_sync(0xffffffffu, slot0, lane & 7);
-                        if (lane < 8)
-                            tma_load_3d_hint(dst + S::code_off(lane * 16), (c & 1) ? &a.vmap : &a.kmap, codes_at(it.kvh), 0, s0,
-                                             &full[slot], kv_pol);
-                        else if (lane < 16)
-                            tma_load_3d_hint(dst + S::scale_off((lane - 8) * 16), (c & 1) ? &a.vsmap : &a.ksmap,
-                                             scales_at(it.kvh), 0, s0, &full[slot], kv_pol);
+                    if constexpr (F4) {
+                        // the codes, a box per page; the scales, 16 bytes a row
+                        if (lane < kBN / 16)
+                            tma_load_3d_hint(dst + S::code_off(lane * 16), (c & 1) ? &a.vmap : &a.kmap, codes_at(it.kvh), 0,
+                                             slot0, &full[slot], kv_pol);
+                        const uint8_t *src = ((c & 1) ? a.v_cache : a.k_cache) + scales_at(it.kvh);
+#pragma unroll
+                        for (int i = 0; i < kBN / 32; ++i) {
+                            const int s0 = __shfl_sync(0xffffffffu, slot0, 2 * i + (lane >> 4));
+                            const bool in = s0 < a.num_slots;          // else zeros
+                            cp_async16_zfill(dst + S::scale_off(32 * i + lane),
+                                             src + (in ? (int64_t)(s0 + (lane & 15)) * a.lay.row_bytes : 0), in);
+                        }
+                        cp_async_mbar_arrive_noinc(&full[slot]);
                     } else if (lane < kBN / 16) {
                         const CUtensorMap *map = (c & 1) ? &a.vmap : &a.kmap;
                         if constexpr (F8) {           // one (D bytes x 16 rows) box per page
@@ -1196,9 +1208,7 @@ cudaError_t prefill_setup(const pa_prefill_params &p, PrefillArgs &a, int &T) {
         a.lay = fp4_layout(p.num_kv_heads, p.head_dim);
         if (p.page_size == 16 &&
             (!make_map_fp4(&a.kmap, p.k_cache, a.lay.row_bytes, num_slots, p.head_dim / 2) ||
-             !make_map_fp4(&a.vmap, p.v_cache, a.lay.row_bytes, num_slots, p.head_dim / 2) ||
-             !make_map_fp4(&a.ksmap, p.k_cache, a.lay.row_bytes, num_slots, 16) ||
-             !make_map_fp4(&a.vsmap, p.v_cache, a.lay.row_bytes, num_slots, 16)))
+             !make_map_fp4(&a.vmap, p.v_cache, a.lay.row_bytes, num_slots, p.head_dim / 2)))
             return cudaErrorNotSupported;
     } else if (p.page_size == 16) {
         auto mk = f8 ? make_map_fp8 : make_map;
