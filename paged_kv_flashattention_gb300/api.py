@@ -77,6 +77,11 @@ PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_FP4 = 0, 1, 2
 _FP8_DTYPES = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
 
 
+def _need_at_least(t: torch.Tensor | None, name: str, n: int):
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{name} must hold at least {n} elements")
+
+
 def _kv_dtype(k_cache: torch.Tensor, v_cache: torch.Tensor, asked: int | None = None) -> int:
     """PA_KV_BF16 for bf16 pools, PA_KV_FP8_E4M3 for E4M3 codes (uint8 or
     torch.float8_e4m3fn); PA_KV_FP4 only where the caller asks for it (4-bit
@@ -560,6 +565,12 @@ def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k,
     if out is None:
         out = torch.empty_like(q)
     _need(out, "out", torch.bfloat16, dev)
+    if kvd == PA_KV_FP4:
+        _need_at_least(out, "out", q.numel())
+        if not page_table.shape[0] + 1 >= cu_seqlens_k.numel() == cu_seqlens_q.numel() >= 1:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k must hold num_seqs + 1 entries, page_table a row per sequence")
+        if lse is not None and lse.shape[1] < total_q:
+            raise ValueError("lse must be [Hq, >= total_q] with unit inner stride")
     if lse is not None:
         _need(lse, "lse", torch.float32, dev, contiguous=False)
         if lse.dim() != 2 or lse.shape[0] != Hq or lse.stride(1) != 1:
@@ -603,6 +614,12 @@ def _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_seqlen_k,
         raise ValueError("head_dim of q and the pool differ")
     if kvd == PA_KV_FP8_E4M3:
         _need_scales(k_scale, v_scale, Hkv, q.device)
+    if kvd == PA_KV_FP4:
+        _need_at_least(cache_seqlens, "cache_seqlens", B)
+        _need_at_least(out, "out", q.numel())
+        _need_at_least(lse, "lse", B * Hq)
+        if page_table.shape[0] < B:
+            raise ValueError("page_table must have a row per sequence")
     return _lib.DecodeParams(
         q=_ptr(q), k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), page_table=_ptr(page_table),
         page_table_stride=page_table.stride(0) if page_table is not None else 0,

@@ -39,17 +39,28 @@ class DecodeGraphRunner:
     Fixed device buffers: ``q`` [max_B, Hq, d] bf16, ``page_table`` [max_B,
     ncols] int32, ``cache_seqlens`` [max_B] int32, ``out`` and ``lse``, and one
     workspace sized for the largest bucket.  ``run(lengths)`` pads to the
-    bucket, uploads the lengths and replays; rows past the batch are dummies."""
+    bucket, uploads the lengths and replays; rows past the batch are dummies.
+    Pools of 4-bit rows take ``kv_dtype=PA_KV_FP4``, ``k_scale``, ``v_scale``
+    and ``head_dim`` (such a pool's shape does not tell it)."""
 
     def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor, *, num_q_heads: int,
                  max_seqlen_k: int, buckets=(1, 2, 4, 8, 16, 32, 64, 128, 256),
                  page_size: int | None = None, scale: float | None = None, kv_chunk: int = 0,
                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
-                 sliding_window: int = 0):
+                 sliding_window: int = 0, kv_dtype: int | None = None, head_dim: int | None = None):
         self.k_cache, self.v_cache = k_cache, v_cache
         self.k_scale, self.v_scale = k_scale, v_scale
         self.device = k_cache.device
-        num_pages, P, Hkv, d = api._pool_geometry(k_cache, v_cache, page_size)
+        self.kv_dtype = api._kv_dtype(k_cache, v_cache, kv_dtype)
+        if self.kv_dtype == api.PA_KV_FP4:
+            if head_dim is None:
+                raise ValueError("head_dim is required for 4-bit pools")
+            num_pages, P, Hkv, d = api._fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, int(head_dim),
+                                                     self.device)
+        else:
+            num_pages, P, Hkv, d = api._pool_geometry(k_cache, v_cache, page_size)
+            if head_dim is not None and head_dim != d:
+                raise ValueError("head_dim does not match the pool shape")
         self.page_size, self.head_dim, self.num_q_heads = P, d, int(num_q_heads)
         self.max_seqlen_k = int(max_seqlen_k)
         self.scale = float(1.0 / math.sqrt(d) if scale is None else scale)
@@ -65,7 +76,8 @@ class DecodeGraphRunner:
         self.out = torch.zeros((max_b, self.num_q_heads, d), dtype=torch.bfloat16, device=dev)
         self.lse = torch.zeros((max_b, self.num_q_heads), dtype=torch.float32, device=dev)
         need = api.decode_workspace_size((max_b, self.num_q_heads, d), k_cache, self.max_seqlen_k,
-                                         page_size=page_size, kv_chunk=self.kv_chunk)
+                                         page_size=page_size, kv_chunk=self.kv_chunk, kv_dtype=self.kv_dtype,
+                                         num_kv_heads=Hkv)
         self.workspace = torch.empty(max(16, need), dtype=torch.uint8, device=dev)
         self.lengths_host = torch.zeros(max_b, dtype=torch.int32, pin_memory=True)
         self.graphs: dict[int, torch.cuda.CUDAGraph] = {}
@@ -75,7 +87,8 @@ class DecodeGraphRunner:
         api.decode(self.q[:b], self.k_cache, self.v_cache, self.page_table[:b], self.cache_seqlens[:b],
                    self.max_seqlen_k, scale=self.scale, page_size=self.page_size, out=self.out[:b],
                    lse=self.lse[:b], workspace=self.workspace, kv_chunk=self.kv_chunk,
-                   k_scale=self.k_scale, v_scale=self.v_scale, sliding_window=self.sliding_window)
+                   k_scale=self.k_scale, v_scale=self.v_scale, sliding_window=self.sliding_window,
+                   kv_dtype=self.kv_dtype)
 
     def capture(self) -> None:
         """Capture one graph per bucket (the buffers hold empty requests, so

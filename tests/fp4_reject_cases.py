@@ -56,6 +56,28 @@ DECODE_CASES = [
                                  kv_chunk=1 << 16), UNSUPPORTED),
     ("no_sequences", dict(num_seqs=0), OK),
 ]
+PREFILL = dict(q=0x1000, k_cache=0x2000, v_cache=0x3000, page_table=0x4000, page_table_stride=64, total_q=100,
+               cu_seqlens_q=0x5000, cu_seqlens_k=0x6000, num_seqs=2, max_seqlen_q=64, max_seqlen_k=512, num_q_heads=8,
+               num_kv_heads=2, head_dim=128, page_size=16, num_pages=1000, causal=1, scale=0.1, out=0x7000, lse=None,
+               lse_stride=0, kv_dtype=2, k_scale=0x9000, v_scale=0x9100, scheduler=0xA000)
+PREFILL_CASES = [
+    ("no_scales", dict(v_scale=None), INVALID),
+    ("kv_dtype3", dict(kv_dtype=3), INVALID),
+    ("head_dim32", dict(head_dim=32), UNSUPPORTED),
+    ("page8", dict(page_size=8), UNSUPPORTED),
+    ("group3", dict(num_q_heads=6), UNSUPPORTED),
+    ("misaligned_pool", dict(k_cache=0x2008), INVALID),
+    ("table_stride", dict(page_table_stride=31), INVALID),
+    ("scale_zero", dict(scale=0.0), INVALID),
+    ("no_scheduler", dict(scheduler=None), INVALID),
+    ("no_tokens", dict(total_q=0), OK),
+]
+# One launch for prefill and decode takes bf16 and FP8 pools only.
+MIXED_CASES = [
+    ("both_4bit", {}, {}, UNSUPPORTED),
+    ("prefill_4bit", {}, dict(kv_dtype=1), UNSUPPORTED),
+    ("decode_4bit", dict(kv_dtype=1), {}, UNSUPPORTED),
+]
 BATCH = dict(cached_len=0x1000, extend_len=0x2000, num_seqs=4, max_seqlen_k=100, page_size=16, token_table=0x3000,
              token_table_stride=100, token_table_rows=8, table_idx=0x4000, free_pages=0x5000, num_free_pages=8, num_tokens=40,
              cu_seqlens_q=0x6000, cu_seqlens_k=0x7000, cache_seqlens=0x8000, positions=0x9000, slot_mapping=0xA000,
@@ -82,6 +104,8 @@ def expected():
     out.update({f"load/{i}": s for i, _, s in STORE_CASES})
     out.update({f"rope/{i}": s for i, _, s in ROPE_CASES})
     out.update({f"decode/{i}": s for i, _, s in DECODE_CASES})
+    out.update({f"prefill/{i}": s for i, _, s in PREFILL_CASES})
+    out.update({f"mixed/{i}": s for i, _, _, s in MIXED_CASES})
     out.update({f"batch/{i}": s for i, _, s in BATCH_CASES})
     return out
 
@@ -105,6 +129,12 @@ def run_all() -> dict:
     for i, kw, _ in DECODE_CASES:
         p = _lib.DecodeParams(**{**DECODE, **kw})
         rec(f"decode/{i}", lib.pa_decode(ctypes.byref(p), None))
+    for i, kw, _ in PREFILL_CASES:
+        p = _lib.PrefillParams(**{**PREFILL, **kw})
+        rec(f"prefill/{i}", lib.pa_prefill(ctypes.byref(p), None))
+    for i, kp, kd, _ in MIXED_CASES:
+        p, d = _lib.PrefillParams(**{**PREFILL, **kp}), _lib.DecodeParams(**{**DECODE, **kd})
+        rec(f"mixed/{i}", lib.pa_mixed_batch(ctypes.byref(p), ctypes.byref(d), None))
     for i, kw, _ in BATCH_CASES:
         p = _lib.BatchParams(**{**BATCH, **kw})
         rec(f"batch/{i}", lib.pa_build_batch(ctypes.byref(p), None))

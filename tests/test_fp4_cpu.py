@@ -119,3 +119,39 @@ def test_binding_decode_sizes():
         pa.decode_workspace_size(shape, kc, 4096, kv_dtype=pa.PA_KV_FP4)
     with pytest.raises(ValueError):
         pa.decode_workspace_size(shape, flat, 4096, kv_dtype=pa.PA_KV_FP4, num_kv_heads=8)
+
+
+def test_binding_attention_checks():
+    """Arrays that are too small for the call are refused before any launch."""
+    import paged_kv_flashattention_gb300 as pa
+    kc, vc = _pools(hkv=2, d=64)
+    g = torch.ones(2)
+    q = torch.zeros((3, 8, 64), dtype=torch.bfloat16)
+    pt, lens, cu = (torch.zeros(s, dtype=torch.int32) for s in ((3, 4), (3,), (4,)))
+    sched = torch.zeros(2, dtype=torch.int32)
+    kw = dict(k_scale=g, v_scale=g, kv_dtype=pa.PA_KV_FP4)
+
+    def refused(fn, *a, error=ValueError, **over):
+        with pytest.raises(error):
+            fn(*a, **{**kw, **over})
+
+    for fn in (pa.decode, pa.decode_noalloc):
+        refused(fn, q, kc, vc, pt[:2], lens, 64)
+        refused(fn, q, kc, vc, pt, lens[:2], 64)
+        refused(fn, q, kc, vc, pt, lens, 64, out=q[:2])
+        refused(fn, q, kc, vc, pt, lens, 64, lse=torch.zeros((2, 8)))
+        refused(fn, q, kc, vc, pt, lens, 64, k_scale=None)
+        refused(fn, q, kc, vc, pt, lens, 64, k_scale=g[:1], v_scale=g[:1])    # rows of another length
+        refused(fn, q, kc, vc, pt, lens, 64, page_size=1)
+        refused(fn, q[..., :32].contiguous(), kc, vc, pt, lens, 64)
+        refused(fn, q, kc.view(torch.int8), vc, pt, lens, 64, error=TypeError)
+    pre = (q, kc, vc, pt, cu, cu, 3, 64)
+    refused(pa.prefill, *pre[:3], pt[:2], *pre[4:], scheduler=sched)
+    refused(pa.prefill, *pre[:5], cu[:3], *pre[6:], scheduler=sched)
+    refused(pa.prefill, *pre, scheduler=sched, out=q[:2])
+    refused(pa.prefill, *pre, scheduler=sched, lse=torch.zeros((8, 2)))
+    refused(pa.prefill, *pre, scheduler=sched, v_scale=g[:1])
+    refused(pa.prefill, *pre, scheduler=sched[:1])
+    refused(pa.DecodeGraphRunner, kc, vc, num_q_heads=8, max_seqlen_k=64)                         # no head_dim
+    refused(pa.DecodeGraphRunner, kc, vc, num_q_heads=8, max_seqlen_k=64, head_dim=64, v_scale=None)
+    refused(pa.DecodeGraphRunner, kc, vc, num_q_heads=8, max_seqlen_k=64, head_dim=128)

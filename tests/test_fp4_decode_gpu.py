@@ -245,3 +245,33 @@ def test_captured_with_new_lengths(cuda_device):
     ref = fp4.attention(W.bf16_bits_to_f32(p.q), f.kr, f.vr, pt, np.arange(10), np.concatenate([[0], np.cumsum(short)]),
                         num_kv_heads=8, page_size=16, k_scale=f.ks, v_scale=f.vs, scale=p.scale)
     check(runs[1][2], runs[1][3], ref, "captured, shorter")
+
+
+def test_graph_runner(cuda_device):
+    """Bucketed graphs over 4-bit pools: real rows right, dummies empty, and
+    the same graph after the lengths change."""
+    import paged_kv_flashattention_gb300 as pa
+    rng = np.random.default_rng(45)
+    L = rng.integers(1, 700, 20).astype(np.int32)
+    p = W.small_problem(45, L - 1, np.ones_like(L), num_q_heads=16, num_kv_heads=4, head_dim=64)
+    f = FP4Problem(p, cuda_device, 46)
+    m = f.meta
+    ref = f.oracle()
+    runner = pa.DecodeGraphRunner(f.k_cache, f.v_cache, num_q_heads=16, max_seqlen_k=m.max_seqlen_k, buckets=(1, 8, 32),
+                                  scale=p.scale, k_scale=f.k_scale, v_scale=f.v_scale, kv_dtype=pa.PA_KV_FP4, head_dim=64)
+    runner.capture()
+    for B in (3, 20, 1, 8):
+        out, lse = runner.run(L[:B], q=f.q[:B], page_table=m.page_table[:B])
+        torch.cuda.synchronize()
+        check(out, lse, tuple(x[:B] for x in ref), f"graph B={B}")
+        bucket = pa.bucket_for(runner.buckets, B)
+        assert torch.count_nonzero(runner.out[B:bucket]).item() == 0
+        assert torch.all(torch.isneginf(runner.lse[B:bucket]))
+    short = (L * rng.uniform(0.1, 1.0, 20)).astype(np.int32).clip(1)
+    out, lse = runner.run(short, q=f.q, page_table=m.page_table)
+    torch.cuda.synchronize()
+    from oracle_pins import _meta
+    _, _, _, pt = _meta(p)
+    ref = fp4.attention(W.bf16_bits_to_f32(p.q), f.kr, f.vr, pt, np.arange(21), np.concatenate([[0], np.cumsum(short)]),
+                        num_kv_heads=4, page_size=16, k_scale=f.ks, v_scale=f.vs, scale=p.scale)
+    check(out, lse, ref, "graph, shorter")
