@@ -580,10 +580,13 @@ def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k,
         if block_mask.dim() != 3 or block_mask.shape[0] != cu_seqlens_q.numel() - 1:
             raise ValueError("block_mask must be [num_seqs, q_blocks, k_blocks]")
     if scheduler is None:
-        scheduler = prefill_scheduler(dev)
-    _need(scheduler, "scheduler", torch.int32, dev)
-    if scheduler.numel() < sched_ints:
-        raise ValueError(f"scheduler must hold {sched_ints} int32")
+        scheduler = _sched_arrays.get((dev.index, _stream(q)))
+        if scheduler is None:
+            scheduler = prefill_scheduler(dev)
+    else:
+        _need(scheduler, "scheduler", torch.int32, dev)
+        if scheduler.numel() < sched_ints:
+            raise ValueError(f"scheduler must hold {sched_ints} int32")
     p = _lib.PrefillParams(
         q=_ptr(q), k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), page_table=_ptr(page_table),
         page_table_stride=page_table.stride(0), total_q=total_q, cu_seqlens_q=_ptr(cu_seqlens_q),
