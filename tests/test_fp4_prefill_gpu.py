@@ -43,6 +43,23 @@ def test_extend_partial_hit(cuda_device, page):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("extra", [0, 128, 5000, 300000])
+def test_length_bound_above_the_lengths(cuda_device, extra):
+    """max_seqlen_k is only a bound: the same bits whichever order of the work
+    it leads to, requests without keys or rows among them."""
+    p = W.small_problem(62, [0, 700, 0, 128, 127, 1, 0], [300, 128, 0, 256, 257, 1, 64], num_q_heads=8, num_kv_heads=4,
+                        head_dim=128)
+    f = FP4Problem(p, cuda_device, 63)
+    m = f.meta
+    check(*f.prefill(), f.oracle(), "exact bound")
+    cols = -(-(m.max_seqlen_k + extra) // 16)
+    wide = torch.full((7, cols), 1 << 30, dtype=torch.int32, device=cuda_device)
+    wide[:, :m.page_table.shape[1]] = m.page_table
+    m.page_table, m.max_seqlen_k = wide, m.max_seqlen_k + extra
+    for kw in (dict(), dict(max_ctas=3)):
+        check(*f.prefill(**kw), f.oracle(), f"bound + {extra} {kw}")
+
+
 @pytest.mark.parametrize("page", [1, 16])
 @pytest.mark.parametrize("window", [1, 17, 200])
 @pytest.mark.parametrize("hq,hkv,d", [(16, 8, 128), (4, 4, 64)])
