@@ -327,7 +327,7 @@ cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cud
     if (e != cudaSuccess) return e;
     return launch_lse_combine(a.o_part, a.lse_part, nullptr, a.ws_header, a.ws_prefix, a.head_groups,
                               g * plan.heads_per_cta, p.num_q_heads, p.num_seqs * p.num_q_heads,
-                              plan.max_splits, p.head_dim, p.out, p.lse, stream);
+                              plan.max_splits, p.head_dim, p.out, p.lse, stream, p.overlap_previous != 0);
 }
 
 cudaError_t launch_lse_combine(const float *o_partial, const float *lse_partial,
@@ -335,7 +335,7 @@ cudaError_t launch_lse_combine(const float *o_partial, const float *lse_partial,
                                const int32_t *seg_prefix, int32_t head_groups,
                                int32_t heads_per_group, int32_t heads_per_seq, int32_t num_rows,
                                int32_t max_splits, int32_t head_dim, void *out, float *lse_out,
-                               cudaStream_t stream) {
+                               cudaStream_t stream, bool after_all) {
     if (num_rows == 0) return cudaSuccess;
     const int rows_per_block = 8;
     const int blocks = (num_rows + rows_per_block - 1) / rows_per_block;
@@ -347,9 +347,12 @@ cudaError_t launch_lse_combine(const float *o_partial, const float *lse_partial,
     cudaLaunchAttribute attr[1];
     // after the split kernel (seg_header given) the combine is its
     // programmatic dependent: its launch is prepared while the split kernel's
-    // last CTAs finish, and griddepcontrol.wait holds it until they have
+    // last CTAs finish, and griddepcontrol.wait holds it until they have; but
+    // a split kernel that overlaps the kernel before it says nothing about that
+    // one, so the combine then waits for all of the stream's earlier work
+    // (after_all), and a dependent launch of the next call with it
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = seg_header != nullptr ? 1 : 0;
+    attr[0].val.programmaticStreamSerializationAllowed = seg_header != nullptr && !after_all ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (head_dim == 64)

@@ -589,9 +589,17 @@ cudaError_t launch_fp4_combine(const Fp4DecodeArgs &a, const pa_decode_params &p
     constexpr int W = kCombineThreads / 32;
     auto kern = p.head_dim == 64 ? (share ? fp4_combine_kernel<64, W> : fp4_combine_kernel<64, 1>)
                                  : (share ? fp4_combine_kernel<128, W> : fp4_combine_kernel<128, 1>);
-    return launch_after(kern, (unsigned)((rows + per_block - 1) / per_block), kCombineThreads, 0, stream, a.o_part,
-                        a.lse_part, a.ws_header, a.ws_prefix, a.head_groups, heads_per_group, p.num_q_heads, rows,
-                        plan.max_splits, static_cast<__nv_bfloat16 *>(p.out), p.lse);
+    const unsigned blocks = (unsigned)((rows + per_block - 1) / per_block);
+    auto *out = static_cast<__nv_bfloat16 *>(p.out);
+    if (a.overlap_previous) {
+        // the split kernel did not wait for the kernel before it: an ordinary
+        // launch waits for both
+        kern<<<blocks, kCombineThreads, 0, stream>>>(a.o_part, a.lse_part, a.ws_header, a.ws_prefix, a.head_groups,
+                                                     heads_per_group, p.num_q_heads, rows, plan.max_splits, out, p.lse);
+        return cudaGetLastError();
+    }
+    return launch_after(kern, blocks, kCombineThreads, 0, stream, a.o_part, a.lse_part, a.ws_header, a.ws_prefix,
+                        a.head_groups, heads_per_group, p.num_q_heads, rows, plan.max_splits, out, p.lse);
 }
 
 template <int D, int HPC>

@@ -56,7 +56,7 @@ cudaError_t launch_lse_combine(const float *o_partial, const float *lse_partial,
                                const int32_t *seg_prefix, int32_t head_groups,
                                int32_t heads_per_group, int32_t heads_per_seq, int32_t num_rows,
                                int32_t max_splits, int32_t head_dim, void *out, float *lse_out,
-                               cudaStream_t stream);
+                               cudaStream_t stream, bool after_all = false);
 
 cudaError_t launch_prefill(const pa_prefill_params &p, cudaStream_t stream);
 cudaError_t launch_prefill_fp4(const pa_prefill_params &p, cudaStream_t stream);

@@ -2,7 +2,9 @@
 // while the kernel before it in the stream drains, and calls after_previous()
 // before it touches memory: that returns once the earlier grid has completed
 // and its writes are visible.  Every thread that can exit calls it, so "this
-// grid has completed" implies the same of all before it.  Measured on the small
+// grid has completed" implies the same of all before it; a decode's split kernel
+// that overlaps the kernel before it does not, and its combine is launched
+// ordinarily, after both.  Measured on the small
 // calls: 0.3 to 0.6 us less per kernel.  Letting the next kernel's CTAs onto the
 // SMs at the start of this one (griddepcontrol.launch_dependents) costs more
 // than it gives: 64 decode sequences 24.2 -> 26.3 us, a batch plan 12.6 -> 14.1.

@@ -62,14 +62,19 @@
 // own and the same two warps widen them into an f16 slot: E2M1 to f16 by the
 // hardware conversion, times the block's scale (exact in f16).  k_scale is a
 // factor of the scores here, so Q only changes from bf16 to f16.
-// What bounds it: the two warps' way from a landed tile to a widened one
-// (loads, conversion, stores, proxy fence).  Eight extend requests (171 GFLOP):
-// as built 230 us; a timing copy without the scales 224; that with nothing
-// widened 181, which is the bf16 kernel's 180.
-// Slower: the scales as a second TMA box per page (239), read by the widening
-// warps from global memory (335); a fourth warpgroup for the widening (248 -
-// 298: the softmax spills); one warp per tile (267); four slots widened in place
-// (262).
+// What bounds it: the softmax chain of the bf16 kernel, and beside it the two
+// warps' way from a landed tile to a widened one (about 1500 clocks a tile, of
+// a period of 2000).  Eight extend requests over prefixes of up to 4096 keys (171
+// GFLOP): as built 200 us; timing copies without the conversion 190, without
+// the product with the scale 185, without the reads of the landed tile 190,
+// with nothing widened 179.
+// Slower, each against the kernel it was tried on (241 to 200 us): the scales as a
+// second TMA box per page (+8) or read by the widening warps from global memory
+// (+94); a fourth warpgroup for the widening (+7 to +57: the softmax spills); one
+// warp per tile (+6); four slots widened in place (+1); the landed slot freed
+// before the conversion (+11) or waiting for the free f16 slot only after the reads
+// (+3); reading tile c + 1 before converting tile c (+104); a rolled loop over a
+// tile's chunks (+14).
 #pragma once
 
 #include <cuda.h>

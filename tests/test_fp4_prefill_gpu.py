@@ -120,6 +120,49 @@ def test_decode_equals_prefill_of_one_token(cuda_device):
         check(out, lse, ref, "one token")
 
 
+@pytest.mark.parametrize("fp4", [False, True])
+def test_next_call_waits_for_an_overlapped_prefill(cuda_device, fp4):
+    """A decode that runs beside a longer prefill, then calls that rewrite what
+    the prefill reads (its page table; 4-bit rows): they come after it."""
+    import paged_kv_flashattention_gb300 as pa
+    from pa_harness import bf16_dev
+    dev = cuda_device
+    p = W.small_problem(98, [3000, 2000], [600, 500], num_q_heads=16, num_kv_heads=4, head_dim=128)
+    f = FP4Problem(p, dev, 99)
+    m = f.meta
+    kw = dict(scale=p.scale)
+    kc, vc = f.k_cache, f.v_cache
+    if fp4:
+        kw.update(k_scale=f.k_scale, v_scale=f.v_scale, kv_dtype=pa.PA_KV_FP4)
+    else:
+        kc, vc = (torch.randn((p.num_pages, 16, 4, 128), device=dev).to(torch.bfloat16) for _ in range(2))
+    args = (m.cu_seqlens_q, m.cu_seqlens_k, m.max_seqlen_q, m.max_seqlen_k)
+    want = pa.prefill(f.q, kc, vc, m.page_table, *args, **kw)
+    qd = bf16_dev(W.normal_bf16(np.random.default_rng(1), (2, 16, 128)), dev)
+    lens = torch.tensor([40, 70], dtype=torch.int32, device=dev)
+    table = m.page_table.clone()
+    ws = torch.empty(max(16, pa.decode_workspace_size(qd.shape, kc, 80, **({"kv_dtype": pa.PA_KV_FP4, "num_kv_heads": 4}
+                                                                         if fp4 else {}))), dtype=torch.uint8, device=dev)
+    # a plan whose page table is the one the prefill reads
+    pl = pa.BatchPlanner(dev, 2, 2, m.max_seqlen_k, 16)
+    pl.page_table[:2, :table.shape[1]] = table
+    tt = torch.zeros((2, m.max_seqlen_k), dtype=torch.int32, device=dev)
+    idx = torch.arange(2, dtype=torch.int32, device=dev)
+    one = torch.ones(2, dtype=torch.int32, device=dev)
+    slots = torch.arange(64, dtype=torch.int32, device=dev)
+    k = torch.ones((64, 4, 128), dtype=torch.bfloat16, device=dev)
+    out, out_d = torch.empty_like(f.q), torch.empty_like(qd)
+    torch.cuda.synchronize()
+    pa.prefill(f.q, kc, vc, pl.page_table[:2], *args, out=out, max_ctas=4, **kw)
+    pa.decode(qd, kc, vc, table, lens, 80, out=out_d, workspace=ws, overlap_previous=True, max_ctas=64, **kw)
+    pl.build(one * (m.max_seqlen_k - 1), one, tt, idx)
+    if fp4:
+        pa.store_kv_fp4(k, k, slots, kc, vc, f.k_scale, f.v_scale)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert int(pl.page_table[:2, :table.shape[1]].abs().sum()) == 0, "the plan was built"
+
+
 @pytest.mark.parametrize("page,hq,hkv,d", [(16, 32, 8, 128), (1, 8, 2, 64)])
 def test_serving_over_a_4bit_cache(cuda_device, page, hq, hkv, d):
     """The operators together: the plan gives new prompts their pages, the
