@@ -65,16 +65,16 @@
 // What bounds it: the softmax chain of the bf16 kernel, and beside it the two
 // warps' way from a landed tile to a widened one (about 1500 clocks a tile, of
 // a period of 2000).  Eight extend requests over prefixes of up to 4096 keys (171
-// GFLOP): as built 200 us; timing copies without the conversion 190, without
-// the product with the scale 185, without the reads of the landed tile 190,
-// with nothing widened 179.
-// Slower, each against the kernel it was tried on (241 to 200 us): the scales as a
+// GFLOP): as built 191 us.  Timing copies of an earlier state, 200 us: without
+// the conversion 190, without the product with the scale 185, without the reads of
+// the landed tile 190, with nothing widened 179.
+// Slower, each against the kernel it was tried on (241 to 191 us): the scales as a
 // second TMA box per page (+8) or read by the widening warps from global memory
 // (+94); a fourth warpgroup for the widening (+7 to +57: the softmax spills); one
 // warp per tile (+6); four slots widened in place (+1); the landed slot freed
-// before the conversion (+11) or waiting for the free f16 slot only after the reads
+// before the conversion (+11) or the free f16 slot awaited only after the reads
 // (+3); reading tile c + 1 before converting tile c (+104); a rolled loop over a
-// tile's chunks (+14).
+// tile's chunks (+14); an item's first K tile widened before its Q (+23).
 #pragma once
 
 #include <cuda.h>
@@ -315,19 +315,25 @@ struct PrefillSmem {
     static constexpr int kLTile = F4 ? kBN * (D / 2 + 16) : F8 ? kTileBytes / 2 : kTileBytes;   // a tile as loaded
     static constexpr int kQ = 0;                           // T query tiles
     static constexpr int kRing = T * kTileBytes;           // ring of loaded tiles
-    static constexpr int kStageBytes = 4 * T * 4096;      // 32 rows x 64 columns bf16 per warp
+    // 4-bit: columns of output staged at a time; 64 200 us, 32 191, none (each
+    // thread its own row) 194, and 78, 75 and 82 on sixteen requests of 512 rows.
+    static constexpr int kStageCols = F4 ? 32 : 64;
+    static constexpr int kStageBytes = 4 * T * 64 * kStageCols;      // 32 rows x kStageCols columns bf16 per warp
     static constexpr int kAvail = 232448 - 1024 - kRing - kStageBytes - 512;
     // FP8, d = 128 (in place): an E4M3 tile lands in the upper half of its f16
     // slot (row r's 128 codes where the f16 row r of the upper 64 columns
     // goes) and is widened where it lies, so the slots serve both rings.
     // FP8, d = 64: a ring of widened f16 tiles (2..4 slots) and a separate
     // ring of loaded tiles from the rest.
-    // 4-bit: 3 to 6 widened tiles, the rest loaded ones (10 KiB at d = 128).
+    // 4-bit: three widened tiles, the rest loaded ones (10 KiB at d = 128).  Four
+    // widened tiles, in the space of the output staging, are slower (eight
+    // extend requests 216 us against 194 with three, both without staging; one
+    // head per item 110 against 106).
     static constexpr bool kInPlace = F8 && !F4 && D == 128;
     static constexpr int kFitTiles = kAvail / kTileBytes;
     static constexpr int kCSlotsFit = (kAvail / 2) / kTileBytes;
     static constexpr int kCSlots = !F8 ? 0
-                                 : F4 ? (D == 64 ? 6 : T == 2 ? 3 : 4)
+                                 : F4 ? 3
                                  : kInPlace ? (kFitTiles > 8 ? 8 : kFitTiles)
                                             : (kCSlotsFit > 4 ? 4 : (kCSlotsFit < 2 ? 2 : kCSlotsFit));
     static constexpr int kSlotsFit = kInPlace ? kCSlots : (kAvail - kCSlots * kTileBytes) / kLTile;
@@ -1142,43 +1148,47 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             const int64_t tok = (int64_t)it.q0 + qi;
             const int h = it.h0 + k;
             const float inv = (l_run > 0.f ? 1.f / l_run : 0.f) * (F8 ? __ldg(a.v_scale + it.kvh) : 1.f);
-            // Through the warp's staging buffer, 64 columns at a time: each
+            // Through the warp's staging buffer, 64 (4-bit: 32) columns at a time: each
             // thread writes its row (16-byte pieces, XOR-swizzled by row so
             // the writes and reads below are free of bank conflicts), then the
-            // warp stores 4 rows x 128 contiguous bytes per instruction.
-            uint8_t *stage = smem + S::kStage + warp * 4096;
+            // warp stores 4 rows x 128 (8 x 64) contiguous bytes per instruction.
+            constexpr int kCols = S::kStageCols;
+            uint8_t *stage = smem + S::kStage + warp * (64 * kCols);
+            // row r's piece u lies at piece u ^ swz(r)
+            auto swz = [](int r) { return kCols == 64 ? r & 7 : (r >> 1) & 3; };
             const int rw = lane;                                   // row within the warp's 32
 #pragma unroll 1
-            for (int half = 0; half < D / 64; ++half) {
-                // both 32-column loads in flight before one wait
-                uint32_t orr[64];
+            for (int part = 0; part < D / kCols; ++part) {
+                // all 32-column loads in flight before one wait
+                uint32_t orr[kCols];
                 if (n_kv > 0) {                       // CTA-uniform
-                    tmem_ld32(o_tm + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&orr[0]));
-                    tmem_ld32(o_tm + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&orr[32]));
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 32)
+                        tmem_ld32(o_tm + part * kCols + e, *reinterpret_cast<uint32_t(*)[32]>(&orr[e]));
                     tmem_wait_ld();
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) orr[e] = 0u;
+                    for (int e = 0; e < kCols; ++e) orr[e] = 0u;
                 }
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
+                for (int u = 0; u < kCols / 8; ++u) {
                     uint4 w;
                     w.x = pack_bf16x2(__uint_as_float(orr[8 * u + 0]) * inv, __uint_as_float(orr[8 * u + 1]) * inv);
                     w.y = pack_bf16x2(__uint_as_float(orr[8 * u + 2]) * inv, __uint_as_float(orr[8 * u + 3]) * inv);
                     w.z = pack_bf16x2(__uint_as_float(orr[8 * u + 4]) * inv, __uint_as_float(orr[8 * u + 5]) * inv);
                     w.w = pack_bf16x2(__uint_as_float(orr[8 * u + 6]) * inv, __uint_as_float(orr[8 * u + 7]) * inv);
-                    *reinterpret_cast<uint4 *>(stage + rw * 128 + ((u ^ (rw & 7)) * 16)) = w;
+                    *reinterpret_cast<uint4 *>(stage + rw * (2 * kCols) + ((u ^ swz(rw)) * 16)) = w;
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int rr = i * 4 + (lane >> 3);
-                    const int q = lane & 7;
-                    const uint4 val = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((q ^ (rr & 7)) * 16));
+                for (int i = 0; i < kCols / 8; ++i) {
+                    const int rr = i * (256 / kCols) + lane / (kCols / 8);
+                    const int q = lane % (kCols / 8);
+                    const uint4 val = *reinterpret_cast<const uint4 *>(stage + rr * (2 * kCols) + ((q ^ swz(rr)) * 16));
                     const int rt = (warp & 3) * 32 + rr;                // row within the tile
                     if (rt < it.rows_here) {
                         const int64_t t = (int64_t)it.q0 + it.tile * kBM + rt;
-                        *reinterpret_cast<uint4 *>(a.out + (t * a.num_q_heads + h) * D + half * 64 + q * 8) = val;
+                        *reinterpret_cast<uint4 *>(a.out + (t * a.num_q_heads + h) * D + part * kCols + q * 8) = val;
                     }
                 }
                 __syncwarp();
