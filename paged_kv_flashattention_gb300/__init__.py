@@ -1,8 +1,8 @@
 """Paged-KV exact attention for GB300 (sm_103a).
 
 A small C-ABI library (``libpa.so``, declared in ``include/pa.h``) with
-hand-written CUDA kernels for the KV-cache store (bf16, or FP8 E4M3 with
-per-head scales), varlen causal prefill / extend attention over a page table,
+hand-written CUDA kernels for the KV-cache store (bf16, FP8 E4M3 with
+per-head scales, or 4-bit rows with block scales), the batch's metadata, varlen causal prefill / extend attention over a page table,
 split-KV decode and the log-sum-exp combine, and both attention halves of a
 mixed batch in one launch; this package is its thin torch binding.  PyTorch
 provides device memory and streams only.

@@ -15,9 +15,9 @@
 // loads a token's cos / sin once for all its heads while a short one still
 // spreads over the GPU.  The rotary gives a lane both members of its eight
 // pairs; keys then change places by shuffles for the quantiser.
-// Bound: long batches by HBM and the latency of the loads in flight (rotary,
-// 8192 tokens: 4.6 TB/s; store 3.1, most of it the divisions; load 4.3), short
-// ones by launch latency (2 to 4 us).
+// Bound: long batches by issue and the latency of the loads in flight (8192
+// tokens: rotary 4.7 TB/s, store 3.6, load 4.4), short ones by launch latency (2
+// to 4 us).
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -54,6 +54,21 @@ struct Fp4StoreArgs {
     int32_t upw;                  // units a warp takes
 };
 
+// Two products, two fused multiply-adds, each rounded on its own.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, t;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 t, x, y, z;\n\tmov.b64 {%0, %1}, t;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 // Codes (8 bytes) and scale of a block of 16 bf16.
 __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], float g, uint2 &codes, uint32_t &scale) {
     // magnitudes of bf16 compare like the integers of their bits
@@ -65,7 +80,11 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], float g, uint
     scale = 0x7f;                                    // NaN
     if (m > 0x7f80u) return;                         // a NaN in the block
     const float amax = __uint_as_float(m << 16);
-    const float want = __fdiv_rn(__fdiv_rn(amax, g), 6.f);
+    // RN(x / 6) by the division below (1/6 is rounded correctly); beyond 2688 the
+    // scale is 448 anyway
+    const float most = fminf(__fdiv_rn(amax, g), 65536.f);
+    const float sixth = 1.f / 6.f, near6 = __fmul_rn(most, sixth);
+    const float want = __fmaf_rn(__fmaf_rn(near6, 6.f, -most), -sixth, near6);
     uint16_t sc;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sc) : "f"(0.f), "f"(want));
     scale = sc & 0xffu;
@@ -83,25 +102,28 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], float g, uint
     // Blocks near the ends of fp32's range take the plain division.
     const float r = __frcp_rn(step);
     const bool normal = step > 1e-30f && step < 1e30f && amax < 1e30f;
-    uint32_t c[2] = {0u, 0u};
+    uint32_t c[2];
+    const float2 r2 = make_float2(r, r), nr2 = make_float2(-r, -r), step2 = make_float2(step, step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float lo = bf16lo(w[i]), hi = bf16hi(w[i]);
-        float a, b;
-        if (normal) {
-            a = __fmul_rn(lo, r);
-            b = __fmul_rn(hi, r);
-            // (written with -e, which keeps the sign of a zero)
-            a = __fmaf_rn(-__fmaf_rn(a, step, -lo), r, a);
-            b = __fmaf_rn(-__fmaf_rn(b, step, -hi), r, b);
-        } else {
-            a = __fdiv_rn(lo, step);
-            b = __fdiv_rn(hi, step);
+    for (int h = 0; h < 2; ++h) {
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = make_float2(bf16lo(w[4 * h + i]), bf16hi(w[4 * h + i]));
+            if (normal) {
+                const float2 a = mul2(v, r2);
+                // (the negative remainder times -r keeps the sign of a zero)
+                x[i] = fma2(fma2(a, step2, make_float2(-v.x, -v.y)), nr2, a);
+            } else {
+                x[i] = make_float2(__fdiv_rn(v.x, step), __fdiv_rn(v.y, step));
+            }
         }
-        uint32_t two;
-        asm("{\n\t.reg .b8 t;\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-            "mov.b16 x, {t, t};\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(two) : "f"(b), "f"(a));
-        c[i >> 2] |= (two & 0xffu) << (8 * (i & 3));
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+            "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+            : "=r"(c[h])
+            : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
     }
     codes = make_uint2(c[0], c[1]);
 }
@@ -191,11 +213,11 @@ __device__ __forceinline__ void regroup16(const Fp4StoreArgs &a, int first, int 
 }
 
 // UG: units whose loads go out together.  The rotary on 8192 tokens (32 + 8
-// heads of 128, 178 MB): two units at 64 registers 38.8 us, at 80 44.0, at 106
-// 53.5; one unit at 64 41.8; four at 123 50.9.  When a lane held 16 consecutive
+// heads of 128, 178 MB): two units at 64 registers 38.0 us; earlier, when that
+// was 38.8, at 80 44.0, at 106 53.5, one unit at 64 41.8, four at 123 50.9.  When a lane held 16 consecutive
 // elements and fetched their partners through memory it was 63 us, by shuffles
-// 49.  The plain store of the same tokens (43 MB) is 14 us with one unit, 15 to
-// 16 with more.
+// 49.  The plain store of the same tokens (43 MB) is 12.1 us with one unit, 12.4
+// with two; 14.0 before its products were packed by two.
 template <int D, bool ROPE, int UG>
 __global__ void __launch_bounds__(256, 4) fp4_store_kernel(const Fp4StoreArgs a) {
     constexpr int kLanes = D / 16;                   // lanes of a head
