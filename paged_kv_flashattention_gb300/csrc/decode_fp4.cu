@@ -6,7 +6,9 @@
 //   - The list counts units of 16 keys that start at multiples of 16 in their
 //     sequence, so that a unit never straddles two 16-token pages: its rows are
 //     one contiguous run of the pool when a row is one head group, and a unit
-//     is two bulk copies (K, V) instead of 32.
+//     is two bulk copies (K, V) instead of 32; with more groups it is two
+//     tensor-map boxes of 16 rows (21 sequences, 103,000 keys, 16 heads of 128:
+//     56 us, by rows 88).
 //   - A CTA takes one head group (gs KV heads, one consumer warp each).
 //   - The codes are widened in registers: E2M1 to f16 by the hardware
 //     conversion, times the block's E4M3 scale (exact in f16, fp4.cuh), and
@@ -41,12 +43,14 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "decode_impl.cuh"
 #include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pdl.cuh"
+#include "tensor_map.cuh"
 
 namespace pa {
 
@@ -83,6 +87,16 @@ struct Fp4DecodeArgs {
     int32_t *ws_header;           // [0] = T, in units
     int32_t *ws_prefix;           // [B+1] exclusive prefix of the sequences' units
 };
+
+// Page size 16 and more than one head group (BOX): the pools as rows of 32-bit
+// words.  An instantiation of its own: the boxes in the code of all calls cost
+// 256 contexts up to 32768 keys 445 us instead of 423.
+struct Fp4Maps {
+    CUtensorMap k, v;
+};
+struct Fp4NoMaps {};
+template <bool BOX>
+using Fp4MapsOf = std::conditional_t<BOX, Fp4Maps, Fp4NoMaps>;
 
 template <int D, int HPC>
 struct Fp4Smem {
@@ -164,13 +178,20 @@ struct UnitWalk {
     }
 };
 
+// A box of 16 rows of one head group; x in 32-bit words (a multiple of 4).
+__device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map, int x, int row, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(row), "r"(smem_u32(bar)) : "memory");
+}
+
 // The producer warp: units [g0, g1) of the list into the ring.
-template <int D, int HPC>
-__device__ void fp4_produce(const Fp4DecodeArgs &a, const int32_t *prefix, int T, int g0, int g1,
+template <int D, int HPC, bool BOX>
+__device__ void fp4_produce(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, const int32_t *prefix, int T, int g0, int g1,
                             uint8_t *ring, uint64_t *full, uint64_t *empty, int lane) {
     using S = Fp4Smem<D, HPC>;
     const bool paged = a.page_size == 16;
-    const bool run = paged && a.head_groups == 1;    // a unit is one contiguous run of rows
+    const bool run = !BOX && paged;                  // one head group: a unit is one contiguous run of rows
     int ctr = 0;
     UnitWalk walk{prefix, a.num_seqs, a.head_groups, T, g0, g1};
     int b, hg, u0, u1, split, span;
@@ -198,15 +219,20 @@ __device__ void fp4_produce(const Fp4DecodeArgs &a, const int32_t *prefix, int T
             const int n0 = max(lo - key, 0), n1 = min(L - key, kUnit);   // keys of the unit that are seen
             const int slot = ctr % S::kStages, round = ctr / S::kStages;
             if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1)) return;
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2u * (n1 - n0) * S::kRow);
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2u * (BOX ? kUnit : n1 - n0) * S::kRow);   // a box is loaded whole
             __syncwarp();
             int64_t page = __shfl_sync(0xffffffffu, now, paged ? i : (lane & 15));
             const int tok = lane & 15;
-            const bool mine = run ? (lane & 15) == 0 : (tok >= n0 && tok < n1);
+            const bool mine = BOX || run ? (lane & 15) == 0 : (tok >= n0 && tok < n1);
             if (mine) {
                 if (page < 0 || page >= a.num_pages) {           // never read outside the pool
                     raise_error(PA_DEVERR_PAGE_RANGE);
                     page = 0;
+                }
+                if constexpr (BOX) {
+                    tma_load_rows(ring + slot * S::kStage + (lane >> 4) * (kUnit * S::kRow), lane < 16 ? &maps.k : &maps.v,
+                                  hg * (S::kRow / 4), (int)page * 16, &full[slot]);
+                    continue;
                 }
                 const int at = run ? n0 : tok;
                 const int64_t row = paged ? page * 16 + at : page;
@@ -479,8 +505,9 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T
     }
 }
 
-template <int D, int HPC>
-__global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas) decode_fp4_kernel(const Fp4DecodeArgs a) {
+template <int D, int HPC, bool BOX>
+__global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas)
+decode_fp4_kernel(const Fp4DecodeArgs a, const __grid_constant__ Fp4MapsOf<BOX> maps) {
     using S = Fp4Smem<D, HPC>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kRing);
@@ -505,7 +532,7 @@ __global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas) decode
         if (threadIdx.x == 0) a.ws_header[0] = T;
     }
     const int g0 = (int)min((int64_t)blockIdx.x * T, (int64_t)total), g1 = min(total - g0, T) + g0;
-    if (warp == HPC) fp4_produce<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, lane);
+    if (warp == HPC) fp4_produce<D, HPC, BOX>(a, maps, prefix, T, g0, g1, smem, full, empty, lane);
     else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
 }
 
@@ -602,11 +629,12 @@ cudaError_t launch_fp4_combine(const Fp4DecodeArgs &a, const pa_decode_params &p
                         a.head_groups, heads_per_group, p.num_q_heads, rows, plan.max_splits, out, p.lse);
 }
 
-template <int D, int HPC>
-cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const pa_decode_params &p, int64_t useful, cudaStream_t stream) {
+template <int D, int HPC, bool BOX>
+cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, const pa_decode_params &p, int64_t useful,
+                         cudaStream_t stream) {
     using S = Fp4Smem<D, HPC>;
     const size_t smem = S::kRing + 2 * S::kStages * sizeof(uint64_t) + ((size_t)a.num_seqs + 1) * sizeof(int32_t);
-    auto kern = decode_fp4_kernel<D, HPC>;
+    auto kern = decode_fp4_kernel<D, HPC, BOX>;
     // CTAs per SM of the last (device, size), so that a serving loop's calls
     // skip both queries; the limit is raised to the device's once and for all.
     static std::atomic<uint64_t> last{0};
@@ -629,7 +657,56 @@ cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const pa_decode_params &p, int6
     int64_t grid = (int64_t)num_sms() * per_sm;
     if (p.max_ctas > 0 && grid > p.max_ctas) grid = p.max_ctas;
     if (grid > useful) grid = useful;
-    return launch_after(kern, (unsigned)grid, (HPC + 1) * 32, smem, stream, a);
+    return launch_after(kern, (unsigned)grid, (HPC + 1) * 32, smem, stream, a, maps);
+}
+
+template <bool BOX>
+cudaError_t dispatch_fp4(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, int heads, const pa_decode_params &p,
+                         int64_t useful, cudaStream_t stream) {
+    if (p.head_dim == 64) {
+        if (heads == 1) return launch_fp4_t<64, 1, BOX>(a, maps, p, useful, stream);
+        if (heads == 2) return launch_fp4_t<64, 2, BOX>(a, maps, p, useful, stream);
+        if (heads == 4) return launch_fp4_t<64, 4, BOX>(a, maps, p, useful, stream);
+        if (heads == 8) return launch_fp4_t<64, 8, BOX>(a, maps, p, useful, stream);
+    } else {
+        if (heads == 1) return launch_fp4_t<128, 1, BOX>(a, maps, p, useful, stream);
+        if (heads == 2) return launch_fp4_t<128, 2, BOX>(a, maps, p, useful, stream);
+        if (heads == 4) return launch_fp4_t<128, 4, BOX>(a, maps, p, useful, stream);
+        if (heads == 8) return launch_fp4_t<128, 8, BOX>(a, maps, p, useful, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+// 2-D map (32-bit words of a row, rows) of a 4-bit pool with a box of 16 rows
+// of one head group.
+bool make_map_rows(CUtensorMap *m, const void *base, const Fp4Layout &lay, int64_t rows) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)lay.row_bytes / 4, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)lay.row_bytes};
+    cuuint32_t box[2] = {(cuuint32_t)lay.group_bytes / 4, kUnit};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The keys of a sequence that its query can see, up to whole units: a window
+// may begin and end inside one.
+int64_t reach(const pa_decode_params &p) {
+    const int64_t all = ((int64_t)p.max_seqlen_k + kUnit - 1) / kUnit * kUnit;
+    if (p.sliding_window <= 0) return all;
+    const int64_t seen = ((int64_t)p.sliding_window + kUnit - 2) / kUnit * kUnit + kUnit;
+    return seen < all ? seen : all;
+}
+
+// The automatic smallest range for `keys` a sequence: what spreads the batch at
+// its longest over every SM, between 64 keys and 1/32 of the longest sequence.
+int32_t smallest_range(const pa_decode_params &p, int64_t keys, int groups) {
+    int64_t most = (keys / 32 + kUnit - 1) / kUnit * kUnit;
+    if (most < 64) most = 64;
+    const int64_t even = (p.num_seqs * keys * groups / num_sms() + kUnit - 1) / kUnit * kUnit;
+    return (int32_t)(even < 64 ? 64 : even > most ? most : even);
 }
 
 }  // namespace
@@ -638,18 +715,23 @@ DecodePlan plan_decode_fp4(const pa_decode_params &p) {
     DecodePlan plan{};
     const Fp4Layout lay = fp4_layout(p.num_kv_heads, p.head_dim);
     plan.heads_per_cta = lay.gs;
-    // Smallest range: the caller's, else what spreads the batch at its longest
-    // over every SM, between 64 keys and 1/32 of the longest context.
-    int32_t chunk = p.kv_chunk;
+    // With a window the ranges are those of the keys it leaves (31 sequences of
+    // 14141 keys, window 15: 42 us with the ranges of 14141 keys, most CTAs idle),
+    // but a row has no more of them than without it: a workspace sized without
+    // the window holds both.
+    const int64_t seen = reach(p);
+    int64_t chunk = p.kv_chunk;
     if (chunk <= 0) {
-        int32_t most = (p.max_seqlen_k / 32 + 15) / 16 * 16;
-        if (most < 64) most = 64;
-        const int64_t keys = (int64_t)p.num_seqs * p.max_seqlen_k * lay.groups;
-        const int64_t even = (keys / num_sms() + 15) / 16 * 16;
-        chunk = even < 64 ? 64 : even > most ? most : (int32_t)even;
+        chunk = smallest_range(p, p.max_seqlen_k, lay.groups);
+        const int64_t splits = (p.max_seqlen_k + chunk - 1) / chunk;
+        if (seen < p.max_seqlen_k) {
+            const int64_t fewest = ((seen + splits - 1) / splits + kUnit - 1) / kUnit * kUnit;
+            chunk = smallest_range(p, seen, lay.groups);
+            if (chunk < fewest) chunk = fewest;
+        }
     }
-    plan.kv_chunk = chunk;
-    plan.max_splits = (p.max_seqlen_k + chunk - 1) / chunk + 1;
+    plan.kv_chunk = (int32_t)chunk;
+    plan.max_splits = (int32_t)((seen + chunk - 1) / chunk) + 1;
     const size_t rows = (size_t)p.num_seqs * p.num_q_heads * plan.max_splits;
     const size_t header = 256 + (((size_t)p.num_seqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
     const size_t obytes = (rows * p.head_dim * sizeof(float) + 255) / 256 * 256;
@@ -688,19 +770,17 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
     a.ws_header = w.ws_header;
     a.ws_prefix = w.ws_prefix;
     // every sequence at its longest, ranges at their smallest
-    const int64_t units = ((int64_t)p.max_seqlen_k + kUnit - 1) / kUnit * p.num_seqs * lay.groups;
+    const int64_t units = reach(p) / kUnit * p.num_seqs * lay.groups;
     const int64_t useful = (units + a.min_units - 1) / a.min_units + 1;
-    cudaError_t e = cudaErrorInvalidValue;
-    if (p.head_dim == 64) {
-        if (lay.gs == 1) e = launch_fp4_t<64, 1>(a, p, useful, stream);
-        if (lay.gs == 2) e = launch_fp4_t<64, 2>(a, p, useful, stream);
-        if (lay.gs == 4) e = launch_fp4_t<64, 4>(a, p, useful, stream);
-        if (lay.gs == 8) e = launch_fp4_t<64, 8>(a, p, useful, stream);
+    cudaError_t e;
+    if (p.page_size == 16 && lay.groups > 1) {
+        Fp4Maps maps;
+        if (!make_map_rows(&maps.k, p.k_cache, lay, p.num_pages * 16) ||
+            !make_map_rows(&maps.v, p.v_cache, lay, p.num_pages * 16))
+            return cudaErrorNotSupported;
+        e = dispatch_fp4<true>(a, maps, lay.gs, p, useful, stream);
     } else {
-        if (lay.gs == 1) e = launch_fp4_t<128, 1>(a, p, useful, stream);
-        if (lay.gs == 2) e = launch_fp4_t<128, 2>(a, p, useful, stream);
-        if (lay.gs == 4) e = launch_fp4_t<128, 4>(a, p, useful, stream);
-        if (lay.gs == 8) e = launch_fp4_t<128, 8>(a, p, useful, stream);
+        e = dispatch_fp4<false>(a, Fp4NoMaps{}, lay.gs, p, useful, stream);
     }
     if (e != cudaSuccess) return e;
     return launch_fp4_combine(a, p, a.group * lay.gs, plan, stream);

@@ -78,7 +78,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -86,6 +85,7 @@
 #include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "tensor_map.cuh"
 
 namespace pa {
 namespace {
@@ -1207,19 +1207,6 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         __syncwarp();
         tmem_dealloc(tmem, 512);
     }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess && q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
 }
 
 // 3-D bf16 map (d, heads, rows) with a (64, 1, box_rows) box, 128-byte swizzle.

@@ -61,6 +61,42 @@ def test_windows(cuda_device, page, window):
     assert pa.device_error() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (16, 16, 64), (24, 12, 128)])
+@pytest.mark.parametrize("window", [1, 15, 333])
+def test_window_ranges(cuda_device, hq, hkv, d, window):
+    """Many sequences of which a window leaves little: ranges sized by the
+    window, a workspace sized without it (the binding's)."""
+    import paged_kv_flashattention_gb300 as pa
+    rng = np.random.default_rng(51)
+    L = rng.integers(1, 1500, 40).astype(np.int32)
+    L[7] = 1
+    p = W.small_problem(51, L - 1, np.ones_like(L), num_q_heads=hq, num_kv_heads=hkv, head_dim=d)
+    f = FP4Problem(p, cuda_device, 52)
+    ref = f.oracle(window=window)
+    need = pa.decode_workspace_size(f.q.shape, f.k_cache, f.meta.max_seqlen_k, kv_dtype=pa.PA_KV_FP4, num_kv_heads=hkv)
+    ws = torch.empty(need, dtype=torch.uint8, device=cuda_device)
+    for kw in (dict(workspace=ws), dict(kv_chunk=32)):
+        out, lse = f.decode(sliding_window=window, **kw)
+        check(out, lse, ref, f"window {window} {hq}/{hkv} d{d} {list(kw)}")
+
+
+@pytest.mark.parametrize("page_bad", [-1, 1 << 30])
+def test_bad_page_between_head_groups(cuda_device, page_bad):
+    """A page outside the pool where a row is several head groups: the error
+    bit, and the other sequences right."""
+    import paged_kv_flashattention_gb300 as pa
+    L = np.array([50, 200, 90], np.int32)
+    p = W.small_problem(53, L - 1, np.ones_like(L), num_q_heads=16, num_kv_heads=16, head_dim=128)
+    f = FP4Problem(p, cuda_device, 54)
+    ref = f.oracle()
+    f.meta.page_table = f.meta.page_table.clone()
+    f.meta.page_table[1, 3] = page_bad
+    out, lse = f.decode()
+    assert pa.device_error() == pa.PA_DEVERR_PAGE_RANGE
+    keep = [0, 2]
+    check(out[keep], lse[keep], tuple(x[keep] for x in ref), "beside a bad page")
+
+
 def test_ragged_batch_d64(cuda_device):
     """64 sequences of U[128, 4096] keys, 32 / 8 heads of 64."""
     f = FP4Problem(W.config(2), cuda_device, 21)
