@@ -18,8 +18,9 @@
 // request by bisection.  Entries of the token table are read below c_b and
 // written from c_b on, so the order of the two does not matter.
 // Bound: launch latency and the CTA's prefix (two dependent passes over L2)
-// for a decode step, the token table's 32-byte sectors (one per page at page
-// size 16) for large tables.
+// for a decode step (256 requests 7.4 us), the token table's 32-byte sectors
+// (one per page at page size 16) and the bisections for large tables (1000
+// requests of up to 8500 keys, 256,000 new tokens 12.5 us).
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pdl.cuh"

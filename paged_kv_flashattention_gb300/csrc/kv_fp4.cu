@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(256, 4) fp4_store_kernel(const Fp4StoreArgs a)
 }
 
 // Rows back as bf16: code * block scale is exact, times the head's scale
-// rounded in fp32, then to bf16.
+// rounded in fp32, then to bf16.  8192 rows of 8 heads of 128 (43 MB): 9.7 us;
+// with half the units per warp 8.7, but 5.9 instead of 4.9 on rows of 3 heads of
+// 64.
 template <int D>
 __global__ void __launch_bounds__(256) fp4_load_kernel(const int32_t *__restrict__ slots, int64_t num_tokens,
                                                        const uint8_t *__restrict__ k_cache,
