@@ -18,9 +18,9 @@
 // request by bisection.  Entries of the token table are read below c_b and
 // written from c_b on, so the order of the two does not matter.
 // Bound: launch latency and the CTA's prefix (two dependent passes over L2)
-// for a decode step (256 requests 7.4 us), the token table's 32-byte sectors
+// for a decode step (256 requests 7.3 us), the token table's 32-byte sectors
 // (one per page at page size 16) and the bisections for large tables (1000
-// requests of up to 8500 keys, 256,000 new tokens 12.5 us).
+// requests of up to 8408 keys, 253,000 new tokens 9.4 us).
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pdl.cuh"
@@ -31,7 +31,10 @@ PA_ERROR_WORD_ACCESSOR(error_word_batch)
 
 namespace {
 
-constexpr int kThreads = 256;
+// Two CTAs of 512 threads per SM: 9.4 us on the 1000 requests; four of 256 12.5,
+// one of 1024 10.5, four of 512 11.4 (every CTA forms the prefixes).
+constexpr int kThreads = 512;
+constexpr int kCtasPerSm = 2;
 
 struct Lens {
     int cached, extend;           // 0, 0 for a request whose lengths break the call's bounds
@@ -193,7 +196,7 @@ cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream) {
     }
     const int64_t cols = ((int64_t)p.max_seqlen_k + p.page_size - 1) / p.page_size;
     int64_t blocks = (p.num_tokens + cols * p.num_seqs + kThreads - 1) / kThreads;
-    const int64_t cap = (int64_t)num_sms() * 4;
+    const int64_t cap = (int64_t)num_sms() * kCtasPerSm;
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;
     return launch_after(build_batch_kernel, (unsigned)blocks, kThreads, smem, stream, p);

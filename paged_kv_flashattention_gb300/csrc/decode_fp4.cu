@@ -37,7 +37,8 @@
 // 2.5 per clock (64 conversions, 64 multiplies, 16 MMAs, the rest of the softmax
 // and addresses).  256 log-uniform contexts up to 32768 (2.38 GB): 423 us, 5.6
 // TB/s, 0.83 of the measured copy bandwidth; one unit at a time 428 us, with
-// 64-bit walks and six more live registers 448 (spills), 472 before the pairs.
+// 64-bit walks and six more live registers 448 (more spills), 472 before the
+// pairs.
 // At D = 64 half the bytes come with more than half the instructions: 64
 // sequences of up to 4096 keys 24 us, 0.40.
 #include <cuda_bf16.h>
