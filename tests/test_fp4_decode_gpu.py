@@ -311,3 +311,19 @@ def test_graph_runner(cuda_device):
     ref = fp4.attention(W.bf16_bits_to_f32(p.q), f.kr, f.vr, pt, np.arange(21), np.concatenate([[0], np.cumsum(short)]),
                         num_kv_heads=4, page_size=16, k_scale=f.ks, v_scale=f.vs, scale=p.scale)
     check(out, lse, ref, "graph, shorter")
+
+
+def test_many_sequences(cuda_device):
+    """Thousands of short sequences, empty ones among them: more than a warp's
+    or a CTA's share of the prefix."""
+    rng = np.random.default_rng(57)
+    L = rng.integers(1, 40, 4000).astype(np.int32)
+    p = W.small_problem(57, L - 1, np.ones_like(L), num_q_heads=4, num_kv_heads=2, head_dim=64)
+    f = FP4Problem(p, cuda_device, 58)
+    empty = rng.random(4000) < 0.1
+    lens = np.where(empty, 0, L).astype(np.int32)
+    f.meta.cache_seqlens = dev_np(lens, cuda_device)
+    out, lse = f.decode()
+    want, want_l, mag = f.oracle()
+    want[empty], want_l[empty], mag[empty] = 0, -np.inf, 0
+    check(out, lse, (want, want_l, mag), "4000 sequences")

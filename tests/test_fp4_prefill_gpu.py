@@ -43,6 +43,16 @@ def test_extend_partial_hit(cuda_device, page):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+def test_many_requests(cuda_device):
+    """More requests than the class order takes: the order by tile number."""
+    rng = np.random.default_rng(64)
+    cached, ext = rng.integers(0, 200, 1500).astype(np.int32), rng.integers(0, 5, 1500).astype(np.int32)
+    ext[700] = 260
+    p = W.small_problem(64, cached, ext, num_q_heads=4, num_kv_heads=2, head_dim=64)
+    f = FP4Problem(p, cuda_device, 65)
+    check(*f.prefill(), f.oracle(), "1500 requests")
+
+
 @pytest.mark.parametrize("extra", [0, 128, 5000, 300000])
 def test_length_bound_above_the_lengths(cuda_device, extra):
     """max_seqlen_k is only a bound: the same bits whichever order of the work
