@@ -35,8 +35,10 @@ def _check(status: int, lib=None):
 
 
 # The raw handle of the current stream of a device index; without it (another
-# torch) through the Stream object, 2 us instead of 0.1.
+# torch) through the Stream object, 2 us instead of 0.1.  The current device
+# without the public function's check that CUDA is initialised.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(t: torch.Tensor | None = None) -> int:
@@ -50,12 +52,15 @@ def _call(fn, t: torch.Tensor, *args):
     """fn(*args, current stream) of libpa with t's device current."""
     if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-    stream = _stream(t)
-    if t.get_device() == torch.cuda.current_device():
-        _check(fn(*args, stream))
+    index = t.get_device()
+    stream = _raw_stream(index) if _raw_stream is not None else _stream(t)
+    if index == _current_device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, stream))
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != PA_OK:
+        _check(status)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
