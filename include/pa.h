@@ -11,6 +11,7 @@
  *   pa_build_seqlens     per-request boundaries from the three lengths (host)
  *   pa_build_page_table  per-request page table from the token-granular table
  *   pa_build_batch       boundaries, positions, slots and page table from lengths on the device
+ *   pa_build_batch_from  the same, new pages taken from where a device cursor stands
  *   pa_prefill           varlen causal prefill / extend attention
  *   pa_decode            one-query-per-sequence split-KV decode attention
  *   pa_decode_noalloc    the same, with fixed library-owned split scratch
@@ -296,7 +297,9 @@ pa_status pa_build_page_table(const int32_t *token_table, int64_t token_table_st
  * they are assigned here: a token goes on its request's last page while that
  * has room, then on pages taken from free_pages in request order; the slots are
  * also written to token_table[table_idx[b], cached_len ..].  The first
- * totals[3] entries of free_pages are then in use.  Rows of table_idx must
+ * totals[3] entries of free_pages are then in use: every call takes from the
+ * first entry on, so the caller moves the list on before the next call or
+ * replay (pa_build_batch_from does it on the device).  Rows of table_idx must
  * differ, and slots below cached_len on one page be consecutive, as this call
  * assigns them.
  * Device data that breaks the call's bounds: a negative length or device_len >
@@ -332,6 +335,20 @@ typedef struct {
 } pa_batch_params;
 
 pa_status pa_build_batch(const pa_batch_params *p, void *stream);
+
+/*
+ * pa_build_batch_from - pa_build_batch whose place in the free list lives on
+ * the device, so that a captured step replayed any number of times gives every
+ * page out once.  free_cursor: device int32 [2], zero at first (NULL =
+ * pa_build_batch; needs free_pages).  The call takes pages from
+ * free_pages[free_cursor[0]] on and moves free_cursor[0] past the pages it took,
+ * at most to num_free_pages; free_cursor[1] is the call's own and zero between
+ * calls.  Calls that share a cursor must follow one another (one stream, or
+ * ordered by events).  Once pages have been given back, write a new list and
+ * zero the cursor between two calls.  A cursor outside [0, num_free_pages]
+ * counts as a list that is used up.
+ */
+pa_status pa_build_batch_from(const pa_batch_params *p, int32_t *free_cursor, void *stream);
 
 /*
  * pa_prefill - varlen prefill / extend attention ([T] s.10-15, [M]).

@@ -87,6 +87,7 @@ SIGNATURES = {
     "pa_build_seqlens": (ctypes.c_int, [c_p, c_p, c_i32, c_p, c_p, c_p, c_p, c_p]),
     "pa_build_page_table": (ctypes.c_int, [c_p, c_i64, c_i64, c_p, c_i32, c_i32, c_i32, c_p, c_i32, c_p]),
     "pa_build_batch": (ctypes.c_int, [ctypes.POINTER(BatchParams), c_p]),
+    "pa_build_batch_from": (ctypes.c_int, [ctypes.POINTER(BatchParams), c_p, c_p]),
     "pa_prefill": (ctypes.c_int, [ctypes.POINTER(PrefillParams), c_p]),
     "pa_decode_workspace_size": (c_size, [ctypes.POINTER(DecodeParams)]),
     "pa_decode_kv_chunk": (c_i32, [ctypes.POINTER(DecodeParams)]),

@@ -382,7 +382,8 @@ def build_page_table(token_table: torch.Tensor, table_idx: torch.Tensor, max_seq
 def build_batch(cached_len: torch.Tensor, extend_len: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor,
                 page_size: int, max_seqlen_k: int, *, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
                 cache_seqlens: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
-                page_table: torch.Tensor, totals: torch.Tensor, free_pages: torch.Tensor | None = None) -> None:
+                page_table: torch.Tensor, totals: torch.Tensor, free_pages: torch.Tensor | None = None,
+                free_cursor: torch.Tensor | None = None) -> None:
     """A batch's metadata from lengths on the device, in one launch
     (``pa_build_batch``; ``metadata.BatchPlanner`` owns the outputs).
     cached_len, extend_len, table_idx: int32 [B]; token_table: int32 [rows, >=
@@ -391,7 +392,11 @@ def build_batch(cached_len: torch.Tensor, extend_len: torch.Tensor, token_table:
     tokens), page_table [>= B, >= ceil(max_seqlen_k / page_size)] (columns past
     a request's pages are left as they were), totals [4] (new tokens, longest
     extend, longest length, new pages).  ``free_pages`` (int32): take the new
-    tokens' pages from it and enter their slots in ``token_table``."""
+    tokens' pages from its first entries and enter their slots in
+    ``token_table``; the caller moves the list on by totals[3] before the next
+    call.  With ``free_cursor`` (int32 [2] on the device, zeros at first) they
+    are taken from entry free_cursor[0] on, which the call moves on itself
+    (``pa_build_batch_from``): a captured call needs it."""
     dev = token_table.device
     B = cached_len.numel()
     for t, n in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k"), (cache_seqlens, "cache_seqlens"),
@@ -408,7 +413,7 @@ def build_batch(cached_len: torch.Tensor, extend_len: torch.Tensor, token_table:
     if page_table.shape[0] < B or page_table.shape[1] < -(-max_k // P):
         raise ValueError(f"page_table must be at least [{B}, {-(-max_k // P)}]")
     out = _BatchOut(cu_seqlens_q, cu_seqlens_k, cache_seqlens, positions, slot_mapping, page_table, totals)
-    _build_batch(cached_len, extend_len, token_table, table_idx, P, max_k, out, free_pages)
+    _build_batch(cached_len, extend_len, token_table, table_idx, P, max_k, out, free_pages, free_cursor)
 
 
 _BatchOut = collections.namedtuple("_BatchOut", "cu_seqlens_q cu_seqlens_k cache_seqlens positions slot_mapping "
@@ -421,7 +426,7 @@ def _need_rows(t, name, dev):
         raise ValueError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
 
 
-def _build_batch(cached_len, extend_len, token_table, table_idx, page_size, max_seqlen_k, out, free_pages):
+def _build_batch(cached_len, extend_len, token_table, table_idx, page_size, max_seqlen_k, out, free_pages, free_cursor):
     """build_batch into checked outputs (the attributes of ``out``)."""
     dev = out.totals.device
     _need(cached_len, "cached_len", torch.int32, dev)
@@ -430,6 +435,12 @@ def _build_batch(cached_len, extend_len, token_table, table_idx, page_size, max_
     _need_rows(token_table, "token_table", dev)
     if free_pages is not None:
         _need(free_pages, "free_pages", torch.int32, dev)
+    if free_cursor is not None:
+        _need(free_cursor, "free_cursor", torch.int32, dev)
+        if free_pages is None:
+            raise ValueError("free_cursor needs free_pages")
+        if free_cursor.numel() < 2:
+            raise ValueError("free_cursor must hold 2 int32")
     B, width = cached_len.numel(), token_table.shape[1]
     if extend_len.numel() != B or table_idx.numel() != B:
         raise ValueError("cached_len, extend_len and table_idx must hold one entry per request")
@@ -444,7 +455,7 @@ def _build_batch(cached_len, extend_len, token_table, table_idx, page_size, max_
         0 if free_pages is None else free_pages.numel(), out.positions.numel(), out.cu_seqlens_q.data_ptr(),
         out.cu_seqlens_k.data_ptr(), out.cache_seqlens.data_ptr(), out.positions.data_ptr(), out.slot_mapping.data_ptr(),
         pt.data_ptr(), max(pt.stride(0), pt.shape[1]), out.totals.data_ptr())
-    _call(_lib.load().pa_build_batch, out.totals, ctypes.byref(p))
+    _call(_lib.load().pa_build_batch_from, out.totals, ctypes.byref(p), _ptr(free_cursor))
 
 
 def _pool_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, page_size: int | None):

@@ -17,6 +17,11 @@
 // its share of the tokens and of the page-table entries, finding an element's
 // request by bisection.  Entries of the token table are read below c_b and
 // written from c_b on, so the order of the two does not matter.
+//
+// With a cursor (pa_build_batch_from) the list starts at free_pages[cursor[0]].
+// Every CTA reads that before it counts itself in cursor[1]; the CTA that counts
+// last moves cursor[0] past the pages taken and clears cursor[1], so nothing
+// waits and the next launch in the stream finds both ready.
 // Bound: launch latency and the CTA's prefix (two dependent passes over L2)
 // for a decode step (256 requests 7.3 us), the token table's 32-byte sectors
 // (one per page at page size 16) and the bisections for large tables (1000
@@ -90,19 +95,25 @@ __device__ __forceinline__ int floor_div(int x, int P) {
     return q;
 }
 
-// The page of new page number n of the batch; -1 once the list is used up.
-__device__ __forceinline__ int free_page(const pa_batch_params &p, int n) {
-    if (n < p.num_free_pages) return p.free_pages[n];
+// The page of new page number n of the batch; -1 once the list, from entry
+// `from` on, is used up.
+__device__ __forceinline__ int free_page(const pa_batch_params &p, int from, int n) {
+    if (n < p.num_free_pages - from) return p.free_pages[from + n];
     raise_error(PA_DEVERR_NO_PAGES);
     return -1;
 }
 
-__global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_params p) {
+__global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_params p, int32_t *cursor) {
     extern __shared__ int32_t smem[];
     __shared__ int32_t warp_sums[kThreads / 32];
+    __shared__ int32_t list_from;
     after_previous();
     const int B = p.num_seqs, P = p.page_size;
     const bool take = p.free_pages != nullptr;
+    if (threadIdx.x == 0) {                          // (a cursor outside the list: a list that is used up)
+        const int at = cursor != nullptr ? *reinterpret_cast<volatile int32_t *>(cursor) : 0;
+        list_from = at < 0 || at > p.num_free_pages ? p.num_free_pages : at;
+    }
     int32_t *cq = smem;                              // [B + 1] new tokens
     int32_t *cp = cq + B + 1;                        // [B + 1] pages
     int32_t *cn = cp + B + 1;                        // [B + 1] pages to take
@@ -118,6 +129,14 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_pa
     running_sum(cp, B, warp_sums);
     if (take) running_sum(cn, B, warp_sums);
     const int total = cq[B], pages = cp[B];
+    const int from = list_from;                      // (read after the barriers above)
+    if (cursor != nullptr && threadIdx.x == 0) {
+        __threadfence();                             // this CTA's read of cursor[0] before its count
+        if (atomicAdd(&cursor[1], 1) == (int)gridDim.x - 1) {
+            cursor[0] = from + min(cn[B], p.num_free_pages - from);
+            cursor[1] = 0;
+        }
+    }
 
     const int64_t stride = (int64_t)gridDim.x * kThreads;
     const int64_t me = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -131,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_pa
                 int32_t *row = p.token_table + r.row * p.token_table_stride;
                 if (take) {
                     const int fresh = pos / P - pages_of(r.cached, P);
-                    const int page = fresh >= 0 ? free_page(p, cn[b] + fresh) : floor_div(row[r.cached - 1], P);
+                    const int page = fresh >= 0 ? free_page(p, from, cn[b] + fresh) : floor_div(row[r.cached - 1], P);
                     slot = page >= 0 ? page * P + pos % P : -1;
                     row[pos] = slot;
                 } else {
@@ -148,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_pa
         int page = -1;
         if (r.row >= 0) {
             const int fresh = c - pages_of(r.cached, P);
-            page = take && fresh >= 0 ? free_page(p, cn[b] + fresh)
+            page = take && fresh >= 0 ? free_page(p, from, cn[b] + fresh)
                                       : floor_div(p.token_table[r.row * p.token_table_stride + (int64_t)c * P], P);
         }
         p.page_table[(int64_t)b * p.page_table_stride + c] = page;
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const pa_batch_pa
 
 }  // namespace
 
-cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream) {
+cudaError_t launch_build_batch(const pa_batch_params &p, int32_t *free_cursor, cudaStream_t stream) {
     const size_t smem = 3 * ((size_t)p.num_seqs + 1) * sizeof(int32_t);
     if (smem > 40 * 1024) {                          // more than a CTA has without asking (with the static part)
         cudaError_t e = cudaFuncSetAttribute(build_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
@@ -199,7 +218,7 @@ cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream) {
     const int64_t cap = (int64_t)num_sms() * kCtasPerSm;
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;
-    return launch_after(build_batch_kernel, (unsigned)blocks, kThreads, smem, stream, p);
+    return launch_after(build_batch_kernel, (unsigned)blocks, kThreads, smem, stream, p, free_cursor);
 }
 
 }  // namespace pa

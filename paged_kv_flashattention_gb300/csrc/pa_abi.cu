@@ -306,7 +306,9 @@ pa_status pa_build_page_table(const int32_t *token_table, int64_t token_table_st
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_page_table launch");
 }
 
-pa_status pa_build_batch(const pa_batch_params *p, void *stream) {
+pa_status pa_build_batch(const pa_batch_params *p, void *stream) { return pa_build_batch_from(p, nullptr, stream); }
+
+pa_status pa_build_batch_from(const pa_batch_params *p, int32_t *free_cursor, void *stream) {
     g_last_error[0] = 0;
     if (p == nullptr) return fail(PA_ERR_INVALID, "params is NULL");
     if (p->num_seqs < 0 || p->max_seqlen_k < 0 || p->num_tokens < 0 || p->token_table_rows < 0 || p->num_free_pages < 0)
@@ -324,7 +326,8 @@ pa_status pa_build_batch(const pa_batch_params *p, void *stream) {
                             !p->page_table))
         return fail(PA_ERR_INVALID, "NULL pointer");
     if (p->num_tokens > 0 && (!p->positions || !p->slot_mapping)) return fail(PA_ERR_INVALID, "NULL pointer");
-    cudaError_t e = launch_build_batch(*p, static_cast<cudaStream_t>(stream));
+    if (free_cursor != nullptr && p->free_pages == nullptr) return fail(PA_ERR_INVALID, "free_cursor without free_pages");
+    cudaError_t e = launch_build_batch(*p, free_cursor, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_batch launch");
 }
 

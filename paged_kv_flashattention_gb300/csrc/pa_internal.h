@@ -34,7 +34,7 @@ cudaError_t launch_build_page_table(const int32_t *token_table, int64_t tt_strid
                                     int32_t page_size, int32_t *page_table, int32_t pt_stride,
                                     cudaStream_t stream);
 
-cudaError_t launch_build_batch(const pa_batch_params &p, cudaStream_t stream);
+cudaError_t launch_build_batch(const pa_batch_params &p, int32_t *free_cursor, cudaStream_t stream);
 
 // Decode plan: keys per split, splits of the longest sequence, KV heads per CTA.
 struct DecodePlan {

@@ -177,7 +177,10 @@ class BatchPlanner:
     """The batch's metadata from lengths that live on the device, without the
     host: boundaries, positions, slots and page table in one launch into fixed
     buffers, so a captured graph (``build``, the stores, the attention) follows
-    the lengths from replay to replay.  Page-table entries past a request's
+    the lengths from replay to replay.  A captured ``build`` that takes pages
+    needs ``free_cursor``: without it every replay takes the first entries of
+    the list again, and the caller has to move the list on between replays
+    (``totals[3]`` entries of it are in use).  Page-table entries past a request's
     pages keep what earlier batches left there (-1 at first); the attention
     never reads them.  Each ``build`` overwrites the buffers of the one before:
     use one planner per batch in flight."""
@@ -200,9 +203,12 @@ class BatchPlanner:
         self._batches: dict[int, DeviceBatch] = {}
 
     def build(self, cached_len: torch.Tensor, extend_len: torch.Tensor, token_table: torch.Tensor,
-              table_idx: torch.Tensor, *, free_pages: torch.Tensor | None = None) -> DeviceBatch:
+              table_idx: torch.Tensor, *, free_pages: torch.Tensor | None = None,
+              free_cursor: torch.Tensor | None = None) -> DeviceBatch:
         """Plan the batch of cached_len / extend_len (int32 [B], B <= max_seqs)
-        whose requests are the rows table_idx of token_table."""
+        whose requests are the rows table_idx of token_table.  ``free_pages``:
+        take the new tokens' pages from this list; ``free_cursor`` (int32 [2],
+        zeros at first): the entries taken so far, moved on by each call."""
         B = cached_len.numel()
         b = self._batches.get(B)
         if b is None:                                # the views for this batch size
@@ -213,5 +219,6 @@ class BatchPlanner:
                 cu_seqlens_q=self.cu_seqlens[0, :B + 1], cu_seqlens_k=self.cu_seqlens[1, :B + 1],
                 cache_seqlens=self.cache_seqlens[:B], positions=self.tokens[0], slot_mapping=self.tokens[1],
                 page_table=self.page_table[:B], totals=self.totals)
-        api._build_batch(cached_len, extend_len, token_table, table_idx, self.page_size, self.max_seqlen_k, b, free_pages)
+        api._build_batch(cached_len, extend_len, token_table, table_idx, self.page_size, self.max_seqlen_k, b, free_pages,
+                         free_cursor)
         return b
