@@ -308,6 +308,8 @@ pa_status pa_build_page_table(const int32_t *token_table, int64_t token_table_st
  * table_idx entry outside the table gives slots and pages -1, takes no pages
  * and raises PA_DEVERR_TABLE_INDEX; a free list that is too short gives slots
  * and pages -1 for the rest and raises PA_DEVERR_NO_PAGES.
+ * The lengths, table_idx and free_pages must not lie on an output (a next
+ * step's cached_len is a copy of cache_seqlens, not cache_seqlens itself).
  * All pointers are device int32.  num_seqs <= 16384; num_seqs * max_seqlen_k
  * and num_tokens below 2^31.
  */

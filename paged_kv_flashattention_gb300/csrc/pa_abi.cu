@@ -306,6 +306,29 @@ pa_status pa_build_page_table(const int32_t *token_table, int64_t token_table_st
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_page_table launch");
 }
 
+// The first of the batch plan's one-dimensional inputs that lies on one of its
+// one-dimensional outputs, or null.  Every CTA reads the inputs while others
+// write the outputs.
+static const char *batch_overlap(const pa_batch_params &p, const int32_t *free_cursor) {
+    struct Range {
+        const int32_t *at;
+        int64_t n;
+        const char *name;
+    };
+    const int64_t B = p.num_seqs;
+    const Range in[] = {{p.cached_len, B, "cached_len"}, {p.extend_len, B, "extend_len"}, {p.table_idx, B, "table_idx"},
+                        {p.free_pages, p.num_free_pages, "free_pages"}, {free_cursor, 2, "free_cursor"}};
+    const Range out[] = {{p.cu_seqlens_q, B + 1, ""}, {p.cu_seqlens_k, B + 1, ""}, {p.cache_seqlens, B, ""},
+                         {p.positions, p.num_tokens, ""}, {p.slot_mapping, p.num_tokens, ""}, {p.totals, 4, ""},
+                         {free_cursor, 2, ""}};
+    for (const Range &i : in)
+        for (const Range &o : out)
+            if (i.at != nullptr && o.at != nullptr && i.n > 0 && o.n > 0 && i.at < o.at + o.n && o.at < i.at + i.n &&
+                !(i.at == free_cursor && o.at == free_cursor))
+                return i.name;
+    return nullptr;
+}
+
 pa_status pa_build_batch(const pa_batch_params *p, void *stream) { return pa_build_batch_from(p, nullptr, stream); }
 
 pa_status pa_build_batch_from(const pa_batch_params *p, int32_t *free_cursor, void *stream) {
@@ -327,6 +350,8 @@ pa_status pa_build_batch_from(const pa_batch_params *p, int32_t *free_cursor, vo
         return fail(PA_ERR_INVALID, "NULL pointer");
     if (p->num_tokens > 0 && (!p->positions || !p->slot_mapping)) return fail(PA_ERR_INVALID, "NULL pointer");
     if (free_cursor != nullptr && p->free_pages == nullptr) return fail(PA_ERR_INVALID, "free_cursor without free_pages");
+    if (const char *name = batch_overlap(*p, free_cursor))
+        return fail(PA_ERR_INVALID, "%s overlaps an output of the call", name);
     cudaError_t e = launch_build_batch(*p, free_cursor, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_batch launch");
 }

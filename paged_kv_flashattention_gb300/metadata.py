@@ -206,7 +206,9 @@ class BatchPlanner:
               table_idx: torch.Tensor, *, free_pages: torch.Tensor | None = None,
               free_cursor: torch.Tensor | None = None) -> DeviceBatch:
         """Plan the batch of cached_len / extend_len (int32 [B], B <= max_seqs)
-        whose requests are the rows table_idx of token_table.  ``free_pages``:
+        whose requests are the rows table_idx of token_table.  The lengths
+        must not be the planner's own buffers (copy ``cache_seqlens`` for the
+        next step).  ``free_pages``:
         take the new tokens' pages from this list; ``free_cursor`` (int32 [2],
         zeros at first): the entries taken so far, moved on by each call."""
         B = cached_len.numel()
