@@ -171,7 +171,8 @@ int64_t pa_fp4_row_bytes(int32_t num_kv_heads, int32_t head_dim);
  * pa_store_kv_fp4 - KV-cache store into a 4-bit pool.
  * k, v:             device bf16 [num_tokens, Hkv, head_dim]
  * k_cache, v_cache: device bytes [num_slots, pa_fp4_row_bytes(Hkv, head_dim)]
- * k_scale, v_scale: device fp32 [Hkv], positive and finite
+ * k_scale, v_scale: device fp32 [Hkv], positive and finite, or 0 for a head that is
+ * all zeros (its rows read as zeros, its keys all score 0)
  * slot_mapping: as for pa_store_kv.
  */
 pa_status pa_store_kv_fp4(const void *k, const void *v, const int32_t *slot_mapping,

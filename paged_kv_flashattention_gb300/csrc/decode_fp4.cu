@@ -402,7 +402,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T
         int lo;
         const int L = seq_keys(a, b, lo);
         const int first = lo / kUnit;
-        const float sl2 = a.scale_log2 * __ldg(a.k_scale + kvh);     // raw score -> log2 units
+        const float sl2 = fp4_score_scale(a.scale_log2, __ldg(a.k_scale + kvh));     // raw score -> log2 units
         const float lazy = kLazyRescale / sl2;
         uint32_t qb[KS][2];
 #pragma unroll

@@ -62,6 +62,16 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// The factor that takes raw scores to log2 units, the head's K scale in it.  A
+// scale of zero (an all-zero head's) would make 0 * -inf = NaN of the masked
+// scores; the smallest normal number, 2^-126, leaves them -inf and every other
+// score, at most 2^35 raw (128 products of 2688 and 65504), zero to within
+// 2^-91.  A NaN stays one.
+__device__ __forceinline__ float fp4_score_scale(float scale_log2, float k_scale) {
+    const float s = scale_log2 * k_scale;
+    return s < 1.17549435e-38f ? 1.17549435e-38f : s;
+}
+
 // One f16 of a pair in both halves.
 __device__ __forceinline__ uint32_t f16_dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
 __device__ __forceinline__ uint32_t f16_dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }

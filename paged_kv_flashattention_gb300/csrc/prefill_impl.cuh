@@ -1053,7 +1053,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         if (v < 0) break;
         prefill_item<T, EXT, kClasses>(a, v, it);
         if constexpr (F4) {
-            sl2 = a.scale_log2 * __ldg(a.k_scale + it.kvh);
+            sl2 = fp4_score_scale(a.scale_log2, __ldg(a.k_scale + it.kvh));
             c2 = make_float2(sl2, sl2);
         }
         const int n_kv = it.n_kv, Lk = it.Lk, off = it.off, min_vis = it.min_vis;

@@ -59,3 +59,19 @@ def test_nan_scale_stays_nan(cuda_device, kernel):
     want = torch.zeros_like(out, dtype=torch.bool)
     want[:, 4:6] = True
     assert torch.equal(torch.isnan(out), want)
+
+
+def test_store(cuda_device):
+    """A head of zero scale stores codes of zero, whatever its values, and reads
+    back as zeros; the heads beside it keep theirs."""
+    import paged_kv_flashattention_gb300 as pa
+    hkv, d, T = 4, 64, 9
+    x = torch.randn((T, hkv, d), device=cuda_device).bfloat16()
+    x[:, 1] = 0                                                # all zeros at scale zero, and head 2 not
+    g = torch.tensor([2e-3, 0.0, 0.0, 2e-3], device=cuda_device)
+    pools = [torch.full((16, pa.fp4_row_bytes(hkv, d)), 255, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    slots = torch.arange(T, dtype=torch.int32, device=cuda_device)
+    pa.store_kv_fp4(x, x, slots, *pools, g, g)
+    for back in pa.load_kv_fp4(slots, *pools, g, g, d):
+        assert not back[:, 1:3].any()
+        assert bool(torch.isfinite(back).all()) and bool((back[:, [0, 3]].float().abs().amax(-1) > 0.5).all())
