@@ -102,17 +102,16 @@ __global__ void __launch_bounds__((HPC + 1) * 32) decode_kernel(const DecodeArgs
 // One warp per row (a (sequence, head) pair): merge its splits by LSE.
 template <int D>
 __global__ void __launch_bounds__(256) lse_combine_kernel(
-    const float *__restrict__ o_part, const float *__restrict__ lse_part,
-    const int32_t *__restrict__ splits_per_row, const int32_t *__restrict__ seg_header,
-    const int32_t *__restrict__ seg_prefix, int32_t head_groups, int32_t heads_per_group,
-    int32_t heads_per_seq, int32_t num_rows, int32_t max_splits,
-    __nv_bfloat16 *__restrict__ out, float *__restrict__ lse_out) {
+    const float *o_part, const float *lse_part, const int32_t *splits_per_row, const int32_t *seg_header,
+    const int32_t *seg_prefix, int32_t head_groups, int32_t heads_per_group, int32_t heads_per_seq, int32_t num_rows,
+    int32_t max_splits, __nv_bfloat16 *out, float *lse_out) {
     constexpr int VPL = D / 32;
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     // after decode this kernel runs as its programmatic dependent: wait until
     // that grid has completed and its partials are visible (a no-op when
-    // launched normally)
+    // launched normally).  The split kernel writes them while this one is
+    // resident, so they are read by plain loads (csrc/pdl.cuh).
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row >= num_rows) return;
     int n = max_splits;

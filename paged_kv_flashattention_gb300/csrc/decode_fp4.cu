@@ -402,7 +402,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T
         int lo;
         const int L = seq_keys(a, b, lo);
         const int first = lo / kUnit;
-        const float sl2 = fp4_score_scale(a.scale_log2, __ldg(a.k_scale + kvh));     // raw score -> log2 units
+        const float sl2 = fp4_score_scale(a.scale_log2, a.k_scale[kvh]);     // raw score -> log2 units
         const float lazy = kLazyRescale / sl2;
         uint32_t qb[KS][2];
 #pragma unroll
@@ -411,7 +411,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T
             const uint2 *qrow = reinterpret_cast<const uint2 *>(a.q + ((int64_t)b * a.num_q_heads + h0 + r8) * D + q4 * (D / 4));
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                const uint2 w = __ldg(qrow + kk);
+                const uint2 w = qrow[kk];
                 qb[kk][0] = f16x2_of(bf16lo(w.x), bf16hi(w.x));
                 qb[kk][1] = f16x2_of(bf16lo(w.y), bf16hi(w.y));
             }
@@ -491,7 +491,7 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T
                 raise_error(PA_DEVERR_SEQLENS);
                 continue;
             }
-            const float inv = (l == 0.f ? 0.f : 1.f / l) * __ldg(a.v_scale + kvh);       // a NaN stays one
+            const float inv = (l == 0.f ? 0.f : 1.f / l) * a.v_scale[kvh];       // a NaN stays one
             const int64_t r = ((int64_t)b * a.num_q_heads + h0 + hh) * a.max_splits + split;
             float *orow = a.o_part + r * D + r8 * (D / 8);
 #pragma unroll
@@ -545,9 +545,9 @@ constexpr int kCombineThreads = 256;
 
 template <int D, int W>
 __global__ void __launch_bounds__(kCombineThreads) fp4_combine_kernel(
-    const float *__restrict__ o_part, const float *__restrict__ lse_part, const int32_t *__restrict__ header,
-    const int32_t *__restrict__ prefix, int32_t head_groups, int32_t heads_per_group, int32_t heads_per_seq,
-    int32_t num_rows, int32_t max_splits, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse_out) {
+    const float *o_part, const float *lse_part, const int32_t *header, const int32_t *prefix, int32_t head_groups,
+    int32_t heads_per_group, int32_t heads_per_seq, int32_t num_rows, int32_t max_splits, __nv_bfloat16 *out,
+    float *lse_out) {
     constexpr int kLanes = D / 4;                    // lanes of a slot, four elements each
     constexpr int kSlots = 32 * W / kLanes;          // slots in flight
     __shared__ float top[kCombineThreads / 32], dens[kCombineThreads / kLanes];

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(256, 4) fp4_store_kernel(const Fp4StoreArgs a)
                 const int h = off[g] / (2 * D);
                 uint2 codes;
                 uint32_t scale;
-                quantise16(w[g], __ldg((is_k ? a.k_scale : a.v_scale) + h), codes, scale);
+                quantise16(w[g], (is_k ? a.k_scale : a.v_scale)[h], codes, scale);
                 const int hg = h & (a.lay.gs - 1);   // gs is a power of two
                 uint8_t *row = (is_k ? a.k_cache : a.v_cache) + (int64_t)slot * a.lay.row_bytes +
                                (h / a.lay.gs) * a.lay.group_bytes;
@@ -303,11 +303,10 @@ __global__ void __launch_bounds__(256, 4) fp4_store_kernel(const Fp4StoreArgs a)
 // with half the units per warp 8.7, but 5.9 instead of 4.9 on rows of 3 heads of
 // 64.
 template <int D>
-__global__ void __launch_bounds__(256) fp4_load_kernel(const int32_t *__restrict__ slots, int64_t num_tokens,
-                                                       const uint8_t *__restrict__ k_cache,
-                                                       const uint8_t *__restrict__ v_cache, int64_t num_slots,
-                                                       int32_t num_kv_heads, const float *__restrict__ k_scale,
-                                                       const float *__restrict__ v_scale, uint8_t *k_out,
+__global__ void __launch_bounds__(256) fp4_load_kernel(const int32_t *slots, int64_t num_tokens,
+                                                       const uint8_t *k_cache, const uint8_t *v_cache,
+                                                       int64_t num_slots, int32_t num_kv_heads,
+                                                       const float *k_scale, const float *v_scale, uint8_t *k_out,
                                                        uint8_t *v_out, Fp4Layout lay, int32_t upw) {
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
     after_previous();
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(256) fp4_load_kernel(const int32_t *__restrict
                 const uint8_t *row = (is_k ? k_cache : v_cache) + slot * lay.row_bytes + (h / lay.gs) * lay.group_bytes;
                 const uint2 codes = *reinterpret_cast<const uint2 *>(row + hg * (D / 2) + blk * 8);
                 const uint32_t s = f16_dup_lo(e4m3x2_to_f16x2(row[lay.code_bytes + hg * kLanes + blk]));
-                const float g = __ldg((is_k ? k_scale : v_scale) + h);
+                const float g = (is_k ? k_scale : v_scale)[h];
                 uint32_t r[8];
                 e2m1x8_to_f16x8(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&r[0]));
                 e2m1x8_to_f16x8(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&r[4]));

@@ -4,10 +4,17 @@
 // and its writes are visible.  Every thread that can exit calls it, so "this
 // grid has completed" implies the same of all before it; a decode's split kernel
 // that overlaps the kernel before it does not, and its combine is launched
-// ordinarily, after both.  Measured on the small
-// calls: 0.3 to 0.6 us less per kernel.  Letting the next kernel's CTAs onto the
-// SMs at the start of this one (griddepcontrol.launch_dependents) costs more
-// than it gives: 64 decode sequences 24.2 -> 26.3 us, a batch plan 12.6 -> 14.1.
+// ordinarily, after both.
+//
+// Whatever a kernel before may have written (pools, partials, q, slots, scales)
+// is read by plain loads: the read-only path (__ldg, const __restrict__
+// parameters) is for data that nothing writes while the kernel runs, and the
+// compiler may move such a load before the wait.
+//
+// Measured on the small calls: 0.3 to 0.6 us less per kernel.  Letting the next
+// kernel's CTAs onto the SMs at the start of this one
+// (griddepcontrol.launch_dependents) costs more than it gives: 64 decode
+// sequences 24.2 -> 26.3 us, a batch plan 12.6 -> 14.1.
 #pragma once
 
 #include <cuda_runtime.h>
