@@ -477,8 +477,10 @@ typedef struct {
 
 /* Bytes of workspace pa_decode needs for these parameters (always > 0: a
  * header, a length prefix, and partials for at most
- * ceil(max_seqlen_k / kv_chunk) + 1 splits per (sequence, head)).  Reads
- * only host fields of *p. */
+ * ceil(max_seqlen_k / kv_chunk) + 1 splits per (sequence, head)).  A workspace
+ * of this size serves every smaller num_seqs too; on 4-bit pools, where the
+ * automatic split depends on the batch, also every smaller max_seqlen_k and any
+ * sliding window (ask without one).  Reads only host fields of *p. */
 size_t pa_decode_workspace_size(const pa_decode_params *p);
 /* The minimum split pa_decode will use for these parameters. */
 int32_t pa_decode_kv_chunk(const pa_decode_params *p);
@@ -531,7 +533,8 @@ pa_status pa_mixed_batch(const pa_prefill_params *pre, const pa_decode_params *d
  * PA_DECODE_NOALLOC_SCRATCH_BYTES = 32 MiB, held on every GPU that loads the
  * library until the process exits).  The caller still passes q, the pools,
  * the metadata and out/lse.
- *  - Sizes whose split scratch (pa_decode_workspace_size) exceeds 32 MiB are
+ *  - Sizes whose split scratch (the call's own part of
+ *    pa_decode_workspace_size) exceeds 32 MiB are
  *    rejected with PA_ERR_UNSUPPORTED and a message; nothing is launched.
  *  - The first call on a device (with that device current) looks up the
  *    scratch address with cudaGetSymbolAddress; make that first call before

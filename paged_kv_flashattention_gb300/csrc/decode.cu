@@ -305,6 +305,7 @@ DecodePlan plan_decode(const pa_decode_params &p) {
     const size_t header = 256 + (((size_t)p.num_seqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
     const size_t obytes = (rows * p.head_dim * sizeof(float) + 255) / 256 * 256;
     plan.workspace_bytes = header + obytes + rows * sizeof(float);
+    plan.workspace_any = plan.workspace_bytes;
     return plan;
 }
 

@@ -710,6 +710,29 @@ int32_t smallest_range(const pa_decode_params &p, int64_t keys, int groups) {
     return (int32_t)(even < 64 ? 64 : even > most ? most : even);
 }
 
+// Bytes of the workspace layout (decode_setup) with `slots` partials per query head.
+size_t workspace_of(const pa_decode_params &p, size_t slots) {
+    const size_t rows = slots * p.num_q_heads;
+    const size_t header = 256 + (((size_t)p.num_seqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
+    const size_t obytes = (rows * p.head_dim * sizeof(float) + 255) / 256 * 256;
+    return header + obytes + rows * sizeof(float);
+}
+
+// At least the partials per query head, num_seqs * max_splits, of any batch of up
+// to num_seqs sequences that see up to `keys` keys each, under smallest_range's
+// ranges R.  A row has ceil(keys / R) + 1 slots, and R is 64 or more: at most
+// ceil(keys / 64) + 1; and either 1/32 of the keys rounded down or more, at most 34
+// slots, or at least 80 and 80/81 of num_seqs * keys * groups / SMs (a quotient
+// rounded down), at most 1.0125 SMs / (groups * num_seqs) + 3.  Every bound times
+// num_seqs grows with num_seqs and with keys.
+size_t most_slots(const pa_decode_params &p, int64_t keys, int groups) {
+    const int64_t n = p.num_seqs;
+    const int64_t by_floor = n * ((keys + 63) / 64 + 1);
+    const int64_t by_sms = ((int64_t)num_sms() * 81 + 80 * groups - 1) / (80 * groups) + 3 * n;
+    const int64_t rest = by_sms > 34 * n ? by_sms : 34 * n;
+    return (size_t)(by_floor < rest ? by_floor : rest);
+}
+
 }  // namespace
 
 DecodePlan plan_decode_fp4(const pa_decode_params &p) {
@@ -733,10 +756,11 @@ DecodePlan plan_decode_fp4(const pa_decode_params &p) {
     }
     plan.kv_chunk = (int32_t)chunk;
     plan.max_splits = (int32_t)((seen + chunk - 1) / chunk) + 1;
-    const size_t rows = (size_t)p.num_seqs * p.num_q_heads * plan.max_splits;
-    const size_t header = 256 + (((size_t)p.num_seqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
-    const size_t obytes = (rows * p.head_dim * sizeof(float) + 255) / 256 * 256;
-    plan.workspace_bytes = header + obytes + rows * sizeof(float);
+    plan.workspace_bytes = workspace_of(p, (size_t)p.num_seqs * plan.max_splits);
+    // The automatic ranges get shorter with fewer sequences and with other
+    // bounds, so that a smaller batch can need more (32 query heads, 4096 keys: 4
+    // sequences 2.51 MB, 3 2.63 MB); the size reported holds them all.
+    plan.workspace_any = p.kv_chunk > 0 ? plan.workspace_bytes : workspace_of(p, most_slots(p, seen, lay.groups));
     return plan;
 }
 

@@ -460,7 +460,7 @@ static pa_status check_decode(const pa_decode_params *p) {
 
 size_t pa_decode_workspace_size(const pa_decode_params *p) {
     if (check_decode(p) != PA_OK) return 0;
-    return decode_plan(*p).workspace_bytes;
+    return decode_plan(*p).workspace_any;
 }
 
 int32_t pa_decode_kv_chunk(const pa_decode_params *p) {

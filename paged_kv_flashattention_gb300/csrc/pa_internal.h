@@ -41,7 +41,8 @@ struct DecodePlan {
     int32_t kv_chunk;
     int32_t max_splits;
     int32_t heads_per_cta;
-    size_t workspace_bytes;
+    size_t workspace_bytes;       // of this call
+    size_t workspace_any;         // of any call with num_seqs and max_seqlen_k up to these: the size reported
 };
 DecodePlan plan_decode(const pa_decode_params &p);
 DecodePlan plan_decode_fp4(const pa_decode_params &p);      // 4-bit pools (decode_fp4.cu)
