@@ -325,6 +325,7 @@ def rope_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     if q_out is None:
         q_out = torch.empty_like(q)
     _need(q_out, "q_out", torch.bfloat16, dev)
+    _need_at_least(q_out, "q_out", q.numel())
     p = _lib.RopeStoreParams(
         q=_ptr(q), q_out=_ptr(q_out), k=_ptr(k), v=_ptr(v), positions=_ptr(positions),
         cos_sin=_ptr(cos_sin), max_pos=cos_sin.shape[0], rot_dim=cos_sin.shape[1],
