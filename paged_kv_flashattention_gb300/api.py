@@ -586,11 +586,11 @@ def _prefill_params(q, k_cache, v_cache, page_table, cu_seqlens_q, cu_seqlens_k,
         _need_at_least(out, "out", q.numel())
         if not page_table.shape[0] + 1 >= cu_seqlens_k.numel() == cu_seqlens_q.numel() >= 1:
             raise ValueError("cu_seqlens_q and cu_seqlens_k must hold num_seqs + 1 entries, page_table a row per sequence")
-        if lse is not None and lse.shape[1] < total_q:
-            raise ValueError("lse must be [Hq, >= total_q] with unit inner stride")
     if lse is not None:
         _need(lse, "lse", torch.float32, dev, contiguous=False)
         if lse.dim() != 2 or lse.shape[0] != Hq or lse.stride(1) != 1:
+            raise ValueError("lse must be [Hq, >= total_q] with unit inner stride")
+        if kvd == PA_KV_FP4 and lse.shape[1] < total_q:
             raise ValueError("lse must be [Hq, >= total_q] with unit inner stride")
     if block_mask is not None:
         _need(block_mask, "block_mask", torch.uint8, dev)

@@ -21,3 +21,13 @@ def test_rotated_q(fp4):
     for small in (q[:2], torch.zeros((T, hq, d - 16), dtype=torch.bfloat16), q[:0]):
         with pytest.raises(ValueError, match="q_out"):
             pa.rope_store_kv(q, k, k, i, cs, i, *pools(fp4), q_out=small, **kw)
+
+
+@pytest.mark.parametrize("shape", [(8 * 3,), (3, 8, 1), (7, 3), (8, 2)])
+def test_prefill_lse(shape):
+    import paged_kv_flashattention_gb300 as pa
+    q = torch.zeros((3, 8, 64), dtype=torch.bfloat16)
+    pt, cu, g = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.ones(2)
+    with pytest.raises(ValueError, match="lse must be"):
+        pa.prefill(q, *pools(True), pt, cu, cu, 3, 64, lse=torch.zeros(shape), scheduler=torch.zeros(2, dtype=torch.int32),
+                   k_scale=g, v_scale=g, kv_dtype=pa.PA_KV_FP4)
