@@ -176,8 +176,8 @@ struct StepCursor {
 // ones, so persistent CTAs taking items round robin start with the longest
 // work.  Returns false for a hole (request b has fewer than k + 1 tiles).
 //
-// CLASSES, with a.classes > 0 (causal 4-bit calls without window and mask, at
-// most kMaxClassRows rows): k counts classes of 128 key positions from the
+// CLASSES, with a.classes > 0 (causal 4-bit calls without window and mask, more
+// items than CTAs, at most kMaxClassRows rows): k counts classes of 128 key positions from the
 // far end, and request b's item of a class is its tile whose first row lies
 // there, so the keys an item reads never grow along the list whatever the
 // requests' prefixes are.  Eight requests over prefixes of up to 4096 keys, 512
@@ -405,7 +405,11 @@ constexpr int kGatherWarpsMax = 3;
 // producer/MMA warpgroup lowers its to 128: 256 * 184 + 128 * 128 = 63,488.
 constexpr int kSoftmaxRegs = 184;
 // A row of the class list costs a 32nd of a warp's test, whether it has work or
-// not: 2048 rows are 64 tests, some 5 us when nearly all of them are holes.
+// not: 8 ns, 16 us at 2048 rows.  Classes against tile numbers, us, at the exact
+// bound on the keys and at one of 2048 rows: eight extend requests 193 and 206
+// against 215; sixteen over prefixes of up to 16384 keys (1824 rows) 460 against
+// 572; 500 prompts of up to 512 tokens (2000 rows) 1261 against 1429; but sixteen
+// prompts of 512 tokens 75 and 91 against 75.
 constexpr int kMaxClassRows = 2048;
 constexpr int kItemRing = 4;      // items published ahead of the consumers
 constexpr int kControlRegs = 128;
@@ -1299,7 +1303,14 @@ cudaError_t prefill_setup(const pa_prefill_params &p, PrefillArgs &a, int &T) {
     if (p.kv_dtype == PA_KV_FP4 && p.causal && p.sliding_window == 0 && p.block_mask == nullptr) {
         const int64_t longest = p.max_seqlen_k > p.max_seqlen_q ? p.max_seqlen_k : p.max_seqlen_q;
         const int64_t classes = (longest + kBM - 1) / kBM;
-        if (classes * p.num_seqs <= kMaxClassRows) max_tiles = a.classes = (int32_t)classes;
+        // With a CTA for every item the order changes nothing, and a loose bound on
+        // the keys costs only holes: three short requests 14 us, 30 in classes
+        // under a bound of 2046 rows.
+        const int64_t by_rows = (int64_t)p.total_q / kBM + p.num_seqs, by_bound = max_tiles * p.num_seqs;
+        const int64_t items = (by_rows < by_bound ? by_rows : by_bound) * (p.num_q_heads / T);
+        int64_t ctas = num_sms();
+        if (p.max_ctas > 0 && p.max_ctas < ctas) ctas = p.max_ctas;
+        if (items > ctas && classes * p.num_seqs <= kMaxClassRows) max_tiles = a.classes = (int32_t)classes;
     }
     const int64_t virt = max_tiles * p.num_seqs * (p.num_q_heads / T);
     if (virt > INT32_MAX) return cudaErrorNotSupported;
