@@ -1,5 +1,5 @@
 """Oracle of the 4-bit KV cache (numpy, fp64): the row format, its store and
-read-back, attention over 4-bit pools, and the batch plan from lengths.
+read-back, and attention over 4-bit pools.
 
 TEST INFRASTRUCTURE ONLY, like the rest of the package: nothing is shared with
 the library.  Everything is written from the format's definition in

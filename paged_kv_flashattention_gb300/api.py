@@ -543,7 +543,8 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_
     returns out bf16 [total_q, Hq, d]; lse (optional) fp32 [Hq, total_q].
     Pools are bf16, or E4M3 codes (uint8 / float8_e4m3fn) with fp32
     per-KV-head ``k_scale`` and ``v_scale``, or, with ``kv_dtype=PA_KV_FP4``,
-    4-bit rows with such scales (``store_kv_fp4``).  ``scheduler`` is the int32 [2]
+    4-bit rows with such scales (``store_kv_fp4``); on those q is rounded to
+    f16, so |q| must stay below 65504.  ``scheduler`` is the int32 [2]
     work-counter array of the launch (zero between launches); by default the
     array cached for the current stream (``prefill_scheduler``).
     ``block_mask``: optional uint8 [B, nq, nk] on the device; entry
@@ -698,8 +699,9 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_t
     """Split-KV decode: q bf16 [B, Hq, d] -> out bf16 [B, Hq, d]; lse fp32 [B, Hq].
     Pools are bf16, or E4M3 codes (uint8 / float8_e4m3fn) with fp32 per-KV-head
     ``k_scale`` and ``v_scale``, or, with ``kv_dtype=PA_KV_FP4``, 4-bit rows
-    with such scales (``store_kv_fp4``).  ``workspace`` (a uint8 CUDA tensor) is
-    allocated here when not given."""
+    with such scales (``store_kv_fp4``); on those q is rounded to f16, so |q|
+    must stay below 65504.  ``workspace`` (a uint8 CUDA tensor) is allocated
+    here when not given."""
     dev = q.device
     _need(q, "q", torch.bfloat16, dev)
     kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
