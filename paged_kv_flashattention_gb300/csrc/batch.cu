@@ -22,10 +22,11 @@
 // Every CTA reads that before it counts itself in cursor[1]; the CTA that counts
 // last moves cursor[0] past the pages taken and clears cursor[1], so nothing
 // waits and the next launch in the stream finds both ready.
-// Bound: launch latency and the CTA's prefix (two dependent passes over L2)
-// for a decode step (256 requests 7.3 us), the token table's 32-byte sectors
-// (one per page at page size 16) and the bisections for large tables (1000
-// requests of up to 8408 keys, 253,000 new tokens 9.4 us).
+// Bound: launch latency and the CTA's chain (two dependent passes over L2, three
+// prefix sums, 64-bit divisions per request and element) for a decode step (256
+// requests 7.5 us), the token table's 32-byte sectors (one per page at page size
+// 16), the bisections and the lengths read again per element for large tables
+// (1000 requests of up to 8408 keys, 253,000 new tokens 9.6 us).
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pdl.cuh"
@@ -36,7 +37,7 @@ PA_ERROR_WORD_ACCESSOR(error_word_batch)
 
 namespace {
 
-// Two CTAs of 512 threads per SM: 9.4 us on the 1000 requests; four of 256 12.5,
+// Two CTAs of 512 threads per SM: 9.6 us on the 1000 requests; four of 256 12.5,
 // one of 1024 10.5, four of 512 11.4 (every CTA forms the prefixes).
 constexpr int kThreads = 512;
 constexpr int kCtasPerSm = 2;

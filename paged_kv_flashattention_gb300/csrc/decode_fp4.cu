@@ -38,9 +38,11 @@
 // and addresses).  256 log-uniform contexts up to 32768 (2.38 GB): 423 us, 5.6
 // TB/s, 0.83 of the measured copy bandwidth; one unit at a time 428 us, with
 // 64-bit walks and six more live registers 448 (more spills), 472 before the
-// pairs.
+// pairs.  As built <128, 8> has 96 registers, for two CTAs an SM, and spills 80
+// bytes a thread.
 // At D = 64 half the bytes come with more than half the instructions: 64
-// sequences of up to 4096 keys 24 us, 0.40.
+// sequences of up to 4096 keys 24 us, 0.40.  One sequence of 20011 keys takes 14.8
+// us: ranges sized by SMs fill half of the CTA slots.
 #include <cuda_bf16.h>
 
 #include <atomic>

@@ -15,9 +15,10 @@
 // loads a token's cos / sin once for all its heads while a short one still
 // spreads over the GPU.  The rotary gives a lane both members of its eight
 // pairs; keys then change places by shuffles for the quantiser.
-// Bound: long batches by issue and the latency of the loads in flight (8192
-// tokens: rotary 4.7 TB/s, store 3.6, load 4.4), short ones by launch latency (2
-// to 4 us).
+// Bound: long batches by the latency of their loads, which wait for the token's
+// slot (and position), and by issue (8192 tokens: rotary 4.8 TB/s, store 3.6, load
+// 4.4; neither issue, 56 to 64 %, nor DRAM is full), short ones by launch latency
+// (2 to 4 us).
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"

@@ -65,9 +65,10 @@
 // What bounds it: the softmax chain of the bf16 kernel, and beside it the two
 // warps' way from a landed tile to a widened one (about 1500 clocks a tile, of
 // a period of 2000).  Eight extend requests over prefixes of up to 4096 keys (171
-// GFLOP): as built 191 us.  Timing copies of an earlier state, 200 us: without
+// GFLOP): as built 193 us.  Timing copies of an earlier state, 200 us: without
 // the conversion 190, without the product with the scale 185, without the reads of
-// the landed tile 190, with nothing widened 179.
+// the landed tile 190, with nothing widened 179.  At the launch's 168 registers
+// <128, 2> spills 100 bytes a thread.
 // Slower, each against the kernel it was tried on (241 to 191 us): the scales as a
 // second TMA box per page (+8) or read by the widening warps from global memory
 // (+94); a fourth warpgroup for the widening (+7 to +57: the softmax spills); one
@@ -177,12 +178,12 @@ struct StepCursor {
 // work.  Returns false for a hole (request b has fewer than k + 1 tiles).
 //
 // CLASSES, with a.classes > 0 (causal 4-bit calls without window and mask, more
-// items than CTAs, at most kMaxClassRows rows): k counts classes of 128 key positions from the
-// far end, and request b's item of a class is its tile whose first row lies
-// there, so the keys an item reads never grow along the list whatever the
-// requests' prefixes are.  Eight requests over prefixes of up to 4096 keys, 512
-// items on 152 CTAs: the busiest CTA's share of the steps falls from 1.20 to
-// 1.03 of the mean.
+// items than CTAs, at most kMaxClassRows rows): k counts classes of 128 key
+// positions from the far end, and request b's item of a class is its tile whose
+// first row lies there, so the keys an item reads never grow along the list
+// whatever the requests' prefixes are.  Eight requests over prefixes of up to
+// 4096 keys, 512 items on 152 CTAs: the busiest CTA's share of the steps falls
+// from 1.20 to 1.03 of the mean.
 template <int T, bool EXT = false, bool CLASSES = false>
 __device__ __forceinline__ bool prefill_item(const PrefillArgs &a, int v, PrefillItem &it) {
     const int groups = a.num_q_heads / T;
