@@ -17,6 +17,9 @@
  *   pa_decode_noalloc    the same, with fixed library-owned split scratch
  *   pa_mixed_batch       a continuous batch (prefill + decode) in one launch
  *   pa_lse_combine       merge of split partial results by log-sum-exp
+ *   pa_decode_shared     decode of sequences that share prefixes, each prefix read once
+ *   pa_beam_select       beam search: the best continuations over beams and vocabulary
+ *   pa_beam_reorder      the paged states follow the beams that were chosen
  *
  * Sources (web pages; section names as printed on them):
  *  [T] "Transformer inference kernels: GEMM·Attention·FlashAttention·Fusion
@@ -561,6 +564,158 @@ pa_status pa_decode_noalloc(const pa_decode_params *p, void *stream);
 pa_status pa_lse_combine(const float *o_partial, const float *lse_partial,
                          const int32_t *splits_per_row, int32_t num_rows, int32_t max_splits,
                          int32_t head_dim, void *out, float *lse_out, void *stream);
+
+/*
+ * pa_decode_shared - pa_decode for a batch in which groups of sequences share
+ * their first keys (beams or samples of one request, requests behind one
+ * system prompt; [M]'s prefix caching puts the same pages in their table
+ * rows).  The result is pa_decode's, but the keys that a group shares are
+ * read once for the group and not once for each sequence:
+ *   keys [0, P) of group g through the table row of the group's first
+ *   sequence, keys [P, cache_seqlens[b]) through sequence b's own row,
+ *   P = prefix_lens[b], the same for every sequence of the group,
+ * merged by log-sum-exp ([T] s.12 and s.16).  P need not be a multiple of the
+ * page size (the first sequence's row then gives the prefix's last page and
+ * each other row a page of its own that holds the same keys).
+ *  - Groups are runs of consecutive sequences: group g is sequences
+ *    cu_groups[g] .. cu_groups[g+1] - 1, cu_groups[0] = 0; it may be empty.
+ *    Sequences from cu_groups[num_groups] on belong to no group; their
+ *    prefix_lens are 0 and they are decoded as pa_decode does.
+ *  - A sequence with cache_seqlens 0 (a padding row) gives O = 0, lse = -inf
+ *    whatever its group's prefix is, but the first sequence of a group has
+ *    to hold the prefix's pages in its row.
+ *  - Device data that breaks the bounds of the call raises
+ *    PA_DEVERR_SEQLENS: a group that is longer than max_group or not a run of
+ *    the batch, a prefix that is longer than max_prefix or than its
+ *    sequence, that differs from its group's or has no group, more than
+ *    max_suffix keys behind it.  Such a sequence's output is undefined (but
+ *    written); nothing outside the pools and the outputs is touched.
+ *  - Arithmetic: as pa_prefill over the prefix and pa_decode behind it, on
+ *    each type of pool; the partials are 32 bits.
+ *  - dec.sliding_window, dec.max_ctas and dec.overlap_previous must be 0.
+ *  - The workspace (pa_decode_shared_workspace_size bytes) serves every call
+ *    with bounds and counts up to these.  Calls that may run at the same time
+ *    need one each.
+ */
+typedef struct {
+    pa_decode_params dec;        /* as for pa_decode; lse optional */
+    const int32_t *cu_groups;    /* device int32 [num_groups + 1] */
+    const int32_t *prefix_lens;  /* device int32 [num_seqs] */
+    int32_t num_groups;          /* 0: pa_decode (cu_groups and prefix_lens are not read) */
+    int32_t max_group;           /* >= the sequences of every group; <= num_seqs */
+    int32_t max_prefix;          /* >= every prefix; <= max_seqlen_k */
+    int32_t max_suffix;          /* >= the keys of every sequence behind its prefix; <= max_seqlen_k */
+} pa_decode_shared_params;
+
+/* Reads only host fields of *p; 0 for parameters that the call would refuse. */
+size_t pa_decode_shared_workspace_size(const pa_decode_shared_params *p);
+pa_status pa_decode_shared(const pa_decode_shared_params *p, void *stream);
+
+/*
+ * pa_beam_select - the selection step of beam search ([M]'s sampling step, for
+ * beams; the pages do not describe beam search, this library's reading is the
+ * usual one).  For group g with its beams k and x the logits of a beam:
+ *   total[k, v] = scores[g, k] + x[k, v] - ln sum_w exp(x[k, w])
+ *   the num_out largest totals of the group, largest first, equal ones by
+ *   k * vocab + v, smallest first: their totals, beams and tokens.
+ * Totals are formed and compared in 64 bits (their order decides which beams
+ * live on) and rounded to fp32 once.  Of a row's exponentials those of its
+ * largest logits are summed in 64 bits, the others in 32.
+ *  - finished (optional): a beam with a non-zero entry has ended; it offers
+ *    itself with pad_token and total scores[g, k], its logits are not read.
+ *  - A logit that is NaN or +inf counts as -inf, as does a score.  Candidates
+ *    of total -inf come last (banned words, beams of score -inf, the other
+ *    tokens of a finished beam), in the order of k * vocab + v.
+ *  - A row starts at element row * logits_stride for row = g * beams + k; any
+ *    stride >= vocab, and logits aligned to 16 bytes.
+ *  - 1 <= beams <= 64, 1 <= num_out <= 128 and <= vocab, vocab < 2^24,
+ *    num_groups * beams <= 65535.
+ * The workspace may be shared by calls that follow one another.
+ */
+typedef enum { PA_LOGITS_BF16 = 0, PA_LOGITS_F16 = 1, PA_LOGITS_F32 = 2 } pa_logits_dtype;
+typedef struct {
+    const void *logits;          /* device [num_groups * beams, logits_stride] */
+    int32_t logits_dtype;        /* pa_logits_dtype */
+    int64_t logits_stride;       /* elements */
+    const float *scores;         /* device fp32 [num_groups, beams] */
+    const uint8_t *finished;     /* device [num_groups, beams] or NULL */
+    int32_t pad_token;           /* 0 <= pad_token < vocab */
+    int32_t num_groups;
+    int32_t beams;
+    int32_t vocab;
+    int32_t num_out;
+    float *out_scores;           /* device fp32 [num_groups, num_out]; may be scores itself if num_out = beams */
+    int32_t *out_parents;        /* device int32 [num_groups, num_out]: beam of the group */
+    int32_t *out_tokens;         /* device int32 [num_groups, num_out] */
+    void *workspace;             /* device, 16-byte aligned */
+    size_t workspace_bytes;
+} pa_beam_select_params;
+
+size_t pa_beam_select_workspace_size(const pa_beam_select_params *p);
+pa_status pa_beam_select(const pa_beam_select_params *p, void *stream);
+
+/*
+ * pa_beam_reorder - the paged states follow a selection: sequence i of a group
+ * becomes the continuation of its parent p = parents[g, i] (an index in the
+ * group).  With L = seqlens of the sequences, the same for a whole group, and
+ * row(i) the token-table row table_idx[g * beams + i]:
+ *   for a sequence with p != i, all from the state before the call:
+ *     slots [prefix, L - L % page_size) of row(i) become row(p)'s: full pages
+ *     are shared, nothing writes to them any more;
+ *     if L % page_size != 0, the last page's L % page_size rows of K and V are
+ *     copied, in every pool, from row(p)'s last page to page spare_pages[i];
+ *     row(i)'s last L % page_size slots are that page's, and spare_pages[i]
+ *     becomes the page that row(i) had there;
+ *     history row i (optional) becomes history row p.
+ *   A sequence with p = i stays as it is.
+ * So a sequence writes to pages of its own only: its last page while that is
+ * partly filled, and its spare page, both its alone before and after the call
+ * (for sequences that start from a shared prompt: rows that already name
+ * pages of their own for the prompt's partly filled last page; the first call,
+ * with the prompt's beam as every parent, fills them).  Page size 1 copies no
+ * rows and does not read spare_pages.  No lengths change; the next token's
+ * slot is the plan's business (pa_build_batch_from goes on with the last page
+ * while it has room).
+ *  - prefix_lens (optional): slots below prefix_lens[i] are the same in every
+ *    row of the group and are left alone.
+ *  - Columns of a row from L on, and rows that table_idx does not name, stay as
+ *    they are.
+ *  - Device data that breaks the bounds: a parent outside [0, beams) counts
+ *    as the sequence itself, as does a table_idx outside the table (its own or
+ *    its parent's): PA_DEVERR_TABLE_INDEX; a group whose lengths differ, are
+ *    negative or longer than max_seqlen_k is left alone: PA_DEVERR_SEQLENS; a
+ *    page outside the pools is not copied: PA_DEVERR_PAGE_RANGE.
+ *  - Entries of table_idx, spare pages and partly filled last pages occur once
+ *    each; no buffer of the call lies on another.
+ * Pools are rows of row_bytes bytes (bf16, E4M3 or 4-bit rows alike), a
+ * multiple of 16, [num_pages, page_size, row_bytes], the same for all
+ * num_pools of them (K and V of every layer).  The pointers are read during
+ * the call, on the host.
+ */
+#define PA_BEAM_REORDER_MAX_POOLS 256
+typedef struct {
+    const int32_t *parents;      /* device int32 [num_groups, beams] */
+    int32_t num_groups;
+    int32_t beams;               /* <= 64 */
+    int32_t page_size;
+    int32_t max_seqlen_k;        /* >= every length; <= token_table_stride */
+    int32_t *token_table;        /* device int32 [token_table_rows, token_table_stride] */
+    int64_t token_table_stride;
+    int64_t token_table_rows;
+    const int32_t *table_idx;    /* device int32 [num_groups * beams] */
+    const int32_t *seqlens;      /* device int32 [num_groups * beams] */
+    const int32_t *prefix_lens;  /* device int32 [num_groups * beams] or NULL */
+    int32_t *spare_pages;        /* device int32 [num_groups * beams]; NULL with page_size 1 */
+    void *const *pools;          /* HOST array of num_pools device pointers */
+    int32_t num_pools;           /* 0 .. PA_BEAM_REORDER_MAX_POOLS */
+    int64_t num_pages;
+    int64_t row_bytes;
+    int32_t *history;            /* device int32 [num_groups * beams, history_stride] or NULL */
+    int64_t history_stride;
+    int32_t history_len;         /* columns that move */
+} pa_beam_reorder_params;
+
+pa_status pa_beam_reorder(const pa_beam_reorder_params *p, void *stream);
 
 #ifdef __cplusplus
 }

@@ -9,9 +9,10 @@ provides device memory and streams only.
 """
 from .api import (PA_DEVERR_NO_PAGES, PA_DEVERR_PAGE_RANGE, PA_DEVERR_POSITION, PA_DEVERR_SEQLENS, PA_DEVERR_TABLE_INDEX,
                   PA_DEVERR_TIMEOUT, PA_KV_BF16, PA_KV_FP4, PA_KV_FP8_E4M3, PA_MIXED_SCHEDULER_INTS, PagedAttentionError,
-                  abi_version,
+                  abi_version, beam_reorder, beam_select, beam_select_workspace_size,
                   build_batch, build_page_table,
-                  build_seqlens, decode, decode_noalloc, decode_kv_chunk, decode_workspace_size,
+                  build_seqlens, decode, decode_noalloc, decode_kv_chunk, decode_shared, decode_shared_workspace_size,
+                  decode_workspace_size,
                   device_error, fp4_row_bytes, load_kv_fp4, lse_combine, mixed_batch, prefill, prefill_scheduler, rope_cos_sin_table,
                   rope_store_kv, store_kv, store_kv_fp4, store_kv_fp8)
 
@@ -20,7 +21,8 @@ from .metadata import BatchPlanner
 
 __all__ = [
     "PagedAttentionError", "abi_version", "build_batch", "BatchPlanner", "build_page_table", "build_seqlens", "decode",
-    "decode_noalloc",
+    "decode_noalloc", "decode_shared", "decode_shared_workspace_size", "beam_select", "beam_select_workspace_size",
+    "beam_reorder",
     "decode_kv_chunk", "decode_workspace_size", "device_error", "lse_combine", "mixed_batch", "prefill",
     "prefill_scheduler",
     "DecodeGraphRunner", "bucket_for",

@@ -71,6 +71,30 @@ class BatchParams(ctypes.Structure):
     ]
 
 
+class DecodeSharedParams(ctypes.Structure):
+    _fields_ = [
+        ("dec", DecodeParams), ("cu_groups", c_p), ("prefix_lens", c_p), ("num_groups", c_i32), ("max_group", c_i32),
+        ("max_prefix", c_i32), ("max_suffix", c_i32),
+    ]
+
+
+class BeamSelectParams(ctypes.Structure):
+    _fields_ = [
+        ("logits", c_p), ("logits_dtype", c_i32), ("logits_stride", c_i64), ("scores", c_p), ("finished", c_p),
+        ("pad_token", c_i32), ("num_groups", c_i32), ("beams", c_i32), ("vocab", c_i32), ("num_out", c_i32),
+        ("out_scores", c_p), ("out_parents", c_p), ("out_tokens", c_p), ("workspace", c_p), ("workspace_bytes", c_size),
+    ]
+
+
+class BeamReorderParams(ctypes.Structure):
+    _fields_ = [
+        ("parents", c_p), ("num_groups", c_i32), ("beams", c_i32), ("page_size", c_i32), ("max_seqlen_k", c_i32),
+        ("token_table", c_p), ("token_table_stride", c_i64), ("token_table_rows", c_i64), ("table_idx", c_p),
+        ("seqlens", c_p), ("prefix_lens", c_p), ("spare_pages", c_p), ("pools", ctypes.POINTER(c_p)), ("num_pools", c_i32),
+        ("num_pages", c_i64), ("row_bytes", c_i64), ("history", c_p), ("history_stride", c_i64), ("history_len", c_i32),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "pa_abi_version": (ctypes.c_int, []),
@@ -95,6 +119,11 @@ SIGNATURES = {
     "pa_decode_noalloc": (ctypes.c_int, [ctypes.POINTER(DecodeParams), c_p]),
     "pa_mixed_batch": (ctypes.c_int, [ctypes.POINTER(PrefillParams), ctypes.POINTER(DecodeParams), c_p]),
     "pa_lse_combine": (ctypes.c_int, [c_p, c_p, c_p, c_i32, c_i32, c_i32, c_p, c_p, c_p]),
+    "pa_decode_shared_workspace_size": (c_size, [ctypes.POINTER(DecodeSharedParams)]),
+    "pa_decode_shared": (ctypes.c_int, [ctypes.POINTER(DecodeSharedParams), c_p]),
+    "pa_beam_select_workspace_size": (c_size, [ctypes.POINTER(BeamSelectParams)]),
+    "pa_beam_select": (ctypes.c_int, [ctypes.POINTER(BeamSelectParams), c_p]),
+    "pa_beam_reorder": (ctypes.c_int, [ctypes.POINTER(BeamReorderParams), c_p]),
 }
 
 

@@ -826,3 +826,241 @@ def lse_combine(o_partial: torch.Tensor, lse_partial: torch.Tensor,
     _check(lib.pa_lse_combine(_ptr(o_partial), _ptr(lse_partial), _ptr(splits_per_row), R, S, d,
                               _ptr(out), _ptr(lse), _stream(o_partial)), lib)
     return out
+
+
+def _shared_bounds(B: int, max_seqlen_k: int, max_prefix, max_suffix, max_group):
+    """The bounds of a decode over shared prefixes, by default the batch's own."""
+    return (B if max_group is None else int(max_group), max_seqlen_k if max_prefix is None else int(max_prefix),
+            max_seqlen_k if max_suffix is None else int(max_suffix))
+
+
+def decode_shared_workspace_size(q_shape, k_cache: torch.Tensor, max_seqlen_k: int, num_groups: int, *,
+                                 max_prefix: int | None = None, max_suffix: int | None = None, max_group: int | None = None,
+                                 page_size: int | None = None, kv_chunk: int = 0, kv_dtype: int | None = None,
+                                 num_kv_heads: int | None = None) -> int:
+    """Workspace bytes of ``decode_shared`` for a batch of shape ``q_shape``
+    in up to ``num_groups`` groups, under these bounds (``decode_shared`` says
+    what they bound).  4-bit pools need ``kv_dtype=PA_KV_FP4`` and
+    ``num_kv_heads``."""
+    dec = _decode_sizes(q_shape, k_cache, max_seqlen_k, page_size, kv_chunk, kv_dtype, num_kv_heads)
+    bounds = _shared_bounds(int(q_shape[0]), int(max_seqlen_k), max_prefix, max_suffix, max_group)
+    lib = _lib.load()
+    need = int(lib.pa_decode_shared_workspace_size(ctypes.byref(_lib.DecodeSharedParams(dec, None, None, int(num_groups), *bounds))))
+    if need == 0:
+        raise ValueError(lib.pa_last_error().decode(errors="replace"))
+    return need
+
+
+def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                  cache_seqlens: torch.Tensor, max_seqlen_k: int, cu_groups: torch.Tensor, prefix_lens: torch.Tensor, *,
+                  max_prefix: int | None = None, max_suffix: int | None = None, max_group: int | None = None,
+                  scale: float | None = None, page_size: int | None = None, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, kv_chunk: int = 0,
+                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                  kv_dtype: int | None = None) -> torch.Tensor:
+    """``decode`` of a batch in which groups of consecutive sequences share
+    their first keys; each group's prefix is read once (``pa_decode_shared``).
+    q bf16 [B, Hq, d] -> out bf16 [B, Hq, d]; lse fp32 [B, Hq]; pools as for
+    ``decode``.  cu_groups: int32 [num_groups + 1], group g is sequences
+    cu_groups[g] .. cu_groups[g+1] - 1; prefix_lens: int32 [B], the keys that
+    sequence b shares with its group, equal within one, read through the
+    page-table row of its first sequence, 0 for sequences behind the last
+    group.  ``max_prefix`` and ``max_suffix`` bound the keys of a sequence in
+    its prefix and behind it (default max_seqlen_k), ``max_group`` the
+    sequences of a group (default B); tight bounds make a small workspace and
+    few idle CTAs."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, _ = q.shape
+    kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
+    if kvd != PA_KV_FP4:                              # (4-bit pools: _fp4_geometry)
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, n, k_cache.dtype, dev)
+    for t, n in ((cache_seqlens, "cache_seqlens"), (cu_groups, "cu_groups"), (prefix_lens, "prefix_lens")):
+        _need(t, n, torch.int32, dev)
+    _need_rows(page_table, "page_table", dev)
+    if cache_seqlens.numel() != B or prefix_lens.numel() != B or page_table.shape[0] < B:
+        raise ValueError("cache_seqlens and prefix_lens must hold one entry per sequence, page_table a row")
+    if cu_groups.numel() < 1:
+        raise ValueError("cu_groups must hold num_groups + 1 entries")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, dev)
+    if out.numel() != q.numel():
+        raise ValueError("out must have q's size")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev)
+        if lse.numel() != B * Hq:
+            raise ValueError("lse must be [B, Hq]")
+    max_k, groups = int(max_seqlen_k), cu_groups.numel() - 1
+    bounds = _shared_bounds(B, max_k, max_prefix, max_suffix, max_group)
+    if workspace is None:
+        need = decode_shared_workspace_size(
+            q.shape, k_cache, max_k, groups, max_group=bounds[0], max_prefix=bounds[1], max_suffix=bounds[2], page_size=page_size,
+            kv_chunk=kv_chunk, kv_dtype=kvd, num_kv_heads=k_scale.numel() if kvd == PA_KV_FP4 and k_scale is not None else None)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    dec = _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_k, scale, page_size, out, lse, workspace, kv_chunk,
+                         k_scale, v_scale, kv_dtype=kvd)
+    dec.page_table_stride = max(page_table.stride(0), page_table.shape[1])
+    if page_table.shape[1] * dec.page_size < max_k:
+        raise ValueError(f"page_table must have ceil({max_k} / {dec.page_size}) columns")
+    p = _lib.DecodeSharedParams(dec, cu_groups.data_ptr(), prefix_lens.data_ptr(), groups, *bounds)
+    _call(_lib.load().pa_decode_shared, q, ctypes.byref(p))
+    return out
+
+
+_LOGITS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+@functools.lru_cache(maxsize=256)
+def _select_workspace(groups: int, beams: int, vocab: int, num_out: int) -> int:
+    lib = _lib.load()
+    p = _lib.BeamSelectParams(num_groups=groups, beams=beams, vocab=vocab, num_out=num_out)
+    need = int(lib.pa_beam_select_workspace_size(ctypes.byref(p)))
+    message = lib.pa_last_error().decode(errors="replace")
+    if message:
+        raise ValueError(message)
+    return need
+
+
+def beam_select_workspace_size(num_groups: int, beams: int, vocab: int, num_out: int) -> int:
+    """Workspace bytes of ``beam_select`` for these sizes."""
+    return _select_workspace(int(num_groups), int(beams), int(vocab), int(num_out))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None = None, *,
+                finished: torch.Tensor | None = None, pad_token: int = 0, out_scores: torch.Tensor | None = None,
+                parents: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None):
+    """Beam search's selection (``pa_beam_select``): per group the ``num_out``
+    (default: the number of beams) largest of scores + log_softmax(logits)
+    over beams and vocabulary.  logits: bf16, fp16 or fp32 [groups * beams, V]
+    or [groups, beams, V], rows of unit stride at any distance; scores: fp32
+    [groups, beams]; finished: uint8 or bool [groups, beams], non-zero for a
+    beam that has ended (it offers itself, with ``pad_token``).  Returns
+    (scores fp32, parents int32, tokens int32), each [groups, num_out], best
+    first, equal totals by the lower beam, then the lower token; out_scores
+    may be ``scores``."""
+    dev = logits.device
+    if logits.dtype not in _LOGITS_DTYPES:
+        raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    _need(scores, "scores", torch.float32, dev)
+    if scores.dim() != 2:
+        raise ValueError("scores must be [groups, beams]")
+    G, K = scores.shape
+    if logits.dim() == 3 and logits.shape[:2] == (G, K):
+        if G > 1 and K > 1 and logits.stride(0) != K * logits.stride(1):
+            raise ValueError("the rows of logits must lie at one distance from each other")
+        stride = logits.stride(1) if K > 1 else logits.stride(0)
+    elif logits.dim() == 2 and logits.shape[0] == G * K:
+        stride = logits.stride(0)
+    else:
+        raise ValueError(f"logits must be [{G * K}, V] or [{G}, {K}, V]")
+    V = logits.shape[-1]
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("the rows of logits must have unit stride")
+    if G * K <= 1:
+        stride = max(stride, V)
+    n = K if num_out is None else int(num_out)
+    if finished is not None:
+        if finished.dtype not in (torch.uint8, torch.bool):
+            raise TypeError(f"finished must be uint8 or bool, got {finished.dtype}")
+        _need(finished, "finished", finished.dtype, dev)
+        if finished.shape != (G, K):
+            raise ValueError("finished must be [groups, beams]")
+    outs = []
+    for t, name, dtype in ((out_scores, "out_scores", torch.float32), (parents, "parents", torch.int32),
+                           (tokens, "tokens", torch.int32)):
+        if t is None:
+            t = torch.empty((G, n), dtype=dtype, device=dev)
+        else:
+            _need(t, name, dtype, dev)
+            if t.shape != (G, n):
+                raise ValueError(f"{name} must be [{G}, {n}]")
+        outs.append(t)
+    if workspace is None:
+        workspace = torch.empty(_select_workspace(G, K, V, n), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    p = _lib.BeamSelectParams(
+        logits.data_ptr(), _LOGITS_DTYPES[logits.dtype], stride, scores.data_ptr(), _ptr(finished), int(pad_token), G, K, V, n,
+        outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size())
+    _call(_lib.load().pa_beam_select, logits, ctypes.byref(p))
+    return tuple(outs)
+
+
+def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor, seqlens: torch.Tensor,
+                 spare_pages: torch.Tensor | None, k_caches, v_caches, *, page_size: int | None = None,
+                 prefix_lens: torch.Tensor | None = None, history: torch.Tensor | None = None,
+                 max_seqlen_k: int | None = None) -> None:
+    """The paged states follow a selection, in place (``pa_beam_reorder``):
+    sequence i of a group becomes the continuation of sequence parents[g, i].
+    parents: int32 [groups, beams]; token_table: int32 [rows, width];
+    table_idx, seqlens, spare_pages, prefix_lens: int32 [groups * beams], the
+    lengths equal within a group; k_caches, v_caches: the pools of every layer
+    (lists, or one tensor each), all of one shape, [num_pages, page_size, ...]
+    or, with ``page_size``, [slots, ...]; history: int32 [groups * beams, T].
+    A moved sequence shares its parent's full pages, and the parent's partly
+    filled last page is copied into its spare page; its own last page becomes
+    its spare page.  ``spare_pages`` may be None with page size 1.
+    ``max_seqlen_k`` (default: the table's width) bounds the lengths."""
+    dev = token_table.device
+    k_caches = [k_caches] if isinstance(k_caches, torch.Tensor) else list(k_caches)
+    v_caches = [v_caches] if isinstance(v_caches, torch.Tensor) else list(v_caches)
+    pools = k_caches + v_caches
+    if len(k_caches) != len(v_caches) or not pools:
+        raise ValueError("k_caches and v_caches must hold one pool per layer")
+    first = pools[0]
+    for t in pools:
+        _need(t, "every pool", first.dtype, dev)
+        if t.shape != first.shape:
+            raise ValueError("the pools must have one shape")
+    P = page_size
+    if P is None:
+        if first.dim() < 3:
+            raise ValueError("page_size is required for [slots, row] pools")
+        P = first.shape[1]
+    P = int(P)
+    if first.dim() == 4 or (first.dim() == 3 and page_size is None) or (first.dim() == 3 and first.dtype == torch.uint8 and
+                                                                        first.shape[1] == P):
+        if first.shape[1] != P:
+            raise ValueError("page_size does not match the pool shape")
+        num_pages, slots = first.shape[0], first.shape[0] * P
+    else:
+        slots = first.shape[0]
+        num_pages = slots // P if P > 0 else 0
+    row_bytes = first.numel() // max(slots, 1) * first.element_size()
+    _need(parents, "parents", torch.int32, dev)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [groups, beams]")
+    G, K = parents.shape
+    _need_rows(token_table, "token_table", dev)
+    width = token_table.shape[1]
+    max_k = width if max_seqlen_k is None else int(max_seqlen_k)
+    if max_k > width:
+        raise ValueError(f"token_table must be at least {max_k} wide")
+    if spare_pages is None and P > 1:
+        raise ValueError("spare_pages is required for page sizes over 1")
+    for t, name in ((table_idx, "table_idx"), (seqlens, "seqlens"), (spare_pages, "spare_pages"), (prefix_lens, "prefix_lens")):
+        if t is not None:
+            _need(t, name, torch.int32, dev)
+            if t.numel() != G * K:
+                raise ValueError(f"{name} must hold one entry per sequence ({G * K})")
+    if history is not None:
+        _need_rows(history, "history", dev)
+        if history.shape[0] != G * K:
+            raise ValueError(f"history must have a row per sequence ({G * K})")
+    p = _lib.BeamReorderParams(
+        parents=parents.data_ptr(), num_groups=G, beams=K, page_size=P, max_seqlen_k=max_k, token_table=token_table.data_ptr(),
+        token_table_stride=max(token_table.stride(0), width), token_table_rows=token_table.shape[0],
+        table_idx=table_idx.data_ptr(), seqlens=seqlens.data_ptr(), prefix_lens=_ptr(prefix_lens), spare_pages=_ptr(spare_pages),
+        pools=(ctypes.c_void_p * len(pools))(*[t.data_ptr() for t in pools]), num_pools=len(pools), num_pages=num_pages,
+        row_bytes=row_bytes, history=_ptr(history) or None if history is not None and history.numel() else None,
+        history_stride=max(history.stride(0), history.shape[1]) if history is not None else 0,
+        history_len=history.shape[1] if history is not None and history.numel() else 0)
+    _call(_lib.load().pa_beam_reorder, token_table, ctypes.byref(p))

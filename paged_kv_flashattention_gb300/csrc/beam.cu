@@ -1,0 +1,638 @@
+// Beam search over a paged cache: the selection over beams and vocabulary, and
+// the reordering of the paged states that follows it.
+//
+// Selection.  total[k, v] = score[k] + x[k, v] - lse[k], the n largest of a
+// group's beams * V totals.  Within a row the order is that of x, so one pass
+// over the logits finds each chunk's n largest and its part of lse; a second
+// launch, one CTA per group, forms lse and the totals in 64 bits and merges the
+// chunks' lists.
+//   - A chunk keeps a threshold that at least n of its elements reach: at first
+//     the least of its warps' ceil(n / 8)-th largest thread maxima of the first
+//     tile, then the n-th largest found.  Elements above it go to a buffer in
+//     shared memory (with n = 8 about 22 of the first 2048, fewer of every later
+//     tile), all others into the sum of exponentials at once, with the threshold
+//     as reference: it bounds them.  A buffer that fills up is cut to its n
+//     largest.  An entry's rank among the buffer's is its place in the list.
+//   - Two candidates of different beams are ordered by sums that differ by
+//     lse: an error of lse of 1e-7 swaps neighbours of a batch of 64 groups once
+//     in a hundred steps.  So the n largest exponentials are summed in 64 bits,
+//     and the rest, each off by about 2^-22 of itself, in 32 per thread over a few
+//     hundred elements and then in 64: about 1e-8 of the sum.
+//   - Columns belong to threads by their number, whatever the row's alignment,
+//     so that equal rows give equal sums and their ties go by index.
+//
+// Reordering.  Rows of the partly filled last pages are one contiguous run of a
+// page, copied into the child's spare page first (CTAs of one sequence and a few
+// pools each); a second launch permutes the token-table rows and histories, a
+// thread per column, which holds the column's values of all beams.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pdl.cuh"
+
+namespace pa {
+
+PA_ERROR_WORD_ACCESSOR(error_word_beam)
+
+namespace {
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kElems = 8;                            // columns of a thread in a tile
+constexpr int kTile = kSelThreads * kElems;
+constexpr int kKept = 512;                           // entries that stay in the buffer between tiles
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct ChunkSum {
+    double top;                   // the chunk's largest logit (-inf: no finite one)
+    double sum;                   // sum of exp(x - top)
+};
+
+struct SelectArgs {
+    const void *logits;
+    int64_t stride;
+    const float *scores;
+    const uint8_t *finished;
+    int32_t pad, groups, beams, vocab, n;
+    int32_t chunks, chunk;        // chunks of a row, columns of a chunk (a multiple of kTile)
+    float2 *lists;                // [rows][chunks][n]: logit, column as bits (0xffffffff: none)
+    ChunkSum *sums;               // [rows][chunks]
+    float *out_scores;
+    int32_t *out_parents;
+    int32_t *out_tokens;
+};
+
+// Scores that are no numbers count as -inf.
+__device__ __forceinline__ float cleaned(float x) { return x < INFINITY ? x : -INFINITY; }
+
+__device__ __forceinline__ bool beam_reads(const SelectArgs &a, int row) {
+    return !(a.finished != nullptr && a.finished[row] != 0) && cleaned(a.scores[row]) != -INFINITY;
+}
+
+// Floats as unsigned words in the same order; -0 as 0.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+// A larger logit, then a smaller column, gives a larger key.
+__device__ __forceinline__ uint64_t key_of(float x, int col) { return (uint64_t)ordered(x) << 32 | (uint32_t)~col; }
+__device__ __forceinline__ float key_value(uint64_t k) { return unordered((uint32_t)(k >> 32)); }
+
+template <int DT>
+__device__ __forceinline__ float element(const void *row, int64_t i) {
+    if constexpr (DT == PA_LOGITS_F32) return static_cast<const float *>(row)[i];
+    else if constexpr (DT == PA_LOGITS_F16) return __half2float(static_cast<const __half *>(row)[i]);
+    else return __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i]);
+}
+
+// kElems columns as loaded: whole 16-byte words that begin `skew` bytes before the
+// first column, or (skew 0 then) single elements.
+template <int DT>
+struct Columns {
+    static constexpr int kBytes = DT == PA_LOGITS_F32 ? 4 : 2;
+    static constexpr int kWords = kElems * kBytes / 4;
+    uint32_t w[kWords + 4];
+    bool whole;
+
+    // Columns col .. of a row that ends at `end`, -inf behind it.  Words are read
+    // only if they end inside the row.
+    __device__ __forceinline__ void load(const uint8_t *row, int skew, int col, int end) {
+        whole = col + kElems + (skew != 0 ? 16 / kBytes : 0) <= end;
+        if (whole) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(row + (int64_t)col * kBytes - skew);
+#pragma unroll
+            for (int i = 0; i < kWords / 4 + 1; ++i) {
+                if (i == kWords / 4 && skew == 0) break;
+                const uint4 v = p[i];
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        } else {
+            uint32_t e[kElems];
+#pragma unroll
+            for (int i = 0; i < kElems; ++i) {
+                const bool in = col + i < end;
+                if constexpr (kBytes == 4) e[i] = in ? reinterpret_cast<const uint32_t *>(row)[col + i] : 0xff800000u;
+                else e[i] = in ? reinterpret_cast<const uint16_t *>(row)[col + i] : DT == PA_LOGITS_F16 ? 0xfc00u : 0xff80u;
+            }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = kBytes == 4 ? e[i] : e[2 * i] | e[2 * i + 1] << 16;
+        }
+    }
+
+    __device__ __forceinline__ void values(int skew, float (&x)[kElems]) {
+        if (whole && skew != 0) {                    // (the same for all whole threads of a row)
+            if (skew & 8)
+#pragma unroll
+                for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
+            if (skew & 4)
+#pragma unroll
+                for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
+            if (skew & 2)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) {
+            if constexpr (DT == PA_LOGITS_F32) {
+                x[i] = __uint_as_float(w[i]);
+            } else if constexpr (DT == PA_LOGITS_BF16) {
+                x[i] = (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+            } else {
+                const __half2 h = *reinterpret_cast<const __half2 *>(&w[i / 2]);
+                x[i] = (i & 1) ? __high2float(h) : __low2float(h);
+            }
+            x[i] = cleaned(x[i]);
+        }
+    }
+};
+
+// The m-th largest of the warp's values (1 <= m <= 32).
+__device__ __forceinline__ uint32_t warp_mth(uint32_t v, int m, int lane) {
+    uint32_t top = 0;
+    for (int i = 0; i < m; ++i) {
+        top = __reduce_max_sync(0xffffffffu, v);
+        const unsigned who = __ballot_sync(0xffffffffu, v == top);
+        if (lane == __ffs(who) - 1) v = 0;
+    }
+    return top;
+}
+
+// A value that at least n of the CTA's thread maxima reach (0 is below all
+// values): the least of the warps' ceil(n / warps)-th largest.
+__device__ __forceinline__ uint32_t block_floor(uint32_t top, int n, uint32_t *scratch) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t mine = warp_mth(top, (n + kSelWarps - 1) / kSelWarps, lane);
+    if (lane == 0) scratch[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    uint32_t least = scratch[0];
+#pragma unroll
+    for (int w = 1; w < kSelWarps; ++w) least = min(least, scratch[w]);
+    return least;
+}
+
+__device__ __forceinline__ double block_sum(double v, double *scratch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) s += scratch[w];
+    return s;
+}
+
+// The largest value below an ordered word's (-0 is 0).
+__device__ __forceinline__ float value_below(uint32_t k) { return unordered(k - 1 == 0x7fffffffu ? k - 2 : k - 1); }
+
+// A buffer is cut when it holds more than this; it then has room for another tile
+// (round), every element of which may be an entry.
+__device__ __forceinline__ int kept_limit(int n) { return 32 + 2 * n; }
+
+template <int DT>
+__global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const SelectArgs a) {
+    __shared__ uint64_t buf[kKept + kTile];
+    __shared__ uint64_t best[128];
+    __shared__ unsigned long long dropped;
+    __shared__ double sums[kSelWarps];
+    __shared__ uint32_t scratch[kSelWarps];
+    __shared__ int count;
+    after_previous();
+    const int t = threadIdx.x, lane = t & 31;
+    const int row_id = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
+    if (!beam_reads(a, row_id)) return;
+    constexpr int kBytes = DT == PA_LOGITS_F32 ? 4 : 2;
+    const uint8_t *row = static_cast<const uint8_t *>(a.logits) + (int64_t)row_id * a.stride * kBytes;
+    const int skew = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
+    const int from = c * a.chunk, end = min(from + a.chunk, a.vocab);
+    const int n = min(a.n, end - from), limit = kept_limit(n);
+    if (t == 0) {
+        count = 0;
+        dropped = 0;
+    }
+
+    // Elements above thr are entries of the buffer; those at or below it are in
+    // `rest`, the sum of 2^((x - ref) log2 e) with ref = thr.
+    float thr = -INFINITY, ref = 0.f, rest = 0.f;
+    auto term = [&](float x) { return fast_exp2((x - ref) * kLog2e); };
+    auto raise = [&](float to) {                     // a new threshold, the same for the CTA
+        const float r = to == -INFINITY ? 0.f : to;
+        rest = rest > 0.f ? rest * fast_exp2((ref - r) * kLog2e) : 0.f;
+        thr = to;
+        ref = r;
+    };
+    // Cuts the buffer's m entries to the n largest, in order, in best; the n-th is
+    // the new threshold and the others go into rest: as whole multiples of 2^-32, so
+    // that their order in the buffer, which is chance, does not matter.  Every thread.
+    auto cut = [&](int m) {
+        uint32_t out = 0;
+        for (int e = t, i = 0; e < m; e += kSelThreads, ++i) {
+            const uint64_t k = buf[e];
+            int rank = 0;
+#pragma unroll 8
+            for (int j = 0; j < m; ++j) rank += buf[j] > k;
+            if (rank < n) best[rank] = k;
+            else out |= 1u << i;
+        }
+        __syncthreads();
+        if (m < n) return m;
+        raise(key_value(best[n - 1]));
+        if (out != 0) {
+            unsigned long long sum = 0;
+            for (int e = t, i = 0; e < m; e += kSelThreads, ++i)
+                if (out >> i & 1u) sum += (unsigned long long)__float2ull_rn(term(key_value(buf[e])) * 0x1p32f);
+            atomicAdd(&dropped, sum);
+        }
+        __syncthreads();
+        if (t == 0) {
+            rest += (float)dropped * 0x1p-32f;
+            dropped = 0;
+        }
+        return n;
+    };
+
+    Columns<DT> ahead;
+    ahead.load(row, skew, from + t * kElems, end);
+    for (int tile = from; tile < end; tile += kTile) {
+        float x[kElems];
+        const int col = tile + t * kElems;
+        Columns<DT> now = ahead;
+        if (tile + kTile < end) ahead.load(row, skew, col + kTile, end);
+        now.values(skew, x);
+        if (tile == from) {
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
+            const uint32_t least = block_floor(ordered(top), n, scratch);
+            // elements of that value are entries too
+            if (least > ordered(-INFINITY)) raise(value_below(least));
+        }
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) {
+            if (x[i] > thr) {
+                last = atomicAdd(&count, 1);
+                buf[last] = key_of(x[i], col + i);
+                ++last;
+            } else if (thr != -INFINITY) {
+                rest += term(x[i]);
+            }
+        }
+        if (__syncthreads_or(last > limit)) {
+            const int kept = cut(count);             // limit >= n: n entries stay
+            if (t < kept) buf[t] = best[t];
+            if (t == 0) count = kept;
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    const int kept = cut(count);
+    // The list; its exponentials in 64 bits.
+    const int64_t at = (int64_t)row_id * a.chunks + c;
+    float2 *list = a.lists + at * a.n;
+    const float top = kept > 0 ? key_value(best[0]) : -INFINITY;
+    double sum = rest > 0.f ? (double)rest * exp((double)ref - (double)top) : 0.0;
+    for (int e = t; e < kept; e += kSelThreads) {
+        const float x = key_value(best[e]);
+        list[e] = make_float2(x, __int_as_float((int)~(uint32_t)best[e]));
+        sum += exp((double)x - (double)top);
+    }
+    sum = block_sum(sum, sums);
+    if (t == 0) a.sums[at] = ChunkSum{(double)top, sum};
+    // Fewer finite logits than n: the first columns of the others.
+    if (kept < a.n && t < 32) {
+        int have = kept;
+        for (int col = from; col < end && have < n; col += 32) {
+            const bool none = col + lane < end && cleaned(element<DT>(row, col + lane)) == -INFINITY;
+            const unsigned who = __ballot_sync(0xffffffffu, none);
+            const int place = have + __popc(who & ((1u << lane) - 1u));
+            if (none && place < n) list[place] = make_float2(-INFINITY, __int_as_float(col + lane));
+            have += __popc(who);
+        }
+        for (int e = n + lane; e < a.n; e += 32) list[e] = make_float2(-INFINITY, __uint_as_float(0xffffffffu));
+    }
+}
+
+// One CTA per group: lse of its beams, the totals of the lists' entries, the n
+// largest of those.  Entries pass the threshold in rounds, as above; beams whose
+// logits are not read offer what they have in place of their first list.
+constexpr int kRound = 4 * kSelThreads;
+constexpr int kBuf2 = kKept + kRound;
+
+__global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectArgs a) {
+    __shared__ double tot[kBuf2], best_tot[128], lses[64];
+    __shared__ uint32_t idx[kBuf2], best_idx[128];
+    __shared__ float score[64];
+    __shared__ uint8_t state[64];                    // 0: reads its logits, 1: ended, 2: score -inf
+    __shared__ uint32_t scratch[kSelWarps];
+    __shared__ int count;
+    after_previous();
+    const int t = threadIdx.x, lane = t & 31, g = blockIdx.x;
+    const int K = a.beams, S = a.chunks, n = a.n, limit = kept_limit(n);
+    for (int k = t; k < K; k += kSelThreads) {
+        const float s = cleaned(a.scores[g * K + k]);
+        score[k] = s;
+        state[k] = s == -INFINITY ? 2 : a.finished != nullptr && a.finished[g * K + k] != 0 ? 1 : 0;
+    }
+    if (t == 0) count = 0;
+    __syncthreads();
+    for (int k = t >> 5; k < K; k += kSelWarps) {    // lse, a warp per beam
+        double l = 0.0;
+        if (state[k] == 0) {
+            const ChunkSum *cs = a.sums + ((int64_t)g * K + k) * S;
+            double top = -INFINITY, sum = 0.0;
+            for (int c = lane; c < S; c += 32) top = fmax(top, cs[c].top);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (top > -INFINITY)
+                for (int c = lane; c < S; c += 32) sum += cs[c].sum * exp(cs[c].top - top);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = top + log(sum);                      // (no finite logit: not used)
+        }
+        if (lane == 0) lses[k] = l;
+    }
+    __syncthreads();
+
+    const unsigned per_beam = (unsigned)(S * n), entries = (unsigned)K * per_beam;
+    auto entry = [&](unsigned e, double &v, uint32_t &at) {
+        const int k = (int)(e / per_beam), r = (int)(e % per_beam);
+        v = -INFINITY;
+        at = 0xffffffffu;
+        if (state[k] == 0) {
+            const float2 x = a.lists[((int64_t)g * K + k) * per_beam + r];
+            const uint32_t col = __float_as_uint(x.y);
+            if (col != 0xffffffffu) {
+                at = (uint32_t)k << 24 | col;
+                if (x.x != -INFINITY) v = (double)score[k] + ((double)x.x - lses[k]);
+            }
+        } else if (r < n) {                          // n <= vocab columns
+            int col = r;
+            if (state[k] == 1) {
+                col = r == 0 ? a.pad : r - 1 + (r - 1 >= a.pad);
+                if (r == 0) v = (double)score[k];
+            }
+            at = (uint32_t)k << 24 | (uint32_t)col;
+        }
+    };
+    double thr = -INFINITY;                          // with thr_idx: the n-th best so far
+    uint32_t thr_idx = 0xffffffffu;
+    auto better = [](double x, uint32_t i, double y, uint32_t j) { return x > y || (x == y && i < j); };
+    // Ranks the buffer's m entries; the n best, in order, into best.
+    auto cut = [&](int m) {
+        for (int e = t; e < m; e += kSelThreads) {
+            const double v = tot[e];
+            const uint32_t at = idx[e];
+            int rank = 0;
+            for (int i = 0; i < m; ++i) rank += better(tot[i], idx[i], v, at);
+            if (rank < n) {
+                best_tot[rank] = v;
+                best_idx[rank] = at;
+            }
+        }
+        __syncthreads();
+        return min(m, n);
+    };
+    for (unsigned e0 = 0; e0 < entries; e0 += kRound) {
+        double v[kRound / kSelThreads];
+        uint32_t at[kRound / kSelThreads];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kRound / kSelThreads; ++i) {
+            at[i] = 0xffffffffu;
+            const unsigned e = e0 + i * kSelThreads + t;
+            if (e < entries) entry(e, v[i], at[i]);
+            if (at[i] != 0xffffffffu) top = max(top, ordered(__double2float_rd(v[i])));
+        }
+        uint32_t least = 0;                          // (no value's word is 0)
+        if (e0 == 0) least = block_floor(top, n, scratch);
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < kRound / kSelThreads; ++i) {
+            if (at[i] == 0xffffffffu || ordered(__double2float_rd(v[i])) < least || !better(v[i], at[i], thr, thr_idx)) continue;
+            last = atomicAdd(&count, 1);
+            tot[last] = v[i];
+            idx[last] = at[i];
+            ++last;
+        }
+        if (__syncthreads_or(last > limit)) {
+            const int kept = cut(count);
+            if (t < kept) {
+                tot[t] = best_tot[t];
+                idx[t] = best_idx[t];
+            }
+            if (t == 0) count = kept;
+            __syncthreads();
+            if (kept == n) {
+                thr = best_tot[n - 1];
+                thr_idx = best_idx[n - 1];
+            }
+        }
+    }
+    __syncthreads();
+    cut(count);
+    for (int e = t; e < n; e += kSelThreads) {
+        const uint32_t at = best_idx[e];
+        a.out_scores[(int64_t)g * n + e] = (float)best_tot[e];
+        a.out_parents[(int64_t)g * n + e] = (int)(at >> 24);
+        a.out_tokens[(int64_t)g * n + e] = (int)(at & 0xffffffu);
+    }
+}
+
+// ------------------------------------------------------------- reordering ---
+struct ReorderArgs {
+    pa_beam_reorder_params p;
+    void *pools[PA_BEAM_REORDER_MAX_POOLS];
+};
+
+// Length of group g's sequences, -1 if they differ or break the bounds (every
+// thread of the CTA, the answer for all).
+__device__ __forceinline__ int group_length(const pa_beam_reorder_params &p, int g) {
+    const int32_t *lens = p.seqlens + (int64_t)g * p.beams;
+    const int L = lens[0];
+    bool bad = L < 0 || L > p.max_seqlen_k;
+    for (int k = threadIdx.x; k < p.beams; k += blockDim.x) bad |= lens[k] != L;
+    return __syncthreads_or(bad) ? -1 : L;
+}
+
+__device__ __forceinline__ bool row_ok(const pa_beam_reorder_params &p, int row) { return row >= 0 && row < p.token_table_rows; }
+
+// The parent of beam i of group g if it moves, else i itself.
+__device__ __forceinline__ int parent_of(const pa_beam_reorder_params &p, int g, int i) {
+    const int64_t base = (int64_t)g * p.beams;
+    const int q = p.parents[base + i];
+    if (q == i) return i;
+    if (q < 0 || q >= p.beams || !row_ok(p, p.table_idx[base + i]) || !row_ok(p, p.table_idx[base + q])) {
+        raise_error(PA_DEVERR_TABLE_INDEX);
+        return i;
+    }
+    return q;
+}
+
+constexpr int kCopyThreads = 256;
+
+// CTA (sequence, slice of the pools): the rows of the parent's last page into the
+// sequence's spare page.
+__global__ void __launch_bounds__(kCopyThreads) reorder_copy_kernel(const __grid_constant__ ReorderArgs a, int slices) {
+    const pa_beam_reorder_params &p = a.p;
+    after_previous();
+    const int seq = blockIdx.x / slices, slice = blockIdx.x % slices;
+    const int g = seq / p.beams, i = seq % p.beams;
+    const int parent = p.parents[seq];
+    if (parent == i) return;
+    const int L = group_length(p, g);
+    const int part = L % p.page_size;
+    if (L <= 0 || part == 0) return;
+    const int q = parent_of(p, g, i);
+    if (q == i) return;
+    const int32_t slot = p.token_table[p.table_idx[(int64_t)g * p.beams + q] * p.token_table_stride + L - 1];
+    const int32_t src = slot >= 0 ? slot / p.page_size : -1, dst = p.spare_pages[seq];
+    if (src < 0 || src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
+        if (threadIdx.x == 0) raise_error(PA_DEVERR_PAGE_RANGE);
+        return;
+    }
+    const int64_t page_words = p.row_bytes / 16 * p.page_size;
+    const int words = (int)(p.row_bytes / 16 * part);
+    for (int k = slice; k < p.num_pools; k += slices) {
+        uint4 *pool = static_cast<uint4 *>(a.pools[k]);
+        const uint4 *from = pool + src * page_words;
+        uint4 *to = pool + dst * page_words;
+        constexpr int U = 8;
+        for (int w0 = threadIdx.x; w0 < words; w0 += U * kCopyThreads) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (w0 + u * kCopyThreads < words) v[u] = from[w0 + u * kCopyThreads];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (w0 + u * kCopyThreads < words) to[w0 + u * kCopyThreads] = v[u];
+        }
+    }
+}
+
+constexpr int kColumns = 128;                        // columns of a CTA, a multiple of every page size
+
+// CTA (group, block of columns): first the token table's blocks, then the
+// histories'.  The CTA of a group's last slots also turns the spare pages over.
+__global__ void __launch_bounds__(kColumns) reorder_rows_kernel(const pa_beam_reorder_params p, int table_blocks, int blocks) {
+    extern __shared__ int32_t vals[];                // [beams][kColumns], each thread its own column
+    __shared__ int parents[64], spares[64], firsts[64];
+    __shared__ int64_t rows[64];                     // a row's first cell, -1 outside the table
+    after_previous();
+    const int g = blockIdx.x / blocks, block = blockIdx.x % blocks, t = threadIdx.x;
+    const int64_t base = (int64_t)g * p.beams;
+    const bool table = block < table_blocks;
+    const int col = (table ? block : block - table_blocks) * kColumns + t;
+    const int L = group_length(p, g);
+    if (L < 0) {
+        if (t == 0) raise_error(PA_DEVERR_SEQLENS);
+        return;
+    }
+    const int part = L % p.page_size, full = L - part;       // slots from `full` on lie on the last page
+    const int ends = table ? L : p.history_len;
+    if (col - t >= ends) return;
+    const bool last = table && part > 0 && col - t + kColumns >= L;
+    bool moves = false;
+    for (int k = t; k < p.beams; k += kColumns) {
+        const int q = parent_of(p, g, k);
+        const int idx = p.table_idx[base + k];
+        parents[k] = q;
+        rows[k] = !table ? (base + k) * p.history_stride : row_ok(p, idx) ? idx * p.token_table_stride : -1;
+        firsts[k] = table && p.prefix_lens != nullptr ? p.prefix_lens[base + k] : 0;
+        spares[k] = last ? p.spare_pages[base + k] : -1;
+        moves |= q != k && (last || col - t + kColumns > firsts[k]);
+    }
+    if (!__syncthreads_or(moves) || col >= ends) return;
+    int32_t *cells = table ? p.token_table : p.history;
+    for (int k = 0; k < p.beams; ++k)
+        if (rows[k] >= 0) vals[k * kColumns + t] = cells[rows[k] + col];
+    for (int k = 0; k < p.beams; ++k) {
+        const int q = parents[k];
+        if (q == k) continue;                        // (else both rows are in the table)
+        int32_t *cell = cells + rows[k] + col;
+        if (table && col >= full) {
+            const int32_t own = vals[k * kColumns + t];
+            *cell = spares[k] >= 0 && spares[k] < p.num_pages ? spares[k] * p.page_size + col - full : -1;
+            if (col == L - 1) p.spare_pages[base + k] = own >= 0 ? own / p.page_size : -1;
+        } else if (col >= firsts[k]) {
+            *cell = vals[q * kColumns + t];
+        }
+    }
+}
+
+template <int DT>
+cudaError_t launch_chunks(const SelectArgs &a, cudaStream_t stream) {
+    return launch_after(select_chunks_kernel<DT>, (unsigned)(a.groups * a.beams * a.chunks), kSelThreads, 0, stream, a);
+}
+
+}  // namespace
+
+// Columns of a chunk: whole tiles, about kCtas CTAs while there are tiles enough
+// (a constant: the workspace's size is the same on every device).
+constexpr int kCtas = 152 * 24;
+SelectPlan plan_select(const pa_beam_select_params &p) {
+    SelectPlan plan{};
+    const int64_t rows = (int64_t)p.num_groups * p.beams, tiles = ((int64_t)p.vocab + kTile - 1) / kTile;
+    int64_t per = rows * tiles / kCtas;
+    if (per < 1) per = 1;
+    const int64_t chunks = (tiles + per - 1) / per;
+    per = (tiles + chunks - 1) / chunks;
+    plan.chunks = (int32_t)((tiles + per - 1) / per);
+    plan.chunk = (int32_t)(per * kTile);
+    plan.list_bytes = (size_t)rows * plan.chunks * p.num_out * sizeof(float2);
+    plan.list_bytes = (plan.list_bytes + 15) / 16 * 16;
+    plan.workspace_bytes = plan.list_bytes + (size_t)rows * plan.chunks * sizeof(ChunkSum);
+    return plan;
+}
+
+cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan, cudaStream_t stream) {
+    SelectArgs a{};
+    a.logits = p.logits;
+    a.stride = p.logits_stride;
+    a.scores = p.scores;
+    a.finished = p.finished;
+    a.pad = p.pad_token;
+    a.groups = p.num_groups;
+    a.beams = p.beams;
+    a.vocab = p.vocab;
+    a.n = p.num_out;
+    a.chunks = plan.chunks;
+    a.chunk = plan.chunk;
+    a.lists = static_cast<float2 *>(p.workspace);
+    a.sums = reinterpret_cast<ChunkSum *>(static_cast<uint8_t *>(p.workspace) + plan.list_bytes);
+    a.out_scores = p.out_scores;
+    a.out_parents = p.out_parents;
+    a.out_tokens = p.out_tokens;
+    const cudaError_t e = p.logits_dtype == PA_LOGITS_F32   ? launch_chunks<PA_LOGITS_F32>(a, stream)
+                          : p.logits_dtype == PA_LOGITS_F16 ? launch_chunks<PA_LOGITS_F16>(a, stream)
+                                                            : launch_chunks<PA_LOGITS_BF16>(a, stream);
+    if (e != cudaSuccess) return e;
+    return launch_after(select_merge_kernel, (unsigned)p.num_groups, kSelThreads, 0, stream, a);
+}
+
+cudaError_t launch_reorder(const pa_beam_reorder_params &p, cudaStream_t stream) {
+    const int seqs = p.num_groups * p.beams;
+    if (p.page_size > 1 && p.num_pools > 0) {
+        ReorderArgs a{};
+        a.p = p;
+        for (int k = 0; k < p.num_pools; ++k) a.pools[k] = p.pools[k];
+        // a few CTAs for every SM; a CTA finds its pages once for its pools
+        int slices = (num_sms() * 8 + seqs - 1) / seqs;
+        if (slices > p.num_pools) slices = p.num_pools;
+        const cudaError_t e = launch_after(reorder_copy_kernel, (unsigned)(seqs * slices), kCopyThreads, 0, stream, a, slices);
+        if (e != cudaSuccess) return e;
+    }
+    const int table_blocks = (p.max_seqlen_k + kColumns - 1) / kColumns;
+    const int blocks = table_blocks + (p.history != nullptr ? (p.history_len + kColumns - 1) / kColumns : 0);
+    if (blocks == 0) return cudaSuccess;
+    pa_beam_reorder_params q = p;
+    if (q.history == nullptr) q.history_len = 0;
+    return launch_after(reorder_rows_kernel, (unsigned)((int64_t)p.num_groups * blocks), kColumns,
+                        (size_t)p.beams * kColumns * sizeof(int32_t), stream, q, table_blocks, blocks);
+}
+
+}  // namespace pa

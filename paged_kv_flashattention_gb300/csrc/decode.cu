@@ -97,6 +97,9 @@ __global__ void __launch_bounds__((HPC + 1) * 32) decode_kernel(const DecodeArgs
     else
         decode_consume<D, G, HPC, F8>(a, prefix, T, g0, g1, ring, full, empty, pbuf, stage_ctr,
                                       warp, lane);
+    // over the keys behind shared prefixes the kernel overlaps the one before it:
+    // it ends after that one, so that the merge need wait for this one alone
+    if (a.first_keys != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One warp per row (a (sequence, head) pair): merge its splits by LSE.
@@ -309,12 +312,17 @@ DecodePlan plan_decode(const pa_decode_params &p) {
     return plan;
 }
 
-cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream) {
-    const DecodeArgs a = decode_setup(p, plan);
+cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream, DecodeTail *tail) {
+    DecodeArgs a = decode_setup(p, plan);
     if (p.num_seqs == 0) return cudaSuccess;
     // Upper bound of useful CTAs: every sequence at max length, minimal split.
-    const int64_t items_max = ((int64_t)p.num_seqs * p.max_seqlen_k * a.head_groups + plan.kv_chunk - 1) /
+    const int64_t longest = tail != nullptr ? tail->max_keys : p.max_seqlen_k;
+    const int64_t items_max = ((int64_t)p.num_seqs * longest * a.head_groups + plan.kv_chunk - 1) /
                               plan.kv_chunk + 1;
+    if (tail != nullptr) {
+        a.first_keys = tail->first_keys;
+        a.max_keys = tail->max_keys;
+    }
     const int g = p.num_q_heads / p.num_kv_heads;
     const bool f8 = p.kv_dtype == PA_KV_FP8_E4M3;
     cudaError_t e;
@@ -325,6 +333,16 @@ cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cud
         e = p.head_dim == 64 ? dispatch_g<64, false>(a, g, plan.heads_per_cta, items_max, stream)
                              : dispatch_g<128, false>(a, g, plan.heads_per_cta, items_max, stream);
     if (e != cudaSuccess) return e;
+    if (tail != nullptr) {
+        tail->o_part = a.o_part;
+        tail->lse_part = a.lse_part;
+        tail->header = a.ws_header;
+        tail->prefix = a.ws_prefix;
+        tail->head_groups = a.head_groups;
+        tail->heads_per_group = g * plan.heads_per_cta;
+        tail->max_splits = plan.max_splits;
+        return cudaSuccess;
+    }
     return launch_lse_combine(a.o_part, a.lse_part, nullptr, a.ws_header, a.ws_prefix, a.head_groups,
                               g * plan.heads_per_cta, p.num_q_heads, p.num_seqs * p.num_q_heads,
                               plan.max_splits, p.head_dim, p.out, p.lse, stream, p.overlap_previous != 0);

@@ -89,6 +89,8 @@ struct Fp4DecodeArgs {
     int32_t overlap_previous;     // do not wait for the kernel before
     int32_t *ws_header;           // [0] = T, in units
     int32_t *ws_prefix;           // [B+1] exclusive prefix of the sequences' units
+    const int32_t *first_keys;    // over shared prefixes: the keys from first_keys[b] on,
+    int32_t max_keys;             // at most so many (null: all)
 };
 
 // Page size 16 and more than one head group (BOX): the pools as rows of 32-bit
@@ -119,6 +121,11 @@ __device__ __forceinline__ int seq_keys(const Fp4DecodeArgs &a, int b, int &lo) 
     int L = a.cache_seqlens[b];
     L = L < 0 ? 0 : (L > a.max_seqlen_k ? a.max_seqlen_k : L);
     lo = (a.window > 0 && L > a.window) ? L - a.window : 0;
+    if (a.first_keys != nullptr) {
+        lo = a.first_keys[b];
+        if (lo < 0 || lo > L) return lo = 0;
+        lo = max(lo, L - a.max_keys);
+    }
     return L;
 }
 
@@ -130,7 +137,12 @@ __device__ __forceinline__ void fp4_prefix(const Fp4DecodeArgs &a, int32_t *pref
         if (given < 0 || given > a.max_seqlen_k) raise_error(PA_DEVERR_SEQLENS);
         int lo;
         const int L = seq_keys(a, b, lo);
-        prefix[b + 1] = L > 0 ? (L - 1) / kUnit - lo / kUnit + 1 : 0;
+        if (a.first_keys != nullptr) {
+            const int first = a.first_keys[b];
+            if ((given > 0 && (first < 0 || given < first)) || (given >= 0 && given - first > a.max_keys && first >= 0))
+                raise_error(PA_DEVERR_SEQLENS);
+        }
+        prefix[b + 1] = L > lo ? (L - 1) / kUnit - lo / kUnit + 1 : 0;
     }
     if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
@@ -537,6 +549,7 @@ decode_fp4_kernel(const Fp4DecodeArgs a, const __grid_constant__ Fp4MapsOf<BOX> 
     const int g0 = (int)min((int64_t)blockIdx.x * T, (int64_t)total), g1 = min(total - g0, T) + g0;
     if (warp == HPC) fp4_produce<D, HPC, BOX>(a, maps, prefix, T, g0, g1, smem, full, empty, lane);
     else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
+    if (a.first_keys != nullptr) after_previous();       // ends after the kernel that it overlaps (decode.cu)
 }
 
 // The log-sum-exp combine (decode.cu's, with its split count): W warps share a
@@ -766,7 +779,7 @@ DecodePlan plan_decode_fp4(const pa_decode_params &p) {
     return plan;
 }
 
-cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream) {
+cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream, DecodeTail *tail) {
     if (p.num_seqs == 0) return cudaSuccess;
     const DecodeArgs w = decode_setup(p, plan);      // the workspace layout
     const Fp4Layout lay = fp4_layout(p.num_kv_heads, p.head_dim);
@@ -796,8 +809,13 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
     a.overlap_previous = p.overlap_previous;
     a.ws_header = w.ws_header;
     a.ws_prefix = w.ws_prefix;
+    if (tail != nullptr) {
+        a.first_keys = tail->first_keys;
+        a.max_keys = tail->max_keys;
+    }
     // every sequence at its longest, ranges at their smallest
-    const int64_t units = reach(p) / kUnit * p.num_seqs * lay.groups;
+    const int64_t longest = tail != nullptr ? ((int64_t)tail->max_keys + 2 * kUnit - 2) / kUnit * kUnit : reach(p);
+    const int64_t units = longest / kUnit * p.num_seqs * lay.groups;
     const int64_t useful = (units + a.min_units - 1) / a.min_units + 1;
     cudaError_t e;
     if (p.page_size == 16 && lay.groups > 1) {
@@ -810,6 +828,16 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
         e = dispatch_fp4<false>(a, Fp4NoMaps{}, lay.gs, p, useful, stream);
     }
     if (e != cudaSuccess) return e;
+    if (tail != nullptr) {
+        tail->o_part = a.o_part;
+        tail->lse_part = a.lse_part;
+        tail->header = a.ws_header;
+        tail->prefix = a.ws_prefix;
+        tail->head_groups = a.head_groups;
+        tail->heads_per_group = a.group * lay.gs;
+        tail->max_splits = a.max_splits;
+        return cudaSuccess;
+    }
     return launch_fp4_combine(a, p, a.group * lay.gs, plan, stream);
 }
 

@@ -65,6 +65,10 @@ struct DecodeArgs {
     int32_t *ws_header;           // [0] = T
     int32_t *ws_prefix;           // [B+1] exclusive prefix of the sequence lengths
     int32_t evict_first;          // K/V row copies with an L2 evict-first policy (beside a prefill)
+    // Decode over shared prefixes (decode_shared.cu): sequence b's keys from
+    // first_keys[b] on, at most max_keys of them; null = all keys.
+    const int32_t *first_keys;
+    int32_t max_keys;
 };
 
 template <int D, int HPC, int EB, int STAGES = stages_for<D, EB, HPC>()>
@@ -159,6 +163,11 @@ __device__ __forceinline__ void decode_prefix(const DecodeArgs &a, int32_t *pref
             L = L < 0 ? 0 : a.max_seqlen_k;
         }
         if (a.window > 0 && L > a.window) L = a.window;     // only the last W keys are read
+        if (a.first_keys != nullptr) {                      // only the keys behind the prefix
+            const int first = a.first_keys[b], n = L - first;
+            if ((L > 0 && (first < 0 || n < 0)) || n > a.max_keys) raise_error(PA_DEVERR_SEQLENS);
+            L = first < 0 || n < 0 ? 0 : min(n, a.max_keys);
+        }
         prefix[b + 1] = L;
     }
     if (threadIdx.x == 0) prefix[0] = 0;

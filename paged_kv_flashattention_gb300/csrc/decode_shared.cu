@@ -1,0 +1,339 @@
+// Decode over shared prefixes: sequences in groups (the beams or samples of one
+// request, requests behind one system prompt) whose first keys are the same.
+//
+//   out[b, h] = softmax over keys [0, L_b) of (scale q[b, h] . K) V
+//
+// splits at the prefix P of b's group (log-sum-exp, "Transformer inference
+// kernels (3/10)", sections 12 and 16): keys [0, P) are read once for the whole
+// group, keys [P, L_b) by the split-KV decode, and one merge joins a row's
+// partials of both.
+//
+// The prefix is a matrix product again: the rows that read KV head kvh of a
+// group are (sequence, query head of kvh), n * Hq / Hkv of them, so prefill's
+// tcgen05 kernel does it (prefill_impl.cuh, SHARED) with tiles of 128 such rows,
+// two tiles per CTA where the largest group fills more than one.  The query tile
+// is one tensor-map box (64 columns, Hq / Hkv heads, 128 Hkv / Hq sequences).
+// Every CTA gets the same number of 128-key steps, whatever the groups are; the
+// partials are written in 32 bits.
+#include "prefill_impl.cuh"
+
+#include "pdl.cuh"
+
+namespace pa {
+
+PA_ERROR_WORD_ACCESSOR(error_word_decode_shared)
+
+namespace {
+
+template <int D, int T, int KV>
+__global__ void __launch_bounds__(128 * (T + 1), 1) shared_prefix_kernel(const __grid_constant__ PrefillArgs a) {
+    prefill_body<D, T, KV != PA_KV_BF16, false, KV == PA_KV_FP4, true>(a);
+}
+
+template <int D, int T, int KV>
+cudaError_t launch_prefix_t(const PrefillArgs &a, unsigned ctas, cudaStream_t stream) {
+    using S = PrefillSmem<D, T, KV != PA_KV_BF16, KV == PA_KV_FP4, true>;
+    static_assert(S::kSlots >= 2 && (KV == PA_KV_BF16 || S::kCSlots >= 2), "ring too small");
+    static_assert(S::kTotal + 1024 <= 232448, "shared memory");
+    // One CTA per SM (it allocates all 512 TMEM columns).
+    const int smem = (S::kTotal + 1024) > 120 * 1024 ? (S::kTotal + 1024) : 120 * 1024;
+    auto kern = shared_prefix_kernel<D, T, KV>;
+    if (T == 2) {
+        static const cudaError_t regs = check_register_split(kern);
+        if (regs != cudaSuccess) return regs;
+    }
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, ctas, 128 * (T + 1), smem, stream, a);
+}
+
+template <int KV>
+cudaError_t launch_prefix(const PrefillArgs &a, int d, int T, unsigned ctas, cudaStream_t stream) {
+    if (d == 128)
+        return T == 2 ? launch_prefix_t<128, 2, KV>(a, ctas, stream) : launch_prefix_t<128, 1, KV>(a, ctas, stream);
+    return T == 2 ? launch_prefix_t<64, 2, KV>(a, ctas, stream) : launch_prefix_t<64, 1, KV>(a, ctas, stream);
+}
+
+struct MergeArgs {
+    SharedArgs sh;
+    DecodeTail tail;              // o_part null: no keys behind the prefixes
+    const int32_t *cache_seqlens;
+    int32_t num_seqs;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t max_seqlen_k;
+    int32_t tile_rows;            // rows of a work item of the prefix kernel
+    __nv_bfloat16 *out;
+    float *lse;
+};
+
+// The group of sequence b (the last g with cu_groups[g] <= b), by a whole warp:
+// 32 probes a step.  num_groups for sequences behind the last group, -1 before
+// the first.
+__device__ __forceinline__ int group_of(const SharedArgs &sh, int b, int lane) {
+    int lo = 0, n = sh.num_groups + 1;
+    for (;;) {
+        const int step = (n + 31) / 32;
+        const int i = lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, i < n && sh.cu_groups[lo + i] <= b);
+        if (m == 0) return lo - 1;                   // (only in the first step)
+        const int last = 31 - __clz(m);
+        lo += last * step;
+        n = min(step, n - last * step);
+        if (step == 1) return lo;
+    }
+}
+
+// One row (sequence, query head) of both lists of partials, merged by
+// log-sum-exp; W warps share a row's slots (decode_fp4.cu's combine says why).  A
+// NaN among the partials stays one.
+constexpr int kMergeThreads = 256;
+
+template <int D, int W>
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const MergeArgs a) {
+    constexpr int kLanes = D / 4;                    // lanes of a slot, four elements each
+    constexpr int kSlots = 32 * W / kLanes;          // slots in flight
+    __shared__ float top[kMergeThreads / 32], dens[kMergeThreads / kLanes];
+    __shared__ float4 part[kMergeThreads];
+    const int t = threadIdx.x % (32 * W), lane = t & 31;
+    const int64_t row = (int64_t)blockIdx.x * (kMergeThreads / (32 * W)) + threadIdx.x / (32 * W);
+    const int64_t num_rows = (int64_t)a.num_seqs * a.num_q_heads;
+    after_previous();                                // the partials are complete
+    int np = 0, ns = 0;                              // partials of the prefix, of the keys behind it
+    if (row < num_rows) {
+        const int b = (int)(row / a.num_q_heads), h = (int)(row % a.num_q_heads);
+        const int group = a.num_q_heads / a.num_kv_heads;
+        const int L = a.cache_seqlens[b], P = a.sh.prefix_lens[b];
+        bool ok = L >= 0 && L <= a.max_seqlen_k && P >= 0 && P <= L && P <= a.sh.max_prefix;
+        if (ok && P > 0) {
+            const int g = group_of(a.sh, b, lane);
+            ok = g >= 0 && g < a.sh.num_groups;      // a prefix without a group
+            if (ok) {
+                const int q0 = a.sh.cu_groups[g], n = a.sh.cu_groups[g + 1] - q0;
+                const int64_t per = a.sh.header[0];
+                ok = q0 >= 0 && n <= a.sh.max_group && a.sh.prefix_lens[q0] == P;
+                const int tiles = (n * group + a.tile_rows - 1) / a.tile_rows, steps = (P + kBN - 1) / kBN;
+                const int64_t start = a.sh.base[g] +
+                                      ((int64_t)(h / group) * tiles + ((b - q0) * group + h % group) / a.tile_rows) * steps;
+                if (ok) np = min((int)((start + steps - 1) / per - start / per + 1), a.sh.max_splits);
+            }
+        }
+        if (!ok && L != 0) raise_error(PA_DEVERR_SEQLENS);
+        if (ok && a.tail.o_part != nullptr) {
+            const int64_t T = a.tail.header[0];
+            const int U = a.tail.prefix[b + 1] - a.tail.prefix[b];
+            const int64_t rs = (int64_t)a.tail.head_groups * a.tail.prefix[b] + (int64_t)(h / a.tail.heads_per_group) * U;
+            ns = U > 0 ? min((int)((rs + U - 1) / T - rs / T + 1), a.tail.max_splits) : 0;
+        } else if (ok && L > P) {
+            raise_error(PA_DEVERR_SEQLENS);          // the call allows no keys behind the prefix
+        }
+    }
+    const int n = np + ns;
+    const float *lp = a.sh.lse_part + row * a.sh.max_splits;
+    const float *ls = a.tail.lse_part + row * a.tail.max_splits - np;
+    auto lse_of = [&](int s) { return s < np ? lp[s] : ls[s]; };
+    float M = -INFINITY;
+    for (int s = t; s < n; s += 32 * W) M = fmaxf(M, lse_of(s));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (W > 1) {
+        if (lane == 0) top[threadIdx.x >> 5] = M;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, top[(threadIdx.x >> 5) / W * W + w]);
+    }
+    const float *op = a.sh.o_part + row * a.sh.max_splits * D + (t % kLanes) * 4;
+    const float *os = a.tail.o_part + (row * a.tail.max_splits - np) * D + (t % kLanes) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+#pragma unroll 4
+    for (int s = t / kLanes; s < n; s += kSlots) {
+        const float l = lse_of(s);
+        if (l == -INFINITY) continue;                // an empty slot may hold anything
+        const float w = __expf(l - M);
+        const float4 x = *reinterpret_cast<const float4 *>((s < np ? op : os) + (int64_t)s * D);
+        den += w;
+        acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w;
+    }
+    if (kSlots > 1) {                                // the lane groups' sums
+        part[threadIdx.x] = acc;
+        if (t % kLanes == 0) dens[threadIdx.x / kLanes] = den;
+        if (W > 1) __syncthreads(); else __syncwarp();
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        den = 0.f;
+        const int base = threadIdx.x - t;
+#pragma unroll
+        for (int g = 0; g < kSlots; ++g) {
+            const float4 x = part[base + g * kLanes + t % kLanes];
+            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+            den += dens[base / kLanes + g];
+        }
+    }
+    if (row >= num_rows || t >= kLanes) return;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    *reinterpret_cast<uint2 *>(a.out + row * D + t * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse != nullptr && t == 0) a.lse[row] = den == 0.f ? -INFINITY : M + __logf(den);
+}
+
+cudaError_t launch_merge(const MergeArgs &a, int d, cudaStream_t stream) {
+    const int64_t rows = (int64_t)a.num_seqs * a.num_q_heads;
+    // A CTA per row while all of them fit on the GPU at once and a row may have
+    // more than a few slots.
+    constexpr int W = kMergeThreads / 32;
+    const bool share = a.sh.max_splits + a.tail.max_splits >= 8 && rows <= num_sms() * 8;
+    const int per_block = share ? 1 : W;
+    auto kern = d == 64 ? (share ? shared_merge_kernel<64, W> : shared_merge_kernel<64, 1>)
+                        : (share ? shared_merge_kernel<128, W> : shared_merge_kernel<128, 1>);
+    return launch_after(kern, (unsigned)((rows + per_block - 1) / per_block), kMergeThreads, 0, stream, a);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// 3-D bf16 map of q (d, Hq, sequences) with a box of 128 rows: `group` heads of
+// 128 / group sequences.
+bool make_map_shared_q(CUtensorMap *m, const pa_decode_params &p) {
+    auto enc = encoder();
+    if (!enc) return false;
+    const cuuint32_t group = (cuuint32_t)(p.num_q_heads / p.num_kv_heads);
+    cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.num_q_heads, (cuuint64_t)p.num_seqs};
+    cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, (cuuint64_t)p.num_q_heads * p.head_dim * 2};
+    cuuint32_t box[3] = {64, group, kBM / group};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p.q), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Steps of the longest list: every group at its largest, every prefix at its longest.
+int64_t most_steps(const pa_decode_shared_params &p, int T) {
+    const int64_t group = p.dec.num_q_heads / p.dec.num_kv_heads;
+    const int64_t tiles = ((int64_t)p.max_group * group + T * kBM - 1) / (T * kBM);
+    const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
+    return p.num_groups * tiles * steps * p.dec.num_kv_heads;
+}
+
+unsigned prefix_ctas(const pa_decode_shared_params &p, int T) {
+    const int64_t steps = most_steps(p, T), sms = num_sms();
+    return (unsigned)(steps < sms ? steps : sms);
+}
+
+}  // namespace
+
+// The decode call over the keys behind the prefixes.  In a 4-bit pool they may
+// begin and end inside a unit of 16 keys.
+pa_decode_params shared_tail_params(const pa_decode_shared_params &p) {
+    pa_decode_params d = p.dec;
+    d.max_seqlen_k = p.max_suffix + (p.dec.kv_dtype == PA_KV_FP4 && p.max_suffix > 0 ? 16 : 0);
+    return d;
+}
+
+SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
+    SharedPlan plan{};
+    const int group = p.dec.num_q_heads / p.dec.num_kv_heads;
+    plan.tiles = (int64_t)p.max_group * group > kBM ? 2 : 1;
+    plan.prefix = p.num_groups > 0 && p.max_prefix > 0 && p.max_group > 0 && p.dec.num_seqs > 0;
+    plan.tail = p.max_suffix > 0;
+    if (plan.prefix) {
+        // A row of n steps: the list has n for each KV head at least, so a range
+        // is n * Hkv / CTAs steps or longer, and n steps lie in at most
+        // ceil(CTAs / Hkv) + 1 ranges.
+        const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
+        const int64_t ranges = (prefix_ctas(p, plan.tiles) + p.dec.num_kv_heads - 1) / p.dec.num_kv_heads + 1;
+        plan.max_splits = (int32_t)(steps < ranges ? steps : ranges);
+        const size_t slots = (size_t)p.dec.num_seqs * p.dec.num_q_heads * plan.max_splits;
+        plan.prefix_bytes = 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t)) +
+                            slots * p.dec.head_dim * sizeof(float) + round256(slots * sizeof(float));
+    }
+    const pa_decode_params tail = shared_tail_params(p);
+    if (plan.tail) {
+        plan.decode = tail.kv_dtype == PA_KV_FP4 ? plan_decode_fp4(tail) : plan_decode(tail);
+        if (tail.kv_dtype != PA_KV_FP4 && tail.kv_chunk == 0) {
+            // automatic ranges: 64 keys or more, and 1/32 of the longest tail or more,
+            // so that a shorter bound may need more than this one
+            const int64_t by_keys = ((int64_t)tail.max_seqlen_k + 63) / 64 + 1;
+            const size_t slots = (size_t)tail.num_seqs * tail.num_q_heads * (by_keys < 33 ? by_keys : 33);
+            plan.decode.workspace_any = 256 + round256(((size_t)tail.num_seqs + 1) * sizeof(int32_t)) +
+                                        round256(slots * tail.head_dim * sizeof(float)) + slots * sizeof(float);
+        }
+    }
+    plan.workspace_bytes = plan.prefix_bytes + plan.decode.workspace_any;
+    if (plan.workspace_bytes < 256) plan.workspace_bytes = 256;
+    return plan;
+}
+
+cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedPlan &plan, cudaStream_t stream) {
+    const pa_decode_params &d = p.dec;
+    MergeArgs m{};
+    m.sh.cu_groups = p.cu_groups;
+    m.sh.prefix_lens = p.prefix_lens;
+    m.sh.num_groups = p.num_groups;
+    m.sh.max_group = p.max_group;
+    m.sh.max_prefix = plan.prefix ? p.max_prefix : 0;
+    m.sh.max_splits = plan.max_splits;
+    uint8_t *ws = static_cast<uint8_t *>(d.workspace);
+    if (plan.prefix) {
+        const size_t slots = (size_t)d.num_seqs * d.num_q_heads * plan.max_splits;
+        uint8_t *o = ws + 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t));
+        m.sh.header = reinterpret_cast<int32_t *>(ws);
+        m.sh.base = reinterpret_cast<int32_t *>(ws + 256);
+        m.sh.o_part = reinterpret_cast<float *>(o);
+        m.sh.lse_part = reinterpret_cast<float *>(o + slots * d.head_dim * sizeof(float));
+        PrefillArgs a{};
+        const int64_t num_slots = d.num_pages * d.page_size;
+        if (!make_map_shared_q(&a.qmap, d)) return cudaErrorNotSupported;
+        if (d.kv_dtype == PA_KV_FP4) a.lay = fp4_layout(d.num_kv_heads, d.head_dim);
+        if (d.page_size == 16) {
+            for (int i = 0; i < 2; ++i) {
+                CUtensorMap *map = i == 0 ? &a.kmap : &a.vmap;
+                const void *pool = i == 0 ? d.k_cache : d.v_cache;
+                const bool ok = d.kv_dtype == PA_KV_FP4 ? make_map_fp4(map, pool, a.lay.row_bytes, num_slots, d.head_dim / 2)
+                                : d.kv_dtype == PA_KV_FP8_E4M3 ? make_map_fp8(map, pool, d.head_dim, d.num_kv_heads, num_slots, 16)
+                                                               : make_map(map, pool, d.head_dim, d.num_kv_heads, num_slots, 16);
+                if (!ok) return cudaErrorNotSupported;
+            }
+        }
+        a.k_cache = static_cast<const uint8_t *>(d.k_cache);
+        a.v_cache = static_cast<const uint8_t *>(d.v_cache);
+        a.page_table = d.page_table;
+        a.pt_stride = d.page_table_stride;
+        a.num_seqs = d.num_seqs;
+        a.num_q_heads = d.num_q_heads;
+        a.num_kv_heads = d.num_kv_heads;
+        a.page_size = d.page_size;
+        a.num_slots = (int32_t)num_slots;
+        a.scale_log2 = d.scale * 1.4426950408889634f;
+        a.k_scale = d.k_scale;
+        a.v_scale = d.v_scale;
+        a.sh = m.sh;
+        const unsigned ctas = prefix_ctas(p, plan.tiles);
+        const cudaError_t e = d.kv_dtype == PA_KV_FP4        ? launch_prefix<PA_KV_FP4>(a, d.head_dim, plan.tiles, ctas, stream)
+                              : d.kv_dtype == PA_KV_FP8_E4M3 ? launch_prefix<PA_KV_FP8_E4M3>(a, d.head_dim, plan.tiles, ctas, stream)
+                                                             : launch_prefix<PA_KV_BF16>(a, d.head_dim, plan.tiles, ctas, stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (plan.tail) {
+        // Its CTAs start as the prefix kernel's leave the SMs; it reads nothing of
+        // that kernel's, which has waited for all that came before.
+        pa_decode_params t = d;
+        t.workspace = ws + plan.prefix_bytes;
+        t.workspace_bytes = d.workspace_bytes - plan.prefix_bytes;
+        t.overlap_previous = plan.prefix ? 1 : 0;
+        m.tail.first_keys = p.prefix_lens;
+        m.tail.max_keys = p.max_suffix;
+        const cudaError_t e = d.kv_dtype == PA_KV_FP4 ? launch_decode_fp4(t, plan.decode, stream, &m.tail)
+                                                      : launch_decode(t, plan.decode, stream, &m.tail);
+        if (e != cudaSuccess) return e;
+    }
+    m.cache_seqlens = d.cache_seqlens;
+    m.num_seqs = d.num_seqs;
+    m.num_q_heads = d.num_q_heads;
+    m.num_kv_heads = d.num_kv_heads;
+    m.max_seqlen_k = d.max_seqlen_k;
+    m.tile_rows = plan.tiles * kBM;
+    m.out = static_cast<__nv_bfloat16 *>(d.out);
+    m.lse = d.lse;
+    return launch_merge(m, d.head_dim, stream);
+}
+
+}  // namespace pa

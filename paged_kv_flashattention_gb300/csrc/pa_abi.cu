@@ -97,7 +97,8 @@ pa_status pa_device_error(int32_t *bits, void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t (*getters[])(int **) = {error_word_store, error_word_decode, error_word_prefill, error_word_mixed,
                                       error_word_fp4, error_word_decode_fp4,
-                                      error_word_prefill_fp4, error_word_batch};
+                                      error_word_prefill_fp4, error_word_batch, error_word_decode_shared,
+                                      error_word_beam};
     int32_t acc = 0;
     for (auto get : getters) {
         int *addr = nullptr;
@@ -574,6 +575,137 @@ pa_status pa_lse_combine(const float *o_partial, const float *lse_partial, const
                                        num_rows, max_splits, head_dim, out, lse_out,
                                        static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "lse_combine launch");
+}
+
+// Validation of a pa_decode_shared call's host fields.
+static pa_status check_shared(const pa_decode_shared_params *p) {
+    if (p == nullptr) return fail(PA_ERR_INVALID, "params is NULL");
+    pa_status st = check_heads(p->dec.num_q_heads, p->dec.num_kv_heads, p->dec.head_dim, p->dec.page_size);
+    if (st != PA_OK) return st;
+    if (p->dec.num_seqs < 0 || p->dec.max_seqlen_k < 0 || p->num_groups < 0 || p->max_group < 0 || p->max_prefix < 0 ||
+        p->max_suffix < 0)
+        return fail(PA_ERR_INVALID, "negative sizes");
+    if (p->max_group > p->dec.num_seqs || p->max_prefix > p->dec.max_seqlen_k || p->max_suffix > p->dec.max_seqlen_k)
+        return fail(PA_ERR_INVALID, "max_group %d, max_prefix %d and max_suffix %d must not exceed num_seqs %d and max_seqlen_k %d",
+                    p->max_group, p->max_prefix, p->max_suffix, p->dec.num_seqs, p->dec.max_seqlen_k);
+    if (p->dec.sliding_window != 0 || p->dec.max_ctas != 0 || p->dec.overlap_previous != 0)
+        return fail(PA_ERR_UNSUPPORTED, "decode over shared prefixes takes no sliding_window, max_ctas or overlap_previous");
+    if (p->num_groups > 16384) return fail(PA_ERR_UNSUPPORTED, "more than 16384 groups in one call");
+    if (p->dec.max_seqlen_k > INT32_MAX - 1024) return fail(PA_ERR_UNSUPPORTED, "max_seqlen_k too large");
+    st = check_decode(&p->dec);
+    if (st != PA_OK) return st;
+    const pa_decode_params tail = shared_tail_params(*p);
+    st = check_decode(&tail);
+    if (st != PA_OK) return st;
+    // the prefix kernel counts the 128-key steps of all work items in 32 bits
+    const int64_t rows = (int64_t)p->max_group * (p->dec.num_q_heads / p->dec.num_kv_heads);
+    const int64_t items = p->num_groups * ((rows + 127) / 128) * p->dec.num_kv_heads;
+    if (items * (((int64_t)p->max_prefix + 127) / 128) > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "%d groups of up to %d sequences over prefixes of up to %d keys exceed 2^31 - 1 steps in one call",
+                    p->num_groups, p->max_group, p->max_prefix);
+    return PA_OK;
+}
+
+size_t pa_decode_shared_workspace_size(const pa_decode_shared_params *p) {
+    g_last_error[0] = 0;
+    if (check_shared(p) != PA_OK) return 0;
+    if (p->num_groups == 0) return decode_plan(p->dec).workspace_any;
+    return plan_decode_shared(*p).workspace_bytes;
+}
+
+pa_status pa_decode_shared(const pa_decode_shared_params *p, void *stream) {
+    g_last_error[0] = 0;
+    pa_status st = check_shared(p);
+    if (st != PA_OK) return st;
+    if (p->num_groups == 0) return pa_decode(&p->dec, stream);
+    if (p->dec.num_seqs == 0) return PA_OK;
+    const pa_decode_params &d = p->dec;
+    const int64_t ncols = ((int64_t)d.max_seqlen_k + d.page_size - 1) / d.page_size;
+    if (d.page_table_stride < ncols) return fail(PA_ERR_INVALID, "page_table_stride too small for max_seqlen_k");
+    if (!d.q || !d.k_cache || !d.v_cache || !d.page_table || !d.cache_seqlens || !d.out || !p->cu_groups || !p->prefix_lens)
+        return fail(PA_ERR_INVALID, "NULL pointer");
+    if (d.kv_dtype != PA_KV_BF16 && (!d.k_scale || !d.v_scale))
+        return fail(PA_ERR_INVALID, "FP8 and 4-bit pools need k_scale and v_scale");
+    if (!aligned16(d.q) || !aligned16(d.k_cache) || !aligned16(d.v_cache) || !aligned16(d.out))
+        return fail(PA_ERR_INVALID, "q, caches and out must be 16-byte aligned");
+    const SharedPlan plan = plan_decode_shared(*p);
+    if (d.workspace == nullptr || d.workspace_bytes < plan.workspace_bytes)
+        return fail(PA_ERR_INVALID, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes, d.workspace_bytes);
+    if (!aligned16(d.workspace)) return fail(PA_ERR_INVALID, "workspace must be 16-byte aligned");
+    cudaError_t e = launch_decode_shared(*p, plan, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "decode over shared prefixes: configuration not supported by this library");
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode_shared launch");
+}
+
+static pa_status check_select(const pa_beam_select_params *p) {
+    if (p == nullptr) return fail(PA_ERR_INVALID, "params is NULL");
+    if (p->num_groups < 0) return fail(PA_ERR_INVALID, "num_groups < 0");
+    if (p->beams < 1 || p->beams > 64) return fail(PA_ERR_UNSUPPORTED, "%d beams, 1 .. 64 are supported", p->beams);
+    if (p->vocab < 1 || p->vocab >= 1 << 24) return fail(PA_ERR_UNSUPPORTED, "vocabulary of %d, 1 .. 2^24 - 1 is supported", p->vocab);
+    if (p->num_out < 1 || p->num_out > 128 || p->num_out > p->vocab)
+        return fail(PA_ERR_UNSUPPORTED, "num_out %d, 1 .. min(128, vocabulary of %d) is supported", p->num_out, p->vocab);
+    if ((int64_t)p->num_groups * p->beams > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 beams in one call");
+    return PA_OK;
+}
+
+size_t pa_beam_select_workspace_size(const pa_beam_select_params *p) {
+    g_last_error[0] = 0;
+    if (check_select(p) != PA_OK) return 0;
+    return plan_select(*p).workspace_bytes;
+}
+
+pa_status pa_beam_select(const pa_beam_select_params *p, void *stream) {
+    g_last_error[0] = 0;
+    pa_status st = check_select(p);
+    if (st != PA_OK) return st;
+    if (p->logits_dtype != PA_LOGITS_BF16 && p->logits_dtype != PA_LOGITS_F16 && p->logits_dtype != PA_LOGITS_F32)
+        return fail(PA_ERR_INVALID, "logits_dtype %d is not a pa_logits_dtype", p->logits_dtype);
+    if (p->logits_stride < p->vocab) return fail(PA_ERR_INVALID, "logits_stride %lld < vocab %d", (long long)p->logits_stride, p->vocab);
+    if (p->pad_token < 0 || p->pad_token >= p->vocab) return fail(PA_ERR_INVALID, "pad_token %d outside the vocabulary", p->pad_token);
+    if (p->num_groups == 0) return PA_OK;
+    if (!p->logits || !p->scores || !p->out_scores || !p->out_parents || !p->out_tokens) return fail(PA_ERR_INVALID, "NULL pointer");
+    if (!aligned16(p->logits)) return fail(PA_ERR_INVALID, "logits must be 16-byte aligned");
+    if (p->out_scores == p->scores && p->num_out != p->beams)
+        return fail(PA_ERR_INVALID, "out_scores may be scores only if num_out is the number of beams");
+    const SelectPlan plan = plan_select(*p);
+    if (p->workspace == nullptr || p->workspace_bytes < plan.workspace_bytes)
+        return fail(PA_ERR_INVALID, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes, p->workspace_bytes);
+    if (!aligned16(p->workspace)) return fail(PA_ERR_INVALID, "workspace must be 16-byte aligned");
+    if ((int64_t)p->num_groups * p->beams * plan.chunks > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "too many beams for one launch");
+    cudaError_t e = launch_select(*p, plan, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "beam_select launch");
+}
+
+pa_status pa_beam_reorder(const pa_beam_reorder_params *p, void *stream) {
+    g_last_error[0] = 0;
+    if (p == nullptr) return fail(PA_ERR_INVALID, "params is NULL");
+    if (p->num_groups < 0 || p->max_seqlen_k < 0 || p->token_table_rows < 0 || p->num_pools < 0 || p->num_pages < 0 ||
+        p->history_len < 0)
+        return fail(PA_ERR_INVALID, "negative sizes");
+    if (p->beams < 1 || p->beams > 64) return fail(PA_ERR_UNSUPPORTED, "%d beams, 1 .. 64 are supported", p->beams);
+    if (p->page_size != 1 && p->page_size != 16) return fail(PA_ERR_UNSUPPORTED, "page_size %d not in {1,16}", p->page_size);
+    if (p->num_pools > PA_BEAM_REORDER_MAX_POOLS)
+        return fail(PA_ERR_UNSUPPORTED, "%d pools, at most %d are supported", p->num_pools, PA_BEAM_REORDER_MAX_POOLS);
+    if (p->token_table_stride < p->max_seqlen_k)
+        return fail(PA_ERR_INVALID, "token_table_stride %lld < max_seqlen_k %d", (long long)p->token_table_stride, p->max_seqlen_k);
+    if (p->history != nullptr && p->history_stride < p->history_len) return fail(PA_ERR_INVALID, "history_stride < history_len");
+    if (p->num_pools > 0 && (p->row_bytes <= 0 || p->row_bytes % 16 != 0 || p->row_bytes > (1 << 20)))
+        return fail(PA_ERR_UNSUPPORTED, "rows of %lld bytes: a positive multiple of 16 up to 2^20 is supported", (long long)p->row_bytes);
+    if (p->num_pages > (int64_t)INT32_MAX / p->page_size) return fail(PA_ERR_UNSUPPORTED, "pool larger than 2^31 slots");
+    const int64_t seqs = (int64_t)p->num_groups * p->beams;
+    if (seqs > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 sequences in one call");
+    const int64_t blocks = ((int64_t)p->max_seqlen_k + 127) / 128 + (p->history != nullptr ? ((int64_t)p->history_len + 127) / 128 : 0);
+    if (p->num_groups * blocks > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "too many columns for one launch");
+    if (seqs == 0) return PA_OK;
+    if (!p->parents || !p->token_table || !p->table_idx || !p->seqlens || (p->page_size > 1 && !p->spare_pages) ||
+        (p->num_pools > 0 && !p->pools))
+        return fail(PA_ERR_INVALID, "NULL pointer");
+    for (int32_t k = 0; k < p->num_pools; ++k) {
+        if (p->pools[k] == nullptr) return fail(PA_ERR_INVALID, "pool %d is NULL", k);
+        if (!aligned16(p->pools[k])) return fail(PA_ERR_INVALID, "pool %d must be 16-byte aligned", k);
+    }
+    cudaError_t e = launch_reorder(*p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "beam_reorder launch");
 }
 
 }  // extern "C"

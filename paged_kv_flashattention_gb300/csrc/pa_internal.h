@@ -46,8 +46,23 @@ struct DecodePlan {
 };
 DecodePlan plan_decode(const pa_decode_params &p);
 DecodePlan plan_decode_fp4(const pa_decode_params &p);      // 4-bit pools (decode_fp4.cu)
-cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream);
-cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream);
+// The split kernel alone, over the keys from first_keys[b] on, at most max_keys
+// of each sequence (the plan's), and where its partials are: decode over
+// shared prefixes merges them with the prefixes'.
+struct DecodeTail {
+    const int32_t *first_keys;
+    int32_t max_keys;
+    float *o_part;                // out: [num_seqs * Hq][max_splits][D]
+    float *lse_part;
+    const int32_t *header;        // [0] = T, keys (4-bit: units) of a range
+    const int32_t *prefix;        // [num_seqs + 1] keys (units) before each sequence
+    int32_t head_groups;
+    int32_t heads_per_group;      // query heads
+    int32_t max_splits;
+};
+cudaError_t launch_decode(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream, DecodeTail *tail = nullptr);
+cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan, cudaStream_t stream,
+                              DecodeTail *tail = nullptr);
 
 // Merge split partials.  Row r's split count is splits_per_row[r] if given;
 // else, with seg_header / seg_prefix (decode), the number of T-row CTA ranges
@@ -61,6 +76,30 @@ cudaError_t launch_lse_combine(const float *o_partial, const float *lse_partial,
 
 cudaError_t launch_prefill(const pa_prefill_params &p, cudaStream_t stream);
 cudaError_t launch_prefill_fp4(const pa_prefill_params &p, cudaStream_t stream);
+// Decode over shared prefixes (decode_shared.cu): the prefixes' partials, the
+// sequences' own, and their merge.  The workspace holds the first two in turn.
+struct SharedPlan {
+    int32_t tiles;                // query tiles per work item (T)
+    int32_t max_splits;           // partials of a query row over its prefix
+    bool prefix, tail;            // whether there is work of either kind
+    DecodePlan decode;            // of the keys behind the prefixes
+    size_t prefix_bytes;
+    size_t workspace_bytes;
+};
+pa_decode_params shared_tail_params(const pa_decode_shared_params &p);
+SharedPlan plan_decode_shared(const pa_decode_shared_params &p);
+cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedPlan &plan, cudaStream_t stream);
+
+// Beam search (beam.cu).
+struct SelectPlan {
+    int32_t chunks, chunk;        // chunks of a row, columns of a chunk
+    size_t list_bytes;
+    size_t workspace_bytes;
+};
+SelectPlan plan_select(const pa_beam_select_params &p);
+cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan, cudaStream_t stream);
+cudaError_t launch_reorder(const pa_beam_reorder_params &p, cudaStream_t stream);
+
 cudaError_t launch_mixed(const pa_prefill_params &pre, const pa_decode_params &dec, cudaStream_t stream);
 
 int num_sms();
@@ -81,5 +120,7 @@ cudaError_t error_word_fp4(int **addr);
 cudaError_t error_word_prefill_fp4(int **addr);
 cudaError_t error_word_batch(int **addr);
 cudaError_t error_word_decode_fp4(int **addr);
+cudaError_t error_word_decode_shared(int **addr);
+cudaError_t error_word_beam(int **addr);
 
 }  // namespace pa

@@ -107,6 +107,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// Prefixes that groups of sequences share (SHARED instantiations, decode_shared.cu):
+// group g is sequences cu_groups[g] .. cu_groups[g + 1] - 1 of the batch, its keys
+// [0, prefix_lens[first sequence]) are read through that sequence's table row.
+struct SharedArgs {
+    const int32_t *cu_groups;
+    const int32_t *prefix_lens;
+    int32_t num_groups;
+    int32_t max_group;            // bounds of the call
+    int32_t max_prefix;
+    int32_t max_splits;
+    float *o_part;                // [num_seqs * Hq][max_splits][D]
+    float *lse_part;
+    int32_t *header;              // [0]: steps of a CTA's range
+    int32_t *base;                // [num_groups + 1]: steps before each group
+};
+
 struct PrefillArgs {
     CUtensorMap qmap;             // bf16 (d, Hq, total_q), box (64, 1, 128)
     CUtensorMap kmap;             // bf16 (d, Hkv, num_slots), box (64, 1, 16)
@@ -140,6 +156,7 @@ struct PrefillArgs {
     Fp4Layout lay;                // 4-bit pools
     int32_t num_ctas;             // CTAs that run the work loop (the last of them resets sched);
                                   // 0: the count passed to prefill_body
+    SharedArgs sh;
 };
 
 // One work item: a 128-row query tile of T query heads of one request.
@@ -149,6 +166,8 @@ struct PrefillItem {
     int n_kv;     // of those, the steps the block mask keeps (all of them without one)
     int j0;       // first 128-key step (a sliding window skips the ones before)
     int lo_max;   // keys below this are outside some row's window: mask there
+    int rows;     // SHARED: rows of the item's T tiles together (rows_here: not used)
+    int split;    // SHARED: the partial's place among its rows' partials
 };
 
 // With a block-sparse mask an item's steps are the kept ones only: every
@@ -302,6 +321,91 @@ __device__ void prefill_sched_done(const PrefillArgs &a, int num_ctas) {
     }
 }
 
+// SHARED.  The work is the list of 128-key steps of every (group, KV head, T
+// query tiles), in that order; a tile's rows are (sequence of the group, query
+// head of the KV head).  CTA c takes the c-th range of `per_cta` steps and cuts it
+// into items where rows of the list end; an item gives one partial (O, lse) per
+// query row, the split it belongs to is its range's place among the ranges that
+// the row's steps lie in.
+struct SharedGroup {
+    int q0, n, P;                 // first sequence, sequences, keys
+};
+
+__device__ __forceinline__ SharedGroup shared_group(const PrefillArgs &a, int g) {
+    SharedGroup r{0, 0, 0};
+    if (g >= a.sh.num_groups) return r;
+    r.q0 = a.sh.cu_groups[g];
+    const int end = a.sh.cu_groups[g + 1];
+    // device data outside the call's bounds: an empty group
+    if (r.q0 < 0 || end < r.q0 || end > a.num_seqs || end - r.q0 > a.sh.max_group) {
+        raise_error(PA_DEVERR_SEQLENS);
+        r.q0 = 0;
+        return r;
+    }
+    r.n = end - r.q0;
+    if (r.n > 0) r.P = a.sh.prefix_lens[r.q0];
+    if (r.P < 0 || r.P > a.sh.max_prefix) {
+        raise_error(PA_DEVERR_SEQLENS);
+        r.P = 0;
+    }
+    return r;
+}
+
+template <int T>
+__device__ __forceinline__ int shared_tiles(const PrefillArgs &a, int n) {
+    return (n * (a.num_q_heads / a.num_kv_heads) + T * kBM - 1) / (T * kBM);
+}
+
+// The producer warp's walk over its range.  Lane i holds group g0 + i.
+template <int T>
+struct SharedWalk {
+    int at, end, per_cta;         // the next step, the range's end
+    int g0, g, before;            // the lanes' first group, the current group, steps before it
+    SharedGroup mine;
+    // The next item of the range into it; false at its end.
+    __device__ bool next(const PrefillArgs &a, PrefillItem &it, int lane) {
+        if (at >= end) return false;
+        for (;;) {
+            if (g - g0 >= 32) {
+                g0 = g;
+                mine = shared_group(a, g0 + lane);
+            }
+            const int q0 = __shfl_sync(0xffffffffu, mine.q0, g - g0), n = __shfl_sync(0xffffffffu, mine.n, g - g0);
+            const int P = __shfl_sync(0xffffffffu, mine.P, g - g0);
+            const int steps = (P + kBN - 1) / kBN, tiles = shared_tiles<T>(a, n);
+            const int cost = steps * tiles * a.num_kv_heads;
+            if (at >= before + cost) {            // ends: the list holds more than `at` steps
+                before += cost;
+                ++g;
+                continue;
+            }
+            const int group = a.num_q_heads / a.num_kv_heads;
+            const int row = (at - before) / steps, row_start = before + row * steps;
+            const int tile = row % tiles;
+            it.b = q0;
+            it.kvh = row / tiles;
+            it.q0 = q0 + tile * (T * kBM / group);
+            it.rows = min(T * kBM, n * group - tile * T * kBM);
+            it.j0 = at - row_start;
+            it.n_kv = min(steps - it.j0, end - at);
+            it.Lk = P;
+            it.split = at / per_cta - row_start / per_cta;
+            at += it.n_kv;
+            return true;
+        }
+    }
+};
+
+// The fields that follow from what SharedWalk gives.
+__device__ __forceinline__ void shared_fill(PrefillItem &it) {
+    it.n_all = it.n_kv;
+    it.kv_end = min(it.Lk, (it.j0 + it.n_kv) * kBN);
+    it.min_vis = it.Lk;
+    it.off = 0;
+    it.lo_max = 0;
+    it.tile = 0;
+}
+
 // Shared memory: T query tiles, then a ring of K-or-V tile slots (as many as
 // fit in 227 KiB next to Q and the output staging, at most 8), then 4 KiB of
 // output staging per softmax warp, then the barriers.  K_j goes to slot
@@ -309,7 +413,7 @@ __device__ void prefill_sched_done(const PrefillArgs &a, int num_ctas) {
 // tiles ahead of the MMAs: with one CTA per SM the loads from L2 are latency
 // bound, and bytes in flight set the rate (at d = 128 with two heads, 4
 // slots measured as fast as 5).
-template <int D, int T, bool F8, bool F4 = false>
+template <int D, int T, bool F8, bool F4 = false, bool SHARED = false>
 struct PrefillSmem {
     static constexpr int kHalves = D / 64;                 // 64-column (128-byte) halves
     static constexpr int kTileBytes = kHalves * 128 * 128; // 128 rows x D, 16-bit elements
@@ -320,7 +424,8 @@ struct PrefillSmem {
     // thread its own row) 194, and 78, 75 and 82 on sixteen requests of 512 rows.
     static constexpr int kStageCols = F4 ? 32 : 64;
     static constexpr int kStageBytes = 4 * T * 64 * kStageCols;      // 32 rows x kStageCols columns bf16 per warp
-    static constexpr int kAvail = 232448 - 1024 - kRing - kStageBytes - 512;
+    static constexpr int kBarBytes = SHARED ? 1024 : 512;            // SHARED: whole items in the ring, and 32 words
+    static constexpr int kAvail = 232448 - 1024 - kRing - kStageBytes - kBarBytes;
     // FP8, d = 128 (in place): an E4M3 tile lands in the upper half of its f16
     // slot (row r's 128 codes where the f16 row r of the upper 64 columns
     // goes) and is widened where it lies, so the slots serve both rings.
@@ -352,7 +457,7 @@ struct PrefillSmem {
     static constexpr int kConv = kInPlace ? kRing : kRing + kSlots * kLTile;
     static constexpr int kStage = kInPlace ? kRing + kCSlots * kTileBytes : kConv + kCSlots * kTileBytes;
     static constexpr int kBars = kStage + kStageBytes;
-    static constexpr int kTotal = kBars + 512;
+    static constexpr int kTotal = kBars + kBarBytes;
 };
 
 // Eight bf16 (one 16-byte piece of a Q tile) to eight f16 of x * s.
@@ -428,10 +533,16 @@ cudaError_t check_register_split(Kernel kern) {
 
 // EXT: the instantiation for sliding windows and block-sparse masks (plain
 // launches keep that arithmetic out of their registers).
-template <int D, int T, bool F8, bool EXT, bool F4 = false>
+//
+// SHARED: decode queries over the prefixes of their groups; T = 2 tiles are two
+// runs of (sequence, head) rows of one KV head.
+template <int D, int T, bool F8, bool EXT, bool F4 = false, bool SHARED = false>
 __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_ctas = 0) {
     static_assert(!F4 || F8, "4-bit pools use the widening path");
-    using S = PrefillSmem<D, T, F8, F4>;
+    static_assert(!SHARED || !EXT, "no masks over shared prefixes");
+    using S = PrefillSmem<D, T, F8, F4, SHARED>;
+    // (a dependent of a SHARED launch does not wait for what came before it)
+    if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
     // A kernel launched after this one as a programmatic dependent (decode
     // sharing the GPU) may start once every CTA of this grid is resident.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -451,7 +562,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     constexpr int NC = F8 ? S::kCSlots : NS;  // slots the MMA reads from
     constexpr int kConverters = F8 ? 2 : 0;
     constexpr bool kInPlace = S::kInPlace;
-    constexpr bool kClasses = F4 && !EXT;      // items in classes of positions (prefill_item)
+    constexpr bool kClasses = F4 && !EXT && !SHARED;      // items in classes of positions (prefill_item)
     auto land = [&](int slot) { return smem + S::kRing + slot * S::kLStride + S::kLOff; };
     uint64_t *q_full = bars;                 // 1: Q tiles of the item loaded
     uint64_t *q_empty = bars + 1;            // 1: every S MMA of the item done
@@ -469,6 +580,9 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                                              //    and (page size 1) the other gather warps
     int *item_idx = reinterpret_cast<int *>(item_empty + R);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_idx + R);
+    // SHARED: the items themselves, 8 words each, and the scan's scratch
+    int4 *items = reinterpret_cast<int4 *>(smem + S::kBars + 512);
+    int *scan = reinterpret_cast<int *>(items + 2 * R);
     // Each role walks the same item list and keeps its own counts of items
     // (phase of q_full / q_empty), items with keys (phase of o_final), key
     // steps (phase of s_full / p_full) and K/V loads (ring slot and phase).
@@ -503,10 +617,66 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         }
         fence_mbar_init();
     }
+    SharedWalk<T> walk{};
+    if constexpr (SHARED) {
+        // steps of the whole list, steps before this thread's groups, and the group
+        // in which this CTA's range starts
+        constexpr int kThreads = 128 * (T + 1);
+        const int per = (a.sh.num_groups + kThreads - 1) / kThreads;
+        const int from = min((int)threadIdx.x * per, a.sh.num_groups), to = min(from + per, a.sh.num_groups);
+        auto cost = [&](int g) {
+            const SharedGroup r = shared_group(a, g);
+            return (r.P + kBN - 1) / kBN * shared_tiles<T>(a, r.n) * a.num_kv_heads;
+        };
+        int run = 0;
+        for (int g = from; g < to; ++g) run += cost(g);
+        int incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        int total = 0, acc = incl - run;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) acc += scan[w];
+            total += scan[w];
+        }
+        walk.per_cta = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+        walk.at = (int)min((int64_t)blockIdx.x * walk.per_cta, (int64_t)total);
+        walk.end = min(total - walk.at, walk.per_cta) + walk.at;
+        for (int g = from; g < to; ++g) {
+            const int c = cost(g);
+            if (walk.at >= acc && walk.at < acc + c) {
+                scan[16] = g;
+                scan[17] = acc;
+            }
+            if (blockIdx.x == 0) a.sh.base[g] = acc;
+            acc += c;
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            a.sh.base[a.sh.num_groups] = total;
+            a.sh.header[0] = walk.per_cta;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The item in ring slot `slot`; false at the end of the list.
+    auto read_item = [&](int slot, PrefillItem &it) {
+        if constexpr (SHARED) {
+            const int4 x = items[2 * slot], y = items[2 * slot + 1];
+            it.b = x.x; it.kvh = x.y; it.q0 = x.z; it.rows = x.w;
+            it.j0 = y.x; it.n_kv = y.y; it.Lk = y.z; it.split = y.w;
+            shared_fill(it);
+            return it.n_kv;
+        } else {
+            return item_idx[slot];
+        }
+    };
 
     // Page size 1 gathers.  gather_rows reads the page-table entries of K or
     // V tile c of item `it` (lane l holds keys l, l + 32, ...); gather_copy
@@ -745,11 +915,34 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         };
         int local = 0, gl = 0;
         PrefillItem it;
+        if constexpr (SHARED) {
+            walk.g = walk.g0 = scan[16];
+            walk.before = scan[17];
+            if (walk.at < walk.end) walk.mine = shared_group(a, walk.g0 + lane);
+        }
+        auto take_shared = [&](int n) {
+            const int slot = n % R;
+            it.n_kv = -1;
+            const bool some = walk.next(a, it, lane);
+            bool ok = true;
+            if (lane == 0) {
+                ok = n < R || mbar_wait(&item_empty[slot], ((n / R) - 1) & 1);
+                if (ok) {
+                    items[2 * slot] = make_int4(it.b, it.kvh, it.q0, it.rows);
+                    items[2 * slot + 1] = make_int4(it.j0, some ? it.n_kv : -1, it.Lk, it.split);
+                    mbar_arrive(&item_full[slot]);
+                }
+            }
+            shared_fill(it);
+            return __shfl_sync(0xffffffffu, (int)ok, 0) && some ? 0 : -1;
+        };
         // An item is taken when the previous one's loads are all issued (not
         // earlier: a CTA that holds an item it has not started keeps it from
         // CTAs that are idle at the end).
-        for (int v; (v = take(local)) >= 0;) {
-            prefill_item<T, EXT, kClasses>(a, v, it);
+        for (int v;;) {
+            if constexpr (SHARED) v = take_shared(local); else v = take(local);
+            if (v < 0) break;
+            if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
             // load 2j is K_j, 2j + 1 is V_j; gl counts loads over the CTA's
             // life.  The Q tiles are loaded once the previous item's last S
             // MMA is done.
@@ -759,9 +952,16 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, T * S::kTileBytes);
                     for (int k = 0; k < T; ++k)
-                        for (int hh = 0; hh < H; ++hh)
-                            tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.h0 + k,
-                                        it.q0 + it.tile * kBM, q_full);
+                        for (int hh = 0; hh < H; ++hh) {
+                            if constexpr (SHARED) {       // a box of the KV head's query heads (zeros past the batch)
+                                const int group = a.num_q_heads / a.num_kv_heads;
+                                tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.kvh * group,
+                                            it.q0 + k * (kBM / group), q_full);
+                            } else {
+                                tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.h0 + k,
+                                            it.q0 + it.tile * kBM, q_full);
+                            }
+                        }
                 }
                 return true;
             };
@@ -817,7 +1017,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             if (!ok) break;
             ++local;
         }
-        if (lane == 0) prefill_sched_done(a, a.num_ctas > 0 ? a.num_ctas : sched_ctas);
+        if (!SHARED && lane == 0) prefill_sched_done(a, a.num_ctas > 0 ? a.num_ctas : sched_ctas);
       } else if (warp != kMma && !paged16 && warp - kMma < kGatherWarps) {
         // --------------------------------- extra gather warps (page 1) ----
         const int g = warp - kMma;                      // 1, 2
@@ -826,12 +1026,12 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         for (;;) {
             const int slot = local % R;
             if (!__all_sync(0xffffffffu, mbar_wait(&item_full[slot], (local / R) & 1))) break;
-            const int v = item_idx[slot];
+            const int v = read_item(slot, it);
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             ++local;
             if (v < 0) break;
-            prefill_item<T, EXT, kClasses>(a, v, it);
+            if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
             if (!gather_item(it, gl, g)) break;
             gl += 2 * it.n_kv;
         }
@@ -844,11 +1044,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         while (ok) {
             const int slot = local % R;
             if (!__all_sync(0xffffffffu, mbar_wait(&item_full[slot], (local / R) & 1))) break;
-            const int v = item_idx[slot];
+            const int v = read_item(slot, it);
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (v < 0) break;
-            prefill_item<T, EXT, kClasses>(a, v, it);
+            if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
             // Q tiles: bf16 -> f16 of q * k_scale, in place
             if (!__all_sync(0xffffffffu, mbar_wait(q_full, local & 1))) break;
             ++local;
@@ -959,22 +1159,23 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 }
                 umma_commit(&s_full[k]);
             };
-            int local = 0, gl = 0, gs = 0;
+            int local = 0, gl = 0, gs = 0, gs1 = 0;   // (gs1: tile 1's steps, SHARED)
             bool ok = true;
             PrefillItem it;
             while (ok) {
                 const int slot = local % R;
                 if (!mbar_wait(&item_full[slot], (local / R) & 1)) break;
-                const int v = item_idx[slot];
+                const int v = read_item(slot, it);
                 mbar_arrive(&item_empty[slot]);
                 if (v < 0) break;
-                prefill_item<T, EXT, kClasses>(a, v, it);
+                if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
                 const int n_kv = it.n_kv;
+                const int tiles = SHARED && it.rows <= kBM ? 1 : T;      // the item's tiles
                 if (!mbar_wait(F8 ? q_conv : q_full, local & 1)) break;
                 if (n_kv > 0) {
                     if (!wait_full(gl)) break;
                     tc_fence_after();
-                    for (int k = 0; k < T; ++k) issue_s(k, gl);
+                    for (int k = 0; k < tiles; ++k) issue_s(k, gl);
                     umma_commit(&mempty[gl % NC]);                       // K_0 consumed
                 }
                 if (n_kv <= 1) umma_commit(q_empty);                     // every S of the item issued
@@ -1003,8 +1204,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                                     make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();                          // generic writes -> the MMA's reads
                     }
-                    for (int k = 0; k < T; ++k) {
-                        if (!mbar_wait(&p_full[k], (gs + j) & 1)) { ok = false; break; }
+                    for (int k = 0; k < tiles; ++k) {
+                        if (!mbar_wait(&p_full[k], ((SHARED && k > 0 ? gs1 : gs) + j) & 1)) { ok = false; break; }
                         if (k == 0 && !wait_full(cv)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t o_tm = tmem + 256 + kOCols * k;
@@ -1012,7 +1213,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             umma_ts(o_tm, tmem + 128 * k + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
                                     (j > 0 || kk > 0) ? 1u : 0u);
-                        if (k == T - 1) umma_commit(&mempty[cv % NC]);   // V_j consumed
+                        if (k == tiles - 1) umma_commit(&mempty[cv % NC]);   // V_j consumed
                         if (j + 1 == n_kv) umma_commit(&o_final[k]);     // O_k of the item complete
                         if (j + 1 < n_kv) {
                             if (k == 0) {
@@ -1020,7 +1221,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                                 tc_fence_after();
                             }
                             issue_s(k, cv + 1);
-                            if (k == T - 1) {
+                            if (k == tiles - 1) {
                                 umma_commit(&mempty[(cv + 1) % NC]);     // K_{j+1} consumed
                                 if (j + 2 == n_kv) umma_commit(q_empty);  // last S of the item
                             }
@@ -1030,6 +1231,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 // (items without keys write zeros and use no MMA)
                 gl += 2 * n_kv;
                 gs += n_kv;
+                if (SHARED && tiles > 1) gs1 += n_kv;
                 ++local;
             }
         }
@@ -1051,18 +1253,31 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         const int slot = local % R;
         ok = __all_sync(0xffffffffu, mbar_wait(&item_full[slot], (local / R) & 1));
         if (!ok) break;
-        const int v = item_idx[slot];
+        const int v = read_item(slot, it);
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[slot]);
         ++local;
         if (v < 0) break;
-        prefill_item<T, EXT, kClasses>(a, v, it);
+        if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
+        if constexpr (SHARED) {
+            it.rows_here = min(max(it.rows - kBM * k, 0), kBM);
+            if (it.rows_here == 0) continue;          // the item has no such tile
+            if (32 * (warp & 3) >= it.rows_here) {    // no row of this warp: it only keeps step
+                for (int j = 0; ok && j < it.n_kv; ++j) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
+                    if (ok) mbar_arrive(&p_full[k]);
+                }
+                gs += it.n_kv;
+                ++fin;
+                continue;
+            }
+        }
         if constexpr (F4) {
             sl2 = fp4_score_scale(a.scale_log2, __ldg(a.k_scale + it.kvh));
             c2 = make_float2(sl2, sl2);
         }
         const int n_kv = it.n_kv, Lk = it.Lk, off = it.off, min_vis = it.min_vis;
-        const int qi = it.tile * kBM + r;             // query index within the request
+        const int qi = it.tile * kBM + r;             // query index within the request (SHARED: not used)
         const bool row_valid = r < it.rows_here;
         const int vis_end = a.causal ? min(Lk, off + qi + 1) : Lk;   // keys [0, vis_end)
         float m_run = -INFINITY;
@@ -1149,7 +1364,48 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         // ---- epilogue: O / l -> bf16, lse
         if (ok && n_kv > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_final[k], fin & 1));
         tc_fence_after();
-        if (ok) {
+        if constexpr (SHARED) {
+            // the rows' partials: O / l in 32 bits through the warp's staging buffer, 128
+            // (4-bit: 64) bytes of a row at a time, and lse
+            if (ok) {
+                constexpr int kCols = S::kStageCols / 2;
+                constexpr int kPieces = kCols / 4;                     // of 16 bytes
+                const int group = a.num_q_heads / a.num_kv_heads;
+                const float inv = (l_run > 0.f ? 1.f / l_run : 0.f) * (F8 ? a.v_scale[it.kvh] : 1.f);
+                uint8_t *stage = smem + S::kStage + warp * (64 * S::kStageCols);
+                auto swz = [](int r) { return kPieces == 8 ? r & 7 : (r >> 1) & 3; };
+                auto slot_of = [&](int rt) {                           // row rt of the tile
+                    const int m = (k * kBM + rt) / group, h = it.kvh * group + (k * kBM + rt) % group;
+                    return ((int64_t)(it.q0 + m) * a.num_q_heads + h) * a.sh.max_splits + it.split;
+                };
+                const bool fits = it.split < a.sh.max_splits;          // always, for lengths within the bounds
+                if (!fits) raise_error(PA_DEVERR_SEQLENS);
+#pragma unroll 1
+                for (int part = 0; part < D / kCols; ++part) {
+                    uint32_t orr[kCols];
+                    if constexpr (kCols == 32) tmem_ld32(o_tm + part * kCols, orr);
+                    else tmem_ld16(o_tm + part * kCols, orr);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < kPieces; ++u)
+                        *reinterpret_cast<float4 *>(stage + lane * (4 * kCols) + ((u ^ swz(lane)) * 16)) =
+                            make_float4(__uint_as_float(orr[4 * u]) * inv, __uint_as_float(orr[4 * u + 1]) * inv,
+                                        __uint_as_float(orr[4 * u + 2]) * inv, __uint_as_float(orr[4 * u + 3]) * inv);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int rr = i * (32 / kPieces) + lane / kPieces, q = lane % kPieces;
+                        const float4 val = *reinterpret_cast<const float4 *>(stage + rr * (4 * kCols) + ((q ^ swz(rr)) * 16));
+                        const int rt = (warp & 3) * 32 + rr;
+                        if (fits && rt < it.rows_here)
+                            *reinterpret_cast<float4 *>(a.sh.o_part + slot_of(rt) * D + part * kCols + q * 4) = val;
+                    }
+                    __syncwarp();
+                }
+                if (fits && row_valid)
+                    a.sh.lse_part[slot_of(r)] = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            }
+        } else if (ok) {
             const int64_t tok = (int64_t)it.q0 + qi;
             const int h = it.h0 + k;
             const float inv = (l_run > 0.f ? 1.f / l_run : 0.f) * (F8 ? __ldg(a.v_scale + it.kvh) : 1.f);
