@@ -7,10 +7,9 @@
 // launch, one CTA per group, forms lse and the totals in 64 bits and merges the
 // chunks' lists.
 //   - A chunk keeps a threshold that at least n of its elements reach: at first
-//     the least of its warps' ceil(n / 8)-th largest thread maxima of the first
-//     tile, then the n-th largest found.  Elements above it go to a buffer in
-//     shared memory (with n = 8 about 22 of the first 2048, fewer of every later
-//     tile), all others into the sum of exponentials at once, with the threshold
+//     the n-th largest of the thread maxima of the first tile, then the n-th
+//     largest found.  Elements above it go to a buffer in shared memory (about n of
+//     each tile of 2048), all others into the sum of exponentials at once, with the threshold
 //     as reference: it bounds them.  A buffer that fills up is cut to its n
 //     largest.  An entry's rank among the buffer's is its place in the list.
 //   - Two candidates of different beams are ordered by sums that differ by
@@ -151,39 +150,32 @@ struct Columns {
     }
 };
 
-// The m-th largest of the warp's values (1 <= m <= 32).
-__device__ __forceinline__ uint32_t warp_mth(uint32_t v, int m, int lane) {
-    uint32_t top = 0;
-    for (int i = 0; i < m; ++i) {
-        top = __reduce_max_sync(0xffffffffu, v);
-        const unsigned who = __ballot_sync(0xffffffffu, v == top);
-        if (lane == __ffs(who) - 1) v = 0;
-    }
-    return top;
-}
-
-// A value that at least n of the CTA's thread maxima reach (0 is below all
-// values): the least of the warps' ceil(n / warps)-th largest.
-__device__ __forceinline__ uint32_t block_floor(uint32_t top, int n, uint32_t *scratch) {
+// A value that n of the CTA's thread maxima reach and few others do: their n-th
+// largest with the bits below `low` cleared (0 is below all values).  One warp
+// finds it bit by bit, 16 bits in about 700 clocks; the least of the warps'
+// (n / warps)-th largest would take 100, but lets through three times as many
+// elements, and all of a tile of which one warp has none.
+__device__ __forceinline__ uint32_t block_floor(uint32_t top, int n, int low, uint32_t (&tops)[kSelThreads]) {
     const int lane = threadIdx.x & 31;
-    const uint32_t mine = warp_mth(top, (n + kSelWarps - 1) / kSelWarps, lane);
-    if (lane == 0) scratch[threadIdx.x >> 5] = mine;
+    tops[threadIdx.x] = top;
     __syncthreads();
-    uint32_t least = scratch[0];
+    if (threadIdx.x < 32) {
+        uint32_t v[kSelWarps];
 #pragma unroll
-    for (int w = 1; w < kSelWarps; ++w) least = min(least, scratch[w]);
-    return least;
-}
-
-__device__ __forceinline__ double block_sum(double v, double *scratch) {
+        for (int i = 0; i < kSelWarps; ++i) v[i] = tops[lane + 32 * i];
+        uint32_t at = 0;
+        for (int bit = 31; bit >= low; --bit) {
+            const uint32_t trial = at | 1u << bit;
+            uint32_t reach = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+            for (int i = 0; i < kSelWarps; ++i) reach += v[i] >= trial;
+            if ((int)__reduce_add_sync(0xffffffffu, reach) >= n) at = trial;
+        }
+        __syncwarp();
+        if (lane == 0) tops[0] = at;
+    }
     __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) s += scratch[w];
-    return s;
+    return tops[0];
 }
 
 // The largest value below an ordered word's (-0 is 0).
@@ -197,9 +189,8 @@ template <int DT>
 __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const SelectArgs a) {
     __shared__ uint64_t buf[kKept + kTile];
     __shared__ uint64_t best[128];
-    __shared__ unsigned long long dropped;
-    __shared__ double sums[kSelWarps];
-    __shared__ uint32_t scratch[kSelWarps];
+    __shared__ uint32_t tops[kSelThreads];
+    __shared__ unsigned long long dropped;           // in units of 2^-32
     __shared__ int count;
     after_previous();
     const int t = threadIdx.x, lane = t & 31;
@@ -267,7 +258,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
             float top = x[0];
 #pragma unroll
             for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
-            const uint32_t least = block_floor(ordered(top), n, scratch);
+            const uint32_t least = block_floor(ordered(top), n, 16, tops);
             // elements of that value are entries too
             if (least > ordered(-INFINITY)) raise(value_below(least));
         }
@@ -291,18 +282,28 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
     }
     __syncthreads();
     const int kept = cut(count);
+    // rest of all threads, each to 2^-32 of the least term of the list, in whole
+    // numbers of two halves
+    const unsigned long long units = __float2ull_rn(rest * 0x1p32f);
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)units & 0xffffffu);
+    const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(units >> 24));
+    if (lane == 0) atomicAdd(&dropped, ((unsigned long long)hi << 24) + lo);
+    __syncthreads();
     // The list; its exponentials in 64 bits.
     const int64_t at = (int64_t)row_id * a.chunks + c;
     float2 *list = a.lists + at * a.n;
     const float top = kept > 0 ? key_value(best[0]) : -INFINITY;
-    double sum = rest > 0.f ? (double)rest * exp((double)ref - (double)top) : 0.0;
-    for (int e = t; e < kept; e += kSelThreads) {
-        const float x = key_value(best[e]);
-        list[e] = make_float2(x, __int_as_float((int)~(uint32_t)best[e]));
-        sum += exp((double)x - (double)top);
+    if (t < 32) {
+        double sum = 0.0;
+        for (int e = lane; e <= kept; e += 32) {     // entry `kept`: the rest, at its reference
+            const float x = e < kept ? key_value(best[e]) : ref;
+            if (e < kept) list[e] = make_float2(x, __int_as_float((int)~(uint32_t)best[e]));
+            if (e < kept || dropped != 0) sum += exp((double)x - (double)top) * (e < kept ? 1.0 : (double)dropped * 0x1p-32);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) a.sums[at] = ChunkSum{(double)top, sum};
     }
-    sum = block_sum(sum, sums);
-    if (t == 0) a.sums[at] = ChunkSum{(double)top, sum};
     // Fewer finite logits than n: the first columns of the others.
     if (kept < a.n && t < 32) {
         int have = kept;
@@ -323,26 +324,32 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
 constexpr int kRound = 4 * kSelThreads;
 constexpr int kBuf2 = kKept + kRound;
 
+// Doubles as unsigned words in the same order; -0 as 0.
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+    return (b >> 63) ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double unordered(uint64_t k) {
+    return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
+}
+
 __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectArgs a) {
-    __shared__ double tot[kBuf2], best_tot[128], lses[64];
-    __shared__ uint32_t idx[kBuf2], best_idx[128];
+    __shared__ uint64_t tot[kBuf2], best_tot[128];
+    __shared__ uint32_t idx[kBuf2], best_idx[128], tops[kSelThreads];
+    __shared__ double lses[64];
     __shared__ float score[64];
     __shared__ uint8_t state[64];                    // 0: reads its logits, 1: ended, 2: score -inf
-    __shared__ uint32_t scratch[kSelWarps];
     __shared__ int count;
     after_previous();
     const int t = threadIdx.x, lane = t & 31, g = blockIdx.x;
     const int K = a.beams, S = a.chunks, n = a.n, limit = kept_limit(n);
-    for (int k = t; k < K; k += kSelThreads) {
-        const float s = cleaned(a.scores[g * K + k]);
-        score[k] = s;
-        state[k] = s == -INFINITY ? 2 : a.finished != nullptr && a.finished[g * K + k] != 0 ? 1 : 0;
-    }
     if (t == 0) count = 0;
-    __syncthreads();
-    for (int k = t >> 5; k < K; k += kSelWarps) {    // lse, a warp per beam
+    for (int k = t >> 5; k < K; k += kSelWarps) {    // a warp per beam: its state, its lse
+        const float s = cleaned(a.scores[g * K + k]);
+        const bool ended = a.finished != nullptr && a.finished[g * K + k] != 0;
+        const int st = s == -INFINITY ? 2 : ended ? 1 : 0;
         double l = 0.0;
-        if (state[k] == 0) {
+        if (st == 0) {
             const ChunkSum *cs = a.sums + ((int64_t)g * K + k) * S;
             double top = -INFINITY, sum = 0.0;
             for (int c = lane; c < S; c += 32) top = fmax(top, cs[c].top);
@@ -354,40 +361,42 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             l = top + log(sum);                      // (no finite logit: not used)
         }
-        if (lane == 0) lses[k] = l;
+        if (lane == 0) {
+            score[k] = s;
+            state[k] = (uint8_t)st;
+            lses[k] = l;
+        }
     }
     __syncthreads();
 
     const unsigned per_beam = (unsigned)(S * n), entries = (unsigned)K * per_beam;
-    auto entry = [&](unsigned e, double &v, uint32_t &at) {
+    // Entry e's ordered total, 0 for none, and its beam and column.
+    auto entry = [&](unsigned e, uint32_t &at) -> uint64_t {
         const int k = (int)(e / per_beam), r = (int)(e % per_beam);
-        v = -INFINITY;
         at = 0xffffffffu;
         if (state[k] == 0) {
             const float2 x = a.lists[((int64_t)g * K + k) * per_beam + r];
             const uint32_t col = __float_as_uint(x.y);
-            if (col != 0xffffffffu) {
-                at = (uint32_t)k << 24 | col;
-                if (x.x != -INFINITY) v = (double)score[k] + ((double)x.x - lses[k]);
-            }
-        } else if (r < n) {                          // n <= vocab columns
-            int col = r;
-            if (state[k] == 1) {
-                col = r == 0 ? a.pad : r - 1 + (r - 1 >= a.pad);
-                if (r == 0) v = (double)score[k];
-            }
-            at = (uint32_t)k << 24 | (uint32_t)col;
+            if (col == 0xffffffffu) return 0;
+            at = (uint32_t)k << 24 | col;
+            return ordered(x.x == -INFINITY ? (double)-INFINITY : (double)score[k] + ((double)x.x - lses[k]));
         }
+        if (r >= n) return 0;                        // n <= vocab columns
+        int col = r;
+        if (state[k] == 1) col = r == 0 ? a.pad : r - 1 + (r - 1 >= a.pad);
+        at = (uint32_t)k << 24 | (uint32_t)col;
+        return ordered(state[k] == 1 && r == 0 ? (double)score[k] : (double)-INFINITY);
     };
-    double thr = -INFINITY;                          // with thr_idx: the n-th best so far
+    uint64_t thr = 0;                                // with thr_idx: the n-th best so far
     uint32_t thr_idx = 0xffffffffu;
-    auto better = [](double x, uint32_t i, double y, uint32_t j) { return x > y || (x == y && i < j); };
+    auto better = [](uint64_t x, uint32_t i, uint64_t y, uint32_t j) { return x > y || (x == y && i < j); };
     // Ranks the buffer's m entries; the n best, in order, into best.
     auto cut = [&](int m) {
         for (int e = t; e < m; e += kSelThreads) {
-            const double v = tot[e];
+            const uint64_t v = tot[e];
             const uint32_t at = idx[e];
             int rank = 0;
+#pragma unroll 4
             for (int i = 0; i < m; ++i) rank += better(tot[i], idx[i], v, at);
             if (rank < n) {
                 best_tot[rank] = v;
@@ -398,22 +407,23 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
         return min(m, n);
     };
     for (unsigned e0 = 0; e0 < entries; e0 += kRound) {
-        double v[kRound / kSelThreads];
+        uint64_t v[kRound / kSelThreads];
         uint32_t at[kRound / kSelThreads];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kRound / kSelThreads; ++i) {
-            at[i] = 0xffffffffu;
             const unsigned e = e0 + i * kSelThreads + t;
-            if (e < entries) entry(e, v[i], at[i]);
-            if (at[i] != 0xffffffffu) top = max(top, ordered(__double2float_rd(v[i])));
+            v[i] = 0;
+            at[i] = 0xffffffffu;
+            if (e < entries) v[i] = entry(e, at[i]);
+            top = max(top, (uint32_t)(v[i] >> 32));
         }
-        uint32_t least = 0;                          // (no value's word is 0)
-        if (e0 == 0) least = block_floor(top, n, scratch);
+        uint32_t least = 0;
+        if (e0 == 0) least = block_floor(top, n, 12, tops);
         int last = 0;
 #pragma unroll
         for (int i = 0; i < kRound / kSelThreads; ++i) {
-            if (at[i] == 0xffffffffu || ordered(__double2float_rd(v[i])) < least || !better(v[i], at[i], thr, thr_idx)) continue;
+            if (v[i] == 0 || (uint32_t)(v[i] >> 32) < least || !better(v[i], at[i], thr, thr_idx)) continue;
             last = atomicAdd(&count, 1);
             tot[last] = v[i];
             idx[last] = at[i];
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
     cut(count);
     for (int e = t; e < n; e += kSelThreads) {
         const uint32_t at = best_idx[e];
-        a.out_scores[(int64_t)g * n + e] = (float)best_tot[e];
+        a.out_scores[(int64_t)g * n + e] = (float)unordered(best_tot[e]);
         a.out_parents[(int64_t)g * n + e] = (int)(at >> 24);
         a.out_tokens[(int64_t)g * n + e] = (int)(at & 0xffffffu);
     }
@@ -573,7 +583,7 @@ cudaError_t launch_chunks(const SelectArgs &a, cudaStream_t stream) {
 
 // Columns of a chunk: whole tiles, about kCtas CTAs while there are tiles enough
 // (a constant: the workspace's size is the same on every device).
-constexpr int kCtas = 152 * 24;
+constexpr int kCtas = 152 * 8;
 SelectPlan plan_select(const pa_beam_select_params &p) {
     SelectPlan plan{};
     const int64_t rows = (int64_t)p.num_groups * p.beams, tiles = ((int64_t)p.vocab + kTile - 1) / kTile;

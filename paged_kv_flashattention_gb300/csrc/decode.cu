@@ -97,9 +97,7 @@ __global__ void __launch_bounds__((HPC + 1) * 32) decode_kernel(const DecodeArgs
     else
         decode_consume<D, G, HPC, F8>(a, prefix, T, g0, g1, ring, full, empty, pbuf, stage_ctr,
                                       warp, lane);
-    // over the keys behind shared prefixes the kernel overlaps the one before it:
-    // it ends after that one, so that the merge need wait for this one alone
-    if (a.first_keys != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.first_keys != nullptr) decode_end_after_previous();
 }
 
 // One warp per row (a (sequence, head) pair): merge its splits by LSE.

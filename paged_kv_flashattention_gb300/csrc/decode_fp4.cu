@@ -549,7 +549,7 @@ decode_fp4_kernel(const Fp4DecodeArgs a, const __grid_constant__ Fp4MapsOf<BOX> 
     const int g0 = (int)min((int64_t)blockIdx.x * T, (int64_t)total), g1 = min(total - g0, T) + g0;
     if (warp == HPC) fp4_produce<D, HPC, BOX>(a, maps, prefix, T, g0, g1, smem, full, empty, lane);
     else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
-    if (a.first_keys != nullptr) after_previous();       // ends after the kernel that it overlaps (decode.cu)
+    if (a.first_keys != nullptr) decode_end_after_previous();
 }
 
 // The log-sum-exp combine (decode.cu's, with its split count): W warps share a

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -79,6 +80,14 @@ struct DecodeSmem {
     static constexpr int kStages = STAGES;
     static constexpr int kRingBytes = kStages * kStageBytes;
 };
+
+// Over the keys behind shared prefixes a split kernel overlaps the kernel before
+// it (the prefixes').  Its last CTA ends after that one, and with it the grid, so
+// that the merge, its dependent, need wait for this kernel alone; the others make
+// room for one another.
+__device__ __forceinline__ void decode_end_after_previous() {
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // Warp-level bf16 MMA, D(16x8, fp32) += A(16x16, row) * B(16x8, col).
 __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -289,9 +298,11 @@ __device__ bool decode_consume(const DecodeArgs &a, const int32_t *prefix, int64
 
         // Q^T fragments of query head h0 + r8 (zero for the padding heads)
         uint32_t qb[KS][2];
+        float sl2 = a.scale_log2;
+        if (F8 && a.first_keys != nullptr) sl2 = fp4_score_scale(sl2, a.k_scale[kvh]);   // beside prefixes: as over those
         if (F8 && r8 < G) {
             // q * k_scale as f16, k index order 4c, 4c+1 | 4c+2, 4c+3 per 16
-            const float ksc = __ldg(a.k_scale + kvh);
+            const float ksc = a.first_keys != nullptr ? 1.f : __ldg(a.k_scale + kvh);
             const uint2 *qrow = reinterpret_cast<const uint2 *>(a.q + ((int64_t)b * a.num_q_heads + h0 + r8) * D);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
@@ -371,10 +382,10 @@ __device__ bool decode_consume(const DecodeArgs &a, const int32_t *prefix, int64
             }
             // log2 domain; tokens past n masked
             float x[4];
-            x[0] = r8 < n ? sc[0] * a.scale_log2 : -INFINITY;
-            x[1] = r8 < n ? sc[1] * a.scale_log2 : -INFINITY;
-            x[2] = r8 + 8 < n ? sc[2] * a.scale_log2 : -INFINITY;
-            x[3] = r8 + 8 < n ? sc[3] * a.scale_log2 : -INFINITY;
+            x[0] = r8 < n ? sc[0] * sl2 : -INFINITY;
+            x[1] = r8 < n ? sc[1] * sl2 : -INFINITY;
+            x[2] = r8 + 8 < n ? sc[2] * sl2 : -INFINITY;
+            x[3] = r8 + 8 < n ? sc[3] * sl2 : -INFINITY;
 
             // ---- online softmax per head over the stage's 16 tokens (lazy
             // rescale: the running maximum moves only by more than 2^8)

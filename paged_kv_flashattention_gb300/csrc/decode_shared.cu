@@ -11,8 +11,8 @@
 // The prefix is a matrix product again: the rows that read KV head kvh of a
 // group are (sequence, query head of kvh), n * Hq / Hkv of them, so prefill's
 // tcgen05 kernel does it (prefill_impl.cuh, SHARED) with tiles of 128 such rows,
-// two tiles per CTA where the largest group fills more than one.  The query tile
-// is one tensor-map box (64 columns, Hq / Hkv heads, 128 Hkv / Hq sequences).
+// two tiles per CTA; where a group fills only one, the tile's key steps go in turn
+// to two softmax halves, each with a partial of its own.  A query tile is one tensor-map box (64 columns, Hq / Hkv heads, 128 Hkv / Hq sequences).
 // Every CTA gets the same number of 128-key steps, whatever the groups are; the
 // partials are written in 32 bits.
 #include "prefill_impl.cuh"
@@ -25,34 +25,36 @@ PA_ERROR_WORD_ACCESSOR(error_word_decode_shared)
 
 namespace {
 
-template <int D, int T, int KV>
-__global__ void __launch_bounds__(128 * (T + 1), 1) shared_prefix_kernel(const __grid_constant__ PrefillArgs a) {
-    prefill_body<D, T, KV != PA_KV_BF16, false, KV == PA_KV_FP4, true>(a);
+template <int D, int KV>
+__global__ void __launch_bounds__(KV == PA_KV_BF16 ? 384 : 512, 1) shared_prefix_kernel(const __grid_constant__ PrefillArgs a) {
+    prefill_body<D, 2, KV != PA_KV_BF16, false, KV == PA_KV_FP4, true>(a);
 }
 
-template <int D, int T, int KV>
+template <int D, int KV>
 cudaError_t launch_prefix_t(const PrefillArgs &a, unsigned ctas, cudaStream_t stream) {
-    using S = PrefillSmem<D, T, KV != PA_KV_BF16, KV == PA_KV_FP4, true>;
-    static_assert(S::kSlots >= 2 && (KV == PA_KV_BF16 || S::kCSlots >= 2), "ring too small");
+    using S = PrefillSmem<D, 2, KV != PA_KV_BF16, KV == PA_KV_FP4, true>;
+    // three slots for the MMAs: K of the next step of a tile's other half beside
+    // K and V of this one
+    static_assert(S::kSlots >= 3 && (KV == PA_KV_BF16 || S::kCSlots >= 3), "ring too small");
     static_assert(S::kTotal + 1024 <= 232448, "shared memory");
     // One CTA per SM (it allocates all 512 TMEM columns).
     const int smem = (S::kTotal + 1024) > 120 * 1024 ? (S::kTotal + 1024) : 120 * 1024;
-    auto kern = shared_prefix_kernel<D, T, KV>;
-    if (T == 2) {
-        static const cudaError_t regs = check_register_split(kern);
-        if (regs != cudaSuccess) return regs;
-    }
+    auto kern = shared_prefix_kernel<D, KV>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, ctas, 128 * (T + 1), smem, stream, a);
+    return launch_after(kern, ctas, KV == PA_KV_BF16 ? 384 : 512, smem, stream, a);
 }
 
 template <int KV>
-cudaError_t launch_prefix(const PrefillArgs &a, int d, int T, unsigned ctas, cudaStream_t stream) {
-    if (d == 128)
-        return T == 2 ? launch_prefix_t<128, 2, KV>(a, ctas, stream) : launch_prefix_t<128, 1, KV>(a, ctas, stream);
-    return T == 2 ? launch_prefix_t<64, 2, KV>(a, ctas, stream) : launch_prefix_t<64, 1, KV>(a, ctas, stream);
+cudaError_t launch_prefix(const PrefillArgs &a, int d, unsigned ctas, cudaStream_t stream) {
+    return d == 128 ? launch_prefix_t<128, KV>(a, ctas, stream) : launch_prefix_t<64, KV>(a, ctas, stream);
 }
+
+constexpr int kItemRows = 2 * kBM;                   // query rows of a work item of the prefix kernel
+
+// Bytes of keys and values behind the prefixes that take an SM as long as a step
+// of the prefix kernel.
+constexpr float kTailBytesPerStep = 200e3f;
 
 struct MergeArgs {
     SharedArgs sh;
@@ -62,7 +64,6 @@ struct MergeArgs {
     int32_t num_q_heads;
     int32_t num_kv_heads;
     int32_t max_seqlen_k;
-    int32_t tile_rows;            // rows of a work item of the prefix kernel
     __nv_bfloat16 *out;
     float *lse;
 };
@@ -85,95 +86,128 @@ __device__ __forceinline__ int group_of(const SharedArgs &sh, int b, int lane) {
 }
 
 // One row (sequence, query head) of both lists of partials, merged by
-// log-sum-exp; W warps share a row's slots (decode_fp4.cu's combine says why).  A
-// NaN among the partials stays one.
+// log-sum-exp.  W warps share a row; warp w takes slots w, w + W, .., 32 at a
+// time: a lane reads one slot's lse and holds its weight, then the warp reads the
+// slots that have any, kBatch of them in flight.  A NaN among the partials stays one.
 constexpr int kMergeThreads = 256;
+constexpr int kBatch = 8;
 
 template <int D, int W>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const MergeArgs a) {
-    constexpr int kLanes = D / 4;                    // lanes of a slot, four elements each
-    constexpr int kSlots = 32 * W / kLanes;          // slots in flight
-    __shared__ float top[kMergeThreads / 32], dens[kMergeThreads / kLanes];
-    __shared__ float4 part[kMergeThreads];
-    const int t = threadIdx.x % (32 * W), lane = t & 31;
-    const int64_t row = (int64_t)blockIdx.x * (kMergeThreads / (32 * W)) + threadIdx.x / (32 * W);
+    constexpr int E = D / 32;                        // elements of a lane
+    __shared__ float tops[kMergeThreads / 32], dens[kMergeThreads / 32];
+    __shared__ float parts[W > 1 ? kMergeThreads / 32 : 1][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
     const int64_t num_rows = (int64_t)a.num_seqs * a.num_q_heads;
+    const int64_t given = (int64_t)blockIdx.x * (kMergeThreads / (32 * W)) + warp / W;
+    const int64_t row = given < num_rows ? given : num_rows - 1;
+    const int b = (int)(row / a.num_q_heads), h = (int)(row % a.num_q_heads);
+    const int group = a.num_q_heads / a.num_kv_heads;
     after_previous();                                // the partials are complete
+    // what does not depend on one another is read together
+    const int L = a.cache_seqlens[b], P = a.sh.prefix_lens[b];
+    const bool has_tail = a.tail.o_part != nullptr;
+    const int T = has_tail ? a.tail.header[0] : 1, u0 = has_tail ? a.tail.prefix[b] : 0, u1 = has_tail ? a.tail.prefix[b + 1] : 0;
+    const int per = a.sh.header != nullptr ? a.sh.header[0] : 1;
+    const int g = a.sh.header != nullptr ? group_of(a.sh, b, lane) : -1;
+    bool ok = L >= 0 && L <= a.max_seqlen_k && P >= 0 && P <= L && P <= a.sh.max_prefix;
     int np = 0, ns = 0;                              // partials of the prefix, of the keys behind it
-    if (row < num_rows) {
-        const int b = (int)(row / a.num_q_heads), h = (int)(row % a.num_q_heads);
-        const int group = a.num_q_heads / a.num_kv_heads;
-        const int L = a.cache_seqlens[b], P = a.sh.prefix_lens[b];
-        bool ok = L >= 0 && L <= a.max_seqlen_k && P >= 0 && P <= L && P <= a.sh.max_prefix;
-        if (ok && P > 0) {
-            const int g = group_of(a.sh, b, lane);
-            ok = g >= 0 && g < a.sh.num_groups;      // a prefix without a group
-            if (ok) {
-                const int q0 = a.sh.cu_groups[g], n = a.sh.cu_groups[g + 1] - q0;
-                const int64_t per = a.sh.header[0];
-                ok = q0 >= 0 && n <= a.sh.max_group && a.sh.prefix_lens[q0] == P;
-                const int tiles = (n * group + a.tile_rows - 1) / a.tile_rows, steps = (P + kBN - 1) / kBN;
-                const int64_t start = a.sh.base[g] +
-                                      ((int64_t)(h / group) * tiles + ((b - q0) * group + h % group) / a.tile_rows) * steps;
-                if (ok) np = min((int)((start + steps - 1) / per - start / per + 1), a.sh.max_splits);
-            }
-        }
-        if (!ok && L != 0) raise_error(PA_DEVERR_SEQLENS);
-        if (ok && a.tail.o_part != nullptr) {
-            const int64_t T = a.tail.header[0];
-            const int U = a.tail.prefix[b + 1] - a.tail.prefix[b];
-            const int64_t rs = (int64_t)a.tail.head_groups * a.tail.prefix[b] + (int64_t)(h / a.tail.heads_per_group) * U;
-            ns = U > 0 ? min((int)((rs + U - 1) / T - rs / T + 1), a.tail.max_splits) : 0;
-        } else if (ok && L > P) {
-            raise_error(PA_DEVERR_SEQLENS);          // the call allows no keys behind the prefix
+    if (ok && P > 0) {
+        ok = g >= 0 && g < a.sh.num_groups;          // else a prefix without a group
+        if (ok) {
+            const int q0 = a.sh.cu_groups[g], n = a.sh.cu_groups[g + 1] - q0, base = a.sh.base[g];
+            ok = q0 >= 0 && n <= a.sh.max_group && a.sh.prefix_lens[q0] == P;
+            const int tiles = (n * group + kItemRows - 1) / kItemRows, steps = (P + kBN - 1) / kBN;
+            const int start = base + ((h / group) * tiles + ((b - q0) * group + h % group) / kItemRows) * steps;
+            if (ok) np = min(2 * ((start + steps - 1) / per - start / per + 1), a.sh.max_splits);
         }
     }
-    const int n = np + ns;
-    const float *lp = a.sh.lse_part + row * a.sh.max_splits;
-    const float *ls = a.tail.lse_part + row * a.tail.max_splits - np;
-    auto lse_of = [&](int s) { return s < np ? lp[s] : ls[s]; };
-    float M = -INFINITY;
-    for (int s = t; s < n; s += 32 * W) M = fmaxf(M, lse_of(s));
+    if (ok && has_tail) {
+        const int U = u1 - u0;
+        const int rs = a.tail.head_groups * u0 + (h / a.tail.heads_per_group) * U;
+        ns = U > 0 ? min((int)(((int64_t)rs + U - 1) / T) - rs / T + 1, a.tail.max_splits) : 0;
+    } else if (L > P) {
+        ok = false;                                  // the call allows no keys behind the prefix
+    }
+    if (!ok && L != 0 && lane == 0) raise_error(PA_DEVERR_SEQLENS);
+    const int n = ok ? np + ns : 0;
+    const float *lp = a.sh.lse_part + row * a.sh.max_splits, *ls = a.tail.lse_part + row * a.tail.max_splits - np;
+    const float *op = a.sh.o_part + row * a.sh.max_splits * D + lane * E;
+    const float *os = a.tail.o_part + (row * a.tail.max_splits - np) * D + lane * E;
+    auto lse_of = [&](int s) { return s >= n ? -INFINITY : s < np ? lp[s] : ls[s]; };
+    const int mine = w + lane * W;                   // this lane's slot of the first 32
+    const float l0 = lse_of(mine);
+    float M = l0;
+    for (int s = mine + 32 * W; s < n; s += 32 * W) M = fmaxf(M, lse_of(s));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (W > 1) {
-        if (lane == 0) top[threadIdx.x >> 5] = M;
+        if (lane == 0) tops[warp] = M;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, top[(threadIdx.x >> 5) / W * W + w]);
+        for (int i = 0; i < W; ++i) M = fmaxf(M, tops[warp - w + i]);
     }
-    const float *op = a.sh.o_part + row * a.sh.max_splits * D + (t % kLanes) * 4;
-    const float *os = a.tail.o_part + (row * a.tail.max_splits - np) * D + (t % kLanes) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
-#pragma unroll 4
-    for (int s = t / kLanes; s < n; s += kSlots) {
-        const float l = lse_of(s);
-        if (l == -INFINITY) continue;                // an empty slot may hold anything
-        const float w = __expf(l - M);
-        const float4 x = *reinterpret_cast<const float4 *>((s < np ? op : os) + (int64_t)s * D);
-        den += w;
-        acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w;
-    }
-    if (kSlots > 1) {                                // the lane groups' sums
-        part[threadIdx.x] = acc;
-        if (t % kLanes == 0) dens[threadIdx.x / kLanes] = den;
-        if (W > 1) __syncthreads(); else __syncwarp();
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        den = 0.f;
-        const int base = threadIdx.x - t;
+    float acc[E], den = 0.f;
 #pragma unroll
-        for (int g = 0; g < kSlots; ++g) {
-            const float4 x = part[base + g * kLanes + t % kLanes];
-            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-            den += dens[base / kLanes + g];
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int s0 = 0; s0 < n; s0 += 32 * W) {
+        const float l = s0 == 0 ? l0 : lse_of(s0 + mine);
+        const float wt = l == -INFINITY ? 0.f : __expf(l - M);       // an empty slot may hold anything
+        den += wt;
+        unsigned live = __ballot_sync(0xffffffffu, wt != 0.f);
+        while (live != 0u) {
+            float v[kBatch][E], f[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = live != 0u ? __ffs(live) - 1 : 32;
+                live &= live - 1u;
+                f[i] = __shfl_sync(0xffffffffu, wt, at & 31);
+                if (at == 32) f[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+                if (at == 32) continue;              // the same on every lane
+                const int s = s0 + w + at * W;
+                const float *from = (s < np ? op : os) + (int64_t)s * D;
+                if constexpr (E == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(from);
+                    v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(from);
+                    v[i][0] = x.x; v[i][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += f[i] * v[i][e];
         }
     }
-    if (row >= num_rows || t >= kLanes) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (W > 1) {
+        if (lane == 0) dens[warp] = den;
+#pragma unroll
+        for (int e = 0; e < E; ++e) parts[W > 1 ? warp : 0][lane * E + e] = acc[e];
+        __syncthreads();
+        if (w != 0) return;
+        den = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            den += dens[warp + i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += parts[W > 1 ? warp + i : 0][lane * E + e];
+        }
+    }
+    if (given >= num_rows) return;
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    *reinterpret_cast<uint2 *>(a.out + row * D + t * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse != nullptr && t == 0) a.lse[row] = den == 0.f ? -INFINITY : M + __logf(den);
+    __nv_bfloat16 *to = a.out + row * D + lane * E;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(to) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (a.lse != nullptr && lane == 0) a.lse[row] = den == 0.f ? -INFINITY : M + __logf(den);
 }
 
 cudaError_t launch_merge(const MergeArgs &a, int d, cudaStream_t stream) {
@@ -205,16 +239,24 @@ bool make_map_shared_q(CUtensorMap *m, const pa_decode_params &p) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Steps of the prefix kernel that cost an SM as much as one key of a sequence
+// costs it in the split decode.
+float tail_steps(const pa_decode_params &d) {
+    const float row = (float)(d.kv_dtype == PA_KV_FP4 ? fp4_layout(d.num_kv_heads, d.head_dim).row_bytes
+                                                      : d.num_kv_heads * d.head_dim * (d.kv_dtype == PA_KV_BF16 ? 2 : 1));
+    return 2.f * row / kTailBytesPerStep;
+}
+
 // Steps of the longest list: every group at its largest, every prefix at its longest.
-int64_t most_steps(const pa_decode_shared_params &p, int T) {
+int64_t most_steps(const pa_decode_shared_params &p) {
     const int64_t group = p.dec.num_q_heads / p.dec.num_kv_heads;
-    const int64_t tiles = ((int64_t)p.max_group * group + T * kBM - 1) / (T * kBM);
+    const int64_t tiles = ((int64_t)p.max_group * group + kItemRows - 1) / kItemRows;
     const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
     return p.num_groups * tiles * steps * p.dec.num_kv_heads;
 }
 
-unsigned prefix_ctas(const pa_decode_shared_params &p, int T) {
-    const int64_t steps = most_steps(p, T), sms = num_sms();
+unsigned prefix_ctas(const pa_decode_shared_params &p) {
+    const int64_t steps = most_steps(p), sms = num_sms();
     return (unsigned)(steps < sms ? steps : sms);
 }
 
@@ -230,8 +272,6 @@ pa_decode_params shared_tail_params(const pa_decode_shared_params &p) {
 
 SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
     SharedPlan plan{};
-    const int group = p.dec.num_q_heads / p.dec.num_kv_heads;
-    plan.tiles = (int64_t)p.max_group * group > kBM ? 2 : 1;
     plan.prefix = p.num_groups > 0 && p.max_prefix > 0 && p.max_group > 0 && p.dec.num_seqs > 0;
     plan.tail = p.max_suffix > 0;
     if (plan.prefix) {
@@ -239,10 +279,10 @@ SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
         // is n * Hkv / CTAs steps or longer, and n steps lie in at most
         // ceil(CTAs / Hkv) + 1 ranges.
         const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
-        const int64_t ranges = (prefix_ctas(p, plan.tiles) + p.dec.num_kv_heads - 1) / p.dec.num_kv_heads + 1;
-        plan.max_splits = (int32_t)(steps < ranges ? steps : ranges);
+        const int64_t ranges = (prefix_ctas(p) + p.dec.num_kv_heads - 1) / p.dec.num_kv_heads + 1;
+        plan.max_splits = 2 * (int32_t)(steps < ranges ? steps : ranges);      // two halves of each
         const size_t slots = (size_t)p.dec.num_seqs * p.dec.num_q_heads * plan.max_splits;
-        plan.prefix_bytes = 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t)) +
+        plan.prefix_bytes = 256 + 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t)) +
                             slots * p.dec.head_dim * sizeof(float) + round256(slots * sizeof(float));
     }
     const pa_decode_params tail = shared_tail_params(p);
@@ -271,7 +311,8 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
     m.sh.max_group = p.max_group;
     m.sh.max_prefix = plan.prefix ? p.max_prefix : 0;
     m.sh.max_splits = plan.max_splits;
-    uint8_t *ws = static_cast<uint8_t *>(d.workspace);
+    // (the partials are stored 32 bytes at a time)
+    uint8_t *ws = reinterpret_cast<uint8_t *>(round256(reinterpret_cast<uintptr_t>(d.workspace)));
     if (plan.prefix) {
         const size_t slots = (size_t)d.num_seqs * d.num_q_heads * plan.max_splits;
         uint8_t *o = ws + 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t));
@@ -306,17 +347,20 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
         a.k_scale = d.k_scale;
         a.v_scale = d.v_scale;
         a.sh = m.sh;
-        const unsigned ctas = prefix_ctas(p, plan.tiles);
-        const cudaError_t e = d.kv_dtype == PA_KV_FP4        ? launch_prefix<PA_KV_FP4>(a, d.head_dim, plan.tiles, ctas, stream)
-                              : d.kv_dtype == PA_KV_FP8_E4M3 ? launch_prefix<PA_KV_FP8_E4M3>(a, d.head_dim, plan.tiles, ctas, stream)
-                                                             : launch_prefix<PA_KV_BF16>(a, d.head_dim, plan.tiles, ctas, stream);
+        a.sh.seqlens = d.cache_seqlens;
+        a.sh.sms = num_sms();
+        a.sh.tail_steps = plan.tail ? tail_steps(d) : 0.f;
+        const unsigned ctas = prefix_ctas(p);
+        const cudaError_t e = d.kv_dtype == PA_KV_FP4        ? launch_prefix<PA_KV_FP4>(a, d.head_dim, ctas, stream)
+                              : d.kv_dtype == PA_KV_FP8_E4M3 ? launch_prefix<PA_KV_FP8_E4M3>(a, d.head_dim, ctas, stream)
+                                                             : launch_prefix<PA_KV_BF16>(a, d.head_dim, ctas, stream);
         if (e != cudaSuccess) return e;
     }
     if (plan.tail) {
         // Its CTAs start as the prefix kernel's leave the SMs; it reads nothing of
         // that kernel's, which has waited for all that came before.
         pa_decode_params t = d;
-        t.workspace = ws + plan.prefix_bytes;
+        t.workspace = static_cast<uint8_t *>(d.workspace) + plan.prefix_bytes;
         t.workspace_bytes = d.workspace_bytes - plan.prefix_bytes;
         t.overlap_previous = plan.prefix ? 1 : 0;
         m.tail.first_keys = p.prefix_lens;
@@ -330,7 +374,6 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
     m.num_q_heads = d.num_q_heads;
     m.num_kv_heads = d.num_kv_heads;
     m.max_seqlen_k = d.max_seqlen_k;
-    m.tile_rows = plan.tiles * kBM;
     m.out = static_cast<__nv_bfloat16 *>(d.out);
     m.lse = d.lse;
     return launch_merge(m, d.head_dim, stream);

@@ -121,6 +121,9 @@ struct SharedArgs {
     float *lse_part;
     int32_t *header;              // [0]: steps of a CTA's range
     int32_t *base;                // [num_groups + 1]: steps before each group
+    const int32_t *seqlens;       // the sequences' lengths
+    float tail_steps;             // steps that take as long as a key behind the prefixes (0: none there)
+    int32_t sms;
 };
 
 struct PrefillArgs {
@@ -356,42 +359,43 @@ __device__ __forceinline__ int shared_tiles(const PrefillArgs &a, int n) {
     return (n * (a.num_q_heads / a.num_kv_heads) + T * kBM - 1) / (T * kBM);
 }
 
-// The producer warp's walk over its range.  Lane i holds group g0 + i.
+// The producer warp's walk over its range.  Lane i holds group ahead + i of the
+// groups to come, read when the first of them is reached.
 template <int T>
 struct SharedWalk {
     int at, end, per_cta;         // the next step, the range's end
-    int g0, g, before;            // the lanes' first group, the current group, steps before it
-    SharedGroup mine;
+    int g, before;                // the current group, steps before it
+    int ahead;                    // -64: none read yet
+    SharedGroup now, mine;
     // The next item of the range into it; false at its end.
     __device__ bool next(const PrefillArgs &a, PrefillItem &it, int lane) {
         if (at >= end) return false;
+        const int group = a.num_q_heads / a.num_kv_heads;
         for (;;) {
-            if (g - g0 >= 32) {
-                g0 = g;
-                mine = shared_group(a, g0 + lane);
-            }
-            const int q0 = __shfl_sync(0xffffffffu, mine.q0, g - g0), n = __shfl_sync(0xffffffffu, mine.n, g - g0);
-            const int P = __shfl_sync(0xffffffffu, mine.P, g - g0);
-            const int steps = (P + kBN - 1) / kBN, tiles = shared_tiles<T>(a, n);
+            const int steps = (now.P + kBN - 1) / kBN, tiles = shared_tiles<T>(a, now.n);
             const int cost = steps * tiles * a.num_kv_heads;
-            if (at >= before + cost) {            // ends: the list holds more than `at` steps
-                before += cost;
-                ++g;
-                continue;
+            if (at < before + cost) {
+                const int row = (at - before) / steps, row_start = before + row * steps;
+                const int tile = row % tiles;
+                it.b = now.q0;
+                it.kvh = row / tiles;
+                it.q0 = now.q0 + tile * (T * kBM / group);
+                it.rows = min(T * kBM, now.n * group - tile * T * kBM);
+                it.j0 = at - row_start;
+                it.n_kv = min(steps - it.j0, end - at);
+                it.Lk = now.P;
+                it.split = at / per_cta - row_start / per_cta;
+                at += it.n_kv;
+                return true;
             }
-            const int group = a.num_q_heads / a.num_kv_heads;
-            const int row = (at - before) / steps, row_start = before + row * steps;
-            const int tile = row % tiles;
-            it.b = q0;
-            it.kvh = row / tiles;
-            it.q0 = q0 + tile * (T * kBM / group);
-            it.rows = min(T * kBM, n * group - tile * T * kBM);
-            it.j0 = at - row_start;
-            it.n_kv = min(steps - it.j0, end - at);
-            it.Lk = P;
-            it.split = at / per_cta - row_start / per_cta;
-            at += it.n_kv;
-            return true;
+            before += cost;                       // ends: the list holds more than `at` steps
+            if (++g >= ahead + 32) {
+                ahead = g;
+                mine = shared_group(a, g + lane);
+            }
+            now.q0 = __shfl_sync(0xffffffffu, mine.q0, g - ahead);
+            now.n = __shfl_sync(0xffffffffu, mine.n, g - ahead);
+            now.P = __shfl_sync(0xffffffffu, mine.P, g - ahead);
         }
     }
 };
@@ -423,7 +427,7 @@ struct PrefillSmem {
     // 4-bit: columns of output staged at a time; 64 200 us, 32 191, none (each
     // thread its own row) 194, and 78, 75 and 82 on sixteen requests of 512 rows.
     static constexpr int kStageCols = F4 ? 32 : 64;
-    static constexpr int kStageBytes = 4 * T * 64 * kStageCols;      // 32 rows x kStageCols columns bf16 per warp
+    static constexpr int kStageBytes = SHARED ? 0 : 4 * T * 64 * kStageCols;     // 32 rows x kStageCols columns bf16 per warp
     static constexpr int kBarBytes = SHARED ? 1024 : 512;            // SHARED: whole items in the ring, and 32 words
     static constexpr int kAvail = 232448 - 1024 - kRing - kStageBytes - kBarBytes;
     // FP8, d = 128 (in place): an E4M3 tile lands in the upper half of its f16
@@ -539,7 +543,7 @@ cudaError_t check_register_split(Kernel kern) {
 template <int D, int T, bool F8, bool EXT, bool F4 = false, bool SHARED = false>
 __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_ctas = 0) {
     static_assert(!F4 || F8, "4-bit pools use the widening path");
-    static_assert(!SHARED || !EXT, "no masks over shared prefixes");
+    static_assert(!SHARED || (!EXT && T == 2), "over shared prefixes: no masks, two tiles");
     using S = PrefillSmem<D, T, F8, F4, SHARED>;
     // (a dependent of a SHARED launch does not wait for what came before it)
     if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -560,7 +564,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     // warps widen tiles instead
     constexpr int kGatherWarps = F8 ? 1 : (NS - 1 < kGatherWarpsMax ? NS - 1 : kGatherWarpsMax);
     constexpr int NC = F8 ? S::kCSlots : NS;  // slots the MMA reads from
-    constexpr int kConverters = F8 ? 2 : 0;
+    constexpr int kConverters = !F8 ? 0 : SHARED ? 4 : 2;      // SHARED: a warpgroup of its own
+    constexpr int kWideRows = F8 ? kBN / kConverters : kBN;     // rows of a tile that one of them widens
     constexpr bool kInPlace = S::kInPlace;
     constexpr bool kClasses = F4 && !EXT && !SHARED;      // items in classes of positions (prefill_item)
     auto land = [&](int slot) { return smem + S::kRing + slot * S::kLStride + S::kLOff; };
@@ -582,7 +587,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_idx + R);
     // SHARED: the items themselves, 8 words each, and the scan's scratch
     int4 *items = reinterpret_cast<int4 *>(smem + S::kBars + 512);
-    int *scan = reinterpret_cast<int *>(items + 2 * R);
+    int *scan = reinterpret_cast<int *>(items + 2 * R), *start = scan + 32;
     // Each role walks the same item list and keeps its own counts of items
     // (phase of q_full / q_empty), items with keys (phase of o_final), key
     // steps (phase of s_full / p_full) and K/V loads (ring slot and phase).
@@ -619,39 +624,58 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     }
     SharedWalk<T> walk{};
     if constexpr (SHARED) {
-        // steps of the whole list, steps before this thread's groups, and the group
-        // in which this CTA's range starts
-        constexpr int kThreads = 128 * (T + 1);
+        // Steps of the whole list, steps before this thread's groups, and the group in
+        // which this CTA's range starts.  The ranges go to as many CTAs as the prefixes'
+        // share of the call's work; the others leave their SMs to the keys behind
+        // the prefixes (the next launch), which would else wait for the end of these.
+        constexpr int kThreads = F8 ? 512 : 384;
         const int per = (a.sh.num_groups + kThreads - 1) / kThreads;
         const int from = min((int)threadIdx.x * per, a.sh.num_groups), to = min(from + per, a.sh.num_groups);
-        auto cost = [&](int g) {
-            const SharedGroup r = shared_group(a, g);
+        auto cost = [&](const SharedGroup &r) {
             return (r.P + kBN - 1) / kBN * shared_tiles<T>(a, r.n) * a.num_kv_heads;
         };
-        int run = 0;
-        for (int g = from; g < to; ++g) run += cost(g);
+        const SharedGroup own = shared_group(a, from);           // (empty behind the last)
+        const int own_cost = cost(own);
+        int run = from < to ? own_cost : 0;
+        for (int g = from + 1; g < to; ++g) run += cost(shared_group(a, g));
+        float keys = 0.f;                                        // behind the prefixes
+        if (a.sh.tail_steps > 0.f)
+            for (int b = threadIdx.x; b < a.num_seqs; b += kThreads) keys += (float)max(a.sh.seqlens[b] - a.sh.prefix_lens[b], 0);
         int incl = run;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        if (lane == 31) scan[warp] = incl;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        if (lane == 31) {
+            scan[warp] = incl;
+            scan[16 + warp] = __float_as_int(keys);
+        }
         __syncthreads();
         int total = 0, acc = incl - run;
+        keys = 0.f;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) acc += scan[w];
             total += scan[w];
+            keys += __int_as_float(scan[16 + w]);
         }
-        walk.per_cta = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+        const float share = (float)total / ((float)total + keys * a.sh.tail_steps);
+        const int ctas = max(1, min((int)gridDim.x, __float2int_rn(share * (float)a.sh.sms)));
+        walk.per_cta = max(1, (total + ctas - 1) / ctas);
         walk.at = (int)min((int64_t)blockIdx.x * walk.per_cta, (int64_t)total);
         walk.end = min(total - walk.at, walk.per_cta) + walk.at;
         for (int g = from; g < to; ++g) {
-            const int c = cost(g);
+            const SharedGroup r = g == from ? own : shared_group(a, g);
+            const int c = g == from ? own_cost : cost(r);
             if (walk.at >= acc && walk.at < acc + c) {
-                scan[16] = g;
-                scan[17] = acc;
+                start[0] = g;
+                start[1] = acc;
+                start[2] = r.q0;
+                start[3] = r.n;
+                start[4] = r.P;
             }
             if (blockIdx.x == 0) a.sh.base[g] = acc;
             acc += c;
@@ -826,7 +850,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     };
 
     // Tile c of item `it` from its 4-bit landing slot to f16 in the swizzled
-    // layout: warp cw widens rows [64 cw, 64 cw + 64).  A lane takes 16-byte
+    // layout: warp cw widens kWideRows rows from kWideRows cw on.  A lane takes 16-byte
     // chunks of codes (32 elements, two blocks) of the rows = lane mod 8, so
     // that each store of a warp's quarter covers all banks; all its loads go out
     // first (in groups of four chunks 282 us against 267, of two 299).  Rows at
@@ -834,7 +858,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     auto widen4 = [&](const PrefillItem &it, int c, int cw, const uint8_t *src, uint8_t *dst) {
         constexpr int kChunks = D / 32;               // chunks of a row
         constexpr int kRows = 32 / kChunks;           // rows of a pass: 8 or 16
-        constexpr int kPasses = 64 / kRows;
+        constexpr int kPasses = kWideRows / kRows;
         int live = kBN;
         if (c >= 2 * it.n_kv - 2 && StepCursor().at<EXT>(a, it, it.n_kv - 1) == it.n_all - 1)
             live = it.kv_end - (it.j0 + it.n_all - 1) * kBN;
@@ -844,14 +868,14 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         uint32_t sc[kPasses];
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int r = 64 * cw + i * kRows + lane % kRows;
+            const int r = kWideRows * cw + i * kRows + lane % kRows;
             x[i] = *reinterpret_cast<const uint4 *>(src + S::code_off(r, ch));
             sc[i] = *reinterpret_cast<const uint16_t *>(src + S::scale_off(r) + sub + 2 * ch);
             if (r >= live) sc[i] = 0u;
         }
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int r = 64 * cw + i * kRows + lane % kRows;
+            const int r = kWideRows * cw + i * kRows + lane % kRows;
             const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
             const uint32_t s[2] = {f16_dup_lo(s2), f16_dup_hi(s2)};
             const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -869,7 +893,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
 
     if (warp >= kProducer) {
         // ------------------------------------- producer / MMA warpgroup ----
-        if (T == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (T == 2 && !SHARED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
       if (warp == kProducer) {
         // ----------------------------------------------------- producer ----
         if (lane == 0) {
@@ -916,9 +940,12 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         int local = 0, gl = 0;
         PrefillItem it;
         if constexpr (SHARED) {
-            walk.g = walk.g0 = scan[16];
-            walk.before = scan[17];
-            if (walk.at < walk.end) walk.mine = shared_group(a, walk.g0 + lane);
+            if (walk.at < walk.end) {
+                walk.g = start[0];
+                walk.before = start[1];
+                walk.now = SharedGroup{start[2], start[3], start[4]};
+            }
+            walk.ahead = -64;                          // below every group's number - 32
         }
         auto take_shared = [&](int n) {
             const int slot = n % R;
@@ -955,8 +982,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                         for (int hh = 0; hh < H; ++hh) {
                             if constexpr (SHARED) {       // a box of the KV head's query heads (zeros past the batch)
                                 const int group = a.num_q_heads / a.num_kv_heads;
-                                tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.kvh * group,
-                                            it.q0 + k * (kBM / group), q_full);
+                                // (the second half of a tile of up to 64 rows has them from row 64 on)
+                                const int seq = it.rows <= kBM / 2 ? it.q0 - k * (kBM / 2 / group)
+                                                : it.rows <= kBM   ? it.q0
+                                                                   : it.q0 + k * (kBM / group);
+                                tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.kvh * group, seq, q_full);
                             } else {
                                 tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.h0 + k,
                                             it.q0 + it.tile * kBM, q_full);
@@ -1035,9 +1065,9 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             if (!gather_item(it, gl, g)) break;
             gl += 2 * it.n_kv;
         }
-      } else if (F8 && warp > kMma) {
-        // -------------------------------------- FP8 widening (2 warps) ----
-        const int cw = warp - kMma - 1;                 // 0, 1: rows [64 cw, 64 cw + 64)
+      } else if (F8 && warp >= (SHARED ? kMma + 3 : kMma + 1)) {
+        // -------------------------------- FP8 widening (kConverters warps) ----
+        const int cw = warp - (SHARED ? kMma + 3 : kMma + 1);      // rows [kWideRows cw, + kWideRows)
         int local = 0, gl = 0;
         bool ok = true;
         PrefillItem it;
@@ -1052,9 +1082,9 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             // Q tiles: bf16 -> f16 of q * k_scale, in place
             if (!__all_sync(0xffffffffu, mbar_wait(q_full, local & 1))) break;
             ++local;
-            const float ksc = F4 ? 1.f : __ldg(a.k_scale + it.kvh);
+            const float ksc = F4 || SHARED ? 1.f : __ldg(a.k_scale + it.kvh);
 #pragma unroll 4
-            for (int i = cw * 32 + lane; i < T * S::kTileBytes / 16; i += 64) {
+            for (int i = cw * 32 + lane; i < T * S::kTileBytes / 16; i += 32 * kConverters) {
                 uint4 *pq = reinterpret_cast<uint4 *>(sQ + i * 16);
                 *pq = bf16x8_to_f16x8_scaled(*pq, ksc);
             }
@@ -1086,18 +1116,18 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 // overwrite only rows of the same group
                 constexpr int kGroup = 4;
 #pragma unroll 1
-                for (int i0 = 0; i0 < 64 * D / 512; i0 += kGroup) {
+                for (int i0 = 0; i0 < kWideRows * D / 512; i0 += kGroup) {
                     uint4 x[kGroup];
 #pragma unroll
                     for (int u = 0; u < kGroup; ++u) {
-                        const int byte = (i0 + u) * 512 + lane * 16;   // within this warp's 64 rows
-                        x[u] = *reinterpret_cast<const uint4 *>(src + (64 * cw + byte / D) * D + (byte % D));
+                        const int byte = (i0 + u) * 512 + lane * 16;   // within this warp's rows
+                        x[u] = *reinterpret_cast<const uint4 *>(src + (kWideRows * cw + byte / D) * D + (byte % D));
                     }
                     if (kInPlace) __syncwarp();
 #pragma unroll
                     for (int u = 0; u < kGroup; ++u) {
                         const int byte = (i0 + u) * 512 + lane * 16;
-                        const int rr = 64 * cw + byte / D;
+                        const int rr = kWideRows * cw + byte / D;
                         const int q = (byte % D) / 16;      // 16 codes: d = 16 q .. 16 q + 15
                         uint4 lo, hi;
                         e4m3x4_to_f16x4(x[u].x, lo.x, lo.y);
@@ -1118,8 +1148,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if (c == 2 * it.n_kv - 1 && (it.kv_end & 15) && StepCursor().at<EXT>(a, it, it.n_kv - 1) == it.n_all - 1) {
                     __syncwarp();
                     const int kbase = (it.j0 + it.n_all - 1) * kBN;
-                    const int r0 = max(it.kv_end - kbase, 64 * cw);
-                    const int r1 = min(((it.kv_end + 15) & ~15) - kbase, 64 * cw + 64);
+                    const int r0 = max(it.kv_end - kbase, kWideRows * cw);
+                    const int r1 = min(((it.kv_end + 15) & ~15) - kbase, kWideRows * cw + kWideRows);
                     for (int i = lane; i < (r1 - r0) * (D / 8); i += 32) {
                         const int row = r0 + i / (D / 8), ch = i % (D / 8);
                         *reinterpret_cast<uint4 *>(dst + (ch / 8) * 16384 + row * 128 + (ch % 8) * 16) =
@@ -1159,6 +1189,71 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 }
                 umma_commit(&s_full[k]);
             };
+            // The last page of a request is loaded whole (one
+            // 16-token TMA box), so rows of the item's last V tile
+            // at keys >= kv_end hold slots the store never wrote.
+            // P is 0 there, but 0 * NaN is not: clear those rows
+            // (at most 15, up to the end of the page; later pages
+            // are zero-filled by the TMA) once the tile has landed,
+            // while the softmax of this step still runs.  (FP8
+            // tiles are cleared by the widening warps.)
+            auto clear_tail = [&](const PrefillItem &it, int j, int cv) {
+                if (!F8 && paged16 && (it.kv_end & 15) && j + 1 == it.n_kv &&
+                    StepCursor().at<EXT>(a, it, j) == it.n_all - 1) {
+                    if (!wait_full(cv)) return false;
+                    const int kbase = (it.j0 + it.n_all - 1) * kBN;      // the item's last step
+                    const int r0 = it.kv_end - kbase;                  // first row past the keys
+                    const int r1 = ((it.kv_end + 15) & ~15) - kbase;   // end of its page
+                    uint8_t *vt = land(cv % NS);
+                    for (int row = r0; row < r1; ++row)
+#pragma unroll
+                        for (int ch = 0; ch < D / 8; ++ch)
+                            *reinterpret_cast<uint4 *>(vt + (ch / 8) * 16384 + row * 128 + (ch % 8) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();                          // generic writes -> the MMA's reads
+                }
+                return true;
+            };
+            // SHARED, an item of one tile: its two halves take the steps in turn,
+            // half k steps k, k + 2, .. with its copy of Q into its own S_k and O_k, so
+            // that one half's softmax runs beside the other's MMAs.  Order: S(0), S(1),
+            // PV(0), S(2), PV(1), S(3), ..
+            auto mma_halves = [&](const PrefillItem &it, int local, int gl, int gs0, int gs1) {
+                const int n_kv = it.n_kv;
+                if (!mbar_wait(F8 ? q_conv : q_full, local & 1)) return false;
+                auto issue = [&](int j) {                 // S of step j
+                    const int c = gl + 2 * j, k = j & 1;
+                    if (!wait_full(c)) return false;
+                    tc_fence_after();
+                    const uint64_t dq = dq0 + (uint64_t)((k * S::kTileBytes) >> 4);
+                    const uint64_t dk = dk0 + (uint64_t)(((c % NC) * S::kTileBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t o = (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4);
+                        umma_ss(tmem + 128 * k, dq + o, dk + o, idesc_s, kk > 0);
+                    }
+                    umma_commit(&s_full[k]);
+                    umma_commit(&mempty[c % NC]);
+                    if (j + 1 == n_kv) umma_commit(q_empty);
+                    return true;
+                };
+                if (!issue(0) || (n_kv > 1 && !issue(1))) return false;
+                for (int j = 0; j < n_kv; ++j) {
+                    const int k = j & 1, cv = gl + 2 * j + 1;
+                    if (!clear_tail(it, j, cv)) return false;
+                    if (!mbar_wait(&p_full[k], ((k ? gs1 : gs0) + j / 2) & 1) || !wait_full(cv)) return false;
+                    tc_fence_after();
+                    const uint64_t dv = dv0 + (uint64_t)(((cv % NC) * S::kTileBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        umma_ts(tmem + 256 + kOCols * k, tmem + 128 * k + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
+                                (j > 1 || kk > 0) ? 1u : 0u);
+                    umma_commit(&mempty[cv % NC]);
+                    if (j + 2 >= n_kv) umma_commit(&o_final[k]);
+                    if (j + 2 < n_kv && !issue(j + 2)) return false;
+                }
+                return true;
+            };
             int local = 0, gl = 0, gs = 0, gs1 = 0;   // (gs1: tile 1's steps, SHARED)
             bool ok = true;
             PrefillItem it;
@@ -1170,41 +1265,29 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if (v < 0) break;
                 if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
                 const int n_kv = it.n_kv;
-                const int tiles = SHARED && it.rows <= kBM ? 1 : T;      // the item's tiles
+                if constexpr (SHARED) {
+                    if (it.rows <= kBM) {
+                        if (!mma_halves(it, local, gl, gs, gs1)) break;
+                        gl += 2 * n_kv;
+                        gs += (n_kv + 1) / 2;
+                        gs1 += n_kv / 2;
+                        ++local;
+                        continue;
+                    }
+                }
                 if (!mbar_wait(F8 ? q_conv : q_full, local & 1)) break;
                 if (n_kv > 0) {
                     if (!wait_full(gl)) break;
                     tc_fence_after();
-                    for (int k = 0; k < tiles; ++k) issue_s(k, gl);
+                    for (int k = 0; k < T; ++k) issue_s(k, gl);
                     umma_commit(&mempty[gl % NC]);                       // K_0 consumed
                 }
                 if (n_kv <= 1) umma_commit(q_empty);                     // every S of the item issued
                 for (int j = 0; ok && j < n_kv; ++j) {
                     const int cv = gl + 2 * j + 1;
                     const uint64_t dv = dv0 + (uint64_t)(((cv % NC) * S::kTileBytes) >> 4);
-                    if (!F8 && paged16 && (it.kv_end & 15) && j + 1 == n_kv &&
-                        StepCursor().at<EXT>(a, it, j) == it.n_all - 1) {
-                        // The last page of a request is loaded whole (one
-                        // 16-token TMA box), so rows of the item's last V tile
-                        // at keys >= kv_end hold slots the store never wrote.
-                        // P is 0 there, but 0 * NaN is not: clear those rows
-                        // (at most 15, up to the end of the page; later pages
-                        // are zero-filled by the TMA) once the tile has landed,
-                        // while the softmax of this step still runs.  (FP8
-                        // tiles are cleared by the widening warps.)
-                        if (!wait_full(cv)) { ok = false; break; }
-                        const int kbase = (it.j0 + it.n_all - 1) * kBN;      // the item's last step
-                        const int r0 = it.kv_end - kbase;                  // first row past the keys
-                        const int r1 = ((it.kv_end + 15) & ~15) - kbase;   // end of its page
-                        uint8_t *vt = land(cv % NS);
-                        for (int row = r0; row < r1; ++row)
-#pragma unroll
-                            for (int ch = 0; ch < D / 8; ++ch)
-                                *reinterpret_cast<uint4 *>(vt + (ch / 8) * 16384 + row * 128 + (ch % 8) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();                          // generic writes -> the MMA's reads
-                    }
-                    for (int k = 0; k < tiles; ++k) {
+                    if (!clear_tail(it, j, cv)) { ok = false; break; }
+                    for (int k = 0; k < T; ++k) {
                         if (!mbar_wait(&p_full[k], ((SHARED && k > 0 ? gs1 : gs) + j) & 1)) { ok = false; break; }
                         if (k == 0 && !wait_full(cv)) { ok = false; break; }
                         tc_fence_after();
@@ -1213,7 +1296,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             umma_ts(o_tm, tmem + 128 * k + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
                                     (j > 0 || kk > 0) ? 1u : 0u);
-                        if (k == tiles - 1) umma_commit(&mempty[cv % NC]);   // V_j consumed
+                        if (k == T - 1) umma_commit(&mempty[cv % NC]);   // V_j consumed
                         if (j + 1 == n_kv) umma_commit(&o_final[k]);     // O_k of the item complete
                         if (j + 1 < n_kv) {
                             if (k == 0) {
@@ -1221,7 +1304,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                                 tc_fence_after();
                             }
                             issue_s(k, cv + 1);
-                            if (k == tiles - 1) {
+                            if (k == T - 1) {
                                 umma_commit(&mempty[(cv + 1) % NC]);     // K_{j+1} consumed
                                 if (j + 2 == n_kv) umma_commit(q_empty);  // last S of the item
                             }
@@ -1231,11 +1314,158 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 // (items without keys write zeros and use no MMA)
                 gl += 2 * n_kv;
                 gs += n_kv;
-                if (SHARED && tiles > 1) gs1 += n_kv;
+                if (SHARED) gs1 += n_kv;
                 ++local;
             }
         }
       }
+    } else if constexpr (SHARED) {
+        // ---------------------------------- softmax over shared prefixes ----
+        // As below, with half the registers and a quarter of the code: a row's scores
+        // are read from TMEM twice, for the maximum and for the exponentials, in rolled
+        // loops.  The first pass through unrolled code cost a CTA of few steps 3600 to
+        // 10000 clocks of instruction fetches.
+        const int k = warp >> 2;                      // query tile, or half of a single one
+        const int r = threadIdx.x & 127;              // row within the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t s_tm = tmem + lane_base + 128 * k;
+        const uint32_t o_tm = tmem + lane_base + 256 + kOCols * k;
+        const int group = a.num_q_heads / a.num_kv_heads, shift = __ffs(group) - 1;      // 1, 2, 4 or 8
+        float sl2 = a.scale_log2;
+        int fin = 0, gs = 0, local = 0;
+        PrefillItem it;
+        for (bool ok = true; ok;) {
+            const int slot = local % R;
+            if (!__all_sync(0xffffffffu, mbar_wait(&item_full[slot], (local / R) & 1))) break;
+            const int v = read_item(slot, it);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
+            ++local;
+            if (v < 0) break;
+            const bool halves = it.rows <= kBM;       // one tile: this half's steps are k, k + 2, ..
+            // Of a tile of up to 64 rows the second half has its rows from 64 on: its warps
+            // that have rows are on the other schedulers.
+            const int off = it.rows <= kBM / 2 ? k * (kBM / 2) : 0;
+            const int rows = off + (halves ? it.rows : min(it.rows - kBM * k, kBM));     // the rows off .. rows - 1
+            const int n = halves ? (it.n_kv + 1 - k) / 2 : it.n_kv;      // steps of this warp
+            if (32 * (warp & 3) >= rows || 32 * (warp & 3) + 32 <= off) {        // no row of this warp: it only keeps step
+                for (int j = 0; ok && j < n; ++j) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
+                    if (ok) mbar_arrive(&p_full[k]);
+                }
+                gs += n;
+                fin += n > 0;
+                continue;
+            }
+            if constexpr (F8) sl2 = fp4_score_scale(a.scale_log2, a.k_scale[it.kvh]);
+            const float2 c2 = make_float2(sl2, sl2);
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < n; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const int lim = it.Lk - (it.j0 + (halves ? 2 * j + k : j)) * kBN;   // keys of the step
+                float mt = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kBN; c += 64) {
+                    uint32_t sr[64];
+                    tmem_ld32(s_tm + c, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                    tmem_ld32(s_tm + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                    tmem_wait_ld();
+                    if (c + 64 > lim)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (c + i >= lim) sr[i] = __float_as_uint(-INFINITY);
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(sr[i]), __uint_as_float(sr[4 + i]), mt);
+#pragma unroll
+                    for (int e = 8; e < 64; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(sr[e + i]), __uint_as_float(sr[e + 4 + i]));
+                    mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                }
+                const float m_cand = mt * sl2;
+                const bool need = m_cand > m_run + kLazy;            // the lazy maximum, as below
+                const float alpha = need ? fast_exp2(m_run - m_cand) : 1.f;
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t orr[32];
+                        tmem_ld32(o_tm + c, orr);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                        tmem_st16(o_tm + c, *reinterpret_cast<const uint32_t(*)[16]>(&orr[0]));
+                        tmem_st16(o_tm + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&orr[16]));
+                    }
+                }
+                if (need) {
+                    l_run *= alpha;
+                    m_run = m_cand;
+                }
+                const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+                const float2 nm2 = make_float2(-m_use, -m_use);
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // P's 16-bit columns go over S columns that have been read
+#pragma unroll 1
+                for (int c = 0; c < kBN; c += 32) {
+                    uint32_t sr[32], pk[16];
+                    tmem_ld32(s_tm + c, sr);
+                    tmem_wait_ld();
+                    if (c + 32 > lim)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= lim) sr[i] = __float_as_uint(-INFINITY);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
+                        const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        acc[i & 1] = add2(acc[i & 1], p);
+                        pk[i] = F8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
+                    }
+                    tmem_st16(s_tm + c / 2, pk);
+                }
+                const float2 s01 = add2(acc[0], acc[1]);
+                l_run += s01.x + s01.y;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[k]);
+            }
+            if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_final[k], fin & 1));
+            tc_fence_after();
+            gs += n;
+            fin += n > 0;
+            // The row's partial, O / l and lse: a thread writes its row, whole 32-byte
+            // sectors at a time.  A range has two places for it, one for each half.
+            const int m = halves ? r - off : k * kBM + r;
+            const int place = 2 * it.split + (halves ? k : 0);
+            if (2 * it.split + 1 >= a.sh.max_splits) {               // never, for lengths within the bounds
+                if (lane == 0) raise_error(PA_DEVERR_SEQLENS);
+                continue;
+            }
+            const bool mine = ok && r >= off && r < rows;
+            const int64_t at = ((int64_t)(it.q0 + (m >> shift)) * a.num_q_heads + it.kvh * group + (m & (group - 1))) *
+                                   a.sh.max_splits + place;
+            if (mine) {
+                a.sh.lse_part[at] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
+                if (!halves) a.sh.lse_part[at + 1] = -INFINITY;
+            }
+            if (!ok || n == 0) continue;                             // (an empty place may hold anything)
+            const float inv = (l_run == 0.f ? 0.f : 1.f / l_run) * (F8 ? a.v_scale[it.kvh] : 1.f);   // a NaN stays one
+            float *to = a.sh.o_part + at * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t orr[32];
+                tmem_ld32(o_tm + c, orr);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * inv);
+                if (mine)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) st_global_32(to + c + e, &orr[e]);
+            }
+        }
     } else {
         // ------------------------------------------------------ softmax ----
         if (T == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -1253,31 +1483,18 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         const int slot = local % R;
         ok = __all_sync(0xffffffffu, mbar_wait(&item_full[slot], (local / R) & 1));
         if (!ok) break;
-        const int v = read_item(slot, it);
+        const int v = item_idx[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[slot]);
         ++local;
         if (v < 0) break;
-        if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
-        if constexpr (SHARED) {
-            it.rows_here = min(max(it.rows - kBM * k, 0), kBM);
-            if (it.rows_here == 0) continue;          // the item has no such tile
-            if (32 * (warp & 3) >= it.rows_here) {    // no row of this warp: it only keeps step
-                for (int j = 0; ok && j < it.n_kv; ++j) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
-                    if (ok) mbar_arrive(&p_full[k]);
-                }
-                gs += it.n_kv;
-                ++fin;
-                continue;
-            }
-        }
+        prefill_item<T, EXT, kClasses>(a, v, it);
         if constexpr (F4) {
             sl2 = fp4_score_scale(a.scale_log2, __ldg(a.k_scale + it.kvh));
             c2 = make_float2(sl2, sl2);
         }
         const int n_kv = it.n_kv, Lk = it.Lk, off = it.off, min_vis = it.min_vis;
-        const int qi = it.tile * kBM + r;             // query index within the request (SHARED: not used)
+        const int qi = it.tile * kBM + r;             // query index within the request
         const bool row_valid = r < it.rows_here;
         const int vis_end = a.causal ? min(Lk, off + qi + 1) : Lk;   // keys [0, vis_end)
         float m_run = -INFINITY;
@@ -1364,48 +1581,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         // ---- epilogue: O / l -> bf16, lse
         if (ok && n_kv > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_final[k], fin & 1));
         tc_fence_after();
-        if constexpr (SHARED) {
-            // the rows' partials: O / l in 32 bits through the warp's staging buffer, 128
-            // (4-bit: 64) bytes of a row at a time, and lse
-            if (ok) {
-                constexpr int kCols = S::kStageCols / 2;
-                constexpr int kPieces = kCols / 4;                     // of 16 bytes
-                const int group = a.num_q_heads / a.num_kv_heads;
-                const float inv = (l_run > 0.f ? 1.f / l_run : 0.f) * (F8 ? a.v_scale[it.kvh] : 1.f);
-                uint8_t *stage = smem + S::kStage + warp * (64 * S::kStageCols);
-                auto swz = [](int r) { return kPieces == 8 ? r & 7 : (r >> 1) & 3; };
-                auto slot_of = [&](int rt) {                           // row rt of the tile
-                    const int m = (k * kBM + rt) / group, h = it.kvh * group + (k * kBM + rt) % group;
-                    return ((int64_t)(it.q0 + m) * a.num_q_heads + h) * a.sh.max_splits + it.split;
-                };
-                const bool fits = it.split < a.sh.max_splits;          // always, for lengths within the bounds
-                if (!fits) raise_error(PA_DEVERR_SEQLENS);
-#pragma unroll 1
-                for (int part = 0; part < D / kCols; ++part) {
-                    uint32_t orr[kCols];
-                    if constexpr (kCols == 32) tmem_ld32(o_tm + part * kCols, orr);
-                    else tmem_ld16(o_tm + part * kCols, orr);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < kPieces; ++u)
-                        *reinterpret_cast<float4 *>(stage + lane * (4 * kCols) + ((u ^ swz(lane)) * 16)) =
-                            make_float4(__uint_as_float(orr[4 * u]) * inv, __uint_as_float(orr[4 * u + 1]) * inv,
-                                        __uint_as_float(orr[4 * u + 2]) * inv, __uint_as_float(orr[4 * u + 3]) * inv);
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int rr = i * (32 / kPieces) + lane / kPieces, q = lane % kPieces;
-                        const float4 val = *reinterpret_cast<const float4 *>(stage + rr * (4 * kCols) + ((q ^ swz(rr)) * 16));
-                        const int rt = (warp & 3) * 32 + rr;
-                        if (fits && rt < it.rows_here)
-                            *reinterpret_cast<float4 *>(a.sh.o_part + slot_of(rt) * D + part * kCols + q * 4) = val;
-                    }
-                    __syncwarp();
-                }
-                if (fits && row_valid)
-                    a.sh.lse_part[slot_of(r)] = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
-            }
-        } else if (ok) {
+        if (ok) {
             const int64_t tok = (int64_t)it.q0 + qi;
             const int h = it.h0 + k;
             const float inv = (l_run > 0.f ? 1.f / l_run : 0.f) * (F8 ? __ldg(a.v_scale + it.kvh) : 1.f);
