@@ -12,9 +12,11 @@
 // group are (sequence, query head of kvh), n * Hq / Hkv of them, so prefill's
 // tcgen05 kernel does it (prefill_impl.cuh, SHARED) with tiles of 128 such rows,
 // two tiles per CTA; where a group fills only one, the tile's key steps go in turn
-// to two softmax halves, each with a partial of its own.  A query tile is one tensor-map box (64 columns, Hq / Hkv heads, 128 Hkv / Hq sequences).
+// to two softmax halves, and where it fills half or less of one, its rows lie in
+// the tile two or four times, each copy for a share of the keys.  Query rows come in tensor-map boxes of 32 (64 columns, Hq / Hkv
+// heads, 32 Hkv / Hq sequences).
 // Every CTA gets the same number of 128-key steps, whatever the groups are; the
-// partials are written in 32 bits.
+// partials are written in 32 bits, a block of 8 warps' 32 rows for each work item.
 #include "prefill_impl.cuh"
 
 #include "pdl.cuh"
@@ -51,10 +53,6 @@ cudaError_t launch_prefix(const PrefillArgs &a, int d, unsigned ctas, cudaStream
 }
 
 constexpr int kItemRows = 2 * kBM;                   // query rows of a work item of the prefix kernel
-
-// Bytes of keys and values behind the prefixes that take an SM as long as a step
-// of the prefix kernel.
-constexpr float kTailBytesPerStep = 200e3f;
 
 struct MergeArgs {
     SharedArgs sh;
@@ -112,14 +110,28 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     const int g = a.sh.header != nullptr ? group_of(a.sh, b, lane) : -1;
     bool ok = L >= 0 && L <= a.max_seqlen_k && P >= 0 && P <= L && P <= a.sh.max_prefix;
     int np = 0, ns = 0;                              // partials of the prefix, of the keys behind it
+    // Partial s of the prefix: range s / each, copy s % each (of a single tile: two
+    // halves of its copies), at row `first` of lse_part and o_part for s = 0.
+    int each = 1, apart = 0;                         // partials of a range, rows between its copies'
+    int64_t first = 0;
     if (ok && P > 0) {
         ok = g >= 0 && g < a.sh.num_groups;          // else a prefix without a group
         if (ok) {
-            const int q0 = a.sh.cu_groups[g], n = a.sh.cu_groups[g + 1] - q0, base = a.sh.base[g];
+            const int q0 = a.sh.cu_groups[g], n = a.sh.cu_groups[g + 1] - q0;
+            const int2 base = a.sh.base[g];
             ok = q0 >= 0 && n <= a.sh.max_group && a.sh.prefix_lens[q0] == P;
             const int tiles = (n * group + kItemRows - 1) / kItemRows, steps = (P + kBN - 1) / kBN;
-            const int start = base + ((h / group) * tiles + ((b - q0) * group + h % group) / kItemRows) * steps;
-            if (ok) np = min(2 * ((start + steps - 1) / per - start / per + 1), a.sh.max_splits);
+            const int in_group = (b - q0) * group + h % group, tile = in_group / kItemRows, m = in_group % kItemRows;
+            const int row = (h / group) * tiles + tile, start = base.x + row * steps;
+            const int rows = min(n * group - tile * kItemRows, kItemRows);
+            const int c0 = start / per, block = c0 + base.y + row;
+            const int ranges = min((start + steps - 1) / per - c0 + 1, a.sh.max_blocks - block);
+            if (rows <= kBM) {
+                each = 2 * shared_copies(rows);
+                apart = 8 / each * 32;
+            }
+            if (ok) np = max(ranges, 0) * each;
+            first = (int64_t)block * kItemRows + m;
         }
     }
     if (ok && has_tail) {
@@ -131,10 +143,11 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     }
     if (!ok && L != 0 && lane == 0) raise_error(PA_DEVERR_SEQLENS);
     const int n = ok ? np + ns : 0;
-    const float *lp = a.sh.lse_part + row * a.sh.max_splits, *ls = a.tail.lse_part + row * a.tail.max_splits - np;
-    const float *op = a.sh.o_part + row * a.sh.max_splits * D + lane * E;
+    const int shift = __ffs(each) - 1;
+    auto at_of = [&](int s) { return first + (int64_t)(s >> shift) * kItemRows + (s & (each - 1)) * apart; };
+    const float *ls = a.tail.lse_part + row * a.tail.max_splits - np;
     const float *os = a.tail.o_part + (row * a.tail.max_splits - np) * D + lane * E;
-    auto lse_of = [&](int s) { return s >= n ? -INFINITY : s < np ? lp[s] : ls[s]; };
+    auto lse_of = [&](int s) { return s >= n ? -INFINITY : s < np ? a.sh.lse_part[at_of(s)] : ls[s]; };
     const int mine = w + lane * W;                   // this lane's slot of the first 32
     const float l0 = lse_of(mine);
     float M = l0;
@@ -167,7 +180,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
                 for (int e = 0; e < E; ++e) v[i][e] = 0.f;
                 if (at == 32) continue;              // the same on every lane
                 const int s = s0 + w + at * W;
-                const float *from = (s < np ? op : os) + (int64_t)s * D;
+                const float *from = s < np ? a.sh.o_part + at_of(s) * D + lane * E : os + (int64_t)s * D;
                 if constexpr (E == 4) {
                     const float4 x = *reinterpret_cast<const float4 *>(from);
                     v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
@@ -212,10 +225,10 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
 
 cudaError_t launch_merge(const MergeArgs &a, int d, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.num_seqs * a.num_q_heads;
-    // A CTA per row while all of them fit on the GPU at once and a row may have
-    // more than a few slots.
+    // A CTA per row while all of them fit on the GPU at once: rows of few sequences
+    // have the most partials.
     constexpr int W = kMergeThreads / 32;
-    const bool share = a.sh.max_splits + a.tail.max_splits >= 8 && rows <= num_sms() * 8;
+    const bool share = rows <= num_sms() * 8;
     const int per_block = share ? 1 : W;
     auto kern = d == 64 ? (share ? shared_merge_kernel<64, W> : shared_merge_kernel<64, 1>)
                         : (share ? shared_merge_kernel<128, W> : shared_merge_kernel<128, 1>);
@@ -224,27 +237,19 @@ cudaError_t launch_merge(const MergeArgs &a, int d, cudaStream_t stream) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// 3-D bf16 map of q (d, Hq, sequences) with a box of 128 rows: `group` heads of
-// 128 / group sequences.
+// 3-D bf16 map of q (d, Hq, sequences) with a box of 32 rows: `group` heads of
+// 32 / group sequences.
 bool make_map_shared_q(CUtensorMap *m, const pa_decode_params &p) {
     auto enc = encoder();
     if (!enc) return false;
     const cuuint32_t group = (cuuint32_t)(p.num_q_heads / p.num_kv_heads);
     cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.num_q_heads, (cuuint64_t)p.num_seqs};
     cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, (cuuint64_t)p.num_q_heads * p.head_dim * 2};
-    cuuint32_t box[3] = {64, group, kBM / group};
+    cuuint32_t box[3] = {64, group, 32 / group};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p.q), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Steps of the prefix kernel that cost an SM as much as one key of a sequence
-// costs it in the split decode.
-float tail_steps(const pa_decode_params &d) {
-    const float row = (float)(d.kv_dtype == PA_KV_FP4 ? fp4_layout(d.num_kv_heads, d.head_dim).row_bytes
-                                                      : d.num_kv_heads * d.head_dim * (d.kv_dtype == PA_KV_BF16 ? 2 : 1));
-    return 2.f * row / kTailBytesPerStep;
 }
 
 // Steps of the longest list: every group at its largest, every prefix at its longest.
@@ -275,15 +280,15 @@ SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
     plan.prefix = p.num_groups > 0 && p.max_prefix > 0 && p.max_group > 0 && p.dec.num_seqs > 0;
     plan.tail = p.max_suffix > 0;
     if (plan.prefix) {
-        // A row of n steps: the list has n for each KV head at least, so a range
-        // is n * Hkv / CTAs steps or longer, and n steps lie in at most
-        // ceil(CTAs / Hkv) + 1 ranges.
-        const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
-        const int64_t ranges = (prefix_ctas(p) + p.dec.num_kv_heads - 1) / p.dec.num_kv_heads + 1;
-        plan.max_splits = 2 * (int32_t)(steps < ranges ? steps : ranges);      // two halves of each
-        const size_t slots = (size_t)p.dec.num_seqs * p.dec.num_q_heads * plan.max_splits;
-        plan.prefix_bytes = 256 + 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t)) +
-                            slots * p.dec.head_dim * sizeof(float) + round256(slots * sizeof(float));
+        // an item for each range and row of the list, less one (prefill_impl.cuh); a
+        // row for every KV head and 256 query rows of a group, or part of them
+        const int64_t group = p.dec.num_q_heads / p.dec.num_kv_heads;
+        const int64_t whole = (int64_t)p.dec.num_seqs * group / kItemRows + p.num_groups;
+        const int64_t bound = p.num_groups * (((int64_t)p.max_group * group + kItemRows - 1) / kItemRows);
+        plan.max_blocks = (int32_t)(prefix_ctas(p) + (whole < bound ? whole : bound) * p.dec.num_kv_heads);
+        const size_t rows = (size_t)plan.max_blocks * kItemRows;
+        plan.prefix_bytes = 256 + 256 + round256((size_t)p.num_groups * sizeof(int2)) + rows * p.dec.head_dim * sizeof(float) +
+                            rows * sizeof(float);
     }
     const pa_decode_params tail = shared_tail_params(p);
     if (plan.tail) {
@@ -310,16 +315,16 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
     m.sh.num_groups = p.num_groups;
     m.sh.max_group = p.max_group;
     m.sh.max_prefix = plan.prefix ? p.max_prefix : 0;
-    m.sh.max_splits = plan.max_splits;
+    m.sh.max_blocks = plan.max_blocks;
     // (the partials are stored 32 bytes at a time)
     uint8_t *ws = reinterpret_cast<uint8_t *>(round256(reinterpret_cast<uintptr_t>(d.workspace)));
     if (plan.prefix) {
-        const size_t slots = (size_t)d.num_seqs * d.num_q_heads * plan.max_splits;
-        uint8_t *o = ws + 256 + round256(((size_t)p.num_groups + 1) * sizeof(int32_t));
+        const size_t rows = (size_t)plan.max_blocks * kItemRows;
+        uint8_t *o = ws + 256 + round256((size_t)p.num_groups * sizeof(int2));
         m.sh.header = reinterpret_cast<int32_t *>(ws);
-        m.sh.base = reinterpret_cast<int32_t *>(ws + 256);
+        m.sh.base = reinterpret_cast<int2 *>(ws + 256);
         m.sh.o_part = reinterpret_cast<float *>(o);
-        m.sh.lse_part = reinterpret_cast<float *>(o + slots * d.head_dim * sizeof(float));
+        m.sh.lse_part = reinterpret_cast<float *>(o + rows * d.head_dim * sizeof(float));
         PrefillArgs a{};
         const int64_t num_slots = d.num_pages * d.page_size;
         if (!make_map_shared_q(&a.qmap, d)) return cudaErrorNotSupported;
@@ -347,9 +352,6 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
         a.k_scale = d.k_scale;
         a.v_scale = d.v_scale;
         a.sh = m.sh;
-        a.sh.seqlens = d.cache_seqlens;
-        a.sh.sms = num_sms();
-        a.sh.tail_steps = plan.tail ? tail_steps(d) : 0.f;
         const unsigned ctas = prefix_ctas(p);
         const cudaError_t e = d.kv_dtype == PA_KV_FP4        ? launch_prefix<PA_KV_FP4>(a, d.head_dim, ctas, stream)
                               : d.kv_dtype == PA_KV_FP8_E4M3 ? launch_prefix<PA_KV_FP8_E4M3>(a, d.head_dim, ctas, stream)

@@ -177,6 +177,15 @@ __device__ __forceinline__ void prefetch_tmap(const void *tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
 
+// True in one lane of a converged warp.  Code behind it is known to run in a
+// single thread, so that the operands of tcgen05 instructions stay in uniform
+// registers (behind `lane == 0` each cost 50 clocks or more to issue).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------- tcgen05 ---
 // Shared-memory matrix descriptor (tcgen05 form): start address, leading and
 // stride byte offsets (>> 4), descriptor version 1 (bits 46-47) and the

@@ -79,7 +79,7 @@ cudaError_t launch_prefill_fp4(const pa_prefill_params &p, cudaStream_t stream);
 // Decode over shared prefixes (decode_shared.cu): the prefixes' partials, the
 // sequences' own, and their merge.  The workspace holds the first two in turn.
 struct SharedPlan {
-    int32_t max_splits;           // partials of a query row over its prefix
+    int32_t max_blocks;           // blocks of the prefixes' partials
     bool prefix, tail;            // whether there is work of either kind
     DecodePlan decode;            // of the keys behind the prefixes
     size_t prefix_bytes;

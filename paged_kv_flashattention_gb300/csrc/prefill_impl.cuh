@@ -116,14 +116,11 @@ struct SharedArgs {
     int32_t num_groups;
     int32_t max_group;            // bounds of the call
     int32_t max_prefix;
-    int32_t max_splits;
-    float *o_part;                // [num_seqs * Hq][max_splits][D]
-    float *lse_part;
+    int32_t max_blocks;           // blocks of partials, one for each item
+    float *o_part;                // [max_blocks][8 softmax warps][32 rows][D]
+    float *lse_part;              // [max_blocks][8][32]
     int32_t *header;              // [0]: steps of a CTA's range
-    int32_t *base;                // [num_groups + 1]: steps before each group
-    const int32_t *seqlens;       // the sequences' lengths
-    float tail_steps;             // steps that take as long as a key behind the prefixes (0: none there)
-    int32_t sms;
+    int2 *base;                   // [num_groups]: steps and rows of the list before each group
 };
 
 struct PrefillArgs {
@@ -170,7 +167,7 @@ struct PrefillItem {
     int j0;       // first 128-key step (a sliding window skips the ones before)
     int lo_max;   // keys below this are outside some row's window: mask there
     int rows;     // SHARED: rows of the item's T tiles together (rows_here: not used)
-    int split;    // SHARED: the partial's place among its rows' partials
+    int block;    // SHARED: its block of partials
 };
 
 // With a block-sparse mask an item's steps are the kept ones only: every
@@ -327,9 +324,10 @@ __device__ void prefill_sched_done(const PrefillArgs &a, int num_ctas) {
 // SHARED.  The work is the list of 128-key steps of every (group, KV head, T
 // query tiles), in that order; a tile's rows are (sequence of the group, query
 // head of the KV head).  CTA c takes the c-th range of `per_cta` steps and cuts it
-// into items where rows of the list end; an item gives one partial (O, lse) per
-// query row, the split it belongs to is its range's place among the ranges that
-// the row's steps lie in.
+// into items where rows of the list end (a row: one group, KV head and T tiles).
+// An item gives a block of partials (O, lse), numbered by its range plus its row:
+// of two items that follow one another the second has one of the two, or both, one
+// higher.
 struct SharedGroup {
     int q0, n, P;                 // first sequence, sequences, keys
 };
@@ -359,12 +357,18 @@ __device__ __forceinline__ int shared_tiles(const PrefillArgs &a, int n) {
     return (n * (a.num_q_heads / a.num_kv_heads) + T * kBM - 1) / (T * kBM);
 }
 
+// Rows of the list of a group, steps of its prefix.
+template <int T>
+__device__ __forceinline__ int shared_rows(const PrefillArgs &a, const SharedGroup &r) {
+    return r.P > 0 ? shared_tiles<T>(a, r.n) * a.num_kv_heads : 0;
+}
+
 // The producer warp's walk over its range.  Lane i holds group ahead + i of the
 // groups to come, read when the first of them is reached.
 template <int T>
 struct SharedWalk {
-    int at, end, per_cta;         // the next step, the range's end
-    int g, before;                // the current group, steps before it
+    int at, end, range;           // the next step, the range's end and number
+    int g, before, rows;          // the current group, steps and rows of the list before it
     int ahead;                    // -64: none read yet
     SharedGroup now, mine;
     // The next item of the range into it; false at its end.
@@ -375,20 +379,21 @@ struct SharedWalk {
             const int steps = (now.P + kBN - 1) / kBN, tiles = shared_tiles<T>(a, now.n);
             const int cost = steps * tiles * a.num_kv_heads;
             if (at < before + cost) {
-                const int row = (at - before) / steps, row_start = before + row * steps;
+                const int row = (at - before) / steps;
                 const int tile = row % tiles;
                 it.b = now.q0;
                 it.kvh = row / tiles;
                 it.q0 = now.q0 + tile * (T * kBM / group);
                 it.rows = min(T * kBM, now.n * group - tile * T * kBM);
-                it.j0 = at - row_start;
+                it.j0 = at - before - row * steps;
                 it.n_kv = min(steps - it.j0, end - at);
                 it.Lk = now.P;
-                it.split = at / per_cta - row_start / per_cta;
+                it.block = range + rows + row;
                 at += it.n_kv;
                 return true;
             }
             before += cost;                       // ends: the list holds more than `at` steps
+            rows += shared_rows<T>(a, now);
             if (++g >= ahead + 32) {
                 ahead = g;
                 mine = shared_group(a, g + lane);
@@ -399,6 +404,12 @@ struct SharedWalk {
         }
     }
 };
+
+// Copies of a single tile's rows among the 128 of an MMA: each copy's warps take
+// that share of a step's keys, and P is zero in the others' columns.  Where a tile
+// has few rows the softmax is the step's time, and one warp with 32 rows takes
+// 1700 clocks for 128 keys; with four copies every warp works, on 32 of them.
+__device__ __forceinline__ int shared_copies(int rows) { return rows <= kBM / 4 ? 4 : rows <= kBM / 2 ? 2 : 1; }
 
 // The fields that follow from what SharedWalk gives.
 __device__ __forceinline__ void shared_fill(PrefillItem &it) {
@@ -428,7 +439,7 @@ struct PrefillSmem {
     // thread its own row) 194, and 78, 75 and 82 on sixteen requests of 512 rows.
     static constexpr int kStageCols = F4 ? 32 : 64;
     static constexpr int kStageBytes = SHARED ? 0 : 4 * T * 64 * kStageCols;     // 32 rows x kStageCols columns bf16 per warp
-    static constexpr int kBarBytes = SHARED ? 1024 : 512;            // SHARED: whole items in the ring, and 32 words
+    static constexpr int kBarBytes = SHARED ? 1024 : 512;            // SHARED: whole items in the ring, and scratch
     static constexpr int kAvail = 232448 - 1024 - kRing - kStageBytes - kBarBytes;
     // FP8, d = 128 (in place): an E4M3 tile lands in the upper half of its f16
     // slot (row r's 128 codes where the f16 row r of the upper 64 columns
@@ -443,7 +454,7 @@ struct PrefillSmem {
     static constexpr int kFitTiles = kAvail / kTileBytes;
     static constexpr int kCSlotsFit = (kAvail / 2) / kTileBytes;
     static constexpr int kCSlots = !F8 ? 0
-                                 : F4 ? 3
+                                 : F4 ? (SHARED ? 4 : 3)
                                  : kInPlace ? (kFitTiles > 8 ? 8 : kFitTiles)
                                             : (kCSlotsFit > 4 ? 4 : (kCSlotsFit < 2 ? 2 : kCSlotsFit));
     static constexpr int kSlotsFit = kInPlace ? kCSlots : (kAvail - kCSlots * kTileBytes) / kLTile;
@@ -624,66 +635,62 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     }
     SharedWalk<T> walk{};
     if constexpr (SHARED) {
-        // Steps of the whole list, steps before this thread's groups, and the group in
-        // which this CTA's range starts.  The ranges go to as many CTAs as the prefixes'
-        // share of the call's work; the others leave their SMs to the keys behind
-        // the prefixes (the next launch), which would else wait for the end of these.
+        // Steps of the whole list, steps and rows before this thread's groups, and the
+        // group in which this CTA's range starts.
         constexpr int kThreads = F8 ? 512 : 384;
         const int per = (a.sh.num_groups + kThreads - 1) / kThreads;
         const int from = min((int)threadIdx.x * per, a.sh.num_groups), to = min(from + per, a.sh.num_groups);
-        auto cost = [&](const SharedGroup &r) {
-            return (r.P + kBN - 1) / kBN * shared_tiles<T>(a, r.n) * a.num_kv_heads;
-        };
         const SharedGroup own = shared_group(a, from);           // (empty behind the last)
-        const int own_cost = cost(own);
-        int run = from < to ? own_cost : 0;
-        for (int g = from + 1; g < to; ++g) run += cost(shared_group(a, g));
-        float keys = 0.f;                                        // behind the prefixes
-        if (a.sh.tail_steps > 0.f)
-            for (int b = threadIdx.x; b < a.num_seqs; b += kThreads) keys += (float)max(a.sh.seqlens[b] - a.sh.prefix_lens[b], 0);
-        int incl = run;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
-        if (lane == 31) {
-            scan[warp] = incl;
-            scan[16 + warp] = __float_as_int(keys);
-        }
-        __syncthreads();
-        int total = 0, acc = incl - run;
-        keys = 0.f;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) acc += scan[w];
-            total += scan[w];
-            keys += __int_as_float(scan[16 + w]);
-        }
-        const float share = (float)total / ((float)total + keys * a.sh.tail_steps);
-        const int ctas = max(1, min((int)gridDim.x, __float2int_rn(share * (float)a.sh.sms)));
-        walk.per_cta = max(1, (total + ctas - 1) / ctas);
-        walk.at = (int)min((int64_t)blockIdx.x * walk.per_cta, (int64_t)total);
-        walk.end = min(total - walk.at, walk.per_cta) + walk.at;
+        int steps = 0, rows = 0;
         for (int g = from; g < to; ++g) {
             const SharedGroup r = g == from ? own : shared_group(a, g);
-            const int c = g == from ? own_cost : cost(r);
-            if (walk.at >= acc && walk.at < acc + c) {
-                start[0] = g;
-                start[1] = acc;
-                start[2] = r.q0;
-                start[3] = r.n;
-                start[4] = r.P;
+            const int n = shared_rows<T>(a, r);
+            rows += n;
+            steps += n * ((r.P + kBN - 1) / kBN);
+        }
+        int s_incl = steps, r_incl = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, s_incl, o), w = __shfl_up_sync(0xffffffffu, r_incl, o);
+            if (lane >= o) {
+                s_incl += v;
+                r_incl += w;
             }
-            if (blockIdx.x == 0) a.sh.base[g] = acc;
-            acc += c;
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            a.sh.base[a.sh.num_groups] = total;
-            a.sh.header[0] = walk.per_cta;
+        if (lane == 31) {
+            scan[warp] = s_incl;
+            scan[16 + warp] = r_incl;
         }
+        __syncthreads();
+        int total = 0, s_acc = s_incl - steps, r_acc = r_incl - rows;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) {
+                s_acc += scan[w];
+                r_acc += scan[16 + w];
+            }
+            total += scan[w];
+        }
+        const int per_cta = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+        walk.range = blockIdx.x;
+        walk.at = (int)min((int64_t)blockIdx.x * per_cta, (int64_t)total);
+        walk.end = min(total - walk.at, per_cta) + walk.at;
+        for (int g = from; g < to; ++g) {
+            const SharedGroup r = g == from ? own : shared_group(a, g);
+            const int n = shared_rows<T>(a, r), c = n * ((r.P + kBN - 1) / kBN);
+            if (walk.at >= s_acc && walk.at < s_acc + c) {
+                start[0] = g;
+                start[1] = s_acc;
+                start[2] = r_acc;
+                start[3] = r.q0;
+                start[4] = r.n;
+                start[5] = r.P;
+            }
+            if (blockIdx.x == 0) a.sh.base[g] = make_int2(s_acc, r_acc);
+            s_acc += c;
+            r_acc += n;
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) a.sh.header[0] = per_cta;
     }
     tc_fence_before();
     __syncthreads();
@@ -694,7 +701,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         if constexpr (SHARED) {
             const int4 x = items[2 * slot], y = items[2 * slot + 1];
             it.b = x.x; it.kvh = x.y; it.q0 = x.z; it.rows = x.w;
-            it.j0 = y.x; it.n_kv = y.y; it.Lk = y.z; it.split = y.w;
+            it.j0 = y.x; it.n_kv = y.y; it.Lk = y.z; it.block = y.w;
             shared_fill(it);
             return it.n_kv;
         } else {
@@ -943,7 +950,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             if (walk.at < walk.end) {
                 walk.g = start[0];
                 walk.before = start[1];
-                walk.now = SharedGroup{start[2], start[3], start[4]};
+                walk.rows = start[2];
+                walk.now = SharedGroup{start[3], start[4], start[5]};
             }
             walk.ahead = -64;                          // below every group's number - 32
         }
@@ -956,7 +964,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 ok = n < R || mbar_wait(&item_empty[slot], ((n / R) - 1) & 1);
                 if (ok) {
                     items[2 * slot] = make_int4(it.b, it.kvh, it.q0, it.rows);
-                    items[2 * slot + 1] = make_int4(it.j0, some ? it.n_kv : -1, it.Lk, it.split);
+                    items[2 * slot + 1] = make_int4(it.j0, some ? it.n_kv : -1, it.Lk, it.block);
                     mbar_arrive(&item_full[slot]);
                 }
             }
@@ -976,22 +984,26 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             bool ok = true;
             auto load_q = [&]() {
                 if (local > 0 && !mbar_wait(q_empty, (local - 1) & 1)) return false;
+                if constexpr (SHARED) {
+                    // boxes of 32 rows; a single tile holds its rows once, twice or four times
+                    const bool two = it.rows > kBM;
+                    if (lane == 0) {
+                        const int group = a.num_q_heads / a.num_kv_heads;
+                        const int blocks = two ? 8 : 4, distinct = two ? 8 : 4 / shared_copies(it.rows);
+                        mbar_arrive_expect_tx(q_full, blocks * (S::kTileBytes / 4));
+                        for (int i = 0; i < blocks; ++i)
+                            for (int hh = 0; hh < H; ++hh)
+                                tma_load_3d(sQ + (i >> 2) * S::kTileBytes + hh * 16384 + (i & 3) * 4096, &a.qmap, hh * 64,
+                                            it.kvh * group, it.q0 + (i & (distinct - 1)) * (32 / group), q_full);
+                    }
+                    return true;
+                }
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, T * S::kTileBytes);
                     for (int k = 0; k < T; ++k)
-                        for (int hh = 0; hh < H; ++hh) {
-                            if constexpr (SHARED) {       // a box of the KV head's query heads (zeros past the batch)
-                                const int group = a.num_q_heads / a.num_kv_heads;
-                                // (the second half of a tile of up to 64 rows has them from row 64 on)
-                                const int seq = it.rows <= kBM / 2 ? it.q0 - k * (kBM / 2 / group)
-                                                : it.rows <= kBM   ? it.q0
-                                                                   : it.q0 + k * (kBM / group);
-                                tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.kvh * group, seq, q_full);
-                            } else {
-                                tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.h0 + k,
-                                            it.q0 + it.tile * kBM, q_full);
-                            }
-                        }
+                        for (int hh = 0; hh < H; ++hh)
+                            tma_load_3d(sQ + k * S::kTileBytes + hh * 16384, &a.qmap, hh * 64, it.h0 + k,
+                                        it.q0 + it.tile * kBM, q_full);
                 }
                 return true;
             };
@@ -1084,7 +1096,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             ++local;
             const float ksc = F4 || SHARED ? 1.f : __ldg(a.k_scale + it.kvh);
 #pragma unroll 4
-            for (int i = cw * 32 + lane; i < T * S::kTileBytes / 16; i += 32 * kConverters) {
+            for (int i = cw * 32 + lane; i < (SHARED && it.rows <= kBM ? 1 : T) * S::kTileBytes / 16; i += 32 * kConverters) {
                 uint4 *pq = reinterpret_cast<uint4 *>(sQ + i * 16);
                 *pq = bf16x8_to_f16x8_scaled(*pq, ksc);
             }
@@ -1166,7 +1178,9 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         }
       } else if (warp == kMma) {
         // ---------------------------------------------------------- MMA ----
-        if (lane == 0) {
+        bool issues;
+        if constexpr (SHARED) issues = elect_one(); else issues = lane == 0;
+        if (issues) {
             constexpr uint32_t idesc_s = F8 ? umma_idesc_f16(kBM, kBN, false) : umma_idesc_bf16(kBM, kBN, false);
             constexpr uint32_t idesc_o = F8 ? umma_idesc_f16(kBM, D, true) : umma_idesc_bf16(kBM, D, true);
             // the slots the MMAs read (FP8: the widened ring) and their barriers
@@ -1215,7 +1229,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 return true;
             };
             // SHARED, an item of one tile: its two halves take the steps in turn,
-            // half k steps k, k + 2, .. with its copy of Q into its own S_k and O_k, so
+            // half k steps k, k + 2, .. with the same Q into its own S_k and O_k, so
             // that one half's softmax runs beside the other's MMAs.  Order: S(0), S(1),
             // PV(0), S(2), PV(1), S(3), ..
             auto mma_halves = [&](const PrefillItem &it, int local, int gl, int gs0, int gs1) {
@@ -1225,12 +1239,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                     const int c = gl + 2 * j, k = j & 1;
                     if (!wait_full(c)) return false;
                     tc_fence_after();
-                    const uint64_t dq = dq0 + (uint64_t)((k * S::kTileBytes) >> 4);
                     const uint64_t dk = dk0 + (uint64_t)(((c % NC) * S::kTileBytes) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4);
-                        umma_ss(tmem + 128 * k, dq + o, dk + o, idesc_s, kk > 0);
+                        umma_ss(tmem + 128 * k, dq0 + o, dk + o, idesc_s, kk > 0);
                     }
                     umma_commit(&s_full[k]);
                     umma_commit(&mempty[c % NC]);
@@ -1325,12 +1338,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         // are read from TMEM twice, for the maximum and for the exponentials, in rolled
         // loops.  The first pass through unrolled code cost a CTA of few steps 3600 to
         // 10000 clocks of instruction fetches.
-        const int k = warp >> 2;                      // query tile, or half of a single one
-        const int r = threadIdx.x & 127;              // row within the tile = TMEM lane
-        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const int k = warp >> 2, quad = warp & 3;     // query tile, or half of a single one; its rows of 32
+        const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
         const uint32_t s_tm = tmem + lane_base + 128 * k;
         const uint32_t o_tm = tmem + lane_base + 256 + kOCols * k;
-        const int group = a.num_q_heads / a.num_kv_heads, shift = __ffs(group) - 1;      // 1, 2, 4 or 8
         float sl2 = a.scale_log2;
         int fin = 0, gs = 0, local = 0;
         PrefillItem it;
@@ -1343,115 +1354,111 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             ++local;
             if (v < 0) break;
             const bool halves = it.rows <= kBM;       // one tile: this half's steps are k, k + 2, ..
-            // Of a tile of up to 64 rows the second half has its rows from 64 on: its warps
-            // that have rows are on the other schedulers.
-            const int off = it.rows <= kBM / 2 ? k * (kBM / 2) : 0;
-            const int rows = off + (halves ? it.rows : min(it.rows - kBM * k, kBM));     // the rows off .. rows - 1
+            const int copies = halves ? shared_copies(it.rows) : 1;
+            const int blocks = 4 / copies;            // of 32 rows in a copy
+            const int c0 = (quad / blocks) * (kBN / copies), c1 = c0 + kBN / copies;     // this warp's keys of a step
+            const int row0 = 32 * (quad & (blocks - 1)) + (halves ? 0 : kBM * k);        // the item's row of lane 0
             const int n = halves ? (it.n_kv + 1 - k) / 2 : it.n_kv;      // steps of this warp
-            if (32 * (warp & 3) >= rows || 32 * (warp & 3) + 32 <= off) {        // no row of this warp: it only keeps step
+            float m_run = -INFINITY, l_run = 0.f;
+            if (row0 >= it.rows) {                    // no row of this warp: it only keeps step
                 for (int j = 0; ok && j < n; ++j) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
                     if (ok) mbar_arrive(&p_full[k]);
                 }
-                gs += n;
-                fin += n > 0;
-                continue;
-            }
-            if constexpr (F8) sl2 = fp4_score_scale(a.scale_log2, a.k_scale[it.kvh]);
-            const float2 c2 = make_float2(sl2, sl2);
-            float m_run = -INFINITY, l_run = 0.f;
-            for (int j = 0; j < n; ++j) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
-                if (!ok) break;
-                tc_fence_after();
-                const int lim = it.Lk - (it.j0 + (halves ? 2 * j + k : j)) * kBN;   // keys of the step
-                float mt = -INFINITY;
+            } else {
+                if constexpr (F8) sl2 = fp4_score_scale(a.scale_log2, a.k_scale[it.kvh]);
+                const float2 c2 = make_float2(sl2, sl2);
+                for (int j = 0; j < n; ++j) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int lim = it.Lk - (it.j0 + (halves ? 2 * j + k : j)) * kBN;   // keys of the step
+                    float mt = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kBN; c += 64) {
-                    uint32_t sr[64];
-                    tmem_ld32(s_tm + c, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                    tmem_ld32(s_tm + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-                    tmem_wait_ld();
-                    if (c + 64 > lim)
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (c + i >= lim) sr[i] = __float_as_uint(-INFINITY);
-                    float mx[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(sr[i]), __uint_as_float(sr[4 + i]), mt);
-#pragma unroll
-                    for (int e = 8; e < 64; e += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(sr[e + i]), __uint_as_float(sr[e + 4 + i]));
-                    mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                }
-                const float m_cand = mt * sl2;
-                const bool need = m_cand > m_run + kLazy;            // the lazy maximum, as below
-                const float alpha = need ? fast_exp2(m_run - m_cand) : 1.f;
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t orr[32];
-                        tmem_ld32(o_tm + c, orr);
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t sr[32];
+                        tmem_ld32(s_tm + c, sr);
                         tmem_wait_ld();
+                        if (c + 32 > lim)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-                        tmem_st16(o_tm + c, *reinterpret_cast<const uint32_t(*)[16]>(&orr[0]));
-                        tmem_st16(o_tm + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&orr[16]));
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i >= lim) sr[i] = __float_as_uint(-INFINITY);
+                        float mx[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(sr[i]), __uint_as_float(sr[4 + i]), mt);
+#pragma unroll
+                        for (int e = 8; e < 32; e += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(sr[e + i]), __uint_as_float(sr[e + 4 + i]));
+                        mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                     }
-                }
-                if (need) {
-                    l_run *= alpha;
-                    m_run = m_cand;
-                }
-                const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
-                const float2 nm2 = make_float2(-m_use, -m_use);
-                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                // P's 16-bit columns go over S columns that have been read
+                    const float m_cand = mt * sl2;
+                    const bool need = m_cand > m_run + kLazy;            // the lazy maximum, as below
+                    const float alpha = need ? fast_exp2(m_run - m_cand) : 1.f;
+                    if (j > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
-                for (int c = 0; c < kBN; c += 32) {
-                    uint32_t sr[32], pk[16];
-                    tmem_ld32(s_tm + c, sr);
-                    tmem_wait_ld();
-                    if (c + 32 > lim)
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t orr[32];
+                            tmem_ld32(o_tm + c, orr);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= lim) sr[i] = __float_as_uint(-INFINITY);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
-                        const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        acc[i & 1] = add2(acc[i & 1], p);
-                        pk[i] = F8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
+                            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                            tmem_st16(o_tm + c, *reinterpret_cast<const uint32_t(*)[16]>(&orr[0]));
+                            tmem_st16(o_tm + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&orr[16]));
+                        }
                     }
-                    tmem_st16(s_tm + c / 2, pk);
+                    if (need) {
+                        l_run *= alpha;
+                        m_run = m_cand;
+                    }
+                    const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+                    const float2 nm2 = make_float2(-m_use, -m_use);
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // P's 16-bit columns go over S columns that have been read
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t sr[32], pk[16];
+                        tmem_ld32(s_tm + c, sr);
+                        tmem_wait_ld();
+                        if (c + 32 > lim)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i >= lim) sr[i] = __float_as_uint(-INFINITY);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
+                            const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            acc[i & 1] = add2(acc[i & 1], p);
+                            pk[i] = F8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
+                        }
+                        tmem_st16(s_tm + c / 2, pk);
+                    }
+                    if (copies > 1) {                 // the other copies' keys
+                        const uint32_t zero[16] = {};
+                        for (int c = 0; c < kBN; c += 32)
+                            if (c < c0 || c >= c1) tmem_st16(s_tm + c / 2, zero);
+                    }
+                    const float2 s01 = add2(acc[0], acc[1]);
+                    l_run += s01.x + s01.y;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[k]);
                 }
-                const float2 s01 = add2(acc[0], acc[1]);
-                l_run += s01.x + s01.y;
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&p_full[k]);
             }
             if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_final[k], fin & 1));
             tc_fence_after();
             gs += n;
             fin += n > 0;
-            // The row's partial, O / l and lse: a thread writes its row, whole 32-byte
-            // sectors at a time.  A range has two places for it, one for each half.
-            const int m = halves ? r - off : k * kBM + r;
-            const int place = 2 * it.split + (halves ? k : 0);
-            if (2 * it.split + 1 >= a.sh.max_splits) {               // never, for lengths within the bounds
+            if (it.block >= a.sh.max_blocks) {        // never, for groups within the bounds
                 if (lane == 0) raise_error(PA_DEVERR_SEQLENS);
                 continue;
             }
-            const bool mine = ok && r >= off && r < rows;
-            const int64_t at = ((int64_t)(it.q0 + (m >> shift)) * a.num_q_heads + it.kvh * group + (m & (group - 1))) *
-                                   a.sh.max_splits + place;
-            if (mine) {
-                a.sh.lse_part[at] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
-                if (!halves) a.sh.lse_part[at + 1] = -INFINITY;
-            }
-            if (!ok || n == 0) continue;                             // (an empty place may hold anything)
+            // The warp's place of the item's block: O / l and lse of its rows, whole 32-byte
+            // sectors at a time.  Halves and copies have a place each (the merge knows).
+            const int64_t at = ((int64_t)it.block * (4 * T) + warp) * 32 + lane;
+            const bool mine = ok && row0 + lane < it.rows;
+            if (mine) a.sh.lse_part[at] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
+            if (!ok || n == 0 || row0 >= it.rows) continue;          // (an empty place may hold anything)
             const float inv = (l_run == 0.f ? 0.f : 1.f / l_run) * (F8 ? a.v_scale[it.kvh] : 1.f);   // a NaN stays one
             float *to = a.sh.o_part + at * D;
 #pragma unroll 1
