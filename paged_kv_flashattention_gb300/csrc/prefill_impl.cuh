@@ -573,7 +573,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     constexpr int NS = S::kSlots;
     // G < NS gather warps leave the MMA a slot; with FP8 pools the two spare
     // warps widen tiles instead
-    constexpr int kGatherWarps = F8 ? 1 : (NS - 1 < kGatherWarpsMax ? NS - 1 : kGatherWarpsMax);
+    // (SHARED: these warps share the loads of page size 16 too, and widening has its own)
+    constexpr int kGatherWarps = F8 && !SHARED ? 1 : (NS - 1 < kGatherWarpsMax ? NS - 1 : kGatherWarpsMax);
     constexpr int NC = F8 ? S::kCSlots : NS;  // slots the MMA reads from
     constexpr int kConverters = !F8 ? 0 : SHARED ? 4 : 2;      // SHARED: a warpgroup of its own
     constexpr int kWideRows = F8 ? kBN / kConverters : kBN;     // rows of a tile that one of them widens
@@ -629,7 +630,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         for (int k = 0; k < T; ++k) mbar_init(&o_final[k], 1);
         for (int i = 0; i < R; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 1 + 4 * T + (paged16 ? 0 : kGatherWarps - 1) + kConverters);
+            mbar_init(&item_empty[i], 1 + 4 * T + (paged16 && !SHARED ? 0 : kGatherWarps - 1) + kConverters);
         }
         fence_mbar_init();
     }
@@ -856,6 +857,66 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         return true;
     };
 
+    // SHARED, page size 16: the loads of one item that load warp g issues, as above:
+    // loads g, g + kGatherWarps, .. of the CTA.  One elected lane issues a tile's 8 (d =
+    // 128: 16) boxes: 8 lanes with a page each take 600 clocks a tile, one after the
+    // other, which is more than most tiles' MMAs and softmax.  False on a timeout.
+    const uint64_t keep = l2_policy_evict_last();
+    auto load_item = [&](const PrefillItem &it, int gl0, int g) {
+        const int n = 2 * it.n_kv;
+        int c = ((g - gl0) % kGatherWarps + kGatherWarps) % kGatherWarps;
+        auto page_id = [&](int j) {                   // lanes 0..7: the pages of step j, -1 past the keys
+            const int kk = (it.j0 + j) * kBN + lane * 16;
+            return (lane < kBN / 16 && kk < it.kv_end) ? a.page_table[(int64_t)it.b * a.pt_stride + kk / 16] : -1;
+        };
+        int page = c < n ? page_id(c >> 1) : -1;
+        for (; c < n; c += kGatherWarps) {
+            const int gl = gl0 + c;
+            const int kk = (it.j0 + (c >> 1)) * kBN + lane * 16;
+            int slot0 = a.num_slots;                  // its first slot; num_slots: zeros
+            if (lane < kBN / 16 && kk < it.kv_end) {
+                if (page >= 0 && (int64_t)page * 16 < a.num_slots) slot0 = page * 16;
+                else raise_error(PA_DEVERR_PAGE_RANGE);
+            }
+            if (c + kGatherWarps < n) page = page_id((c + kGatherWarps) >> 1);
+            int first[kBN / 16];
+#pragma unroll
+            for (int i = 0; i < kBN / 16; ++i) first[i] = __shfl_sync(0xffffffffu, slot0, i);
+            const int slot = gl % NS, round = gl / NS;
+            if (!__all_sync(0xffffffffu, round == 0 || mbar_wait(&empty[slot], (round - 1) & 1))) return false;
+            uint8_t *dst = land(slot);
+            const CUtensorMap *map = (c & 1) ? &a.vmap : &a.kmap;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[slot], F4 ? kBN * D / 2 : S::kLTile);
+#pragma unroll
+                for (int i = 0; i < kBN / 16; ++i) {
+                    if constexpr (F4) {
+                        tma_load_3d_hint(dst + S::code_off(i * 16, 0), map, codes_at(it.kvh), 0, first[i], &full[slot], keep);
+                    } else if constexpr (F8) {        // one (D bytes x 16 rows) box per page
+                        tma_load_3d_hint(dst + i * 16 * D, map, 0, it.kvh, first[i], &full[slot], keep);
+                    } else {
+#pragma unroll
+                        for (int hh = 0; hh < H; ++hh)
+                            tma_load_3d_hint(dst + hh * 16384 + i * 2048, map, hh * 64, it.kvh, first[i], &full[slot], keep);
+                    }
+                }
+            }
+            __syncwarp();
+            if constexpr (F4) {                       // the scales, 16 bytes a row
+                const uint8_t *src = ((c & 1) ? a.v_cache : a.k_cache) + scales_at(it.kvh);
+#pragma unroll
+                for (int i = 0; i < kBN / 32; ++i) {
+                    const int s0 = lane >> 4 ? first[2 * i + 1] : first[2 * i];
+                    const bool in = s0 < a.num_slots;
+                    cp_async16_zfill(dst + S::scale_off(32 * i + lane),
+                                     src + (in ? (int64_t)(s0 + (lane & 15)) * a.lay.row_bytes : 0), in);
+                }
+                cp_async_mbar_arrive_noinc(&full[slot]);
+            }
+        }
+        return true;
+    };
+
     // Tile c of item `it` from its 4-bit landing slot to f16 in the swizzled
     // layout: warp cw widens kWideRows rows from kWideRows cw on.  A lane takes 16-byte
     // chunks of codes (32 elements, two blocks) of the rows = lane mod 8, so
@@ -987,7 +1048,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if constexpr (SHARED) {
                     // boxes of 32 rows; a single tile holds its rows once, twice or four times
                     const bool two = it.rows > kBM;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const int group = a.num_q_heads / a.num_kv_heads;
                         const int blocks = two ? 8 : 4, distinct = two ? 8 : 4 / shared_copies(it.rows);
                         mbar_arrive_expect_tx(q_full, blocks * (S::kTileBytes / 4));
@@ -996,6 +1057,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                                 tma_load_3d(sQ + (i >> 2) * S::kTileBytes + hh * 16384 + (i & 3) * 4096, &a.qmap, hh * 64,
                                             it.kvh * group, it.q0 + (i & (distinct - 1)) * (32 / group), q_full);
                     }
+                    __syncwarp();
                     return true;
                 }
                 if (lane == 0) {
@@ -1007,7 +1069,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 }
                 return true;
             };
-            if (paged16) {
+            if (SHARED && paged16) {
+                ok = load_q() && load_item(it, gl, 0);
+                gl += 2 * it.n_kv;
+            } else if (paged16) {
                 StepCursor cur;                         // load c belongs to kept step c >> 1
                 int st = cur.at<EXT>(a, it, 0);
                 int page = page_id(it, st);             // pages of the current step
@@ -1060,7 +1125,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             ++local;
         }
         if (!SHARED && lane == 0) prefill_sched_done(a, a.num_ctas > 0 ? a.num_ctas : sched_ctas);
-      } else if (warp != kMma && !paged16 && warp - kMma < kGatherWarps) {
+      } else if (warp != kMma && (SHARED || !paged16) && warp - kMma < kGatherWarps) {
         // --------------------------------- extra gather warps (page 1) ----
         const int g = warp - kMma;                      // 1, 2
         int local = 0, gl = 0;
@@ -1074,7 +1139,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             ++local;
             if (v < 0) break;
             if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
-            if (!gather_item(it, gl, g)) break;
+            if (SHARED && paged16 ? !load_item(it, gl, g) : !gather_item(it, gl, g)) break;
             gl += 2 * it.n_kv;
         }
       } else if (F8 && warp >= (SHARED ? kMma + 3 : kMma + 1)) {
