@@ -843,6 +843,8 @@ def decode_shared_workspace_size(q_shape, k_cache: torch.Tensor, max_seqlen_k: i
     what they bound).  4-bit pools need ``kv_dtype=PA_KV_FP4`` and
     ``num_kv_heads``."""
     dec = _decode_sizes(q_shape, k_cache, max_seqlen_k, page_size, kv_chunk, kv_dtype, num_kv_heads)
+    if kv_dtype != PA_KV_FP4:
+        dec.kv_dtype = _kv_dtype(k_cache, k_cache, kv_dtype)
     bounds = _shared_bounds(int(q_shape[0]), int(max_seqlen_k), max_prefix, max_suffix, max_group)
     lib = _lib.load()
     need = int(lib.pa_decode_shared_workspace_size(ctypes.byref(_lib.DecodeSharedParams(dec, None, None, int(num_groups), *bounds))))

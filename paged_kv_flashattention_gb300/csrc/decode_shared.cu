@@ -11,7 +11,7 @@
 // The prefix is a matrix product again: the rows that read KV head kvh of a
 // group are (sequence, query head of kvh), n * Hq / Hkv of them, so prefill's
 // tcgen05 kernel does it (prefill_impl.cuh, SHARED) with tiles of 128 such rows,
-// two tiles per CTA; where a group fills only one, the tile's key steps go in turn
+// two tiles per CTA (over FP8 and 4-bit pools one); where a group fills only one, the tile's key steps go in turn
 // to two softmax halves, and where it fills half or less of one, its rows lie in
 // the tile two or four times, each copy for a share of the keys.  Query rows come in tensor-map boxes of 32 (64 columns, Hq / Hkv
 // heads, 32 Hkv / Hq sequences).
@@ -52,7 +52,9 @@ cudaError_t launch_prefix(const PrefillArgs &a, int d, unsigned ctas, cudaStream
     return d == 128 ? launch_prefix_t<128, KV>(a, ctas, stream) : launch_prefix_t<64, KV>(a, ctas, stream);
 }
 
-constexpr int kItemRows = 2 * kBM;                   // query rows of a work item of the prefix kernel
+constexpr int kBlockRows = 2 * kBM;                  // rows of a block of partials: 8 softmax warps' 32
+// Query rows of a work item of the prefix kernel (PrefillSmem::kItemTiles tiles).
+constexpr int item_rows(int kv_dtype) { return kv_dtype == PA_KV_BF16 ? 2 * kBM : kBM; }
 
 struct MergeArgs {
     SharedArgs sh;
@@ -62,6 +64,7 @@ struct MergeArgs {
     int32_t num_q_heads;
     int32_t num_kv_heads;
     int32_t max_seqlen_k;
+    int32_t item_rows;
     __nv_bfloat16 *out;
     float *lse;
 };
@@ -120,10 +123,10 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
             const int q0 = a.sh.cu_groups[g], n = a.sh.cu_groups[g + 1] - q0;
             const int2 base = a.sh.base[g];
             ok = q0 >= 0 && n <= a.sh.max_group && a.sh.prefix_lens[q0] == P;
-            const int tiles = (n * group + kItemRows - 1) / kItemRows, steps = (P + kBN - 1) / kBN;
-            const int in_group = (b - q0) * group + h % group, tile = in_group / kItemRows, m = in_group % kItemRows;
+            const int tiles = (n * group + a.item_rows - 1) / a.item_rows, steps = (P + kBN - 1) / kBN;
+            const int in_group = (b - q0) * group + h % group, tile = in_group / a.item_rows, m = in_group % a.item_rows;
             const int row = (h / group) * tiles + tile, start = base.x + row * steps;
-            const int rows = min(n * group - tile * kItemRows, kItemRows);
+            const int rows = min(n * group - tile * a.item_rows, a.item_rows);
             const int c0 = start / per, block = c0 + base.y + row;
             const int ranges = min((start + steps - 1) / per - c0 + 1, a.sh.max_blocks - block);
             if (rows <= kBM) {
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
                 apart = 8 / each * 32;
             }
             if (ok) np = max(ranges, 0) * each;
-            first = (int64_t)block * kItemRows + m;
+            first = (int64_t)block * kBlockRows + m;
         }
     }
     if (ok && has_tail) {
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     if (!ok && L != 0 && lane == 0) raise_error(PA_DEVERR_SEQLENS);
     const int n = ok ? np + ns : 0;
     const int shift = __ffs(each) - 1;
-    auto at_of = [&](int s) { return first + (int64_t)(s >> shift) * kItemRows + (s & (each - 1)) * apart; };
+    auto at_of = [&](int s) { return first + (int64_t)(s >> shift) * kBlockRows + (s & (each - 1)) * apart; };
     const float *ls = a.tail.lse_part + row * a.tail.max_splits - np;
     const float *os = a.tail.o_part + (row * a.tail.max_splits - np) * D + lane * E;
     auto lse_of = [&](int s) { return s >= n ? -INFINITY : s < np ? a.sh.lse_part[at_of(s)] : ls[s]; };
@@ -255,7 +258,7 @@ bool make_map_shared_q(CUtensorMap *m, const pa_decode_params &p) {
 // Steps of the longest list: every group at its largest, every prefix at its longest.
 int64_t most_steps(const pa_decode_shared_params &p) {
     const int64_t group = p.dec.num_q_heads / p.dec.num_kv_heads;
-    const int64_t tiles = ((int64_t)p.max_group * group + kItemRows - 1) / kItemRows;
+    const int64_t per = item_rows(p.dec.kv_dtype), tiles = ((int64_t)p.max_group * group + per - 1) / per;
     const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
     return p.num_groups * tiles * steps * p.dec.num_kv_heads;
 }
@@ -281,12 +284,13 @@ SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
     plan.tail = p.max_suffix > 0;
     if (plan.prefix) {
         // an item for each range and row of the list, less one (prefill_impl.cuh); a
-        // row for every KV head and 256 query rows of a group, or part of them
+        // row for every KV head and item_rows query rows of a group, or part of them
         const int64_t group = p.dec.num_q_heads / p.dec.num_kv_heads;
-        const int64_t whole = (int64_t)p.dec.num_seqs * group / kItemRows + p.num_groups;
-        const int64_t bound = p.num_groups * (((int64_t)p.max_group * group + kItemRows - 1) / kItemRows);
+        const int64_t per = item_rows(p.dec.kv_dtype);
+        const int64_t whole = (int64_t)p.dec.num_seqs * group / per + p.num_groups;
+        const int64_t bound = p.num_groups * (((int64_t)p.max_group * group + per - 1) / per);
         plan.max_blocks = (int32_t)(prefix_ctas(p) + (whole < bound ? whole : bound) * p.dec.num_kv_heads);
-        const size_t rows = (size_t)plan.max_blocks * kItemRows;
+        const size_t rows = (size_t)plan.max_blocks * kBlockRows;
         plan.prefix_bytes = 256 + 256 + round256((size_t)p.num_groups * sizeof(int2)) + rows * p.dec.head_dim * sizeof(float) +
                             rows * sizeof(float);
     }
@@ -319,7 +323,7 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
     // (the partials are stored 32 bytes at a time)
     uint8_t *ws = reinterpret_cast<uint8_t *>(round256(reinterpret_cast<uintptr_t>(d.workspace)));
     if (plan.prefix) {
-        const size_t rows = (size_t)plan.max_blocks * kItemRows;
+        const size_t rows = (size_t)plan.max_blocks * kBlockRows;
         uint8_t *o = ws + 256 + round256((size_t)p.num_groups * sizeof(int2));
         m.sh.header = reinterpret_cast<int32_t *>(ws);
         m.sh.base = reinterpret_cast<int2 *>(ws + 256);
@@ -376,6 +380,7 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
     m.num_q_heads = d.num_q_heads;
     m.num_kv_heads = d.num_kv_heads;
     m.max_seqlen_k = d.max_seqlen_k;
+    m.item_rows = item_rows(d.kv_dtype);
     m.out = static_cast<__nv_bfloat16 *>(d.out);
     m.lse = d.lse;
     return launch_merge(m, d.head_dim, stream);

@@ -608,7 +608,13 @@ static pa_status check_shared(const pa_decode_shared_params *p) {
 
 size_t pa_decode_shared_workspace_size(const pa_decode_shared_params *p) {
     g_last_error[0] = 0;
-    if (check_shared(p) != PA_OK) return 0;
+    pa_decode_shared_params sizes;                   // the call's, whatever its pointers
+    if (p != nullptr) {
+        static const float some_scale = 1.f;
+        sizes = *p;
+        sizes.dec.k_scale = sizes.dec.v_scale = &some_scale;
+    }
+    if (check_shared(p != nullptr ? &sizes : nullptr) != PA_OK) return 0;
     if (p->num_groups == 0) return decode_plan(p->dec).workspace_any;
     return plan_decode_shared(*p).workspace_bytes;
 }

@@ -434,7 +434,11 @@ struct PrefillSmem {
     static constexpr int kTileBytes = kHalves * 128 * 128; // 128 rows x D, 16-bit elements
     static constexpr int kLTile = F4 ? kBN * (D / 2 + 16) : F8 ? kTileBytes / 2 : kTileBytes;   // a tile as loaded
     static constexpr int kQ = 0;                           // T query tiles
-    static constexpr int kRing = T * kTileBytes;           // ring of loaded tiles
+    // SHARED: items of one tile over pools that are widened, so that the rings hold two
+    // more tiles; a second tile would share the widened ones, but its softmax takes
+    // longer than widening them again.
+    static constexpr int kItemTiles = SHARED && F8 ? 1 : T;
+    static constexpr int kRing = kItemTiles * kTileBytes;  // ring of loaded tiles
     // 4-bit: columns of output staged at a time; 64 200 us, 32 191, none (each
     // thread its own row) 194, and 78, 75 and 82 on sixteen requests of 512 rows.
     static constexpr int kStageCols = F4 ? 32 : 64;
@@ -574,10 +578,18 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     // G < NS gather warps leave the MMA a slot; with FP8 pools the two spare
     // warps widen tiles instead
     // (SHARED: these warps share the loads of page size 16 too, and widening has its own)
-    constexpr int kGatherWarps = F8 && !SHARED ? 1 : (NS - 1 < kGatherWarpsMax ? NS - 1 : kGatherWarpsMax);
+    // SHARED over widened pools: K loads by one warp, V loads by another, into rings of
+    // even length, and K and V tiles widened by warps of their own: a slot is always K's
+    // or always V's, so that whoever waits for it has seen its phase before.
+    constexpr int kGatherWarps = F8 ? (SHARED ? 2 : 1) : (NS - 1 < kGatherWarpsMax ? NS - 1 : kGatherWarpsMax);
+    static_assert(!SHARED || !F8 || (NS % 2 == 0 && S::kCSlots % 2 == 0), "rings of even length");
+    constexpr int IT = S::kItemTiles;
     constexpr int NC = F8 ? S::kCSlots : NS;  // slots the MMA reads from
-    constexpr int kConverters = !F8 ? 0 : SHARED ? 4 : 2;      // SHARED: a warpgroup of its own
-    constexpr int kWideRows = F8 ? kBN / kConverters : kBN;     // rows of a tile that one of them widens
+    // Warps that widen: two to a tile.  SHARED has four, two for the K tiles and two
+    // for the V tiles: with all four on each tile the waits and the fence take as long
+    // as the conversion.
+    constexpr int kConverters = !F8 ? 0 : SHARED ? 4 : 2;
+    constexpr int kWideRows = 64;
     constexpr bool kInPlace = S::kInPlace;
     constexpr bool kClasses = F4 && !EXT && !SHARED;      // items in classes of positions (prefill_item)
     auto land = [&](int slot) { return smem + S::kRing + slot * S::kLStride + S::kLOff; };
@@ -614,11 +626,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         mbar_init(q_empty, 1);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], paged16 ? (F4 ? 33 : 1) : 32);   // 4-bit: the boxes, and every lane's scales
-            mbar_init(&empty[s], (F8 && !kInPlace) ? kConverters : 1);
+            mbar_init(&empty[s], (F8 && !kInPlace) ? 2 : 1);
         }
         if (F8) {
             for (int s = 0; s < NC; ++s) {
-                mbar_init(&cfull[s], kConverters);
+                mbar_init(&cfull[s], 2);
                 mbar_init(&cempty[s], 1);
             }
             mbar_init(q_conv, kConverters);
@@ -634,7 +646,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         }
         fence_mbar_init();
     }
-    SharedWalk<T> walk{};
+    SharedWalk<IT> walk{};
     if constexpr (SHARED) {
         // Steps of the whole list, steps and rows before this thread's groups, and the
         // group in which this CTA's range starts.
@@ -645,7 +657,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         int steps = 0, rows = 0;
         for (int g = from; g < to; ++g) {
             const SharedGroup r = g == from ? own : shared_group(a, g);
-            const int n = shared_rows<T>(a, r);
+            const int n = shared_rows<IT>(a, r);
             rows += n;
             steps += n * ((r.P + kBN - 1) / kBN);
         }
@@ -678,7 +690,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         walk.end = min(total - walk.at, per_cta) + walk.at;
         for (int g = from; g < to; ++g) {
             const SharedGroup r = g == from ? own : shared_group(a, g);
-            const int n = shared_rows<T>(a, r), c = n * ((r.P + kBN - 1) / kBN);
+            const int n = shared_rows<IT>(a, r), c = n * ((r.P + kBN - 1) / kBN);
             if (walk.at >= s_acc && walk.at < s_acc + c) {
                 start[0] = g;
                 start[1] = s_acc;
@@ -1047,7 +1059,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if (local > 0 && !mbar_wait(q_empty, (local - 1) & 1)) return false;
                 if constexpr (SHARED) {
                     // boxes of 32 rows; a single tile holds its rows once, twice or four times
-                    const bool two = it.rows > kBM;
+                    const bool two = IT > 1 && it.rows > kBM;
                     if (elect_one()) {
                         const int group = a.num_q_heads / a.num_kv_heads;
                         const int blocks = two ? 8 : 4, distinct = two ? 8 : 4 / shared_copies(it.rows);
@@ -1144,7 +1156,9 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         }
       } else if (F8 && warp >= (SHARED ? kMma + 3 : kMma + 1)) {
         // -------------------------------- FP8 widening (kConverters warps) ----
-        const int cw = warp - (SHARED ? kMma + 3 : kMma + 1);      // rows [kWideRows cw, + kWideRows)
+        const int wid = warp - (SHARED ? kMma + 3 : kMma + 1);
+        const int cw = wid & 1;                         // rows [64 cw, 64 cw + 64)
+        constexpr int kStep = SHARED ? 2 : 1;           // SHARED: warps 0, 1 K tiles, 2, 3 V tiles
         int local = 0, gl = 0;
         bool ok = true;
         PrefillItem it;
@@ -1161,7 +1175,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             ++local;
             const float ksc = F4 || SHARED ? 1.f : __ldg(a.k_scale + it.kvh);
 #pragma unroll 4
-            for (int i = cw * 32 + lane; i < (SHARED && it.rows <= kBM ? 1 : T) * S::kTileBytes / 16; i += 32 * kConverters) {
+            for (int i = wid * 32 + lane; i < (SHARED ? IT : T) * S::kTileBytes / 16; i += 32 * kConverters) {
                 uint4 *pq = reinterpret_cast<uint4 *>(sQ + i * 16);
                 *pq = bf16x8_to_f16x8_scaled(*pq, ksc);
             }
@@ -1169,7 +1183,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             __syncwarp();
             if (lane == 0) mbar_arrive(q_conv);
             // K/V tiles: E4M3 rows -> f16 in the swizzled K-major layout
-            for (int c = 0; c < 2 * it.n_kv; ++c, ++gl) {
+            const int gl0 = gl;
+            gl += 2 * it.n_kv;
+            for (int c = SHARED ? wid >> 1 : 0; c < 2 * it.n_kv; c += kStep) {
+                const int gl = gl0 + c;
                 const int ls = gl % NS, cs = gl % NC;
                 ok = __all_sync(0xffffffffu, mbar_wait(&full[ls], (gl / NS) & 1));
                 // (in place the slot was free before it was loaded)
@@ -1344,7 +1361,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 if constexpr (!SHARED) prefill_item<T, EXT, kClasses>(a, v, it);
                 const int n_kv = it.n_kv;
                 if constexpr (SHARED) {
-                    if (it.rows <= kBM) {
+                    if (IT == 1 || it.rows <= kBM) {
                         if (!mma_halves(it, local, gl, gs, gs1)) break;
                         gl += 2 * n_kv;
                         gs += (n_kv + 1) / 2;
