@@ -90,7 +90,7 @@ class BeamReorderParams(ctypes.Structure):
     _fields_ = [
         ("parents", c_p), ("num_groups", c_i32), ("beams", c_i32), ("page_size", c_i32), ("max_seqlen_k", c_i32),
         ("token_table", c_p), ("token_table_stride", c_i64), ("token_table_rows", c_i64), ("table_idx", c_p),
-        ("seqlens", c_p), ("prefix_lens", c_p), ("spare_pages", c_p), ("pools", ctypes.POINTER(c_p)), ("num_pools", c_i32),
+        ("seqlens", c_p), ("prefix_lens", c_p), ("spare_pages", c_p), ("pools", c_p), ("num_pools", c_i32),
         ("num_pages", c_i64), ("row_bytes", c_i64), ("history", c_p), ("history_stride", c_i64), ("history_len", c_i32),
     ]
 

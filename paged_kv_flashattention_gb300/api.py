@@ -6,6 +6,7 @@ non-zero status.  No arithmetic of the attention path happens here.
 """
 from __future__ import annotations
 
+import array
 import collections
 import ctypes
 import functools
@@ -875,42 +876,62 @@ def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     _need(q, "q", torch.bfloat16, dev)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, d]")
-    B, Hq, _ = q.shape
+    B, Hq, d = q.shape
     kvd = _kv_dtype(k_cache, v_cache, kv_dtype)
-    if kvd != PA_KV_FP4:                              # (4-bit pools: _fp4_geometry)
-        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            _need(t, n, k_cache.dtype, dev)
-    for t, n in ((cache_seqlens, "cache_seqlens"), (cu_groups, "cu_groups"), (prefix_lens, "prefix_lens")):
-        _need(t, n, torch.int32, dev)
-    _need_rows(page_table, "page_table", dev)
-    if cache_seqlens.numel() != B or prefix_lens.numel() != B or page_table.shape[0] < B:
+    if kvd == PA_KV_FP4:
+        num_pages, P, Hkv, d = _fp4_geometry(k_cache, v_cache, page_size, k_scale, v_scale, d, dev)
+    else:
+        _need(k_cache, "k_cache", k_cache.dtype, dev)
+        _need(v_cache, "v_cache", k_cache.dtype, dev)
+        num_pages, P, Hkv, pool_d = _pool_geometry(k_cache, v_cache, page_size)
+        if pool_d != d:
+            raise ValueError("head_dim of q and the pool differ")
+        if kvd == PA_KV_FP8_E4M3:
+            _need_scales(k_scale, v_scale, Hkv, dev)
+    _need(cache_seqlens, "cache_seqlens", torch.int32, dev)
+    _need(cu_groups, "cu_groups", torch.int32, dev)
+    _need(prefix_lens, "prefix_lens", torch.int32, dev)
+    _need(page_table, "page_table", torch.int32, dev, False)
+    max_k, groups = int(max_seqlen_k), cu_groups.numel() - 1
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D with unit column stride")
+    (rows, cols), (pt_stride, unit) = page_table.shape, page_table.stride()
+    if unit != 1 or (rows > 1 and pt_stride < cols):
+        raise ValueError("page_table must be 2-D with unit column stride and rows that do not overlap")
+    if cache_seqlens.numel() != B or prefix_lens.numel() != B or rows < B:
         raise ValueError("cache_seqlens and prefix_lens must hold one entry per sequence, page_table a row")
-    if cu_groups.numel() < 1:
+    if cols * P < max_k:
+        raise ValueError(f"page_table must have ceil({max_k} / {P}) columns")
+    if groups < 0:
         raise ValueError("cu_groups must hold num_groups + 1 entries")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, dev)
-    if out.numel() != q.numel():
-        raise ValueError("out must have q's size")
+    else:
+        _need(out, "out", torch.bfloat16, dev)
+        if out.numel() != B * Hq * d:
+            raise ValueError("out must have q's size")
+    lse_ptr = None
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
         if lse.numel() != B * Hq:
             raise ValueError("lse must be [B, Hq]")
-    max_k, groups = int(max_seqlen_k), cu_groups.numel() - 1
+        lse_ptr = lse.data_ptr()
     bounds = _shared_bounds(B, max_k, max_prefix, max_suffix, max_group)
     if workspace is None:
         need = decode_shared_workspace_size(
             q.shape, k_cache, max_k, groups, max_group=bounds[0], max_prefix=bounds[1], max_suffix=bounds[2], page_size=page_size,
-            kv_chunk=kv_chunk, kv_dtype=kvd, num_kv_heads=k_scale.numel() if kvd == PA_KV_FP4 and k_scale is not None else None)
+            kv_chunk=kv_chunk, kv_dtype=kvd, num_kv_heads=Hkv)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
-    dec = _decode_params(q, k_cache, v_cache, page_table, cache_seqlens, max_k, scale, page_size, out, lse, workspace, kv_chunk,
-                         k_scale, v_scale, kv_dtype=kvd)
-    dec.page_table_stride = max(page_table.stride(0), page_table.shape[1])
-    if page_table.shape[1] * dec.page_size < max_k:
-        raise ValueError(f"page_table must have ceil({max_k} / {dec.page_size}) columns")
-    p = _lib.DecodeSharedParams(dec, cu_groups.data_ptr(), prefix_lens.data_ptr(), groups, *bounds)
+    ks = vs = None
+    if kvd != PA_KV_BF16:
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    p = _lib.DecodeSharedParams(
+        (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max(pt_stride, cols), cache_seqlens.data_ptr(),
+         B, max_k, Hq, Hkv, d, P, num_pages, 1.0 / math.sqrt(d) if scale is None else float(scale), out.data_ptr(), lse_ptr,
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(kv_chunk), kvd, ks, vs),
+        cu_groups.data_ptr(), prefix_lens.data_ptr(), groups, *bounds)
     _call(_lib.load().pa_decode_shared, q, ctypes.byref(p))
     return out
 
@@ -1012,37 +1033,38 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
     its spare page.  ``spare_pages`` may be None with page size 1.
     ``max_seqlen_k`` (default: the table's width) bounds the lengths."""
     dev = token_table.device
-    k_caches = [k_caches] if isinstance(k_caches, torch.Tensor) else list(k_caches)
-    v_caches = [v_caches] if isinstance(v_caches, torch.Tensor) else list(v_caches)
-    pools = k_caches + v_caches
-    if len(k_caches) != len(v_caches) or not pools:
+    pools = ([k_caches] if isinstance(k_caches, torch.Tensor) else list(k_caches)) + \
+        ([v_caches] if isinstance(v_caches, torch.Tensor) else list(v_caches))
+    n = 1 if isinstance(k_caches, torch.Tensor) else len(k_caches)
+    if not pools or len(pools) != 2 * n:
         raise ValueError("k_caches and v_caches must hold one pool per layer")
     first = pools[0]
-    for t in pools:
-        _need(t, "every pool", first.dtype, dev)
-        if t.shape != first.shape:
+    dtype, shape = first.dtype, first.shape
+    for t in pools:                                   # (a loop over every layer's pools: the checks of _need in one line)
+        if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+            _need(t, "every pool", dtype, dev)
+        if t.shape != shape:
             raise ValueError("the pools must have one shape")
-    P = page_size
-    if P is None:
-        if first.dim() < 3:
-            raise ValueError("page_size is required for [slots, row] pools")
-        P = first.shape[1]
-    P = int(P)
-    if first.dim() == 4 or (first.dim() == 3 and page_size is None) or (first.dim() == 3 and first.dtype == torch.uint8 and
-                                                                        first.shape[1] == P):
-        if first.shape[1] != P:
+    # [num_pages, page_size, ...], or with page_size also [slots, ...]: heads and
+    # elements, or the bytes of a 4-bit row
+    dims, P = len(shape), page_size
+    paged = dims == 4 or (dims == 3 and (P is None or (dtype == torch.uint8 and shape[1] == P)))
+    if paged:
+        if P is not None and P != shape[1]:
             raise ValueError("page_size does not match the pool shape")
-        num_pages, slots = first.shape[0], first.shape[0] * P
+        num_pages, P = shape[0], shape[1]
+    elif P is None:
+        raise ValueError("page_size is required for [slots, row] pools")
     else:
-        slots = first.shape[0]
-        num_pages = slots // P if P > 0 else 0
-    row_bytes = first.numel() // max(slots, 1) * first.element_size()
+        num_pages = shape[0] // int(P) if int(P) > 0 else 0
+    P = int(P)
+    row_bytes = math.prod(shape[2 if paged else 1:]) * first.element_size()
     _need(parents, "parents", torch.int32, dev)
     if parents.dim() != 2:
         raise ValueError("parents must be [groups, beams]")
     G, K = parents.shape
     _need_rows(token_table, "token_table", dev)
-    width = token_table.shape[1]
+    rows, width = token_table.shape
     max_k = width if max_seqlen_k is None else int(max_seqlen_k)
     if max_k > width:
         raise ValueError(f"token_table must be at least {max_k} wide")
@@ -1053,16 +1075,17 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
             _need(t, name, torch.int32, dev)
             if t.numel() != G * K:
                 raise ValueError(f"{name} must hold one entry per sequence ({G * K})")
+    history_ptr, history_stride, history_len = None, 0, 0
     if history is not None:
         _need_rows(history, "history", dev)
         if history.shape[0] != G * K:
             raise ValueError(f"history must have a row per sequence ({G * K})")
+        if history.numel():
+            history_ptr, history_len = history.data_ptr(), history.shape[1]
+            history_stride = max(history.stride(0), history_len)
+    ptrs = array.array("Q", [t.data_ptr() for t in pools])
     p = _lib.BeamReorderParams(
-        parents=parents.data_ptr(), num_groups=G, beams=K, page_size=P, max_seqlen_k=max_k, token_table=token_table.data_ptr(),
-        token_table_stride=max(token_table.stride(0), width), token_table_rows=token_table.shape[0],
-        table_idx=table_idx.data_ptr(), seqlens=seqlens.data_ptr(), prefix_lens=_ptr(prefix_lens), spare_pages=_ptr(spare_pages),
-        pools=(ctypes.c_void_p * len(pools))(*[t.data_ptr() for t in pools]), num_pools=len(pools), num_pages=num_pages,
-        row_bytes=row_bytes, history=_ptr(history) or None if history is not None and history.numel() else None,
-        history_stride=max(history.stride(0), history.shape[1]) if history is not None else 0,
-        history_len=history.shape[1] if history is not None and history.numel() else 0)
+        parents.data_ptr(), G, K, P, max_k, token_table.data_ptr(), max(token_table.stride(0), width), rows, table_idx.data_ptr(),
+        seqlens.data_ptr(), _ptr(prefix_lens), _ptr(spare_pages), ptrs.buffer_info()[0], len(pools), num_pages, row_bytes,
+        history_ptr, history_stride, history_len)
     _call(_lib.load().pa_beam_reorder, token_table, ctypes.byref(p))

@@ -63,6 +63,17 @@ struct SelectArgs {
     int32_t *out_tokens;
 };
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t ai = *reinterpret_cast<uint64_t *>(&a), bi = *reinterpret_cast<uint64_t *>(&b), r;
+    asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(ai), "l"(bi));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t ai = *reinterpret_cast<uint64_t *>(&a), bi = *reinterpret_cast<uint64_t *>(&b), r;
+    asm("mul.f32x2 %0, %1, %2;" : "=l"(r) : "l"(ai), "l"(bi));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
 // Scores that are no numbers count as -inf.
 __device__ __forceinline__ float cleaned(float x) { return x < INFINITY ? x : -INFINITY; }
 
@@ -145,7 +156,6 @@ struct Columns {
                 const __half2 h = *reinterpret_cast<const __half2 *>(&w[i / 2]);
                 x[i] = (i & 1) ? __high2float(h) : __low2float(h);
             }
-            x[i] = cleaned(x[i]);
         }
     }
 };
@@ -254,23 +264,40 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
         Columns<DT> now = ahead;
         if (tile + kTile < end) ahead.load(row, skew, col + kTile, end);
         now.values(skew, x);
-        if (tile == from) {
-            float top = x[0];
+        float top = x[0];
 #pragma unroll
-            for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
-            const uint32_t least = block_floor(ordered(top), n, 16, tops);
+        for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
+        if (tile == from) {
+            float most = cleaned(x[0]);
+#pragma unroll
+            for (int i = 1; i < kElems; ++i) most = fmaxf(most, cleaned(x[i]));
+            const uint32_t least = block_floor(ordered(most), n, 16, tops);
             // elements of that value are entries too
             if (least > ordered(-INFINITY)) raise(value_below(least));
         }
+        // Most threads have no element above the threshold (a maximum leaves NaN
+        // out, the sum of the terms does not): they add their terms and are done.
         int last = 0;
+        float2 e2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) {
-            if (x[i] > thr) {
-                last = atomicAdd(&count, 1);
-                buf[last] = key_of(x[i], col + i);
-                ++last;
-            } else if (thr != -INFINITY) {
-                rest += term(x[i]);
+        for (int i = 0; i < kElems; i += 2) {
+            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+            e2 = add2(e2, make_float2(fast_exp2(y.x), fast_exp2(y.y)));
+        }
+        const float terms = e2.x + e2.y;
+        if (thr != -INFINITY && top <= thr && terms < INFINITY) {
+            rest += terms;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kElems; ++i) {
+                const float v = cleaned(x[i]);
+                if (v > thr) {
+                    last = atomicAdd(&count, 1);
+                    buf[last] = key_of(v, col + i);
+                    ++last;
+                } else if (thr != -INFINITY) {
+                    rest += term(v);
+                }
             }
         }
         if (__syncthreads_or(last > limit)) {
@@ -388,7 +415,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
         return ordered(state[k] == 1 && r == 0 ? (double)score[k] : (double)-INFINITY);
     };
     uint64_t thr = 0;                                // with thr_idx: the n-th best so far
-    uint32_t thr_idx = 0xffffffffu;
+    uint32_t thr_idx = 0xffffffffu, least = 0;       // least: n entries of the first round have as much
     auto better = [](uint64_t x, uint32_t i, uint64_t y, uint32_t j) { return x > y || (x == y && i < j); };
     // Ranks the buffer's m entries; the n best, in order, into best.
     auto cut = [&](int m) {
@@ -418,7 +445,6 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
             if (e < entries) v[i] = entry(e, at[i]);
             top = max(top, (uint32_t)(v[i] >> 32));
         }
-        uint32_t least = 0;
         if (e0 == 0) least = block_floor(top, n, 12, tops);
         int last = 0;
 #pragma unroll

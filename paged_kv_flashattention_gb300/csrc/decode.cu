@@ -44,6 +44,7 @@
 // d = 2g + 1.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "decode_impl.cuh"
@@ -224,12 +225,24 @@ cudaError_t launch_decode_t(const DecodeArgs &a, int64_t items_max, cudaStream_t
     const size_t smem = S::kRingBytes + 2 * S::kStages * sizeof(uint64_t) +
                         HPC * 8 * kStageTok * sizeof(uint16_t) + (a.num_seqs + 1) * sizeof(int32_t);
     auto kern = decode_kernel<D, G, HPC, F8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // CTAs per SM of the last (device, size), as decode_fp4.cu keeps them
+    static std::atomic<uint64_t> last{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t key = ((uint64_t)(dev + 1) << 40) | ((uint64_t)smem << 8);
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (HPC + 1) * 32, smem);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const uint64_t seen = last.load(std::memory_order_relaxed);
+    if ((seen & ~uint64_t(255)) == key) {
+        per_sm = (int)(seen & 255);
+    } else {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        if (e != cudaSuccess) return e;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (HPC + 1) * 32, smem);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        last.store(key | (uint64_t)per_sm, std::memory_order_relaxed);
+    }
     int64_t grid = (int64_t)num_sms() * per_sm;
     if (a.max_ctas > 0 && grid > a.max_ctas) grid = a.max_ctas;
     if (grid > items_max) grid = items_max;

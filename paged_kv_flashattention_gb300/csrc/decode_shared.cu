@@ -19,6 +19,8 @@
 // partials are written in 32 bits, a block of 8 warps' 32 rows for each work item.
 #include "prefill_impl.cuh"
 
+#include <atomic>
+
 #include "pdl.cuh"
 
 namespace pa {
@@ -42,8 +44,16 @@ cudaError_t launch_prefix_t(const PrefillArgs &a, unsigned ctas, cudaStream_t st
     // One CTA per SM (it allocates all 512 TMEM columns).
     const int smem = (S::kTotal + 1024) > 120 * 1024 ? (S::kTotal + 1024) : 120 * 1024;
     auto kern = shared_prefix_kernel<D, KV>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};           // devices on which the kernel may use that much, of the first 64
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if ((ready.load(std::memory_order_relaxed) & bit) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_after(kern, ctas, KV == PA_KV_BF16 ? 384 : 512, smem, stream, a);
 }
 

@@ -123,7 +123,7 @@ def main():
         args = {**REORDER, **change}
         pools = args.pop("pools", [0x10000, 0x20000])
         arr = (ctypes.c_void_p * 300)(*pools)
-        note(f"reorder-{c}", lib.pa_beam_reorder(ctypes.byref(_lib.BeamReorderParams(pools=arr, **args)), None))
+        note(f"reorder-{c}", lib.pa_beam_reorder(ctypes.byref(_lib.BeamReorderParams(pools=ctypes.addressof(arr), **args)), None))
     for name, fn in (("shared", lib.pa_decode_shared), ("select", lib.pa_beam_select), ("reorder", lib.pa_beam_reorder)):
         assert fn(None, None) == INVALID, name
     print(json.dumps(out))
