@@ -6,10 +6,9 @@
 // over the logits finds each chunk's n largest and its part of lse; a second
 // launch, one CTA per group, forms lse and the totals in 64 bits and merges the
 // chunks' lists.
-//   - A chunk keeps a threshold that at least n of its elements reach: at first
-//     the n-th largest of the thread maxima of the first tile, then the n-th
-//     largest found.  Elements above it go to a buffer in shared memory (about n of
-//     each tile of 2048), all others into the sum of exponentials at once, with the threshold
+//   - A chunk (8192 columns of a CTA, in registers) has a threshold that n of its
+//     elements reach: the n-th largest of its thread maxima.  Elements above it go
+//     to a buffer in shared memory (little more than n), all others into the sum of exponentials at once, with the threshold
 //     as reference: it bounds them.  A buffer that fills up is cut to its n
 //     largest.  An entry's rank among the buffer's is its place in the list.
 //   - Two candidates of different beams are ordered by sums that differ by
@@ -55,7 +54,7 @@ struct SelectArgs {
     const float *scores;
     const uint8_t *finished;
     int32_t pad, groups, beams, vocab, n;
-    int32_t chunks, chunk;        // chunks of a row, columns of a chunk (a multiple of kTile)
+    int32_t chunks;               // chunks of a row
     float2 *lists;                // [rows][chunks][n]: logit, column as bits (0xffffffff: none)
     ChunkSum *sums;               // [rows][chunks]
     float *out_scores;
@@ -134,7 +133,8 @@ struct Columns {
         }
     }
 
-    __device__ __forceinline__ void values(int skew, float (&x)[kElems]) {
+    // Moves the first column to the first word.
+    __device__ __forceinline__ void align(int skew) {
         if (whole && skew != 0) {                    // (the same for all whole threads of a row)
             if (skew & 8)
 #pragma unroll
@@ -146,6 +146,9 @@ struct Columns {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
         }
+    }
+
+    __device__ __forceinline__ void values(float (&x)[kElems]) const {
 #pragma unroll
         for (int i = 0; i < kElems; ++i) {
             if constexpr (DT == PA_LOGITS_F32) {
@@ -193,9 +196,9 @@ __device__ __forceinline__ float value_below(uint32_t k) { return unordered(k - 
 
 // A buffer is cut when it holds more than this; it then has room for another tile
 // (round), every element of which may be an entry.
-__device__ __forceinline__ int kept_limit(int n) { return 32 + 2 * n; }
+__device__ __forceinline__ int kept_limit(int n) { return 16 + n + n / 2; }
 
-template <int DT>
+template <int DT, int U>
 __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const SelectArgs a) {
     __shared__ uint64_t buf[kKept + kTile];
     __shared__ uint64_t best[128];
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
     constexpr int kBytes = DT == PA_LOGITS_F32 ? 4 : 2;
     const uint8_t *row = static_cast<const uint8_t *>(a.logits) + (int64_t)row_id * a.stride * kBytes;
     const int skew = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
-    const int from = c * a.chunk, end = min(from + a.chunk, a.vocab);
+    const int from = c * (U * kTile), end = min(from + U * kTile, a.vocab);
     const int n = min(a.n, end - from), limit = kept_limit(n);
     if (t == 0) {
         count = 0;
@@ -256,50 +259,76 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
         return n;
     };
 
-    Columns<DT> ahead;
-    ahead.load(row, skew, from + t * kElems, end);
-    for (int tile = from; tile < end; tile += kTile) {
+    // The whole chunk in registers, its maxima first: the threshold is then one that
+    // little more than n of its elements reach.
+    Columns<DT> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u].load(row, skew, from + u * kTile + t * kElems, end);
+    float tops_of[U], most = -INFINITY;              // fmaxf: the larger of numbers
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
         float x[kElems];
-        const int col = tile + t * kElems;
-        Columns<DT> now = ahead;
-        if (tile + kTile < end) ahead.load(row, skew, col + kTile, end);
-        now.values(skew, x);
-        float top = x[0];
+        raw[u].align(skew);
+        raw[u].values(x);
+        tops_of[u] = -INFINITY;
 #pragma unroll
-        for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
-        if (tile == from) {
-            float most = cleaned(x[0]);
+        for (int i = 0; i < kElems; ++i) tops_of[u] = fmaxf(tops_of[u], x[i]);
+        if (tops_of[u] == INFINITY) {
 #pragma unroll
-            for (int i = 1; i < kElems; ++i) most = fmaxf(most, cleaned(x[i]));
-            const uint32_t least = block_floor(ordered(most), n, 16, tops);
-            // elements of that value are entries too
-            if (least > ordered(-INFINITY)) raise(value_below(least));
+            for (int i = 0; i < kElems; ++i) most = fmaxf(most, cleaned(x[i]));
+        } else {
+            most = fmaxf(most, tops_of[u]);
         }
-        // Most threads have no element above the threshold (a maximum leaves NaN
-        // out, the sum of the terms does not): they add their terms and are done.
+    }
+    const uint32_t least = block_floor(ordered(most), n, 16, tops);
+    // elements of that value are entries too
+    if (least > ordered(-INFINITY)) raise(value_below(least));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float x[kElems];
+        const int col = from + u * kTile + t * kElems;
+        raw[u].values(x);
+        const float top = tops_of[u];
+        // Most warps have no element above the threshold: they add their terms and are
+        // done.  (A maximum leaves NaN out, the sum of the terms does not; +inf is above
+        // every threshold.)
         int last = 0;
-        float2 e2 = make_float2(0.f, 0.f);
+        float e[kElems];
 #pragma unroll
         for (int i = 0; i < kElems; i += 2) {
             const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
-            e2 = add2(e2, make_float2(fast_exp2(y.x), fast_exp2(y.y)));
+            e[i] = fast_exp2(y.x);
+            e[i + 1] = fast_exp2(y.y);
         }
-        const float terms = e2.x + e2.y;
-        if (thr != -INFINITY && top <= thr && terms < INFINITY) {
-            rest += terms;
-        } else {
+        auto sum_up = [&]() {
+            float2 s = make_float2(e[0], e[1]);
+#pragma unroll
+            for (int i = 2; i < kElems; i += 2) s = add2(s, make_float2(e[i], e[i + 1]));
+            return s.x + s.y;
+        };
+        float terms = sum_up();
+        if (__any_sync(0xffffffffu, top > thr || !(terms < INFINITY))) {
+            uint32_t above = 0;
 #pragma unroll
             for (int i = 0; i < kElems; ++i) {
                 const float v = cleaned(x[i]);
-                if (v > thr) {
-                    last = atomicAdd(&count, 1);
-                    buf[last] = key_of(v, col + i);
-                    ++last;
-                } else if (thr != -INFINITY) {
-                    rest += term(v);
-                }
+                if (v > thr) above |= 1u << i;
+                // a term that is no number: its element is not one either
+                e[i] = v > thr || !(v > -INFINITY) ? 0.f : e[i];
+            }
+            terms = sum_up();
+            while (above != 0u) {
+                const int i = __ffs(above) - 1;
+                above &= above - 1u;
+                float v = x[0];
+#pragma unroll
+                for (int q = 1; q < kElems; ++q) v = i == q ? x[q] : v;
+                last = atomicAdd(&count, 1);
+                buf[last] = key_of(v, col + i);
+                ++last;
             }
         }
+        if (thr != -INFINITY) rest += terms;
         if (__syncthreads_or(last > limit)) {
             const int kept = cut(count);             // limit >= n: n entries stay
             if (t < kept) buf[t] = best[t];
@@ -600,25 +629,23 @@ __global__ void __launch_bounds__(kColumns) reorder_rows_kernel(const pa_beam_re
     }
 }
 
+constexpr int kMostTiles = 4;     // tiles of a chunk where there are CTAs enough
+
 template <int DT>
-cudaError_t launch_chunks(const SelectArgs &a, cudaStream_t stream) {
-    return launch_after(select_chunks_kernel<DT>, (unsigned)(a.groups * a.beams * a.chunks), kSelThreads, 0, stream, a);
+cudaError_t launch_chunks(const SelectArgs &a, int tiles, cudaStream_t stream) {
+    return launch_after(tiles == 1 ? select_chunks_kernel<DT, 1> : select_chunks_kernel<DT, kMostTiles>,
+                        (unsigned)(a.groups * a.beams * a.chunks), kSelThreads, 0, stream, a);
 }
 
 }  // namespace
 
-// Columns of a chunk: whole tiles, about kCtas CTAs while there are tiles enough
-// (a constant: the workspace's size is the same on every device).
-constexpr int kCtas = 152 * 8;
+// A chunk is kMostTiles tiles, or one while the GPU holds all CTAs at once (a
+// constant number: the workspace's size is the same on every device).
 SelectPlan plan_select(const pa_beam_select_params &p) {
     SelectPlan plan{};
     const int64_t rows = (int64_t)p.num_groups * p.beams, tiles = ((int64_t)p.vocab + kTile - 1) / kTile;
-    int64_t per = rows * tiles / kCtas;
-    if (per < 1) per = 1;
-    const int64_t chunks = (tiles + per - 1) / per;
-    per = (tiles + chunks - 1) / chunks;
-    plan.chunks = (int32_t)((tiles + per - 1) / per);
-    plan.chunk = (int32_t)(per * kTile);
+    plan.tiles = rows * tiles <= 152 * 4 ? 1 : kMostTiles;
+    plan.chunks = (int32_t)((tiles + plan.tiles - 1) / plan.tiles);
     plan.list_bytes = (size_t)rows * plan.chunks * p.num_out * sizeof(float2);
     plan.list_bytes = (plan.list_bytes + 15) / 16 * 16;
     plan.workspace_bytes = plan.list_bytes + (size_t)rows * plan.chunks * sizeof(ChunkSum);
@@ -637,15 +664,14 @@ cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan
     a.vocab = p.vocab;
     a.n = p.num_out;
     a.chunks = plan.chunks;
-    a.chunk = plan.chunk;
     a.lists = static_cast<float2 *>(p.workspace);
     a.sums = reinterpret_cast<ChunkSum *>(static_cast<uint8_t *>(p.workspace) + plan.list_bytes);
     a.out_scores = p.out_scores;
     a.out_parents = p.out_parents;
     a.out_tokens = p.out_tokens;
-    const cudaError_t e = p.logits_dtype == PA_LOGITS_F32   ? launch_chunks<PA_LOGITS_F32>(a, stream)
-                          : p.logits_dtype == PA_LOGITS_F16 ? launch_chunks<PA_LOGITS_F16>(a, stream)
-                                                            : launch_chunks<PA_LOGITS_BF16>(a, stream);
+    const cudaError_t e = p.logits_dtype == PA_LOGITS_F32   ? launch_chunks<PA_LOGITS_F32>(a, plan.tiles, stream)
+                          : p.logits_dtype == PA_LOGITS_F16 ? launch_chunks<PA_LOGITS_F16>(a, plan.tiles, stream)
+                                                            : launch_chunks<PA_LOGITS_BF16>(a, plan.tiles, stream);
     if (e != cudaSuccess) return e;
     return launch_after(select_merge_kernel, (unsigned)p.num_groups, kSelThreads, 0, stream, a);
 }

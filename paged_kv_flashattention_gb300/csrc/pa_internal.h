@@ -91,7 +91,7 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
 
 // Beam search (beam.cu).
 struct SelectPlan {
-    int32_t chunks, chunk;        // chunks of a row, columns of a chunk
+    int32_t tiles, chunks;        // tiles of a chunk, chunks of a row
     size_t list_bytes;
     size_t workspace_bytes;
 };
