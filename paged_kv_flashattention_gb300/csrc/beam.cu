@@ -6,11 +6,15 @@
 // over the logits finds each chunk's n largest and its part of lse; a second
 // launch, one CTA per group, forms lse and the totals in 64 bits and merges the
 // chunks' lists.
-//   - A chunk (8192 columns of a CTA, in registers) has a threshold that n of its
-//     elements reach: the n-th largest of its thread maxima.  Elements above it go
-//     to a buffer in shared memory (little more than n), all others into the sum of exponentials at once, with the threshold
-//     as reference: it bounds them.  A buffer that fills up is cut to its n
-//     largest.  An entry's rank among the buffer's is its place in the list.
+//   - A CTA has a threshold that n of its elements reach: the n-th largest of its
+//     thread maxima.  Elements above it go to a buffer in shared memory (little more
+//     than n), all others into the sum of exponentials at once, with the threshold as
+//     reference: it bounds them.  A buffer that fills up is cut to its n largest.  An
+//     entry's rank among the buffer's is its place in the list.
+//   - Finding the threshold, ranking and 64-bit exponentials take a CTA 5 us,
+//     whatever it has read.  Small calls read a chunk into registers and pay that
+//     once; large ones stream the logits by (maximum, sum) of 32 columns, and a CTA
+//     per row reads the few blocks again that hold its n largest.
 //   - Two candidates of different beams are ordered by sums that differ by
 //     lse: an error of lse of 1e-7 swaps neighbours of a batch of 64 groups once
 //     in a hundred steps.  So the n largest exponentials are summed in 64 bits,
@@ -54,9 +58,11 @@ struct SelectArgs {
     const float *scores;
     const uint8_t *finished;
     int32_t pad, groups, beams, vocab, n;
-    int32_t chunks;               // chunks of a row
+    int32_t chunks;               // lists of a row
+    int32_t spans;                // CTAs of a row in the first pass of large calls
     float2 *lists;                // [rows][chunks][n]: logit, column as bits (0xffffffff: none)
     ChunkSum *sums;               // [rows][chunks]
+    float2 *blocks;               // [rows][spans][kSelThreads]: maximum, sum
     float *out_scores;
     int32_t *out_parents;
     int32_t *out_tokens;
@@ -198,81 +204,179 @@ __device__ __forceinline__ float value_below(uint32_t k) { return unordered(k - 
 // (round), every element of which may be an entry.
 __device__ __forceinline__ int kept_limit(int n) { return 16 + n + n / 2; }
 
+// A CTA's n largest of the elements that it is shown, and the sum of all of their
+// exponentials.  Elements above thr are entries of the buffer; those at or below
+// it are in `rest`, each thread's sum of 2^((x - ref) log2 e) with ref = thr.
+struct Chosen {
+    uint64_t buf[kKept + kTile];
+    uint64_t best[128];
+    uint32_t tops[kSelThreads];
+    unsigned long long dropped;                      // in units of 2^-32
+    int count;
+};
+
+struct Chooser {
+    Chosen &sh;
+    int n, limit;
+    float thr, ref, rest;
+
+    __device__ __forceinline__ Chooser(Chosen &s, int n) : sh(s), n(n), limit(kept_limit(n)), thr(-INFINITY), ref(0.f), rest(0.f) {
+        if (threadIdx.x == 0) {
+            sh.count = 0;
+            sh.dropped = 0;
+        }
+    }
+    __device__ __forceinline__ float term(float x) const { return fast_exp2((x - ref) * kLog2e); }
+    // A new threshold, the same for the CTA.
+    __device__ __forceinline__ void raise(float to) {
+        const float r = to == -INFINITY ? 0.f : to;
+        rest = rest > 0.f ? rest * fast_exp2((ref - r) * kLog2e) : 0.f;
+        thr = to;
+        ref = r;
+    }
+    // The first threshold, from the maxima of the threads' elements: elements of
+    // that value are entries too.
+    __device__ __forceinline__ void start(float most) {
+        const uint32_t least = block_floor(ordered(most), n, 16, sh.tops);
+        if (least > ordered(-INFINITY)) raise(value_below(least));
+    }
+    // An element above thr; the entries then (they may be more than the limit).
+    __device__ __forceinline__ int enter(float x, int col) {
+        const int at = atomicAdd(&sh.count, 1);
+        sh.buf[at] = key_of(x, col);
+        return at + 1;
+    }
+    // Cuts the buffer's m entries to the n largest, in order, in best; the n-th is
+    // the new threshold and the others go into rest: as whole multiples of 2^-32, so
+    // that their order in the buffer, which is chance, does not matter.  Every thread.
+    __device__ int cut(int m) {
+        const int t = threadIdx.x;
+        uint32_t out = 0;
+        for (int e = t, i = 0; e < m; e += kSelThreads, ++i) {
+            const uint64_t k = sh.buf[e];
+            int rank = 0;
+#pragma unroll 8
+            for (int j = 0; j < m; ++j) rank += sh.buf[j] > k;
+            if (rank < n) sh.best[rank] = k;
+            else out |= 1u << i;
+        }
+        __syncthreads();
+        if (m < n) return m;
+        raise(key_value(sh.best[n - 1]));
+        if (out != 0) {
+            unsigned long long sum = 0;
+            for (int e = t, i = 0; e < m; e += kSelThreads, ++i)
+                if (out >> i & 1u) sum += (unsigned long long)__float2ull_rn(term(key_value(sh.buf[e])) * 0x1p32f);
+            atomicAdd(&sh.dropped, sum);
+        }
+        __syncthreads();
+        if (t == 0) {
+            rest += (float)sh.dropped * 0x1p-32f;
+            sh.dropped = 0;
+        }
+        return n;
+    }
+    // Between batches of at most kTile elements: room for the next.  `last` is the
+    // thread's last enter().
+    __device__ __forceinline__ void settle(int last) {
+        if (__syncthreads_or(last > limit)) {
+            const int kept = cut(sh.count);          // limit >= n: n entries stay
+            if ((int)threadIdx.x < kept) sh.buf[threadIdx.x] = sh.best[threadIdx.x];
+            if (threadIdx.x == 0) sh.count = kept;
+            __syncthreads();
+        }
+    }
+    // The list, and the sum with the list's exponentials in 64 bits; returns the
+    // list's length.
+    __device__ int finish(float2 *list, ChunkSum *to) {
+        const int lane = threadIdx.x & 31;
+        __syncthreads();
+        const int kept = cut(sh.count);
+        // rest of all threads, each to 2^-32 of the least term of the list, in whole
+        // numbers of two halves
+        const unsigned long long units = __float2ull_rn(rest * 0x1p32f);
+        const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)units & 0xffffffu);
+        const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(units >> 24));
+        if (lane == 0) atomicAdd(&sh.dropped, ((unsigned long long)hi << 24) + lo);
+        __syncthreads();
+        const float top = kept > 0 ? key_value(sh.best[0]) : -INFINITY;
+        if (threadIdx.x < 32) {
+            double sum = 0.0;
+            for (int e = lane; e <= kept; e += 32) { // entry `kept`: the rest, at its reference
+                const float x = e < kept ? key_value(sh.best[e]) : ref;
+                if (e < kept) list[e] = make_float2(x, __int_as_float((int)~(uint32_t)sh.best[e]));
+                if (e < kept || sh.dropped != 0)
+                    sum += exp((double)x - (double)top) * (e < kept ? 1.0 : (double)sh.dropped * 0x1p-32);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) *to = ChunkSum{(double)top, sum};
+        }
+        return kept;
+    }
+};
+
+// Fills a list of `kept` entries up to n with the first columns of [from, end) that
+// are -inf, and to a.n with none.  Warp 0.
+template <int DT>
+__device__ void fill_list(float2 *list, int kept, int n, int most, const uint8_t *row, int from, int end) {
+    const int lane = threadIdx.x & 31;
+    int have = kept;
+    for (int col = from; col < end && have < n; col += 32) {
+        const bool none = col + lane < end && cleaned(element<DT>(row, col + lane)) == -INFINITY;
+        const unsigned who = __ballot_sync(0xffffffffu, none);
+        const int place = have + __popc(who & ((1u << lane) - 1u));
+        if (none && place < n) list[place] = make_float2(-INFINITY, __int_as_float(col + lane));
+        have += __popc(who);
+    }
+    for (int e = n + lane; e < most; e += 32) list[e] = make_float2(-INFINITY, __uint_as_float(0xffffffffu));
+}
+
+__device__ __forceinline__ float max_of(const float (&x)[kElems]) {      // the larger of numbers
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < kElems; ++i) top = fmaxf(top, x[i]);
+    return top;
+}
+__device__ __forceinline__ float sum_of(const float (&x)[kElems]) {
+    float2 s = make_float2(x[0], x[1]);
+#pragma unroll
+    for (int i = 2; i < kElems; i += 2) s = add2(s, make_float2(x[i], x[i + 1]));
+    return s.x + s.y;
+}
+__device__ __forceinline__ void terms_of(const float (&x)[kElems], float ref, float (&e)[kElems]) {
+#pragma unroll
+    for (int i = 0; i < kElems; i += 2) {
+        const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+        e[i] = fast_exp2(y.x);
+        e[i + 1] = fast_exp2(y.y);
+    }
+}
+
+// Small calls: a CTA's chunk of U tiles in registers, its maxima first: the
+// threshold is then one that little more than n of its elements reach.
 template <int DT, int U>
 __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const SelectArgs a) {
-    __shared__ uint64_t buf[kKept + kTile];
-    __shared__ uint64_t best[128];
-    __shared__ uint32_t tops[kSelThreads];
-    __shared__ unsigned long long dropped;           // in units of 2^-32
-    __shared__ int count;
+    __shared__ Chosen shared;
     after_previous();
-    const int t = threadIdx.x, lane = t & 31;
+    const int t = threadIdx.x;
     const int row_id = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
     if (!beam_reads(a, row_id)) return;
     constexpr int kBytes = DT == PA_LOGITS_F32 ? 4 : 2;
     const uint8_t *row = static_cast<const uint8_t *>(a.logits) + (int64_t)row_id * a.stride * kBytes;
     const int skew = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
     const int from = c * (U * kTile), end = min(from + U * kTile, a.vocab);
-    const int n = min(a.n, end - from), limit = kept_limit(n);
-    if (t == 0) {
-        count = 0;
-        dropped = 0;
-    }
-
-    // Elements above thr are entries of the buffer; those at or below it are in
-    // `rest`, the sum of 2^((x - ref) log2 e) with ref = thr.
-    float thr = -INFINITY, ref = 0.f, rest = 0.f;
-    auto term = [&](float x) { return fast_exp2((x - ref) * kLog2e); };
-    auto raise = [&](float to) {                     // a new threshold, the same for the CTA
-        const float r = to == -INFINITY ? 0.f : to;
-        rest = rest > 0.f ? rest * fast_exp2((ref - r) * kLog2e) : 0.f;
-        thr = to;
-        ref = r;
-    };
-    // Cuts the buffer's m entries to the n largest, in order, in best; the n-th is
-    // the new threshold and the others go into rest: as whole multiples of 2^-32, so
-    // that their order in the buffer, which is chance, does not matter.  Every thread.
-    auto cut = [&](int m) {
-        uint32_t out = 0;
-        for (int e = t, i = 0; e < m; e += kSelThreads, ++i) {
-            const uint64_t k = buf[e];
-            int rank = 0;
-#pragma unroll 8
-            for (int j = 0; j < m; ++j) rank += buf[j] > k;
-            if (rank < n) best[rank] = k;
-            else out |= 1u << i;
-        }
-        __syncthreads();
-        if (m < n) return m;
-        raise(key_value(best[n - 1]));
-        if (out != 0) {
-            unsigned long long sum = 0;
-            for (int e = t, i = 0; e < m; e += kSelThreads, ++i)
-                if (out >> i & 1u) sum += (unsigned long long)__float2ull_rn(term(key_value(buf[e])) * 0x1p32f);
-            atomicAdd(&dropped, sum);
-        }
-        __syncthreads();
-        if (t == 0) {
-            rest += (float)dropped * 0x1p-32f;
-            dropped = 0;
-        }
-        return n;
-    };
-
-    // The whole chunk in registers, its maxima first: the threshold is then one that
-    // little more than n of its elements reach.
+    Chooser ch(shared, min(a.n, end - from));
     Columns<DT> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) raw[u].load(row, skew, from + u * kTile + t * kElems, end);
-    float tops_of[U], most = -INFINITY;              // fmaxf: the larger of numbers
+    float tops_of[U], most = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float x[kElems];
         raw[u].align(skew);
         raw[u].values(x);
-        tops_of[u] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kElems; ++i) tops_of[u] = fmaxf(tops_of[u], x[i]);
+        tops_of[u] = max_of(x);
         if (tops_of[u] == INFINITY) {
 #pragma unroll
             for (int i = 0; i < kElems; ++i) most = fmaxf(most, cleaned(x[i]));
@@ -280,98 +384,170 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const Select
             most = fmaxf(most, tops_of[u]);
         }
     }
-    const uint32_t least = block_floor(ordered(most), n, 16, tops);
-    // elements of that value are entries too
-    if (least > ordered(-INFINITY)) raise(value_below(least));
+    ch.start(most);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float x[kElems];
+        float x[kElems], e[kElems];
         const int col = from + u * kTile + t * kElems;
         raw[u].values(x);
-        const float top = tops_of[u];
         // Most warps have no element above the threshold: they add their terms and are
         // done.  (A maximum leaves NaN out, the sum of the terms does not; +inf is above
         // every threshold.)
         int last = 0;
-        float e[kElems];
-#pragma unroll
-        for (int i = 0; i < kElems; i += 2) {
-            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
-            e[i] = fast_exp2(y.x);
-            e[i + 1] = fast_exp2(y.y);
-        }
-        auto sum_up = [&]() {
-            float2 s = make_float2(e[0], e[1]);
-#pragma unroll
-            for (int i = 2; i < kElems; i += 2) s = add2(s, make_float2(e[i], e[i + 1]));
-            return s.x + s.y;
-        };
-        float terms = sum_up();
-        if (__any_sync(0xffffffffu, top > thr || !(terms < INFINITY))) {
+        terms_of(x, ch.ref, e);
+        float terms = sum_of(e);
+        if (__any_sync(0xffffffffu, tops_of[u] > ch.thr || !(terms < INFINITY))) {
             uint32_t above = 0;
 #pragma unroll
             for (int i = 0; i < kElems; ++i) {
                 const float v = cleaned(x[i]);
-                if (v > thr) above |= 1u << i;
+                if (v > ch.thr) above |= 1u << i;
                 // a term that is no number: its element is not one either
-                e[i] = v > thr || !(v > -INFINITY) ? 0.f : e[i];
+                e[i] = v > ch.thr || !(v > -INFINITY) ? 0.f : e[i];
             }
-            terms = sum_up();
+            terms = sum_of(e);
             while (above != 0u) {
                 const int i = __ffs(above) - 1;
                 above &= above - 1u;
                 float v = x[0];
 #pragma unroll
                 for (int q = 1; q < kElems; ++q) v = i == q ? x[q] : v;
-                last = atomicAdd(&count, 1);
-                buf[last] = key_of(v, col + i);
-                ++last;
+                last = ch.enter(v, col + i);
             }
         }
-        if (thr != -INFINITY) rest += terms;
-        if (__syncthreads_or(last > limit)) {
-            const int kept = cut(count);             // limit >= n: n entries stay
-            if (t < kept) buf[t] = best[t];
-            if (t == 0) count = kept;
-            __syncthreads();
-        }
+        if (ch.thr != -INFINITY) ch.rest += terms;
+        ch.settle(last);
     }
-    __syncthreads();
-    const int kept = cut(count);
-    // rest of all threads, each to 2^-32 of the least term of the list, in whole
-    // numbers of two halves
-    const unsigned long long units = __float2ull_rn(rest * 0x1p32f);
-    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)units & 0xffffffu);
-    const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(units >> 24));
-    if (lane == 0) atomicAdd(&dropped, ((unsigned long long)hi << 24) + lo);
-    __syncthreads();
-    // The list; its exponentials in 64 bits.
     const int64_t at = (int64_t)row_id * a.chunks + c;
     float2 *list = a.lists + at * a.n;
-    const float top = kept > 0 ? key_value(best[0]) : -INFINITY;
-    if (t < 32) {
-        double sum = 0.0;
-        for (int e = lane; e <= kept; e += 32) {     // entry `kept`: the rest, at its reference
-            const float x = e < kept ? key_value(best[e]) : ref;
-            if (e < kept) list[e] = make_float2(x, __int_as_float((int)~(uint32_t)best[e]));
-            if (e < kept || dropped != 0) sum += exp((double)x - (double)top) * (e < kept ? 1.0 : (double)dropped * 0x1p-32);
-        }
+    const int kept = ch.finish(list, a.sums + at);
+    if (kept < a.n && t < 32) fill_list<DT>(list, kept, ch.n, a.n, row, from, end);
+}
+
+// Large calls, first pass: of every thread's kBlockTiles x 8 columns their maximum
+// and the sum of exp(x - maximum), nothing else, so that the logits stream through.
+constexpr int kBlockTiles = 4;
+constexpr int kSpan = kBlockTiles * kTile;           // columns of a CTA
+
+template <int DT>
+__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs a) {
+    after_previous();
+    const int t = threadIdx.x;
+    const int row_id = blockIdx.x / a.spans, c = blockIdx.x % a.spans;
+    if (a.finished != nullptr && !beam_reads(a, row_id)) return;
+    constexpr int kBytes = DT == PA_LOGITS_F32 ? 4 : 2;
+    const uint8_t *row = static_cast<const uint8_t *>(a.logits) + (int64_t)row_id * a.stride * kBytes;
+    const int skew = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
+    const int from = c * kSpan + t * kElems;
+    Columns<DT> raw[kBlockTiles];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) a.sums[at] = ChunkSum{(double)top, sum};
+    for (int u = 0; u < kBlockTiles; ++u) raw[u].load(row, skew, from + u * kTile, a.vocab);
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kBlockTiles; ++u) {
+        float x[kElems];
+        raw[u].align(skew);
+        raw[u].values(x);
+        top = fmaxf(top, max_of(x));
     }
-    // Fewer finite logits than n: the first columns of the others.
-    if (kept < a.n && t < 32) {
-        int have = kept;
-        for (int col = from; col < end && have < n; col += 32) {
-            const bool none = col + lane < end && cleaned(element<DT>(row, col + lane)) == -INFINITY;
-            const unsigned who = __ballot_sync(0xffffffffu, none);
-            const int place = have + __popc(who & ((1u << lane) - 1u));
-            if (none && place < n) list[place] = make_float2(-INFINITY, __int_as_float(col + lane));
-            have += __popc(who);
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < kBlockTiles; ++u) {
+        float x[kElems], e[kElems];
+        raw[u].values(x);
+        terms_of(x, top, e);
+        sum += sum_of(e);
+    }
+    if (!(sum < INFINITY)) {                         // NaN or +inf among them, or nothing but -inf
+        top = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < kBlockTiles; ++u) {
+            float x[kElems];
+            raw[u].values(x);
+#pragma unroll
+            for (int i = 0; i < kElems; ++i) top = fmaxf(top, cleaned(x[i]));
         }
-        for (int e = n + lane; e < a.n; e += 32) list[e] = make_float2(-INFINITY, __uint_as_float(0xffffffffu));
+        if (top > -INFINITY) {
+#pragma unroll
+            for (int u = 0; u < kBlockTiles; ++u) {
+                float x[kElems];
+                raw[u].values(x);
+#pragma unroll
+                for (int i = 0; i < kElems; ++i) sum += fast_exp2((cleaned(x[i]) - top) * kLog2e);
+            }
+        }
     }
+    a.blocks[((int64_t)row_id * a.spans + c) * kSelThreads + t] = make_float2(top, sum);
+}
+
+// Second pass, a CTA per row: the n-th largest of the threads' maxima over the
+// blocks is the threshold; only blocks that reach it (little more than n) are read
+// again, of the others their sums count.  Blocks are listed in their order, so that
+// the sums do not depend on chance.
+constexpr int kListed = 1024;
+
+template <int DT>
+__global__ void __launch_bounds__(kSelThreads) select_rows_kernel(const SelectArgs a) {
+    __shared__ Chosen shared;
+    __shared__ int list_of[kListed], warp_count[kSelWarps];
+    after_previous();
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row_id = blockIdx.x;
+    if (!beam_reads(a, row_id)) return;
+    constexpr int kBytes = DT == PA_LOGITS_F32 ? 4 : 2;
+    const uint8_t *row = static_cast<const uint8_t *>(a.logits) + (int64_t)row_id * a.stride * kBytes;
+    const float2 *blocks = a.blocks + (int64_t)row_id * a.spans * kSelThreads;
+    Chooser ch(shared, a.n);
+    float most = -INFINITY;
+#pragma unroll 8
+    for (int c = 0; c < a.spans; ++c) most = fmaxf(most, blocks[c * kSelThreads + t].x);
+    ch.start(most);
+    for (int c = 0; c < a.spans;) {
+        int listed = 0;                              // the same for the CTA
+        for (; c < a.spans && listed + kSelThreads <= kListed; ++c) {
+            const float2 b = blocks[c * kSelThreads + t];
+            const bool again = b.x > ch.thr;
+            if (!again && b.y > 0.f) ch.rest += b.y * ch.term(b.x);
+            const unsigned who = __ballot_sync(0xffffffffu, again);
+            if (__syncthreads_or(again) == 0) continue;
+            if (lane == 0) warp_count[warp] = __popc(who);
+            __syncthreads();
+            int at = listed + __popc(who & ((1u << lane) - 1u));
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w) {
+                if (w < warp) at += warp_count[w];
+                listed += warp_count[w];
+            }
+            if (again) list_of[at] = c * kSelThreads + t;
+        }
+        __syncthreads();
+        // 32 blocks a batch, 8 threads a block, a thread 4 x 1 columns
+        for (int base = 0; base < listed; base += 32) {
+            const int mine = base + (t >> 3);
+            int last = 0;
+            if (mine < listed) {
+                const int id = list_of[mine];
+                const float2 b = blocks[id];
+                if (b.x > ch.thr) {
+                    const int col0 = id / kSelThreads * kSpan + id % kSelThreads * kElems + (t & 7);
+#pragma unroll
+                    for (int u = 0; u < kBlockTiles; ++u) {
+                        const int col = col0 + u * kTile;
+                        const float v = col < a.vocab ? cleaned(element<DT>(row, col)) : -INFINITY;
+                        if (v > ch.thr) last = ch.enter(v, col);
+                        else if (v > -INFINITY) ch.rest += ch.term(v);
+                    }
+                } else if ((t & 7) == 0) {           // the threshold has passed it since
+                    ch.rest += b.y * ch.term(b.x);
+                }
+            }
+            ch.settle(last);
+        }
+        __syncthreads();
+    }
+    float2 *list = a.lists + (int64_t)row_id * a.n;
+    const int kept = ch.finish(list, a.sums + row_id);
+    if (kept < a.n && t < 32) fill_list<DT>(list, kept, ch.n, a.n, row, 0, a.vocab);
 }
 
 // One CTA per group: lse of its beams, the totals of the lists' entries, the n
@@ -630,25 +806,35 @@ __global__ void __launch_bounds__(kColumns) reorder_rows_kernel(const pa_beam_re
 }
 
 constexpr int kMostTiles = 4;     // tiles of a chunk where there are CTAs enough
+constexpr int kSmallTiles = 3000; // tiles of a call whose chunks are not worth a pass of their own
 
 template <int DT>
-cudaError_t launch_chunks(const SelectArgs &a, int tiles, cudaStream_t stream) {
-    return launch_after(tiles == 1 ? select_chunks_kernel<DT, 1> : select_chunks_kernel<DT, kMostTiles>,
-                        (unsigned)(a.groups * a.beams * a.chunks), kSelThreads, 0, stream, a);
+cudaError_t launch_lists(const SelectArgs &a, int tiles, cudaStream_t stream) {
+    const unsigned rows = (unsigned)(a.groups * a.beams);
+    if (tiles > 0)
+        return launch_after(tiles == 1 ? select_chunks_kernel<DT, 1> : select_chunks_kernel<DT, kMostTiles>, rows * a.chunks,
+                            kSelThreads, 0, stream, a);
+    const cudaError_t e = launch_after(select_blocks_kernel<DT>, rows * a.spans, kSelThreads, 0, stream, a);
+    return e != cudaSuccess ? e : launch_after(select_rows_kernel<DT>, rows, kSelThreads, 0, stream, a);
 }
+
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-// A chunk is kMostTiles tiles, or one while the GPU holds all CTAs at once (a
-// constant number: the workspace's size is the same on every device).
+// Calls of up to kSmallTiles tiles: a list per chunk of kMostTiles tiles, or of one
+// while the GPU holds all CTAs at once; larger ones: a list per row by two passes.
+// (Constant numbers: the workspace's size is the same on every device.)
 SelectPlan plan_select(const pa_beam_select_params &p) {
     SelectPlan plan{};
     const int64_t rows = (int64_t)p.num_groups * p.beams, tiles = ((int64_t)p.vocab + kTile - 1) / kTile;
-    plan.tiles = rows * tiles <= 152 * 4 ? 1 : kMostTiles;
-    plan.chunks = (int32_t)((tiles + plan.tiles - 1) / plan.tiles);
-    plan.list_bytes = (size_t)rows * plan.chunks * p.num_out * sizeof(float2);
-    plan.list_bytes = (plan.list_bytes + 15) / 16 * 16;
-    plan.workspace_bytes = plan.list_bytes + (size_t)rows * plan.chunks * sizeof(ChunkSum);
+    plan.tiles = rows * tiles <= 152 * 4 ? 1 : rows * tiles <= kSmallTiles ? kMostTiles : 0;
+    plan.chunks = plan.tiles > 0 ? (int32_t)((tiles + plan.tiles - 1) / plan.tiles) : 1;
+    plan.spans = (int32_t)((tiles + kBlockTiles - 1) / kBlockTiles);
+    plan.list_bytes = round16((size_t)rows * plan.chunks * p.num_out * sizeof(float2));
+    plan.sum_bytes = round16((size_t)rows * plan.chunks * sizeof(ChunkSum));
+    plan.workspace_bytes = plan.list_bytes + plan.sum_bytes;
+    if (plan.tiles == 0) plan.workspace_bytes += (size_t)rows * plan.spans * kSelThreads * sizeof(float2);
     return plan;
 }
 
@@ -664,14 +850,17 @@ cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan
     a.vocab = p.vocab;
     a.n = p.num_out;
     a.chunks = plan.chunks;
-    a.lists = static_cast<float2 *>(p.workspace);
-    a.sums = reinterpret_cast<ChunkSum *>(static_cast<uint8_t *>(p.workspace) + plan.list_bytes);
+    a.spans = plan.spans;
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    a.lists = reinterpret_cast<float2 *>(ws);
+    a.sums = reinterpret_cast<ChunkSum *>(ws + plan.list_bytes);
+    a.blocks = reinterpret_cast<float2 *>(ws + plan.list_bytes + plan.sum_bytes);
     a.out_scores = p.out_scores;
     a.out_parents = p.out_parents;
     a.out_tokens = p.out_tokens;
-    const cudaError_t e = p.logits_dtype == PA_LOGITS_F32   ? launch_chunks<PA_LOGITS_F32>(a, plan.tiles, stream)
-                          : p.logits_dtype == PA_LOGITS_F16 ? launch_chunks<PA_LOGITS_F16>(a, plan.tiles, stream)
-                                                            : launch_chunks<PA_LOGITS_BF16>(a, plan.tiles, stream);
+    const cudaError_t e = p.logits_dtype == PA_LOGITS_F32   ? launch_lists<PA_LOGITS_F32>(a, plan.tiles, stream)
+                          : p.logits_dtype == PA_LOGITS_F16 ? launch_lists<PA_LOGITS_F16>(a, plan.tiles, stream)
+                                                            : launch_lists<PA_LOGITS_BF16>(a, plan.tiles, stream);
     if (e != cudaSuccess) return e;
     return launch_after(select_merge_kernel, (unsigned)p.num_groups, kSelThreads, 0, stream, a);
 }

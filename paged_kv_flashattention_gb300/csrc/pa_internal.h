@@ -91,8 +91,9 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
 
 // Beam search (beam.cu).
 struct SelectPlan {
-    int32_t tiles, chunks;        // tiles of a chunk, chunks of a row
-    size_t list_bytes;
+    int32_t tiles;                // of a chunk; 0: two passes
+    int32_t chunks, spans;        // lists of a row, CTAs of a row in the first pass
+    size_t list_bytes, sum_bytes;
     size_t workspace_bytes;
 };
 SelectPlan plan_select(const pa_beam_select_params &p);
