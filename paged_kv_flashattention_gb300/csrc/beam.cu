@@ -25,8 +25,8 @@
 //
 // Reordering.  Rows of the partly filled last pages are one contiguous run of a
 // page, copied into the child's spare page first (CTAs of one sequence and a few
-// pools each); a second launch permutes the token-table rows and histories, a
-// thread per column, which holds the column's values of all beams.
+// pools each); a second launch, beside it, permutes the token-table rows and
+// histories, a thread per column, which holds the column's values of all beams.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -490,7 +490,7 @@ constexpr int kListed = 1024;
 template <int DT>
 __global__ void __launch_bounds__(kSelThreads) select_rows_kernel(const SelectArgs a) {
     __shared__ Chosen shared;
-    __shared__ int list_of[kListed], warp_count[kSelWarps];
+    __shared__ int list_of[kListed], found[kListed], warp_count[kSelWarps], total;
     after_previous();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row_id = blockIdx.x;
     if (!beam_reads(a, row_id)) return;
@@ -502,40 +502,23 @@ __global__ void __launch_bounds__(kSelThreads) select_rows_kernel(const SelectAr
 #pragma unroll 8
     for (int c = 0; c < a.spans; ++c) most = fmaxf(most, blocks[c * kSelThreads + t].x);
     ch.start(most);
-    for (int c = 0; c < a.spans;) {
-        int listed = 0;                              // the same for the CTA
-        for (; c < a.spans && listed + kSelThreads <= kListed; ++c) {
-            const float2 b = blocks[c * kSelThreads + t];
-            const bool again = b.x > ch.thr;
-            if (!again && b.y > 0.f) ch.rest += b.y * ch.term(b.x);
-            const unsigned who = __ballot_sync(0xffffffffu, again);
-            if (__syncthreads_or(again) == 0) continue;
-            if (lane == 0) warp_count[warp] = __popc(who);
-            __syncthreads();
-            int at = listed + __popc(who & ((1u << lane) - 1u));
-#pragma unroll
-            for (int w = 0; w < kSelWarps; ++w) {
-                if (w < warp) at += warp_count[w];
-                listed += warp_count[w];
-            }
-            if (again) list_of[at] = c * kSelThreads + t;
-        }
-        __syncthreads();
-        // 32 blocks a batch, 8 threads a block, a thread 4 x 1 columns
+    auto read_again = [&](int listed) {              // 32 blocks a batch, 8 threads a block, a thread 4 x 1 columns
         for (int base = 0; base < listed; base += 32) {
             const int mine = base + (t >> 3);
             int last = 0;
             if (mine < listed) {
                 const int id = list_of[mine];
+                const int col0 = id / kSelThreads * kSpan + id % kSelThreads * kElems + (t & 7);
+                float v[kBlockTiles];
+#pragma unroll
+                for (int u = 0; u < kBlockTiles; ++u)
+                    v[u] = col0 + u * kTile < a.vocab ? cleaned(element<DT>(row, col0 + u * kTile)) : -INFINITY;
                 const float2 b = blocks[id];
                 if (b.x > ch.thr) {
-                    const int col0 = id / kSelThreads * kSpan + id % kSelThreads * kElems + (t & 7);
 #pragma unroll
                     for (int u = 0; u < kBlockTiles; ++u) {
-                        const int col = col0 + u * kTile;
-                        const float v = col < a.vocab ? cleaned(element<DT>(row, col)) : -INFINITY;
-                        if (v > ch.thr) last = ch.enter(v, col);
-                        else if (v > -INFINITY) ch.rest += ch.term(v);
+                        if (v[u] > ch.thr) last = ch.enter(v[u], col0 + u * kTile);
+                        else if (v[u] > -INFINITY) ch.rest += ch.term(v[u]);
                     }
                 } else if ((t & 7) == 0) {           // the threshold has passed it since
                     ch.rest += b.y * ch.term(b.x);
@@ -543,7 +526,47 @@ __global__ void __launch_bounds__(kSelThreads) select_rows_kernel(const SelectAr
             }
             ch.settle(last);
         }
+    };
+    if (t == 0) total = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int c = 0; c < a.spans; ++c) {
+        const float2 b = blocks[c * kSelThreads + t];
+        if (b.x > ch.thr) {
+            const int at = atomicAdd(&total, 1);
+            if (at < kListed) found[at] = c * kSelThreads + t;
+        } else if (b.y > 0.f) {
+            ch.rest += b.y * ch.term(b.x);
+        }
+    }
+    __syncthreads();
+    if (total <= kListed) {                          // in the order of their numbers
+        const int m = total;
+        for (int e = t; e < m; e += kSelThreads) {
+            const int id = found[e];
+            int rank = 0;
+            for (int i = 0; i < m; ++i) rank += found[i] < id;
+            list_of[rank] = id;
+        }
         __syncthreads();
+        read_again(m);
+    } else {                                         // rows of equal logits: kSelThreads blocks at a time
+        const float first = ch.thr;
+        for (int c = 0; c < a.spans; ++c) {
+            const bool again = blocks[c * kSelThreads + t].x > first;
+            const unsigned who = __ballot_sync(0xffffffffu, again);
+            if (lane == 0) warp_count[warp] = __popc(who);
+            __syncthreads();
+            int at = __popc(who & ((1u << lane) - 1u)), listed = 0;
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w) {
+                if (w < warp) at += warp_count[w];
+                listed += warp_count[w];
+            }
+            if (again) list_of[at] = c * kSelThreads + t;
+            __syncthreads();
+            read_again(listed);
+        }
     }
     float2 *list = a.lists + (int64_t)row_id * a.n;
     const int kept = ch.finish(list, a.sums + row_id);
@@ -588,7 +611,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (top > -INFINITY)
-                for (int c = lane; c < S; c += 32) sum += cs[c].sum * exp(cs[c].top - top);
+                for (int c = lane; c < S; c += 32) sum += cs[c].sum * (cs[c].top == top ? 1.0 : exp(cs[c].top - top));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             l = top + log(sum);                      // (no finite logit: not used)
@@ -650,7 +673,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
             if (e < entries) v[i] = entry(e, at[i]);
             top = max(top, (uint32_t)(v[i] >> 32));
         }
-        if (e0 == 0) least = block_floor(top, n, 12, tops);
+        if (e0 == 0 && entries > 128) least = block_floor(top, n, 12, tops);
         int last = 0;
 #pragma unroll
         for (int i = 0; i < kRound / kSelThreads; ++i) {
@@ -732,7 +755,10 @@ __global__ void __launch_bounds__(kCopyThreads) reorder_copy_kernel(const __grid
     if (q == i) return;
     const int32_t slot = p.token_table[p.table_idx[(int64_t)g * p.beams + q] * p.token_table_stride + L - 1];
     const int32_t src = slot >= 0 ? slot / p.page_size : -1, dst = p.spare_pages[seq];
-    if (src < 0 || src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
+    // Every thread has read what the next launch overwrites: it may start beside the copies.
+    const bool bad = __syncthreads_or(src < 0 || src >= p.num_pages || dst < 0 || dst >= p.num_pages);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (bad) {
         if (threadIdx.x == 0) raise_error(PA_DEVERR_PAGE_RANGE);
         return;
     }
@@ -759,11 +785,10 @@ constexpr int kColumns = 128;                        // columns of a CTA, a mult
 
 // CTA (group, block of columns): first the token table's blocks, then the
 // histories'.  The CTA of a group's last slots also turns the spare pages over.
-__global__ void __launch_bounds__(kColumns) reorder_rows_kernel(const pa_beam_reorder_params p, int table_blocks, int blocks) {
+__device__ __forceinline__ void reorder_rows(const pa_beam_reorder_params &p, int table_blocks, int blocks) {
     extern __shared__ int32_t vals[];                // [beams][kColumns], each thread its own column
     __shared__ int parents[64], spares[64], firsts[64];
     __shared__ int64_t rows[64];                     // a row's first cell, -1 outside the table
-    after_previous();
     const int g = blockIdx.x / blocks, block = blockIdx.x % blocks, t = threadIdx.x;
     const int64_t base = (int64_t)g * p.beams;
     const bool table = block < table_blocks;
@@ -803,6 +828,16 @@ __global__ void __launch_bounds__(kColumns) reorder_rows_kernel(const pa_beam_re
             *cell = vals[q * kColumns + t];
         }
     }
+}
+
+// after_copies: the launch before is the copies', which has waited for all before it
+// and let this one start once its CTAs had read the table and the spare pages.  The
+// last CTA ends after the copies, and with it the grid.
+__global__ void __launch_bounds__(kColumns) reorder_rows_kernel(const pa_beam_reorder_params p, int table_blocks, int blocks,
+                                                                bool after_copies) {
+    if (!after_copies) after_previous();
+    reorder_rows(p, table_blocks, blocks);
+    if (after_copies && blockIdx.x == gridDim.x - 1) after_previous();
 }
 
 constexpr int kMostTiles = 4;     // tiles of a chunk where there are CTAs enough
@@ -867,7 +902,8 @@ cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan
 
 cudaError_t launch_reorder(const pa_beam_reorder_params &p, cudaStream_t stream) {
     const int seqs = p.num_groups * p.beams;
-    if (p.page_size > 1 && p.num_pools > 0) {
+    const bool copies = p.page_size > 1 && p.num_pools > 0;
+    if (copies) {
         ReorderArgs a{};
         a.p = p;
         for (int k = 0; k < p.num_pools; ++k) a.pools[k] = p.pools[k];
@@ -883,7 +919,7 @@ cudaError_t launch_reorder(const pa_beam_reorder_params &p, cudaStream_t stream)
     pa_beam_reorder_params q = p;
     if (q.history == nullptr) q.history_len = 0;
     return launch_after(reorder_rows_kernel, (unsigned)((int64_t)p.num_groups * blocks), kColumns,
-                        (size_t)p.beams * kColumns * sizeof(int32_t), stream, q, table_blocks, blocks);
+                        (size_t)p.beams * kColumns * sizeof(int32_t), stream, q, table_blocks, blocks, copies);
 }
 
 }  // namespace pa
