@@ -244,6 +244,7 @@ cudaError_t launch_decode_t(const DecodeArgs &a, int64_t items_max, cudaStream_t
         last.store(key | (uint64_t)per_sm, std::memory_order_relaxed);
     }
     int64_t grid = (int64_t)num_sms() * per_sm;
+    if (a.first_keys != nullptr) grid *= 2;          // beside the prefixes' kernel, as SMs become free
     if (a.max_ctas > 0 && grid > a.max_ctas) grid = a.max_ctas;
     if (grid > items_max) grid = items_max;
     if (a.overlap_previous) {

@@ -11,12 +11,13 @@
 // The prefix is a matrix product again: the rows that read KV head kvh of a
 // group are (sequence, query head of kvh), n * Hq / Hkv of them, so prefill's
 // tcgen05 kernel does it (prefill_impl.cuh, SHARED) with tiles of 128 such rows,
-// two tiles per CTA (over FP8 and 4-bit pools one); where a group fills only one, the tile's key steps go in turn
-// to two softmax halves, and where it fills half or less of one, its rows lie in
-// the tile two or four times, each copy for a share of the keys.  Query rows come in tensor-map boxes of 32 (64 columns, Hq / Hkv
-// heads, 32 Hkv / Hq sequences).
+// two tiles per CTA (over FP8 and 4-bit pools one); where a group fills only one,
+// the tile's key steps go in turn to two softmax halves, each with partials of its
+// own.  Query rows come in tensor-map boxes of 32 (64 columns, Hq / Hkv heads,
+// 32 Hkv / Hq sequences).
 // Every CTA gets the same number of 128-key steps, whatever the groups are; the
 // partials are written in 32 bits, a block of 8 warps' 32 rows for each work item.
+// The decode of the other keys runs beside it, on the SMs it leaves (shared_ctas).
 #include "prefill_impl.cuh"
 
 #include <atomic>
@@ -123,9 +124,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     const int g = a.sh.header != nullptr ? group_of(a.sh, b, lane) : -1;
     bool ok = L >= 0 && L <= a.max_seqlen_k && P >= 0 && P <= L && P <= a.sh.max_prefix;
     int np = 0, ns = 0;                              // partials of the prefix, of the keys behind it
-    // Partial s of the prefix: range s / each, copy s % each (of a single tile: two
-    // halves of its copies), at row `first` of lse_part and o_part for s = 0.
-    int each = 1, apart = 0;                         // partials of a range, rows between its copies'
+    // Partial s of the prefix: range s / each, half s % each (of a single tile), at row
+    // `first` of lse_part and o_part for s = 0.
+    int each = 1, apart = 0;                         // partials of a range, rows between them
     int64_t first = 0;
     if (ok && P > 0) {
         ok = g >= 0 && g < a.sh.num_groups;          // else a prefix without a group
@@ -135,13 +136,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
             ok = q0 >= 0 && n <= a.sh.max_group && a.sh.prefix_lens[q0] == P;
             const int tiles = (n * group + a.item_rows - 1) / a.item_rows, steps = (P + kBN - 1) / kBN;
             const int in_group = (b - q0) * group + h % group, tile = in_group / a.item_rows, m = in_group % a.item_rows;
-            const int row = (h / group) * tiles + tile, start = base.x + row * steps;
+            const int row = (h / group) * tiles + tile, start = base.x + row * (steps + kItemSteps) + kItemSteps;
             const int rows = min(n * group - tile * a.item_rows, a.item_rows);
             const int c0 = start / per, block = c0 + base.y + row;
             const int ranges = min((start + steps - 1) / per - c0 + 1, a.sh.max_blocks - block);
-            if (rows <= kBM) {
-                each = 2 * shared_copies(rows);
-                apart = 8 / each * 32;
+            if (rows <= kBM) {                       // two halves, the second in the upper lanes where they are free
+                each = 2;
+                apart = rows <= kBM / 2 ? kBM + kBM / 2 : kBM;
             }
             if (ok) np = max(ranges, 0) * each;
             first = (int64_t)block * kBlockRows + m;
@@ -270,12 +271,38 @@ int64_t most_steps(const pa_decode_shared_params &p) {
     const int64_t group = p.dec.num_q_heads / p.dec.num_kv_heads;
     const int64_t per = item_rows(p.dec.kv_dtype), tiles = ((int64_t)p.max_group * group + per - 1) / per;
     const int64_t steps = ((int64_t)p.max_prefix + kBN - 1) / kBN;
-    return p.num_groups * tiles * steps * p.dec.num_kv_heads;
+    return p.num_groups * tiles * (steps + kItemSteps) * p.dec.num_kv_heads;
 }
 
-unsigned prefix_ctas(const pa_decode_shared_params &p) {
+int most_ctas(const pa_decode_shared_params &p) {
     const int64_t steps = most_steps(p), sms = num_sms();
-    return (unsigned)(steps < sms ? steps : sms);
+    return (int)(steps < sms ? steps : sms);
+}
+
+// Measured, of a step: 3200 clocks for two tiles of head size 128, 5000 where rows are
+// gathered one by one, 1260 over FP8 at 64, 1950 over 4 bits at 128.  The split-KV
+// decode reads 38 GB/s an SM.
+void set_costs(SharedArgs &sh, const pa_decode_shared_params &p) {
+    const pa_decode_params &d = p.dec;
+    const float bytes = d.kv_dtype == PA_KV_BF16 ? 4.f : d.kv_dtype == PA_KV_FP4 ? 1.125f : 2.f;     // of an element, K and V
+    sh.sms = num_sms();
+    sh.step_ns = d.page_size == 1 ? 2600.f : d.kv_dtype == PA_KV_BF16 ? 1700.f : d.kv_dtype == PA_KV_FP4 ? 1000.f : 700.f;
+    sh.key_ns = bytes * (float)(d.head_dim * d.num_kv_heads) / 38.f;
+}
+
+// The prefix kernel's grid beside a tail: at least 3/4 of the SMs, and what is best for
+// the call's bounds.  The kernel may leave more of them (shared_ctas), 4 us later.
+unsigned prefix_ctas(const pa_decode_shared_params &p, const SharedArgs &sh) {
+    const int all = most_ctas(p);
+    if (p.max_suffix == 0 || all < sh.sms) return (unsigned)all;
+    const float steps = (float)most_steps(p) * sh.step_ns;
+    const float rest = shared_rest(sh, (float)p.dec.num_seqs * (float)p.max_suffix, p.dec.num_kv_heads);
+    int best = all;
+    for (int i = 31; i >= 24; --i) {
+        const int n = all * i / 32;
+        if (shared_time(steps, rest, n, sh.sms) < shared_time(steps, rest, best, sh.sms)) best = n;
+    }
+    return (unsigned)best;
 }
 
 }  // namespace
@@ -299,7 +326,7 @@ SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
         const int64_t per = item_rows(p.dec.kv_dtype);
         const int64_t whole = (int64_t)p.dec.num_seqs * group / per + p.num_groups;
         const int64_t bound = p.num_groups * (((int64_t)p.max_group * group + per - 1) / per);
-        plan.max_blocks = (int32_t)(prefix_ctas(p) + (whole < bound ? whole : bound) * p.dec.num_kv_heads);
+        plan.max_blocks = (int32_t)(most_ctas(p) + (whole < bound ? whole : bound) * p.dec.num_kv_heads);
         const size_t rows = (size_t)plan.max_blocks * kBlockRows;
         plan.prefix_bytes = 256 + 256 + round256((size_t)p.num_groups * sizeof(int2)) + rows * p.dec.head_dim * sizeof(float) +
                             rows * sizeof(float);
@@ -330,6 +357,11 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
     m.sh.max_group = p.max_group;
     m.sh.max_prefix = plan.prefix ? p.max_prefix : 0;
     m.sh.max_blocks = plan.max_blocks;
+    set_costs(m.sh, p);
+    if (plan.tail) {
+        m.sh.cache_seqlens = d.cache_seqlens;
+        m.sh.max_suffix = p.max_suffix;
+    }
     // (the partials are stored 32 bytes at a time)
     uint8_t *ws = reinterpret_cast<uint8_t *>(round256(reinterpret_cast<uintptr_t>(d.workspace)));
     if (plan.prefix) {
@@ -366,7 +398,7 @@ cudaError_t launch_decode_shared(const pa_decode_shared_params &p, const SharedP
         a.k_scale = d.k_scale;
         a.v_scale = d.v_scale;
         a.sh = m.sh;
-        const unsigned ctas = prefix_ctas(p);
+        const unsigned ctas = prefix_ctas(p, m.sh);
         const cudaError_t e = d.kv_dtype == PA_KV_FP4        ? launch_prefix<PA_KV_FP4>(a, d.head_dim, ctas, stream)
                               : d.kv_dtype == PA_KV_FP8_E4M3 ? launch_prefix<PA_KV_FP8_E4M3>(a, d.head_dim, ctas, stream)
                                                              : launch_prefix<PA_KV_BF16>(a, d.head_dim, ctas, stream);

@@ -600,7 +600,7 @@ static pa_status check_shared(const pa_decode_shared_params *p) {
     // the prefix kernel counts the 128-key steps of all work items in 32 bits
     const int64_t rows = (int64_t)p->max_group * (p->dec.num_q_heads / p->dec.num_kv_heads);
     const int64_t items = p->num_groups * ((rows + 127) / 128) * p->dec.num_kv_heads;
-    if (items * (((int64_t)p->max_prefix + 127) / 128) > INT32_MAX)
+    if (items * (((int64_t)p->max_prefix + 127) / 128 + 4) > INT32_MAX)
         return fail(PA_ERR_UNSUPPORTED, "%d groups of up to %d sequences over prefixes of up to %d keys exceed 2^31 - 1 steps in one call",
                     p->num_groups, p->max_group, p->max_prefix);
     return PA_OK;

@@ -121,6 +121,11 @@ struct SharedArgs {
     float *lse_part;              // [max_blocks][8][32]
     int32_t *header;              // [0]: steps of a CTA's range
     int2 *base;                   // [num_groups]: steps and rows of the list before each group
+    const int32_t *cache_seqlens;     // null: no keys behind the prefixes
+    int32_t max_suffix;
+    int32_t sms;
+    float step_ns;                // about what a CTA takes for a step,
+    float key_ns;                 // and an SM for a key behind the prefixes, all KV heads of it
 };
 
 struct PrefillArgs {
@@ -328,6 +333,36 @@ __device__ void prefill_sched_done(const PrefillArgs &a, int num_ctas) {
 // An item gives a block of partials (O, lse), numbered by its range plus its row:
 // of two items that follow one another the second has one of the two, or both, one
 // higher.
+//
+// A row counts kItemSteps more than its steps: what it takes to load the queries,
+// start and drain the pipeline and write the partials.  Sixteen groups of 8 over
+// prefixes of 512 to 8192 keys: the busiest CTA 1.36 of the mean without it.
+constexpr int kItemSteps = 4;
+
+// The decode of the keys behind the prefixes starts where this kernel leaves SMs, so
+// the list goes to n of the G SMs and the other CTAs end at once (64 sequences behind
+// 8192 keys: 57 us with the list on every SM, 53 on 32 of them; sixteen groups of 8
+// over FP8 48 and 40 on 118).  About the time of both, for a list of p ns and a rest
+// of t: the longer of the two beside each other, or with n = G one behind the other.
+constexpr float kSharedStart = 8000.f, kTailStart = 7000.f;      // ns before a CTA's first step; a CTA of few keys
+__host__ __device__ inline float shared_time(float p, float t, int n, int G) {
+    return n < G ? fmaxf(p / (float)n + kSharedStart, t / (float)(G - n)) : (p + t) / (float)G + kSharedStart + kTailStart;
+}
+// t for `keys` behind the prefixes: their bytes, and what CTAs of 64 keys take beyond
+// them, eight heads each and two on an SM.
+__host__ __device__ inline float shared_rest(const SharedArgs &sh, float keys, int num_kv_heads) {
+    return keys * sh.key_ns + fminf((float)sh.sms, keys * (float)num_kv_heads * (1.f / 1024)) * kTailStart;
+}
+// n of this call's lengths, of at most the grid: a lane for each 32nd of the SMs.
+__device__ __forceinline__ int shared_ctas(const PrefillArgs &a, int steps, float keys, int lane) {
+    if (keys == 0.f) return gridDim.x;
+    const int G = a.sh.sms, n = max(1, min((lane + 1) * G / 32, (int)gridDim.x));
+    const float ns = shared_time((float)steps * a.sh.step_ns, shared_rest(a.sh, keys, a.num_kv_heads), n, G);
+    // the least, and of the same the most CTAs
+    const unsigned best = __reduce_min_sync(0xffffffffu, ((unsigned)fminf(ns * 0.1f, 1e8f) << 5) | (31 - lane));
+    return __shfl_sync(0xffffffffu, n, 31 - (int)(best & 31));
+}
+
 struct SharedGroup {
     int q0, n, P;                 // first sequence, sequences, keys
 };
@@ -357,7 +392,9 @@ __device__ __forceinline__ int shared_tiles(const PrefillArgs &a, int n) {
     return (n * (a.num_q_heads / a.num_kv_heads) + T * kBM - 1) / (T * kBM);
 }
 
-// Rows of the list of a group, steps of its prefix.
+__device__ __forceinline__ int shared_row_steps(int P) { return (P + kBN - 1) / kBN + kItemSteps; }
+
+// Rows of the list of a group.
 template <int T>
 __device__ __forceinline__ int shared_rows(const PrefillArgs &a, const SharedGroup &r) {
     return r.P > 0 ? shared_tiles<T>(a, r.n) * a.num_kv_heads : 0;
@@ -376,20 +413,25 @@ struct SharedWalk {
         if (at >= end) return false;
         const int group = a.num_q_heads / a.num_kv_heads;
         for (;;) {
-            const int steps = (now.P + kBN - 1) / kBN, tiles = shared_tiles<T>(a, now.n);
-            const int cost = steps * tiles * a.num_kv_heads;
+            const int length = shared_row_steps(now.P), tiles = shared_tiles<T>(a, now.n);
+            const int cost = now.P > 0 ? length * tiles * a.num_kv_heads : 0;
             if (at < before + cost) {
-                const int row = (at - before) / steps;
+                const int row = (at - before) / length;
+                const int from = at - before - row * length, to = min(length, from + (end - at));
+                at += to - from;
+                if (to <= kItemSteps) {                  // the range ends before the row's first step
+                    if (at >= end) return false;
+                    continue;
+                }
                 const int tile = row % tiles;
                 it.b = now.q0;
                 it.kvh = row / tiles;
                 it.q0 = now.q0 + tile * (T * kBM / group);
                 it.rows = min(T * kBM, now.n * group - tile * T * kBM);
-                it.j0 = at - before - row * steps;
-                it.n_kv = min(steps - it.j0, end - at);
+                it.j0 = max(from - kItemSteps, 0);
+                it.n_kv = to - kItemSteps - it.j0;
                 it.Lk = now.P;
                 it.block = range + rows + row;
-                at += it.n_kv;
                 return true;
             }
             before += cost;                       // ends: the list holds more than `at` steps
@@ -404,12 +446,6 @@ struct SharedWalk {
         }
     }
 };
-
-// Copies of a single tile's rows among the 128 of an MMA: each copy's warps take
-// that share of a step's keys, and P is zero in the others' columns.  Where a tile
-// has few rows the softmax is the step's time, and one warp with 32 rows takes
-// 1700 clocks for 128 keys; with four copies every warp works, on 32 of them.
-__device__ __forceinline__ int shared_copies(int rows) { return rows <= kBM / 4 ? 4 : rows <= kBM / 2 ? 2 : 1; }
 
 // The fields that follow from what SharedWalk gives.
 __device__ __forceinline__ void shared_fill(PrefillItem &it) {
@@ -611,7 +647,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_idx + R);
     // SHARED: the items themselves, 8 words each, and the scan's scratch
     int4 *items = reinterpret_cast<int4 *>(smem + S::kBars + 512);
-    int *scan = reinterpret_cast<int *>(items + 2 * R), *start = scan + 32;
+    int *scan = reinterpret_cast<int *>(items + 2 * R), *start = scan + 48;
     // Each role walks the same item list and keeps its own counts of items
     // (phase of q_full / q_empty), items with keys (phase of o_final), key
     // steps (phase of s_full / p_full) and K/V loads (ring slot and phase).
@@ -659,8 +695,14 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             const SharedGroup r = g == from ? own : shared_group(a, g);
             const int n = shared_rows<IT>(a, r);
             rows += n;
-            steps += n * ((r.P + kBN - 1) / kBN);
+            steps += n * shared_row_steps(r.P);
         }
+        float keys = 0.f;                        // behind the prefixes
+        if (a.sh.cache_seqlens != nullptr)
+            for (int b = threadIdx.x; b < a.num_seqs; b += kThreads)
+                keys += (float)max(0, min(a.sh.cache_seqlens[b] - a.sh.prefix_lens[b], a.sh.max_suffix));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
         int s_incl = steps, r_incl = rows;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -673,9 +715,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         if (lane == 31) {
             scan[warp] = s_incl;
             scan[16 + warp] = r_incl;
+            scan[32 + warp] = __float_as_int(keys);
         }
         __syncthreads();
         int total = 0, s_acc = s_incl - steps, r_acc = r_incl - rows;
+        float all_keys = 0.f;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) {
@@ -683,14 +727,16 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 r_acc += scan[16 + w];
             }
             total += scan[w];
+            all_keys += __int_as_float(scan[32 + w]);
         }
-        const int per_cta = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+        const int ctas = shared_ctas(a, total, all_keys, lane);
+        const int per_cta = max(1, (total + ctas - 1) / ctas);
         walk.range = blockIdx.x;
         walk.at = (int)min((int64_t)blockIdx.x * per_cta, (int64_t)total);
         walk.end = min(total - walk.at, per_cta) + walk.at;
         for (int g = from; g < to; ++g) {
             const SharedGroup r = g == from ? own : shared_group(a, g);
-            const int n = shared_rows<IT>(a, r), c = n * ((r.P + kBN - 1) / kBN);
+            const int n = shared_rows<IT>(a, r), c = n * shared_row_steps(r.P);
             if (walk.at >= s_acc && walk.at < s_acc + c) {
                 start[0] = g;
                 start[1] = s_acc;
@@ -1058,11 +1104,12 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             auto load_q = [&]() {
                 if (local > 0 && !mbar_wait(q_empty, (local - 1) & 1)) return false;
                 if constexpr (SHARED) {
-                    // boxes of 32 rows; a single tile holds its rows once, twice or four times
+                    // boxes of 32 rows; a single tile of up to 64 rows holds them twice, the
+                    // second time from row 64 on for its second half
                     const bool two = IT > 1 && it.rows > kBM;
                     if (elect_one()) {
                         const int group = a.num_q_heads / a.num_kv_heads;
-                        const int blocks = two ? 8 : 4, distinct = two ? 8 : 4 / shared_copies(it.rows);
+                        const int blocks = two ? 8 : 4, distinct = two ? 8 : it.rows <= kBM / 2 ? 2 : 4;
                         mbar_arrive_expect_tx(q_full, blocks * (S::kTileBytes / 4));
                         for (int i = 0; i < blocks; ++i)
                             for (int hh = 0; hh < H; ++hh)
@@ -1436,13 +1483,13 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             ++local;
             if (v < 0) break;
             const bool halves = it.rows <= kBM;       // one tile: this half's steps are k, k + 2, ..
-            const int copies = halves ? shared_copies(it.rows) : 1;
-            const int blocks = 4 / copies;            // of 32 rows in a copy
-            const int c0 = (quad / blocks) * (kBN / copies), c1 = c0 + kBN / copies;     // this warp's keys of a step
-            const int row0 = 32 * (quad & (blocks - 1)) + (halves ? 0 : kBM * k);        // the item's row of lane 0
+            // The item's row of lane 0.  Of a tile of up to 64 rows the second half has its
+            // rows from lane 64 on: its warps that have rows are on the other schedulers.
+            const int row0 = 32 * quad + (!halves ? kBM * k : it.rows <= kBM / 2 ? -(kBM / 2) * k : 0);
             const int n = halves ? (it.n_kv + 1 - k) / 2 : it.n_kv;      // steps of this warp
             float m_run = -INFINITY, l_run = 0.f;
-            if (row0 >= it.rows) {                    // no row of this warp: it only keeps step
+            const bool some = row0 >= 0 && row0 < it.rows;
+            if (!some) {                              // no row of this warp: it only keeps step
                 for (int j = 0; ok && j < n; ++j) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&s_full[k], (gs + j) & 1));
                     if (ok) mbar_arrive(&p_full[k]);
@@ -1457,7 +1504,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                     const int lim = it.Lk - (it.j0 + (halves ? 2 * j + k : j)) * kBN;   // keys of the step
                     float mt = -INFINITY;
 #pragma unroll 1
-                    for (int c = c0; c < c1; c += 32) {
+                    for (int c = 0; c < kBN; c += 32) {
                         uint32_t sr[32];
                         tmem_ld32(s_tm + c, sr);
                         tmem_wait_ld();
@@ -1498,7 +1545,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     // P's 16-bit columns go over S columns that have been read
 #pragma unroll 1
-                    for (int c = c0; c < c1; c += 32) {
+                    for (int c = 0; c < kBN; c += 32) {
                         uint32_t sr[32], pk[16];
                         tmem_ld32(s_tm + c, sr);
                         tmem_wait_ld();
@@ -1514,11 +1561,6 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                             pk[i] = F8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
                         }
                         tmem_st16(s_tm + c / 2, pk);
-                    }
-                    if (copies > 1) {                 // the other copies' keys
-                        const uint32_t zero[16] = {};
-                        for (int c = 0; c < kBN; c += 32)
-                            if (c < c0 || c >= c1) tmem_st16(s_tm + c / 2, zero);
                     }
                     const float2 s01 = add2(acc[0], acc[1]);
                     l_run += s01.x + s01.y;
@@ -1536,11 +1578,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 continue;
             }
             // The warp's place of the item's block: O / l and lse of its rows, whole 32-byte
-            // sectors at a time.  Halves and copies have a place each (the merge knows).
+            // sectors at a time.  A single tile's halves have a place each (the merge knows).
             const int64_t at = ((int64_t)it.block * (4 * T) + warp) * 32 + lane;
-            const bool mine = ok && row0 + lane < it.rows;
+            const bool mine = ok && some && row0 + lane < it.rows;
             if (mine) a.sh.lse_part[at] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
-            if (!ok || n == 0 || row0 >= it.rows) continue;          // (an empty place may hold anything)
+            if (!ok || n == 0 || !some) continue;     // (an empty place may hold anything)
             const float inv = (l_run == 0.f ? 0.f : 1.f / l_run) * (F8 ? a.v_scale[it.kvh] : 1.f);   // a NaN stays one
             float *to = a.sh.o_part + at * D;
 #pragma unroll 1
