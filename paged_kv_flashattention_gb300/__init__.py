@@ -3,8 +3,9 @@
 A small C-ABI library (``libpa.so``, declared in ``include/pa.h``) with
 hand-written CUDA kernels for the KV-cache store (bf16, FP8 E4M3 with
 per-head scales, or 4-bit rows with block scales), the batch's metadata, varlen causal prefill / extend attention over a page table,
-split-KV decode and the log-sum-exp combine, and both attention halves of a
-mixed batch in one launch; this package is its thin torch binding.  PyTorch
+split-KV decode and the log-sum-exp combine, both attention halves of a mixed
+batch in one launch, decode over prefixes that sequences share, and beam
+search's selection and reordering; this package is its thin torch binding.  PyTorch
 provides device memory and streams only.
 """
 from .api import (PA_DEVERR_NO_PAGES, PA_DEVERR_PAGE_RANGE, PA_DEVERR_POSITION, PA_DEVERR_SEQLENS, PA_DEVERR_TABLE_INDEX,
@@ -16,13 +17,14 @@ from .api import (PA_DEVERR_NO_PAGES, PA_DEVERR_PAGE_RANGE, PA_DEVERR_POSITION, 
                   device_error, fp4_row_bytes, load_kv_fp4, lse_combine, mixed_batch, prefill, prefill_scheduler, rope_cos_sin_table,
                   rope_store_kv, store_kv, store_kv_fp4, store_kv_fp8)
 
+from .beams import BeamSearch
 from .graphs import DecodeGraphRunner, bucket_for
 from .metadata import BatchPlanner
 
 __all__ = [
     "PagedAttentionError", "abi_version", "build_batch", "BatchPlanner", "build_page_table", "build_seqlens", "decode",
     "decode_noalloc", "decode_shared", "decode_shared_workspace_size", "beam_select", "beam_select_workspace_size",
-    "beam_reorder",
+    "beam_reorder", "BeamSearch",
     "decode_kv_chunk", "decode_workspace_size", "device_error", "lse_combine", "mixed_batch", "prefill",
     "prefill_scheduler",
     "DecodeGraphRunner", "bucket_for",

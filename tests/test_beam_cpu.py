@@ -119,3 +119,36 @@ def test_shared_workspace_serves_smaller_calls(kv_dtype):
         for B, groups, group, prefix, suffix in itertools.product((1, 3, 33, 64), (1, 5, 8), (1, 32, 33, 64), (0, 1, 129, 5000, 32768),
                                                                   (0, 1, 63, 64, 65, 1000, 2047, top)):
             assert size(B, groups, group, prefix, suffix) <= most
+
+
+def _search(**change):
+    import paged_kv_flashattention_gb300 as pa
+    dtype = change.pop("dtype", torch.bfloat16)
+    pool = lambda: torch.zeros((9, 16, 2, 64), dtype=dtype)
+    args = dict(k_caches=[pool(), pool()], v_caches=[pool(), pool()], token_table=torch.zeros((6, 64), dtype=torch.int32),
+                table_idx=torch.arange(6, dtype=torch.int32), num_groups=2, beams=3, num_q_heads=4, head_dim=64, vocab=500,
+                max_seqlen_k=64, spare_pages=torch.arange(6, dtype=torch.int32))
+    args.update(change)
+    return pa.BeamSearch(args.pop("k_caches"), args.pop("v_caches"), args.pop("token_table"), args.pop("table_idx"), **args)
+
+
+@pytest.mark.parametrize("change", [
+    dict(k_caches=[]), dict(v_caches=[torch.zeros((9, 16, 2, 64), dtype=torch.bfloat16)]), dict(num_groups=0), dict(beams=0),
+    dict(beams=4), dict(spare_pages=None), dict(dtype=torch.uint8), dict(vocab=2), dict(k_scales=[torch.ones(2)]),
+    dict(num_q_heads=3), dict(max_prefix=65), dict(head_dim=96),
+])
+def test_search_refuses(change):
+    with pytest.raises((ValueError, TypeError)):
+        _search(**change)
+
+
+def test_search_state():
+    s = _search()
+    s.start(torch.tensor([37, 0]))
+    assert s.lens.tolist() == [37] * 3 + [0] * 3 and s.prefix_lens.tolist() == [32] * 3 + [0] * 3
+    assert s.scores.tolist() == [[0.0, float("-inf"), float("-inf")]] * 2
+    assert s.cu_groups.tolist() == [0, 3, 6]
+    with pytest.raises(ValueError):
+        s.start(torch.tensor([1]))
+    with pytest.raises(ValueError):
+        s.attend(0, torch.zeros((6, 4, 64), dtype=torch.bfloat16))
