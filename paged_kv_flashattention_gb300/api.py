@@ -11,6 +11,7 @@ import collections
 import ctypes
 import functools
 import math
+import operator
 import threading
 
 import numpy as np
@@ -1017,7 +1018,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None 
     return tuple(outs)
 
 
-_tensor_device = torch.Tensor.get_device
+_tensor_device, _tensor_bytes = torch.Tensor.get_device, operator.attrgetter("nbytes")
 
 
 def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor, seqlens: torch.Tensor,
@@ -1043,13 +1044,16 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
         raise ValueError("k_caches and v_caches must hold one pool per layer")
     first = pools[0]
     dtype, shape = first.dtype, first.shape
-    # every layer's pools at once: 30 us for 32 of them one by one
+    # every layer's pools at once (30 us for 32 of them one by one); bits are moved,
+    # so that pools of as many bytes are as good as of one type
+    size = first.nbytes
     if (len(set(map(_tensor_device, pools))) != 1 or not all(map(torch.Tensor.is_contiguous, pools))
-            or any(t.dtype is not dtype for t in pools)):
+            or set(map(_tensor_bytes, pools)) != {size}):
         for t in pools:
             _need(t, "every pool", dtype, dev)
+        raise ValueError("the pools must have one shape")
     _need(first, "every pool", dtype, dev)
-    if len(set(map(torch.Tensor.numel, pools))) != 1 or pools[-1].shape != shape:
+    if pools[-1].shape != shape:
         raise ValueError("the pools must have one shape")
     # [num_pages, page_size, ...], or with page_size also [slots, ...]: heads and
     # elements, or the bytes of a 4-bit row
@@ -1069,6 +1073,7 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
     if parents.dim() != 2:
         raise ValueError("parents must be [groups, beams]")
     G, K = parents.shape
+    N = G * K
     _need_rows(token_table, "token_table", dev)
     rows, width = token_table.shape
     max_k = width if max_seqlen_k is None else int(max_seqlen_k)
@@ -1079,8 +1084,8 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
     for t, name in ((table_idx, "table_idx"), (seqlens, "seqlens"), (spare_pages, "spare_pages"), (prefix_lens, "prefix_lens")):
         if t is not None:
             _need(t, name, torch.int32, dev)
-            if t.numel() != G * K:
-                raise ValueError(f"{name} must hold one entry per sequence ({G * K})")
+            if t.numel() != N:
+                raise ValueError(f"{name} must hold one entry per sequence ({N})")
     history_ptr, history_stride, history_len = None, 0, 0
     if history is not None:
         _need_rows(history, "history", dev)
