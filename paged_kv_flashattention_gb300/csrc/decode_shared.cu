@@ -30,8 +30,10 @@ PA_ERROR_WORD_ACCESSOR(error_word_decode_shared)
 
 namespace {
 
+constexpr int prefix_threads(int kv) { return shared_threads(kv != PA_KV_BF16, kv == PA_KV_FP4); }
+
 template <int D, int KV>
-__global__ void __launch_bounds__(KV == PA_KV_BF16 ? 384 : 512, 1) shared_prefix_kernel(const __grid_constant__ PrefillArgs a) {
+__global__ void __launch_bounds__(prefix_threads(KV), 1) shared_prefix_kernel(const __grid_constant__ PrefillArgs a) {
     prefill_body<D, 2, KV != PA_KV_BF16, false, KV == PA_KV_FP4, true>(a);
 }
 
@@ -55,7 +57,7 @@ cudaError_t launch_prefix_t(const PrefillArgs &a, unsigned ctas, cudaStream_t st
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_after(kern, ctas, KV == PA_KV_BF16 ? 384 : 512, smem, stream, a);
+    return launch_after(kern, ctas, prefix_threads(KV), smem, stream, a);
 }
 
 template <int KV>

@@ -339,6 +339,9 @@ __device__ void prefill_sched_done(const PrefillArgs &a, int num_ctas) {
 // prefixes of 512 to 8192 keys: the busiest CTA 1.36 of the mean without it.
 constexpr int kItemSteps = 4;
 
+// Threads of a CTA: the softmax warps, four that load and issue, those that widen.
+constexpr int shared_threads(bool f8, bool f4) { return 384 + (f4 ? 256 : f8 ? 128 : 0); }
+
 // The decode of the keys behind the prefixes starts where this kernel leaves SMs, so
 // the list goes to n of the G SMs and the other CTAs end at once (64 sequences behind
 // 8192 keys: 57 us with the list on every SM, 53 on 32 of them; sixteen groups of 8
@@ -621,11 +624,14 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     static_assert(!SHARED || !F8 || (NS % 2 == 0 && S::kCSlots % 2 == 0), "rings of even length");
     constexpr int IT = S::kItemTiles;
     constexpr int NC = F8 ? S::kCSlots : NS;  // slots the MMA reads from
-    // Warps that widen: two to a tile.  SHARED has four, two for the K tiles and two
-    // for the V tiles: with all four on each tile the waits and the fence take as long
-    // as the conversion.
-    constexpr int kConverters = !F8 ? 0 : SHARED ? 4 : 2;
-    constexpr int kWideRows = 64;
+    // Warps that widen: two to a tile.  SHARED has two for the K tiles and two for the
+    // V tiles, over 4 bits four and four (groups of 8, head size 128: 62 us with two
+    // each, 57 with four; FP8 40 and 42).  A 4-bit step then takes 1950 clocks, of which
+    // shared memory is busy 1600: 20 KiB land and are read, 64 are widened, 96 go to
+    // the MMAs.
+    constexpr int kWideWarps = SHARED && F4 ? 4 : 2;      // of a tile
+    constexpr int kConverters = !F8 ? 0 : SHARED ? 2 * kWideWarps : kWideWarps;
+    constexpr int kWideRows = kBN / kWideWarps;
     constexpr bool kInPlace = S::kInPlace;
     constexpr bool kClasses = F4 && !EXT && !SHARED;      // items in classes of positions (prefill_item)
     auto land = [&](int slot) { return smem + S::kRing + slot * S::kLStride + S::kLOff; };
@@ -647,7 +653,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_idx + R);
     // SHARED: the items themselves, 8 words each, and the scan's scratch
     int4 *items = reinterpret_cast<int4 *>(smem + S::kBars + 512);
-    int *scan = reinterpret_cast<int *>(items + 2 * R), *start = scan + 48;
+    int *scan = reinterpret_cast<int *>(items + 2 * R), *start = scan + 60;
     // Each role walks the same item list and keeps its own counts of items
     // (phase of q_full / q_empty), items with keys (phase of o_final), key
     // steps (phase of s_full / p_full) and K/V loads (ring slot and phase).
@@ -662,11 +668,11 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         mbar_init(q_empty, 1);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], paged16 ? (F4 ? 33 : 1) : 32);   // 4-bit: the boxes, and every lane's scales
-            mbar_init(&empty[s], (F8 && !kInPlace) ? 2 : 1);
+            mbar_init(&empty[s], (F8 && !kInPlace) ? kWideWarps : 1);
         }
         if (F8) {
             for (int s = 0; s < NC; ++s) {
-                mbar_init(&cfull[s], 2);
+                mbar_init(&cfull[s], kWideWarps);
                 mbar_init(&cempty[s], 1);
             }
             mbar_init(q_conv, kConverters);
@@ -686,7 +692,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     if constexpr (SHARED) {
         // Steps of the whole list, steps and rows before this thread's groups, and the
         // group in which this CTA's range starts.
-        constexpr int kThreads = F8 ? 512 : 384;
+        constexpr int kThreads = shared_threads(F8, F4);
         const int per = (a.sh.num_groups + kThreads - 1) / kThreads;
         const int from = min((int)threadIdx.x * per, a.sh.num_groups), to = min(from + per, a.sh.num_groups);
         const SharedGroup own = shared_group(a, from);           // (empty behind the last)
@@ -714,8 +720,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         }
         if (lane == 31) {
             scan[warp] = s_incl;
-            scan[16 + warp] = r_incl;
-            scan[32 + warp] = __float_as_int(keys);
+            scan[20 + warp] = r_incl;
+            scan[40 + warp] = __float_as_int(keys);
         }
         __syncthreads();
         int total = 0, s_acc = s_incl - steps, r_acc = r_incl - rows;
@@ -724,10 +730,10 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) {
                 s_acc += scan[w];
-                r_acc += scan[16 + w];
+                r_acc += scan[20 + w];
             }
             total += scan[w];
-            all_keys += __int_as_float(scan[32 + w]);
+            all_keys += __int_as_float(scan[40 + w]);
         }
         const int ctas = shared_ctas(a, total, all_keys, lane);
         const int per_cta = max(1, (total + ctas - 1) / ctas);
@@ -981,7 +987,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
     // that each store of a warp's quarter covers all banks; all its loads go out
     // first (in groups of four chunks 282 us against 267, of two 299).  Rows at
     // keys >= kv_end hold slots the store never wrote: a zero scale clears them.
-    auto widen4 = [&](const PrefillItem &it, int c, int cw, const uint8_t *src, uint8_t *dst) {
+    auto widen4 = [&](const PrefillItem &it, int c, int cw, const uint8_t *src, uint8_t *dst, auto &&read) {
         constexpr int kChunks = D / 32;               // chunks of a row
         constexpr int kRows = 32 / kChunks;           // rows of a pass: 8 or 16
         constexpr int kPasses = kWideRows / kRows;
@@ -999,6 +1005,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             sc[i] = *reinterpret_cast<const uint16_t *>(src + S::scale_off(r) + sub + 2 * ch);
             if (r >= live) sc[i] = 0u;
         }
+        read();
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = kWideRows * cw + i * kRows + lane % kRows;
@@ -1204,8 +1211,8 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
       } else if (F8 && warp >= (SHARED ? kMma + 3 : kMma + 1)) {
         // -------------------------------- FP8 widening (kConverters warps) ----
         const int wid = warp - (SHARED ? kMma + 3 : kMma + 1);
-        const int cw = wid & 1;                         // rows [64 cw, 64 cw + 64)
-        constexpr int kStep = SHARED ? 2 : 1;           // SHARED: warps 0, 1 K tiles, 2, 3 V tiles
+        const int cw = wid & (kWideWarps - 1);          // its rows of a tile
+        constexpr int kStep = SHARED ? 2 : 1;           // SHARED: the first half of them K tiles, the other V tiles
         int local = 0, gl = 0;
         bool ok = true;
         PrefillItem it;
@@ -1232,7 +1239,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
             // K/V tiles: E4M3 rows -> f16 in the swizzled K-major layout
             const int gl0 = gl;
             gl += 2 * it.n_kv;
-            for (int c = SHARED ? wid >> 1 : 0; c < 2 * it.n_kv; c += kStep) {
+            for (int c = SHARED ? wid / kWideWarps : 0; c < 2 * it.n_kv; c += kStep) {
                 const int gl = gl0 + c;
                 const int ls = gl % NS, cs = gl % NC;
                 ok = __all_sync(0xffffffffu, mbar_wait(&full[ls], (gl / NS) & 1));
@@ -1243,12 +1250,19 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs &a, int sched_cta
                 const uint8_t *src = land(ls);
                 uint8_t *dst = smem + S::kConv + cs * S::kTileBytes;
                 if constexpr (F4) {
-                    widen4(it, c, cw, src, dst);
+                    // SHARED: the landed slot is free once it is in registers (six slots are
+                    // too few for the loads' latency otherwise)
+                    widen4(it, c, cw, src, dst, [&]() {
+                        if constexpr (SHARED) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&empty[ls]);
+                        }
+                    });
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&cfull[cs]);
-                        mbar_arrive(&empty[ls]);
+                        if (!SHARED) mbar_arrive(&empty[ls]);
                     }
                     continue;
                 }
