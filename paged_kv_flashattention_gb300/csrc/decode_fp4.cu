@@ -89,8 +89,15 @@ struct Fp4DecodeArgs {
     int32_t overlap_previous;     // do not wait for the kernel before
     int32_t *ws_header;           // [0] = T, in units
     int32_t *ws_prefix;           // [B+1] exclusive prefix of the sequences' units
-    const int32_t *first_keys;    // over shared prefixes: the keys from first_keys[b] on,
-    int32_t max_keys;             // at most so many (null: all)
+    static constexpr bool kTail = false;
+};
+// Over shared prefixes: the keys from first_keys[b] on, at most max_keys.  Kernels of
+// their own: asked for in the code of all calls they cost 256 contexts up to 32768
+// keys 432 us instead of 425.
+struct Fp4TailArgs : Fp4DecodeArgs {
+    static constexpr bool kTail = true;
+    const int32_t *first_keys;
+    int32_t max_keys;
 };
 
 // Page size 16 and more than one head group (BOX): the pools as rows of 32-bit
@@ -117,11 +124,12 @@ struct Fp4Smem {
 };
 
 // First key and number of keys of sequence b that its query sees.
-__device__ __forceinline__ int seq_keys(const Fp4DecodeArgs &a, int b, int &lo) {
+template <class Args>
+__device__ __forceinline__ int seq_keys(const Args &a, int b, int &lo) {
     int L = a.cache_seqlens[b];
     L = L < 0 ? 0 : (L > a.max_seqlen_k ? a.max_seqlen_k : L);
     lo = (a.window > 0 && L > a.window) ? L - a.window : 0;
-    if (a.first_keys != nullptr) {
+    if constexpr (Args::kTail) {
         lo = a.first_keys[b];
         if (lo < 0 || lo > L) return lo = 0;
         lo = max(lo, L - a.max_keys);
@@ -130,19 +138,20 @@ __device__ __forceinline__ int seq_keys(const Fp4DecodeArgs &a, int b, int &lo) 
 }
 
 // Exclusive prefix of the sequences' units into prefix[0 .. B] (all threads).
-__device__ __forceinline__ void fp4_prefix(const Fp4DecodeArgs &a, int32_t *prefix) {
+template <class Args>
+__device__ __forceinline__ void fp4_prefix(const Args &a, int32_t *prefix) {
     const int B = a.num_seqs;
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
         const int given = a.cache_seqlens[b];
         if (given < 0 || given > a.max_seqlen_k) raise_error(PA_DEVERR_SEQLENS);
         int lo;
         const int L = seq_keys(a, b, lo);
-        if (a.first_keys != nullptr) {
+        if constexpr (Args::kTail) {
             const int first = a.first_keys[b];
             if ((given > 0 && (first < 0 || given < first)) || (given >= 0 && given - first > a.max_keys && first >= 0))
                 raise_error(PA_DEVERR_SEQLENS);
         }
-        prefix[b + 1] = L > lo ? (L - 1) / kUnit - lo / kUnit + 1 : 0;
+        prefix[b + 1] = L > (Args::kTail ? lo : 0) ? (L - 1) / kUnit - lo / kUnit + 1 : 0;
     }
     if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
@@ -201,8 +210,8 @@ __device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map,
 }
 
 // The producer warp: units [g0, g1) of the list into the ring.
-template <int D, int HPC, bool BOX>
-__device__ void fp4_produce(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, const int32_t *prefix, int T, int g0, int g1,
+template <int D, int HPC, bool BOX, class Args>
+__device__ void fp4_produce(const Args &a, const Fp4MapsOf<BOX> &maps, const int32_t *prefix, int T, int g0, int g1,
                             uint8_t *ring, uint64_t *full, uint64_t *empty, int lane) {
     using S = Fp4Smem<D, HPC>;
     const bool paged = a.page_size == 16;
@@ -398,8 +407,8 @@ __device__ __forceinline__ void fp4_values(const Fp4Lane<D, HPC> &ln, const uint
 // Consumer warp hw: KV head hg * HPC + hw of each segment of the same range.
 // Units are taken in pairs: one vote and one maximum for 32 keys, and two
 // independent score chains in flight.
-template <int D, int HPC>
-__device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T, int g0, int g1,
+template <int D, int HPC, class Args>
+__device__ void fp4_consume(const Args &a, const int32_t *prefix, int T, int g0, int g1,
                             const uint8_t *ring, uint64_t *full, uint64_t *empty, int hw, int lane) {
     using S = Fp4Smem<D, HPC>;
     constexpr int KS = D / 16;                       // k-steps of the score = tiles of O
@@ -520,9 +529,9 @@ __device__ void fp4_consume(const Fp4DecodeArgs &a, const int32_t *prefix, int T
     }
 }
 
-template <int D, int HPC, bool BOX>
+template <int D, int HPC, bool BOX, class Args>
 __global__ void __launch_bounds__((HPC + 1) * 32, Fp4Smem<D, HPC>::kCtas)
-decode_fp4_kernel(const Fp4DecodeArgs a, const __grid_constant__ Fp4MapsOf<BOX> maps) {
+decode_fp4_kernel(const Args a, const __grid_constant__ Fp4MapsOf<BOX> maps) {
     using S = Fp4Smem<D, HPC>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kRing);
@@ -549,7 +558,7 @@ decode_fp4_kernel(const Fp4DecodeArgs a, const __grid_constant__ Fp4MapsOf<BOX> 
     const int g0 = (int)min((int64_t)blockIdx.x * T, (int64_t)total), g1 = min(total - g0, T) + g0;
     if (warp == HPC) fp4_produce<D, HPC, BOX>(a, maps, prefix, T, g0, g1, smem, full, empty, lane);
     else fp4_consume<D, HPC>(a, prefix, T, g0, g1, smem, full, empty, warp, lane);
-    if (a.first_keys != nullptr) decode_end_after_previous();
+    if constexpr (Args::kTail) decode_end_after_previous();
 }
 
 // The log-sum-exp combine (decode.cu's, with its split count): W warps share a
@@ -645,12 +654,12 @@ cudaError_t launch_fp4_combine(const Fp4DecodeArgs &a, const pa_decode_params &p
                         a.head_groups, heads_per_group, p.num_q_heads, rows, plan.max_splits, out, p.lse);
 }
 
-template <int D, int HPC, bool BOX>
-cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, const pa_decode_params &p, int64_t useful,
+template <int D, int HPC, bool BOX, class Args>
+cudaError_t launch_fp4_t(const Args &a, const Fp4MapsOf<BOX> &maps, const pa_decode_params &p, int64_t useful,
                          cudaStream_t stream) {
     using S = Fp4Smem<D, HPC>;
     const size_t smem = S::kRing + 2 * S::kStages * sizeof(uint64_t) + ((size_t)a.num_seqs + 1) * sizeof(int32_t);
-    auto kern = decode_fp4_kernel<D, HPC, BOX>;
+    auto kern = decode_fp4_kernel<D, HPC, BOX, Args>;
     // CTAs per SM of the last (device, size), so that a serving loop's calls
     // skip both queries; the limit is raised to the device's once and for all.
     static std::atomic<uint64_t> last{0};
@@ -676,8 +685,8 @@ cudaError_t launch_fp4_t(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, con
     return launch_after(kern, (unsigned)grid, (HPC + 1) * 32, smem, stream, a, maps);
 }
 
-template <bool BOX>
-cudaError_t dispatch_fp4(const Fp4DecodeArgs &a, const Fp4MapsOf<BOX> &maps, int heads, const pa_decode_params &p,
+template <bool BOX, class Args>
+cudaError_t dispatch_fp4(const Args &a, const Fp4MapsOf<BOX> &maps, int heads, const pa_decode_params &p,
                          int64_t useful, cudaStream_t stream) {
     if (p.head_dim == 64) {
         if (heads == 1) return launch_fp4_t<64, 1, BOX>(a, maps, p, useful, stream);
@@ -783,7 +792,7 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
     if (p.num_seqs == 0) return cudaSuccess;
     const DecodeArgs w = decode_setup(p, plan);      // the workspace layout
     const Fp4Layout lay = fp4_layout(p.num_kv_heads, p.head_dim);
-    Fp4DecodeArgs a{};
+    Fp4TailArgs a{};
     a.q = w.q;
     a.k_cache = w.k_cache;
     a.v_cache = w.v_cache;
@@ -817,15 +826,20 @@ cudaError_t launch_decode_fp4(const pa_decode_params &p, const DecodePlan &plan,
     const int64_t longest = tail != nullptr ? ((int64_t)tail->max_keys + 2 * kUnit - 2) / kUnit * kUnit : reach(p);
     const int64_t units = longest / kUnit * p.num_seqs * lay.groups;
     const int64_t useful = (units + a.min_units - 1) / a.min_units + 1;
+    auto dispatch = [&](auto box, const auto &maps) {
+        constexpr bool kBox = decltype(box)::value;
+        return tail != nullptr ? dispatch_fp4<kBox>(a, maps, lay.gs, p, useful, stream)
+                               : dispatch_fp4<kBox>(static_cast<const Fp4DecodeArgs &>(a), maps, lay.gs, p, useful, stream);
+    };
     cudaError_t e;
     if (p.page_size == 16 && lay.groups > 1) {
         Fp4Maps maps;
         if (!make_map_rows(&maps.k, p.k_cache, lay, p.num_pages * 16) ||
             !make_map_rows(&maps.v, p.v_cache, lay, p.num_pages * 16))
             return cudaErrorNotSupported;
-        e = dispatch_fp4<true>(a, maps, lay.gs, p, useful, stream);
+        e = dispatch(std::true_type{}, maps);
     } else {
-        e = dispatch_fp4<false>(a, Fp4NoMaps{}, lay.gs, p, useful, stream);
+        e = dispatch(std::false_type{}, Fp4NoMaps{});
     }
     if (e != cudaSuccess) return e;
     if (tail != nullptr) {
