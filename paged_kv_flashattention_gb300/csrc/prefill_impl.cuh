@@ -437,9 +437,10 @@ struct SharedWalk {
                 it.block = range + rows + row;
                 return true;
             }
-            before += cost;                       // ends: the list holds more than `at` steps
+            before += cost;
             rows += shared_rows<T>(a, now);
-            if (++g >= ahead + 32) {
+            if (++g >= a.sh.num_groups) return false;      // never, unless the lengths change under the call
+            if (g >= ahead + 32) {
                 ahead = g;
                 mine = shared_group(a, g + lane);
             }

@@ -194,6 +194,18 @@ def test_bounds_may_be_loose(cuda_device):
     check(s, run(s, workspace=ws))
 
 
+@pytest.mark.parametrize("kv", [0, FP8, FP4])
+@pytest.mark.parametrize("prefix,tails,loose", [
+    (16, (3000, 2500, 3001, 1), False), (9000, (0, 1, 0, 0), True), (9000, (0, 0, 0, 0), True), (4000, (4000, 10, 4000, 7), False),
+    (20000, (3, 16, 1, 40), True),
+])
+def test_prefix_beside_tails(cuda_device, prefix, tails, loose, kv):
+    """Prefixes and tails of every proportion, so that few and all of the CTAs take
+    part in the prefix, under tight bounds and loose ones."""
+    s = make(cuda_device, prefix + len(tails), [3, 2], [prefix, prefix // 2], [*tails, 5], 16, 8, 64, 16, kv)
+    check(s, run(s, **(dict(max_prefix=None, max_suffix=None) if loose else {})))
+
+
 def test_padding_rows(cuda_device):
     """Rows of length 0 inside a group with a prefix and behind all groups."""
     s = make(cuda_device, 2, [4, 3], [200, 100], [3, 5, 0, 7, 1, 2, 3, 0], 8, 2, 128, 16, 0, loose=1)
