@@ -593,6 +593,9 @@ pa_status pa_lse_combine(const float *o_partial, const float *lse_partial,
  *  - Arithmetic: as pa_prefill over the prefix and pa_decode behind it, on
  *    each type of pool; the partials are 32 bits.
  *  - dec.sliding_window, dec.max_ctas and dec.overlap_previous must be 0.
+ *  - The SMs are shared out between prefixes and the keys behind them by the
+ *    lengths on the device, and the first launch by the bounds: results are
+ *    good for any bounds that hold, times best for tight ones.
  *  - The workspace (pa_decode_shared_workspace_size bytes) serves every call
  *    with bounds and counts up to these.  Calls that may run at the same time
  *    need one each.

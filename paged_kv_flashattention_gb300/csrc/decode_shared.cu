@@ -282,7 +282,7 @@ int most_ctas(const pa_decode_shared_params &p) {
 }
 
 // Measured, of a step: 3200 clocks for two tiles of head size 128, 5000 where rows are
-// gathered one by one, 1260 over FP8 at 64, 1950 over 4 bits at 128.  The split-KV
+// gathered one by one, 1260 to 1600 over FP8 at 64, 1950 over 4 bits at 128.  The split-KV
 // decode reads 38 GB/s an SM.
 void set_costs(SharedArgs &sh, const pa_decode_shared_params &p) {
     const pa_decode_params &d = p.dec;

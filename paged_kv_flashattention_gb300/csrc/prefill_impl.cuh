@@ -347,7 +347,7 @@ constexpr int shared_threads(bool f8, bool f4) { return 384 + (f4 ? 256 : f8 ? 1
 // 8192 keys: 57 us with the list on every SM, 53 on 32 of them; sixteen groups of 8
 // over FP8 48 and 40 on 118).  About the time of both, for a list of p ns and a rest
 // of t: the longer of the two beside each other, or with n = G one behind the other.
-constexpr float kSharedStart = 8000.f, kTailStart = 7000.f;      // ns before a CTA's first step; a CTA of few keys
+constexpr float kSharedStart = 12000.f, kTailStart = 7000.f;     // ns of a CTA beside its steps; of a CTA of few keys
 __host__ __device__ inline float shared_time(float p, float t, int n, int G) {
     return n < G ? fmaxf(p / (float)n + kSharedStart, t / (float)(G - n)) : (p + t) / (float)G + kSharedStart + kTailStart;
 }
