@@ -211,7 +211,8 @@ struct Chosen {
     uint64_t buf[kKept + kTile];
     uint64_t best[128];
     uint32_t tops[kSelThreads];
-    unsigned long long dropped;                      // in units of 2^-32
+    unsigned long long dropped;                      // in units of 2^-32: of the buffer, until thread 0 takes it
+    unsigned long long whole;                        // in the same units: all threads' rest, once they are through
     int count;
 };
 
@@ -224,6 +225,7 @@ struct Chooser {
         if (threadIdx.x == 0) {
             sh.count = 0;
             sh.dropped = 0;
+            sh.whole = 0;
         }
     }
     __device__ __forceinline__ float term(float x) const { return fast_exp2((x - ref) * kLog2e); }
@@ -293,11 +295,11 @@ struct Chooser {
         __syncthreads();
         const int kept = cut(sh.count);
         // rest of all threads, each to 2^-32 of the least term of the list, in whole
-        // numbers of two halves
+        // numbers of two halves.  Not in `dropped`: thread 0 may not have cleared that.
         const unsigned long long units = __float2ull_rn(rest * 0x1p32f);
         const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)units & 0xffffffu);
         const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(units >> 24));
-        if (lane == 0) atomicAdd(&sh.dropped, ((unsigned long long)hi << 24) + lo);
+        if (lane == 0) atomicAdd(&sh.whole, ((unsigned long long)hi << 24) + lo);
         __syncthreads();
         const float top = kept > 0 ? key_value(sh.best[0]) : -INFINITY;
         if (threadIdx.x < 32) {
@@ -305,8 +307,8 @@ struct Chooser {
             for (int e = lane; e <= kept; e += 32) { // entry `kept`: the rest, at its reference
                 const float x = e < kept ? key_value(sh.best[e]) : ref;
                 if (e < kept) list[e] = make_float2(x, __int_as_float((int)~(uint32_t)sh.best[e]));
-                if (e < kept || sh.dropped != 0)
-                    sum += exp((double)x - (double)top) * (e < kept ? 1.0 : (double)sh.dropped * 0x1p-32);
+                if (e < kept || sh.whole != 0)
+                    sum += exp((double)x - (double)top) * (e < kept ? 1.0 : (double)sh.whole * 0x1p-32);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
