@@ -205,8 +205,8 @@ __device__ __forceinline__ float value_below(uint32_t k) { return unordered(k - 
 __device__ __forceinline__ int kept_limit(int n) { return 16 + n + n / 2; }
 
 // A CTA's n largest of the elements that it is shown, and the sum of all of their
-// exponentials.  Elements above thr are entries of the buffer; those at or below
-// it are in `rest`, each thread's sum of 2^((x - ref) log2 e) with ref = thr.
+// exponentials.  Elements above the threshold are entries of the buffer; the others
+// are in `rest`, each thread's sum of 2^((x - ref) log2 e) with ref = thr, its value.
 struct Chosen {
     uint64_t buf[kKept + kTile];
     uint64_t best[128];
@@ -220,8 +220,12 @@ struct Chooser {
     Chosen &sh;
     int n, limit;
     float thr, ref, rest;
+    // Keys above this one, whose value is thr, are due.  Where columns come in their order
+    // nothing behind a cut of value thr is, and the values alone tell.
+    uint64_t floor;
 
-    __device__ __forceinline__ Chooser(Chosen &s, int n) : sh(s), n(n), limit(kept_limit(n)), thr(-INFINITY), ref(0.f), rest(0.f) {
+    __device__ __forceinline__ Chooser(Chosen &s, int n)
+        : sh(s), n(n), limit(kept_limit(n)), thr(-INFINITY), ref(0.f), rest(0.f), floor(key_of(-INFINITY, 0)) {
         if (threadIdx.x == 0) {
             sh.count = 0;
             sh.dropped = 0;
@@ -230,19 +234,20 @@ struct Chooser {
     }
     __device__ __forceinline__ float term(float x) const { return fast_exp2((x - ref) * kLog2e); }
     // A new threshold, the same for the CTA.
-    __device__ __forceinline__ void raise(float to) {
+    __device__ __forceinline__ void raise(float to, uint64_t key) {
         const float r = to == -INFINITY ? 0.f : to;
         rest = rest > 0.f ? rest * fast_exp2((ref - r) * kLog2e) : 0.f;
         thr = to;
         ref = r;
+        floor = key;
     }
     // The first threshold, from the maxima of the threads' elements: elements of
     // that value are entries too.
     __device__ __forceinline__ void start(float most) {
         const uint32_t least = block_floor(ordered(most), n, 16, sh.tops);
-        if (least > ordered(-INFINITY)) raise(value_below(least));
+        if (least > ordered(-INFINITY)) raise(value_below(least), key_of(value_below(least), 0));
     }
-    // An element above thr; the entries then (they may be more than the limit).
+    // An element above thr, or of a key above floor; the entries then (they may be more than the limit).
     __device__ __forceinline__ int enter(float x, int col) {
         const int at = atomicAdd(&sh.count, 1);
         sh.buf[at] = key_of(x, col);
@@ -264,7 +269,7 @@ struct Chooser {
         }
         __syncthreads();
         if (m < n) return m;
-        raise(key_value(sh.best[n - 1]));
+        raise(key_value(sh.best[n - 1]), sh.best[n - 1]);
         if (out != 0) {
             unsigned long long sum = 0;
             for (int e = t, i = 0; e < m; e += kSelThreads, ++i)
@@ -486,7 +491,9 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
 // Second pass, a CTA per row: the n-th largest of the threads' maxima over the
 // blocks is the threshold; only blocks that reach it (little more than n) are read
 // again, of the others their sums count.  Blocks are listed in their order, so that
-// the sums do not depend on chance.
+// the sums do not depend on chance.  A block's columns lie in four tiles, so a
+// smaller column may come behind a larger one: what is due behind a cut is told by
+// whole keys, of equal values the smaller columns.
 constexpr int kListed = 1024;
 
 template <int DT>
@@ -510,16 +517,16 @@ __global__ void __launch_bounds__(kSelThreads) select_rows_kernel(const SelectAr
             int last = 0;
             if (mine < listed) {
                 const int id = list_of[mine];
-                const int col0 = id / kSelThreads * kSpan + id % kSelThreads * kElems + (t & 7);
+                const int first = id / kSelThreads * kSpan + id % kSelThreads * kElems, col0 = first + (t & 7);
                 float v[kBlockTiles];
 #pragma unroll
                 for (int u = 0; u < kBlockTiles; ++u)
                     v[u] = col0 + u * kTile < a.vocab ? cleaned(element<DT>(row, col0 + u * kTile)) : -INFINITY;
                 const float2 b = blocks[id];
-                if (b.x > ch.thr) {
+                if (key_of(b.x, first) > ch.floor) { // (no key of the block is larger)
 #pragma unroll
                     for (int u = 0; u < kBlockTiles; ++u) {
-                        if (v[u] > ch.thr) last = ch.enter(v[u], col0 + u * kTile);
+                        if (key_of(v[u], col0 + u * kTile) > ch.floor) last = ch.enter(v[u], col0 + u * kTile);
                         else if (v[u] > -INFINITY) ch.rest += ch.term(v[u]);
                     }
                 } else if ((t & 7) == 0) {           // the threshold has passed it since
