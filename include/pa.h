@@ -623,9 +623,9 @@ pa_status pa_decode_shared(const pa_decode_shared_params *p, void *stream);
  *   k * vocab + v, smallest first: their totals, beams and tokens.
  * Totals are formed and compared in 64 bits (their order decides which beams
  * live on) and rounded to fp32 once.  Of a row's exponentials those of its
- *    largest logits are summed in 64 bits, the others in 32: the logarithm is off by
- *    about 1e-7, so that totals of different beams that are nearer to one another
- *    than that may change places; those of one beam never do.
+ * largest logits are summed in 64 bits, the others in 32: the logarithm is off by
+ * about 1e-7, so that totals of different beams that are nearer to one another
+ * than that may change places.
  *  - finished (optional): a beam with a non-zero entry has ended; it offers
  *    itself with pad_token and total scores[g, k], its logits are not read.
  *  - A logit that is NaN or +inf counts as -inf, as does a score.  Candidates

@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kSelThreads) select_rows_kernel(const SelectAr
 }
 
 // One CTA per group: lse of its beams, the totals of the lists' entries, the n
-// largest of those.  Entries pass the threshold in rounds, as above; beams whose
+// largest of those.  lse is kept as the largest logit and the logarithm of the sum:
+// in one number a row of the type's lowest value would lose the logarithm.  Entries pass the threshold in rounds, as above; beams whose
 // logits are not read offer what they have in place of their first list.
 constexpr int kRound = 4 * kSelThreads;
 constexpr int kBuf2 = kKept + kRound;
@@ -604,7 +605,7 @@ __device__ __forceinline__ double unordered(uint64_t k) {
 __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectArgs a) {
     __shared__ uint64_t tot[kBuf2], best_tot[128];
     __shared__ uint32_t idx[kBuf2], best_idx[128], tops[kSelThreads];
-    __shared__ double lses[64];
+    __shared__ double tops_of[64], logs[64];         // lse of a beam = their sum
     __shared__ float score[64];
     __shared__ uint8_t state[64];                    // 0: reads its logits, 1: ended, 2: score -inf
     __shared__ int count;
@@ -616,10 +617,10 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
         const float s = cleaned(a.scores[g * K + k]);
         const bool ended = a.finished != nullptr && a.finished[g * K + k] != 0;
         const int st = s == -INFINITY ? 2 : ended ? 1 : 0;
-        double l = 0.0;
+        double top = -INFINITY, l = 0.0;
         if (st == 0) {
             const ChunkSum *cs = a.sums + ((int64_t)g * K + k) * S;
-            double top = -INFINITY, sum = 0.0;
+            double sum = 0.0;
             for (int c = lane; c < S; c += 32) top = fmax(top, cs[c].top);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -627,12 +628,13 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
                 for (int c = lane; c < S; c += 32) sum += cs[c].sum * (cs[c].top == top ? 1.0 : exp(cs[c].top - top));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = top + log(sum);                      // (no finite logit: not used)
+            l = log(sum);                            // (no finite logit: not used)
         }
         if (lane == 0) {
             score[k] = s;
             state[k] = (uint8_t)st;
-            lses[k] = l;
+            tops_of[k] = top;
+            logs[k] = l;
         }
     }
     __syncthreads();
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
             const uint32_t col = __float_as_uint(x.y);
             if (col == 0xffffffffu) return 0;
             at = (uint32_t)k << 24 | col;
-            return ordered(x.x == -INFINITY ? (double)-INFINITY : (double)score[k] + ((double)x.x - lses[k]));
+            return ordered(x.x == -INFINITY ? (double)-INFINITY : (double)score[k] + (((double)x.x - tops_of[k]) - logs[k]));
         }
         if (r >= n) return 0;                        // n <= vocab columns
         int col = r;
