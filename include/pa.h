@@ -635,7 +635,9 @@ pa_status pa_decode_shared(const pa_decode_shared_params *p, void *stream);
  *    stride >= vocab, and logits aligned to 16 bytes.
  *  - 1 <= beams <= 64, 1 <= num_out <= 128 and <= vocab, vocab < 2^24,
  *    num_groups * beams <= 65535.
- * The workspace may be shared by calls that follow one another.
+ * The workspace may be shared by calls that follow one another; a size reported for
+ * num_groups * beams rows, a vocabulary and num_out serves every call with as many or
+ * fewer of each.
  */
 typedef enum { PA_LOGITS_BF16 = 0, PA_LOGITS_F16 = 1, PA_LOGITS_F32 = 2 } pa_logits_dtype;
 typedef struct {

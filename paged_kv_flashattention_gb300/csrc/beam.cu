@@ -34,6 +34,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pdl.cuh"
@@ -875,16 +877,26 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 // Calls of up to kSmallTiles tiles: a list per chunk of kMostTiles tiles, or of one
 // while the GPU holds all CTAs at once; larger ones: a list per row by two passes.
 // (Constant numbers: the workspace's size is the same on every device.)
+// A smaller call may have more lists than a larger one, so the size reported is the
+// largest of any with as many rows, tiles and entries or fewer: r rows of t tiles have
+// r t lists for r t <= kOneTile, then at most r ceil(t / kMostTiles) <= r t, then r.
 SelectPlan plan_select(const pa_beam_select_params &p) {
+    constexpr int64_t kOneTile = 152 * 4;
     SelectPlan plan{};
     const int64_t rows = (int64_t)p.num_groups * p.beams, tiles = ((int64_t)p.vocab + kTile - 1) / kTile;
-    plan.tiles = rows * tiles <= 152 * 4 ? 1 : rows * tiles <= kSmallTiles ? kMostTiles : 0;
+    plan.tiles = rows * tiles <= kOneTile ? 1 : rows * tiles <= kSmallTiles ? kMostTiles : 0;
     plan.chunks = plan.tiles > 0 ? (int32_t)((tiles + plan.tiles - 1) / plan.tiles) : 1;
     plan.spans = (int32_t)((tiles + kBlockTiles - 1) / kBlockTiles);
-    plan.list_bytes = round16((size_t)rows * plan.chunks * p.num_out * sizeof(float2));
-    plan.sum_bytes = round16((size_t)rows * plan.chunks * sizeof(ChunkSum));
+    auto list_bytes = [&](int64_t lists) { return round16((size_t)lists * p.num_out * sizeof(float2)); };
+    auto sum_bytes = [&](int64_t lists) { return round16((size_t)lists * sizeof(ChunkSum)); };
+    plan.list_bytes = list_bytes(rows * plan.chunks);
+    plan.sum_bytes = sum_bytes(rows * plan.chunks);
     plan.workspace_bytes = plan.list_bytes + plan.sum_bytes;
     if (plan.tiles == 0) plan.workspace_bytes += (size_t)rows * plan.spans * kSelThreads * sizeof(float2);
+    int64_t lists = std::min(rows * tiles, kOneTile);
+    if (rows * tiles > kOneTile)
+        lists = std::max(lists, std::min(rows * ((tiles + kMostTiles - 1) / kMostTiles), (int64_t)kSmallTiles));
+    plan.workspace_any = std::max(plan.workspace_bytes, list_bytes(lists) + sum_bytes(lists));
     return plan;
 }
 

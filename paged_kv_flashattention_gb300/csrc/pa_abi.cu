@@ -657,7 +657,7 @@ static pa_status check_select(const pa_beam_select_params *p) {
 size_t pa_beam_select_workspace_size(const pa_beam_select_params *p) {
     g_last_error[0] = 0;
     if (check_select(p) != PA_OK) return 0;
-    return plan_select(*p).workspace_bytes;
+    return plan_select(*p).workspace_any;
 }
 
 pa_status pa_beam_select(const pa_beam_select_params *p, void *stream) {

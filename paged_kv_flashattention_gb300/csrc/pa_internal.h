@@ -95,6 +95,7 @@ struct SelectPlan {
     int32_t chunks, spans;        // lists of a row, CTAs of a row in the first pass
     size_t list_bytes, sum_bytes;
     size_t workspace_bytes;
+    size_t workspace_any;         // of any call with as many beams, words and num_out or fewer: the size reported
 };
 SelectPlan plan_select(const pa_beam_select_params &p);
 cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan, cudaStream_t stream);
