@@ -626,7 +626,8 @@ pa_status pa_decode_shared(const pa_decode_shared_params *p, void *stream);
  * largest logits are summed in 64 bits, the others in 32: the logarithm is off by
  * about 1e-7, so that totals of different beams that are nearer to one another
  * than that may change places.
- *  - finished (optional): a beam with a non-zero entry has ended; it offers
+ *  - finished (optional): a beam with a non-zero entry has ended (out_finished takes
+ *    the entry along to where the beam goes); it offers
  *    itself with pad_token and total scores[g, k], its logits are not read.
  *  - A logit that is NaN or +inf counts as -inf, as does a score.  Candidates
  *    of total -inf come last (banned words, beams of score -inf, the other
@@ -656,6 +657,8 @@ typedef struct {
     int32_t *out_tokens;         /* device int32 [num_groups, num_out] */
     void *workspace;             /* device, 16-byte aligned */
     size_t workspace_bytes;
+    uint8_t *out_finished;       /* device [num_groups, num_out] or NULL: finished of each one's parent (0 without);
+                                    may be finished itself if num_out = beams */
 } pa_beam_select_params;
 
 size_t pa_beam_select_workspace_size(const pa_beam_select_params *p);

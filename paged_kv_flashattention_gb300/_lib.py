@@ -83,6 +83,7 @@ class BeamSelectParams(ctypes.Structure):
         ("logits", c_p), ("logits_dtype", c_i32), ("logits_stride", c_i64), ("scores", c_p), ("finished", c_p),
         ("pad_token", c_i32), ("num_groups", c_i32), ("beams", c_i32), ("vocab", c_i32), ("num_out", c_i32),
         ("out_scores", c_p), ("out_parents", c_p), ("out_tokens", c_p), ("workspace", c_p), ("workspace_bytes", c_size),
+        ("out_finished", c_p),
     ]
 
 

@@ -959,7 +959,7 @@ def beam_select_workspace_size(num_groups: int, beams: int, vocab: int, num_out:
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None = None, *,
                 finished: torch.Tensor | None = None, pad_token: int = 0, out_scores: torch.Tensor | None = None,
                 parents: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
-                workspace: torch.Tensor | None = None):
+                workspace: torch.Tensor | None = None, out_finished: torch.Tensor | None = None):
     """Beam search's selection (``pa_beam_select``): per group the ``num_out``
     (default: the number of beams) largest of scores + log_softmax(logits)
     over beams and vocabulary.  logits: bf16, fp16 or fp32 [groups * beams, V]
@@ -968,7 +968,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None 
     beam that has ended (it offers itself, with ``pad_token``).  Returns
     (scores fp32, parents int32, tokens int32), each [groups, num_out], best
     first, equal totals by the lower beam, then the lower token; out_scores
-    may be ``scores``."""
+    may be ``scores``.  ``out_finished`` (uint8 or bool [groups, num_out], may be
+    ``finished``) gets each one's parent's entry of ``finished``."""
     dev = logits.device
     if logits.dtype not in _LOGITS_DTYPES:
         raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
@@ -990,12 +991,16 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None 
     if G * K <= 1:
         stride = max(stride, V)
     n = K if num_out is None else int(num_out)
-    if finished is not None:
-        if finished.dtype not in (torch.uint8, torch.bool):
-            raise TypeError(f"finished must be uint8 or bool, got {finished.dtype}")
-        _need(finished, "finished", finished.dtype, dev)
-        if finished.shape != (G, K):
-            raise ValueError("finished must be [groups, beams]")
+    for t, name, width in ((finished, "finished", K), (out_finished, "out_finished", n)):
+        if t is None:
+            continue
+        if t.dtype not in (torch.uint8, torch.bool):
+            raise TypeError(f"{name} must be uint8 or bool, got {t.dtype}")
+        _need(t, name, t.dtype, dev)
+        if t.shape != (G, width):
+            raise ValueError(f"{name} must be [{G}, {width}]")
+    if out_finished is not None and out_finished.dtype == torch.bool and finished is not None and finished.dtype != torch.bool:
+        raise TypeError("out_finished may be bool only if finished is")
     outs = []
     for t, name, dtype in ((out_scores, "out_scores", torch.float32), (parents, "parents", torch.int32),
                            (tokens, "tokens", torch.int32)):
@@ -1013,7 +1018,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None 
     p = _lib.BeamSelectParams(
         logits.data_ptr(), _LOGITS_DTYPES[logits.dtype], stride, scores.data_ptr(), _ptr(finished), int(pad_token), G, K, V, n,
         outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size())
+        workspace.numel() * workspace.element_size(), _ptr(out_finished))
     _call(_lib.load().pa_beam_select, logits, ctypes.byref(p))
     return tuple(outs)
 

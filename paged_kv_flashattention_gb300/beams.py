@@ -7,8 +7,10 @@ are read once), ``select`` (the best continuations over beams and vocabulary)
 and ``advance`` (page tables and partly filled pages follow the chosen beams).
 Lengths, pages, scores and parents stay on the device and nothing waits for it,
 so a whole step can be captured as a CUDA graph and replayed while the lengths
-grow.  Between replays the caller may look at ``tokens`` and ``parents``, set
-``finished`` by its own rule, and refill the list of free pages.
+grow.  ``select`` takes ``finished`` along with the beams, as it does ``scores``:
+the caller ORs in its own rule for the tokens just chosen, within the step or
+between replays.  Between replays it may also look at ``tokens`` and ``parents``
+and refill the list of free pages.
 """
 from __future__ import annotations
 
@@ -117,9 +119,11 @@ class BeamSearch:
 
     def select(self, logits: torch.Tensor):
         """The best ``beams`` continuations of each request, into ``scores``,
-        ``parents`` and ``tokens`` (``beam_select``)."""
+        ``parents`` and ``tokens`` (``beam_select``); a beam's entry of ``finished``
+        becomes its parent's."""
         return api.beam_select(logits, self.scores, self.beams, finished=self.finished, pad_token=self.pad_token,
-                               out_scores=self.scores, parents=self.parents, tokens=self.tokens, workspace=self.workspace)
+                               out_scores=self.scores, parents=self.parents, tokens=self.tokens, workspace=self.workspace,
+                               out_finished=self.finished)
 
     def advance(self, history: torch.Tensor | None = None) -> None:
         """Sequences become the continuations of their parents, in every

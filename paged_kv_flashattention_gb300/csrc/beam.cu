@@ -72,6 +72,7 @@ struct SelectArgs {
     float *out_scores;
     int32_t *out_parents;
     int32_t *out_tokens;
+    uint8_t *out_finished;
 };
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -610,6 +611,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
     __shared__ double tops_of[64], logs[64];         // lse of a beam = their sum
     __shared__ float score[64];
     __shared__ uint8_t state[64];                    // 0: reads its logits, 1: ended, 2: score -inf
+    __shared__ uint8_t flags[64];                    // finished, read before any of it may be overwritten
     __shared__ int count;
     after_previous();
     const int t = threadIdx.x, lane = t & 31, g = blockIdx.x;
@@ -617,8 +619,8 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
     if (t == 0) count = 0;
     for (int k = t >> 5; k < K; k += kSelWarps) {    // a warp per beam: its state, its lse
         const float s = cleaned(a.scores[g * K + k]);
-        const bool ended = a.finished != nullptr && a.finished[g * K + k] != 0;
-        const int st = s == -INFINITY ? 2 : ended ? 1 : 0;
+        const uint8_t flag = a.finished != nullptr ? a.finished[g * K + k] : 0;
+        const int st = s == -INFINITY ? 2 : flag != 0 ? 1 : 0;
         double top = -INFINITY, l = 0.0;
         if (st == 0) {
             const ChunkSum *cs = a.sums + ((int64_t)g * K + k) * S;
@@ -635,6 +637,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
         if (lane == 0) {
             score[k] = s;
             state[k] = (uint8_t)st;
+            flags[k] = flag;
             tops_of[k] = top;
             logs[k] = l;
         }
@@ -721,6 +724,7 @@ __global__ void __launch_bounds__(kSelThreads) select_merge_kernel(const SelectA
         a.out_scores[(int64_t)g * n + e] = (float)unordered(best_tot[e]);
         a.out_parents[(int64_t)g * n + e] = (int)(at >> 24);
         a.out_tokens[(int64_t)g * n + e] = (int)(at & 0xffffffu);
+        if (a.out_finished != nullptr) a.out_finished[(int64_t)g * n + e] = flags[at >> 24];
     }
 }
 
@@ -920,6 +924,7 @@ cudaError_t launch_select(const pa_beam_select_params &p, const SelectPlan &plan
     a.out_scores = p.out_scores;
     a.out_parents = p.out_parents;
     a.out_tokens = p.out_tokens;
+    a.out_finished = p.out_finished;
     const cudaError_t e = p.logits_dtype == PA_LOGITS_F32   ? launch_lists<PA_LOGITS_F32>(a, plan.tiles, stream)
                           : p.logits_dtype == PA_LOGITS_F16 ? launch_lists<PA_LOGITS_F16>(a, plan.tiles, stream)
                                                             : launch_lists<PA_LOGITS_BF16>(a, plan.tiles, stream);

@@ -673,6 +673,8 @@ pa_status pa_beam_select(const pa_beam_select_params *p, void *stream) {
     if (!aligned16(p->logits)) return fail(PA_ERR_INVALID, "logits must be 16-byte aligned");
     if (p->out_scores == p->scores && p->num_out != p->beams)
         return fail(PA_ERR_INVALID, "out_scores may be scores only if num_out is the number of beams");
+    if (p->out_finished != nullptr && p->out_finished == p->finished && p->num_out != p->beams)
+        return fail(PA_ERR_INVALID, "out_finished may be finished only if num_out is the number of beams");
     const SelectPlan plan = plan_select(*p);
     if (p->workspace == nullptr || p->workspace_bytes < plan.workspace_bytes)
         return fail(PA_ERR_INVALID, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes, p->workspace_bytes);
