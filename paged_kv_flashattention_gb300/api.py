@@ -1029,14 +1029,19 @@ _tensor_device, _tensor_bytes = torch.Tensor.get_device, operator.attrgetter("nb
 def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor, seqlens: torch.Tensor,
                  spare_pages: torch.Tensor | None, k_caches, v_caches, *, page_size: int | None = None,
                  prefix_lens: torch.Tensor | None = None, history: torch.Tensor | None = None,
-                 max_seqlen_k: int | None = None) -> None:
+                 max_seqlen_k: int | None = None, kv_dtype: int | None = None) -> None:
     """The paged states follow a selection, in place (``pa_beam_reorder``):
     sequence i of a group becomes the continuation of sequence parents[g, i].
     parents: int32 [groups, beams]; token_table: int32 [rows, width];
     table_idx, seqlens, spare_pages, prefix_lens: int32 [groups * beams], the
     lengths equal within a group; k_caches, v_caches: the pools of every layer
-    (lists, or one tensor each), all of one shape, [num_pages, page_size, ...]
-    or, with ``page_size``, [slots, ...]; history: int32 [groups * beams, T].
+    (lists, or one tensor each), all of one shape, [num_pages, page_size, Hkv, d]
+    or, with ``page_size``, [slots, Hkv, d], of 4-bit rows [num_pages, page_size,
+    row bytes] or [slots, row bytes]; history: int32 [groups * beams, T].
+    ``kv_dtype``, as for ``decode``, tells FP8 from 4-bit pools; without it three
+    dimensions of uint8 are 4-bit pages, unless ``page_size`` is given and either
+    differs from the second one or the third one is a head size (64 or 128 bytes,
+    which no 4-bit row has).
     A moved sequence shares its parent's full pages, and the parent's partly
     filled last page is copied into its spare page; its own last page becomes
     its spare page.  ``spare_pages`` may be None with page size 1.
@@ -1060,16 +1065,20 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
     _need(first, "every pool", dtype, dev)
     if pools[-1].shape != shape:
         raise ValueError("the pools must have one shape")
-    # [num_pages, page_size, ...], or with page_size also [slots, ...]: heads and
-    # elements, or the bytes of a 4-bit row
     dims, P = len(shape), page_size
-    paged = dims == 4 or (dims == 3 and (P is None or (dtype == torch.uint8 and shape[1] == P)))
+    if not 2 <= dims <= 4:
+        raise ValueError("the pools must be [num_pages, page_size, Hkv, d], [slots, Hkv, d] or 4-bit rows")
+    paged = dims == 4
+    if kv_dtype is not None:
+        paged = paged or (dims == 3 and _kv_dtype(first, first, kv_dtype) == PA_KV_FP4)
+    elif dims == 3 and dtype == torch.uint8:
+        paged = P is None or (P == shape[1] and shape[2] not in (64, 128))
     if paged:
         if P is not None and P != shape[1]:
             raise ValueError("page_size does not match the pool shape")
         num_pages, P = shape[0], shape[1]
     elif P is None:
-        raise ValueError("page_size is required for [slots, row] pools")
+        raise ValueError("page_size is required for [slots, ...] pools")
     else:
         num_pages = shape[0] // int(P) if int(P) > 0 else 0
     P = int(P)

@@ -131,4 +131,4 @@ class BeamSearch:
         [num_groups * beams, T]) follow."""
         api.beam_reorder(self.parents, self.token_table, self.table_idx, self.lens, self.spare_pages, self.k_caches,
                          self.v_caches, page_size=self.page_size, prefix_lens=self.prefix_lens, history=history,
-                         max_seqlen_k=self.max_seqlen_k)
+                         max_seqlen_k=self.max_seqlen_k, kv_dtype=self.kv_dtype)
