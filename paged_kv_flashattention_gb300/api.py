@@ -1023,7 +1023,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None 
     return tuple(outs)
 
 
-_tensor_device, _tensor_bytes = torch.Tensor.get_device, operator.attrgetter("nbytes")
+_tensor_device, _tensor_bytes, _tensor_shape = torch.Tensor.get_device, operator.attrgetter("nbytes"), operator.attrgetter("shape")
 
 
 def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor, seqlens: torch.Tensor,
@@ -1055,16 +1055,13 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
     first = pools[0]
     dtype, shape = first.dtype, first.shape
     # every layer's pools at once (30 us for 32 of them one by one); bits are moved,
-    # so that pools of as many bytes are as good as of one type
-    size = first.nbytes
+    # so that elements of as many bytes are as good as of one type
     if (len(set(map(_tensor_device, pools))) != 1 or not all(map(torch.Tensor.is_contiguous, pools))
-            or set(map(_tensor_bytes, pools)) != {size}):
+            or len(set(map(_tensor_bytes, pools))) != 1 or len(set(map(_tensor_shape, pools))) != 1):
         for t in pools:
             _need(t, "every pool", dtype, dev)
         raise ValueError("the pools must have one shape")
     _need(first, "every pool", dtype, dev)
-    if pools[-1].shape != shape:
-        raise ValueError("the pools must have one shape")
     dims, P = len(shape), page_size
     if not 2 <= dims <= 4:
         raise ValueError("the pools must be [num_pages, page_size, Hkv, d], [slots, Hkv, d] or 4-bit rows")

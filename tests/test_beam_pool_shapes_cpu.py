@@ -70,3 +70,15 @@ def test_no_row_of_four_bits_is_a_head_long():
     import paged_kv_flashattention_gb300 as pa
     sizes = {pa.fp4_row_bytes(h, d) for d in (64, 128) for h in range(1, 4096 // d + 1)}     # (all that there are)
     assert not sizes & {64, 128}
+
+
+@pytest.mark.parametrize("place", range(4))
+@pytest.mark.parametrize("other", [(200, 8, 2, 64), (50, 32, 2, 64), (100, 16, 1, 128), (1600, 2, 64), (204800,)])
+def test_every_pool_has_the_same_shape(monkeypatch, place, other):
+    """Pools of as many bytes but of another geometry would be copied at wrong offsets."""
+    pools = [pool(100, 16, 2, 64) for _ in range(4)]
+    assert arguments(monkeypatch, pools) == (100, 16, 128)
+    pools[place] = pool(*other)
+    assert pools[place].nbytes == pools[place - 1].nbytes
+    with pytest.raises(ValueError, match="one shape"):
+        arguments(monkeypatch, pools)
