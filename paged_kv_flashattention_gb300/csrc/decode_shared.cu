@@ -149,6 +149,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
             if (ok) np = max(ranges, 0) * each;
             first = (int64_t)block * kBlockRows + m;
         }
+    } else if (ok && L > 0 && g >= 0 && g < a.sh.num_groups) {
+        const int q0 = a.sh.cu_groups[g];            // none, in a group that has one (the result is right all the same)
+        if (q0 >= 0 && a.sh.prefix_lens[q0] != 0 && lane == 0) raise_error(PA_DEVERR_SEQLENS);
     }
     if (ok && has_tail) {
         const int U = u1 - u0;
