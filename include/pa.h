@@ -597,8 +597,9 @@ pa_status pa_lse_combine(const float *o_partial, const float *lse_partial,
  *    lengths on the device, and the first launch by the bounds: results are
  *    good for any bounds that hold, times best for tight ones.
  *  - The workspace (pa_decode_shared_workspace_size bytes) serves every call
- *    with bounds and counts up to these.  Calls that may run at the same time
- *    need one each.
+ *    with bounds and counts up to these, one without groups among them (which is
+ *    pa_decode's and asks for splits of max_seqlen_k keys).  Calls that may run at
+ *    the same time need one each.
  */
 typedef struct {
     pa_decode_params dec;        /* as for pa_decode; lse optional */

@@ -871,8 +871,7 @@ def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     page-table row of its first sequence, 0 for sequences behind the last
     group.  ``max_prefix`` and ``max_suffix`` bound the keys of a sequence in
     its prefix and behind it (default max_seqlen_k), ``max_group`` the
-    sequences of a group (default B); tight bounds make a small workspace and
-    few idle CTAs."""
+    sequences of a group (default B); tight bounds leave few CTAs idle."""
     dev = q.device
     _need(q, "q", torch.bfloat16, dev)
     if q.dim() != 3:

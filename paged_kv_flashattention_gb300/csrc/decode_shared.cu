@@ -320,6 +320,17 @@ pa_decode_params shared_tail_params(const pa_decode_shared_params &p) {
     return d;
 }
 
+// At least the workspace of any split-KV decode of up to num_seqs sequences of up to
+// max_seqlen_k keys: automatic ranges have 64 keys or more, and 1/32 of the longest
+// sequence or more, so that a shorter bound may need more than this one.
+static size_t split_workspace_any(const pa_decode_params &d, const DecodePlan &plan) {
+    if (d.kv_dtype == PA_KV_FP4 || d.kv_chunk != 0) return plan.workspace_any;
+    const int64_t by_keys = ((int64_t)d.max_seqlen_k + 63) / 64 + 1;
+    const size_t slots = (size_t)d.num_seqs * d.num_q_heads * (by_keys < 33 ? by_keys : 33);
+    return 256 + round256(((size_t)d.num_seqs + 1) * sizeof(int32_t)) + round256(slots * d.head_dim * sizeof(float)) +
+           slots * sizeof(float);
+}
+
 SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
     SharedPlan plan{};
     plan.prefix = p.num_groups > 0 && p.max_prefix > 0 && p.max_group > 0 && p.dec.num_seqs > 0;
@@ -339,17 +350,13 @@ SharedPlan plan_decode_shared(const pa_decode_shared_params &p) {
     const pa_decode_params tail = shared_tail_params(p);
     if (plan.tail) {
         plan.decode = tail.kv_dtype == PA_KV_FP4 ? plan_decode_fp4(tail) : plan_decode(tail);
-        if (tail.kv_dtype != PA_KV_FP4 && tail.kv_chunk == 0) {
-            // automatic ranges: 64 keys or more, and 1/32 of the longest tail or more,
-            // so that a shorter bound may need more than this one
-            const int64_t by_keys = ((int64_t)tail.max_seqlen_k + 63) / 64 + 1;
-            const size_t slots = (size_t)tail.num_seqs * tail.num_q_heads * (by_keys < 33 ? by_keys : 33);
-            plan.decode.workspace_any = 256 + round256(((size_t)tail.num_seqs + 1) * sizeof(int32_t)) +
-                                        round256(slots * tail.head_dim * sizeof(float)) + slots * sizeof(float);
-        }
+        plan.decode.workspace_any = split_workspace_any(tail, plan.decode);
     }
     plan.workspace_bytes = plan.prefix_bytes + plan.decode.workspace_any;
     if (plan.workspace_bytes < 256) plan.workspace_bytes = 256;
+    // (a call without groups decodes every key as pa_decode does)
+    const size_t whole = split_workspace_any(p.dec, p.dec.kv_dtype == PA_KV_FP4 ? plan_decode_fp4(p.dec) : plan_decode(p.dec));
+    plan.workspace_any = whole > plan.workspace_bytes ? whole : plan.workspace_bytes;
     return plan;
 }
 

@@ -615,8 +615,7 @@ size_t pa_decode_shared_workspace_size(const pa_decode_shared_params *p) {
         sizes.dec.k_scale = sizes.dec.v_scale = &some_scale;
     }
     if (check_shared(p != nullptr ? &sizes : nullptr) != PA_OK) return 0;
-    if (p->num_groups == 0) return decode_plan(p->dec).workspace_any;
-    return plan_decode_shared(*p).workspace_bytes;
+    return plan_decode_shared(*p).workspace_any;
 }
 
 pa_status pa_decode_shared(const pa_decode_shared_params *p, void *stream) {

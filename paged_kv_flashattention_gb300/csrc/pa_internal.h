@@ -84,6 +84,7 @@ struct SharedPlan {
     DecodePlan decode;            // of the keys behind the prefixes
     size_t prefix_bytes;
     size_t workspace_bytes;
+    size_t workspace_any;         // of any call with bounds and counts up to these: the size reported
 };
 pa_decode_params shared_tail_params(const pa_decode_shared_params &p);
 SharedPlan plan_decode_shared(const pa_decode_shared_params &p);
