@@ -107,7 +107,8 @@ pa_status pa_device_error(int32_t *bits, void *stream);
  * head scales are factors of the scores and of the output.  FP8 pools hold E4M3
  * codes written by pa_store_kv_fp8 with per-KV-head scales.  On FP8 pools the
  * contractions run in f16 with fp32 accumulation: q * k_scale is rounded to
- * f16 (|q * k_scale| must stay below 65504), P is rounded to f16. */
+ * f16 (|q * k_scale| must stay below 65504; pa_decode_shared keeps the scale out of
+ * q, see there), P is rounded to f16. */
 typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_FP4 = 2 } pa_kv_dtype;
 
 /*
@@ -590,8 +591,12 @@ pa_status pa_lse_combine(const float *o_partial, const float *lse_partial,
  *    sequence, that differs from its group's or has no group, more than
  *    max_suffix keys behind it.  Such a sequence's output is undefined (but
  *    written); nothing outside the pools and the outputs is touched.
- *  - Arithmetic: as pa_prefill over the prefix and pa_decode behind it, on
- *    each type of pool; the partials are 32 bits.
+ *  - Arithmetic: over bf16 and 4-bit pools as pa_prefill over the prefix and
+ *    pa_decode behind it.  Over FP8 pools as over 4-bit ones and not as those two:
+ *    q is rounded to f16 by itself (exact for bf16 values of magnitude 2^-14 ..
+ *    65504; |q| must stay below 65504, and |q * k_scale| need not), k_scale is a
+ *    factor of the scores in 32 bits.  (Without groups the call is pa_decode, and
+ *    its bound on |q * k_scale| holds.)  The partials are 32 bits.
  *  - dec.sliding_window, dec.max_ctas and dec.overlap_previous must be 0.
  *  - The SMs are shared out between prefixes and the keys behind them by the
  *    lengths on the device, and the first launch by the bounds: results are
