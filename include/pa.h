@@ -692,6 +692,12 @@ pa_status pa_beam_select(const pa_beam_select_params *p, void *stream);
  * rows and does not read spare_pages.  No lengths change; the next token's
  * slot is the plan's business (pa_build_batch_from goes on with the last page
  * while it has room).
+ *  - Full pages that no row names any more (of beams that were dropped) are not
+ *    reported: pages are the caller's.  All that a group's rows and spare_pages ever
+ *    name are the pages they named at first and those that its sequences have been
+ *    given since (a plan's slot_mapping / page_size where a position is a multiple of
+ *    page_size); they are free when the request ends, and not before, as any of
+ *    the group's rows may name them.
  *  - prefix_lens (optional): slots below prefix_lens[i] are the same in every
  *    row of the group and are left alone.
  *  - Columns of a row from L on, and rows that table_idx does not name, stay as

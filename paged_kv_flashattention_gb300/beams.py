@@ -11,6 +11,12 @@ grow.  ``select`` takes ``finished`` along with the beams, as it does ``scores``
 the caller ORs in its own rule for the tokens just chosen, within the step or
 between replays.  Between replays it may also look at ``tokens`` and ``parents``
 and refill the list of free pages.
+
+Pages stay the caller's.  A request has the pages that its rows and spare pages
+named at ``start`` and those that ``plan`` has given its beams since
+(``slot_mapping`` // page size where ``positions`` is a multiple of it).  Full
+pages of beams that were dropped are among them and named by no row, so all of
+them return to the free list when the request ends, and not before.
 """
 from __future__ import annotations
 
