@@ -1022,7 +1022,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None 
     return tuple(outs)
 
 
-_tensor_device, _tensor_bytes, _tensor_shape = torch.Tensor.get_device, operator.attrgetter("nbytes"), operator.attrgetter("shape")
+_tensor_device, _element_size, _tensor_shape = torch.Tensor.get_device, torch.Tensor.element_size, operator.attrgetter("shape")
 
 
 def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: torch.Tensor, seqlens: torch.Tensor,
@@ -1056,7 +1056,7 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
     # every layer's pools at once (30 us for 32 of them one by one); bits are moved,
     # so that elements of as many bytes are as good as of one type
     if (len(set(map(_tensor_device, pools))) != 1 or not all(map(torch.Tensor.is_contiguous, pools))
-            or len(set(map(_tensor_bytes, pools))) != 1 or len(set(map(_tensor_shape, pools))) != 1):
+            or len(set(map(_element_size, pools))) != 1 or list(map(_tensor_shape, pools)).count(shape) != len(pools)):
         for t in pools:
             _need(t, "every pool", dtype, dev)
         raise ValueError("the pools must have one shape")
