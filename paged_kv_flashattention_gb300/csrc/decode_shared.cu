@@ -286,7 +286,8 @@ int most_ctas(const pa_decode_shared_params &p) {
 
 // Measured, of a step: 3200 clocks for two tiles of head size 128, 5000 where rows are
 // gathered one by one, 1260 to 1600 over FP8 at 64, 1950 over 4 bits at 128.  The split-KV
-// decode reads 38 GB/s an SM.
+// decode reads 38 GB/s an SM.  One figure per type of pool: other head sizes and groups of
+// a single tile are not measured; a figure that is off costs time only.
 void set_costs(SharedArgs &sh, const pa_decode_shared_params &p) {
     const pa_decode_params &d = p.dec;
     const float bytes = d.kv_dtype == PA_KV_BF16 ? 4.f : d.kv_dtype == PA_KV_FP4 ? 1.125f : 2.f;     // of an element, K and V
