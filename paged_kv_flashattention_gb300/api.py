@@ -951,7 +951,7 @@ def _select_workspace(groups: int, beams: int, vocab: int, num_out: int) -> int:
 
 
 def beam_select_workspace_size(num_groups: int, beams: int, vocab: int, num_out: int) -> int:
-    """Workspace bytes of ``beam_select`` for these sizes."""
+    """Workspace bytes of ``beam_select`` for these sizes and smaller ones."""
     return _select_workspace(int(num_groups), int(beams), int(vocab), int(num_out))
 
 
@@ -1066,7 +1066,7 @@ def beam_reorder(parents: torch.Tensor, token_table: torch.Tensor, table_idx: to
         raise ValueError("the pools must be [num_pages, page_size, Hkv, d], [slots, Hkv, d] or 4-bit rows")
     paged = dims == 4
     if kv_dtype is not None:
-        paged = paged or (dims == 3 and _kv_dtype(first, first, kv_dtype) == PA_KV_FP4)
+        paged = (_kv_dtype(first, first, kv_dtype) == PA_KV_FP4 and dims == 3) or paged
     elif dims == 3 and dtype == torch.uint8:
         paged = P is None or (P == shape[1] and shape[2] not in (64, 128))
     if paged:

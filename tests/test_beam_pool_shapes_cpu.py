@@ -59,10 +59,11 @@ def test_refused(monkeypatch, shape, dtype, kw):
         arguments(monkeypatch, pool(*shape, dtype=dtype), **kw)
 
 
-@pytest.mark.parametrize("dtype,kv", [(torch.bfloat16, FP8), (torch.uint8, BF16), (torch.bfloat16, FP4)])
-def test_kv_dtype_of_another_type(monkeypatch, dtype, kv):
-    with pytest.raises(TypeError):
-        arguments(monkeypatch, pool(100, 16, 144, dtype=dtype), page_size=16, kv_dtype=kv)
+@pytest.mark.parametrize("dtype,kv", [(torch.bfloat16, FP8), (torch.uint8, BF16), (torch.bfloat16, FP4), (torch.uint8, 7)])
+@pytest.mark.parametrize("shape", [(100, 16, 144), (100, 16, 2, 64), (1600, 144)])
+def test_kv_dtype_of_another_type(monkeypatch, shape, dtype, kv):
+    with pytest.raises(ValueError if kv == 7 else TypeError):
+        arguments(monkeypatch, pool(*shape, dtype=dtype), page_size=16, kv_dtype=kv)
 
 
 def test_no_row_of_four_bits_is_a_head_long():
