@@ -3,6 +3,11 @@ import sys
 
 import pytest
 
+# Threads of the oracle that wait for one another sleep: where other work takes the
+# host's CPUs, spinning ones keep the last of them from running (calls of 0.1 ms
+# took 10 to 35).  Read when the OpenMP library is loaded, so before any import of it.
+os.environ.setdefault("OMP_WAIT_POLICY", "passive")
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
