@@ -865,7 +865,7 @@ def decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     """``decode`` of a batch in which groups of consecutive sequences share
     their first keys; each group's prefix is read once (``pa_decode_shared``).
     q bf16 [B, Hq, d] -> out bf16 [B, Hq, d]; lse fp32 [B, Hq]; pools as for
-    ``decode``.  cu_groups: int32 [num_groups + 1], group g is sequences
+    ``decode`` (over FP8 and 4-bit ones |q| must stay below 65504).  cu_groups: int32 [num_groups + 1], group g is sequences
     cu_groups[g] .. cu_groups[g+1] - 1; prefix_lens: int32 [B], the keys that
     sequence b shares with its group, equal within one, read through the
     page-table row of its first sequence, 0 for sequences behind the last
